@@ -10,6 +10,12 @@ The same names as the C ABI: ``pack_planes``, ``pack_scales``,
 ``debug_wait_timeout``; ``BcqWeights`` bundles the packed planes with their
 scales and offsets.  The split-K workspace bcq_gemm needs is kept here, one
 zero-filled buffer per (device, stream), grown on demand.
+
+Beside the binary-coded product: ``quantize_i8``, ``gemm_i8`` and ``linear_i8``
+(8-bit integer codes with a scale for each row of either side), and
+``Kv4Cache`` with ``kv4_append``, ``kv4_read`` and ``kv4_attention`` (a paged
+key/value cache in 4 bits).  Their workspaces are allocated for each call, on
+the call's stream, so calls, streams and captured graphs share none.
 """
 from __future__ import annotations
 
@@ -33,6 +39,7 @@ BCQ_ERR_CUDA = 5
 BCQ_ERR_TIMEOUT = 6
 BCQ_ERR_UNSUPPORTED = 7
 BCQ_ERR_SCRATCH = 8
+BCQ_ERR_PAGE = 9
 NOALLOC_SCRATCH_BYTES = 16 << 20   # BCQ_NOALLOC_SCRATCH_BYTES
 GROUP = 128
 MAX_M = 64
@@ -98,6 +105,24 @@ def lib():
         L.bcq_quantize.argtypes = [P, I, I, I, I, I, P, P, P, P, P]
         L.bcq_quantize_zp.restype = I
         L.bcq_quantize_zp.argtypes = [P, I, I, I, I, I, P, P, P, P, P]
+        Q = ctypes.c_int64
+        L.bcq_quantize_i8.restype = I
+        L.bcq_quantize_i8.argtypes = [P, I, I, I, Q, P, Q, P, P]
+        L.bcq_gemm_i8.restype = I
+        L.bcq_gemm_i8.argtypes = [P, Q, P, P, Q, P, I, I, I, P, I, Q, P]
+        L.bcq_linear_i8_workspace_bytes.restype = S
+        L.bcq_linear_i8_workspace_bytes.argtypes = [I, I]
+        L.bcq_linear_i8.restype = I
+        L.bcq_linear_i8.argtypes = [P, I, Q, P, Q, P, I, I, I, P, Q, P, S, P]
+        L.bcq_kv4_append.restype = I
+        L.bcq_kv4_append.argtypes = [P, P, Q, Q, P, Q, Q, I, I, P, I, P, P, I, P]
+        L.bcq_kv4_read.restype = I
+        L.bcq_kv4_read.argtypes = [P, P, P, I, I, P, I, P, P, I, P]
+        L.bcq_kv4_attention_workspace_bytes.restype = S
+        L.bcq_kv4_attention_workspace_bytes.argtypes = [P, I, I, I, I, I]
+        L.bcq_kv4_attention.restype = I
+        L.bcq_kv4_attention.argtypes = [P, P, Q, Q, I, I, I, P, I, P, P, I, I, I, I, I,
+                                        ctypes.c_float, P, Q, Q, P, P, S, P]
         _lib = L
     return _lib
 
@@ -106,7 +131,10 @@ EXPORTED = ("bcq_status_string", "bcq_version", "bcq_packed_planes_bytes",
             "bcq_pack_planes", "bcq_packed_scales_bytes", "bcq_pack_scales",
             "bcq_workspace_bytes", "bcq_gemm", "bcq_plan_query", "bcq_route_query", "bcq_set_pdl",
             "bcq_gemm_host", "bcq_gemm_noalloc", "bcq_build_lut", "bcq_device_error",
-            "bcq_debug_wait_timeout", "bcq_quantize", "bcq_gemm_zp", "bcq_quantize_zp")
+            "bcq_debug_wait_timeout", "bcq_quantize", "bcq_gemm_zp", "bcq_quantize_zp",
+            "bcq_quantize_i8", "bcq_gemm_i8", "bcq_linear_i8_workspace_bytes", "bcq_linear_i8",
+            "bcq_kv4_append", "bcq_kv4_read", "bcq_kv4_attention_workspace_bytes",
+            "bcq_kv4_attention")
 
 
 def status_string(status: int) -> str:
@@ -557,6 +585,337 @@ def gemm_host(x_host: torch.Tensor, w: BcqWeights, y_host: torch.Tensor,
                                  _ptr(ws), 0 if ws is None else ws.numel(), sh)
     _check(st, "bcq_gemm_host")
     del pr_keep
+
+
+# ------------------------------------------------------- the 8-bit product
+
+_DTYPES = {torch.float16: 0, torch.bfloat16: 1, torch.float32: 2}   # BCQ_F16, BCQ_BF16, BCQ_F32
+I8_MAX_K = 65536
+
+
+def _empty_on(shape, dtype, device, stream):
+    """torch.empty for work on `stream` (the current one when None): memory
+    that the allocator hands out in that stream's order."""
+    if stream is None:
+        return torch.empty(shape, dtype=dtype, device=device)
+    with torch.cuda.stream(stream):
+        t = torch.empty(shape, dtype=dtype, device=device)
+    t.record_stream(torch.cuda.current_stream(device))
+    return t
+
+
+def _need_matrix(t: torch.Tensor, name: str, dtypes, device=None) -> int:
+    """A CUDA matrix of one of `dtypes` whose rows are contiguous; returns the
+    distance of its rows in elements."""
+    if not t.is_cuda:
+        raise ValueError(f"{name} must be a CUDA tensor")
+    if t.dtype not in dtypes:
+        raise ValueError(f"{name} must be one of {[str(d) for d in dtypes]}, got {t.dtype}")
+    if device is not None and t.device != device:
+        raise ValueError(f"{name} is on {t.device}, x on {device}")
+    if t.dim() != 2:
+        raise ValueError(f"{name} must be a matrix")
+    rows, cols = t.shape
+    if cols > 1 and t.stride(1) != 1:
+        raise ValueError(f"{name} must have contiguous rows")
+    if rows <= 1:
+        return -(-cols // 16) * 16     # one row: its distance to the next is never used
+    if t.stride(0) < cols:
+        raise ValueError(f"{name}'s rows overlap")
+    return t.stride(0)
+
+
+def _need_codes(t: torch.Tensor, name: str, device=None) -> int:
+    ld = _need_matrix(t, name, (torch.int8,), device)
+    if ld % 16 or t.data_ptr() % 16:
+        raise ValueError(f"{name}'s rows must start on multiples of 16 bytes (as quantize_i8's do)")
+    return ld
+
+
+def _need_scale(t: torch.Tensor, name: str, rows: int, device) -> None:
+    _need_cuda(t, name, torch.float32)
+    _need_on(t, name, device)
+    if tuple(t.shape) != (rows,):
+        raise ValueError(f"{name} must be [{rows}], got {list(t.shape)}")
+
+
+def _need_product_out(out, M: int, N: int, dtype, device, stream):
+    """(out [M][N] of `dtype`, its row distance): allocated when None."""
+    if out is None:
+        return _empty_on((M, N), dtype, device, stream), N
+    ld = _need_matrix(out, "out", (dtype,), device)
+    if tuple(out.shape) != (M, N):
+        raise ValueError(f"out must be [{M}][{N}], got {list(out.shape)}")
+    return out, ld
+
+
+def quantize_i8(x: torch.Tensor, stream=None):
+    """Rows of x (fp16 or bf16 [M][K]) as 8-bit integers with a scale each
+    (bcq_quantize_i8): (codes int8 [M][K] whose rows start on multiples of 16
+    bytes, scale fp32 [M]); codes * scale is x to half a step.  Activations: a
+    row per token; weights, once: a row per output channel."""
+    ldx = _need_matrix(x, "x", (torch.float16, torch.bfloat16))
+    M, K = x.shape
+    dev = x.device
+    ldq = -(-K // 16) * 16
+    q = _empty_on((M, ldq), torch.int8, dev, stream)
+    scale = _empty_on((M,), torch.float32, dev, stream)
+    with _on(dev):
+        _check(lib().bcq_quantize_i8(_ptr(x), _DTYPES[x.dtype], M, K, ldx, _ptr(q), ldq,
+                                     _ptr(scale), _stream(stream, dev)), "bcq_quantize_i8")
+    return q[:, :K], scale
+
+
+def gemm_i8(x: torch.Tensor, x_scale: torch.Tensor, w: torch.Tensor, w_scale: torch.Tensor,
+            dtype=torch.float16, out: torch.Tensor | None = None, stream=None) -> torch.Tensor:
+    """y[m][n] = x_scale[m] w_scale[n] sum_k x[m][k] w[n][k] (bcq_gemm_i8) for
+    int8 codes x [M][K] and w [N][K] (rows on multiples of 16 bytes) and fp32
+    scales [M] and [N]; y is fp16, bf16 or fp32."""
+    if dtype not in _DTYPES:
+        raise ValueError("dtype must be float16, bfloat16 or float32")
+    ldx = _need_codes(x, "x")
+    dev = x.device
+    ldw = _need_codes(w, "w", dev)
+    M, K = x.shape
+    N = w.shape[0]
+    if w.shape[1] != K:
+        raise ValueError(f"w must be [N][{K}], got {list(w.shape)}")
+    _need_scale(x_scale, "x_scale", M, dev)
+    _need_scale(w_scale, "w_scale", N, dev)
+    out, ldy = _need_product_out(out, M, N, dtype, dev, stream)
+    with _on(dev):
+        _check(lib().bcq_gemm_i8(_ptr(x), ldx, _ptr(x_scale), _ptr(w), ldw, _ptr(w_scale), M, N, K,
+                                 _ptr(out), _DTYPES[dtype], max(ldy, N), _stream(stream, dev)),
+               "bcq_gemm_i8")
+    return out
+
+
+def linear_i8(x: torch.Tensor, w: torch.Tensor, w_scale: torch.Tensor,
+              out: torch.Tensor | None = None, stream=None) -> torch.Tensor:
+    """y = x W^T for fp16 or bf16 x [M][K] and an 8-bit weight (codes w [N][K],
+    w_scale [N]): quantize_i8 of x's rows and gemm_i8 in one call
+    (bcq_linear_i8); y [M][N] has x's type."""
+    ldx = _need_matrix(x, "x", (torch.float16, torch.bfloat16))
+    dev = x.device
+    ldw = _need_codes(w, "w", dev)
+    M, K = x.shape
+    N = w.shape[0]
+    if w.shape[1] != K:
+        raise ValueError(f"w must be [N][{K}], got {list(w.shape)}")
+    _need_scale(w_scale, "w_scale", N, dev)
+    out, ldy = _need_product_out(out, M, N, x.dtype, dev, stream)
+    need = int(lib().bcq_linear_i8_workspace_bytes(M, K))
+    ws = _empty_on((max(need, 16),), torch.uint8, dev, stream)
+    with _on(dev):
+        _check(lib().bcq_linear_i8(_ptr(x), _DTYPES[x.dtype], ldx, _ptr(w), ldw, _ptr(w_scale),
+                                   M, N, K, _ptr(out), max(ldy, N), _ptr(ws), ws.numel(),
+                                   _stream(stream, dev)), "bcq_linear_i8")
+    return out
+
+
+# ---------------------------------------------------- the cache in 4 bits
+
+KV4_GROUP = 64
+
+
+class _Kv4(ctypes.Structure):
+    _fields_ = [("k", ctypes.c_void_p), ("k_param", ctypes.c_void_p), ("v", ctypes.c_void_p),
+                ("v_param", ctypes.c_void_p), ("pages", ctypes.c_int), ("heads", ctypes.c_int),
+                ("page_size", ctypes.c_int), ("head_dim", ctypes.c_int)]
+
+
+@dataclass(frozen=True)
+class Kv4Cache:
+    """A paged key/value cache in 4 bits: codes uint8 [pages][heads][page_size]
+    [D / 2] (byte b holds values 2b, low, and 2b + 1, high) and (scale, offset)
+    fp16 [pages][heads][page_size][D / 64][2] of K and of V."""
+    k: torch.Tensor
+    k_param: torch.Tensor
+    v: torch.Tensor
+    v_param: torch.Tensor
+
+    def __post_init__(self):
+        for name in ("k", "v"):
+            code, param = getattr(self, name), getattr(self, name + "_param")
+            _need_cuda(code, name, torch.uint8)
+            _need_cuda(param, name + "_param", torch.float16)
+            if code.dim() != 4 or code.shape[3] not in (32, 64, 128):
+                raise ValueError(f"{name} must be [pages][heads][page_size][D / 2], D 64, 128 or 256")
+            if tuple(param.shape) != (*code.shape[:3], code.shape[3] * 2 // KV4_GROUP, 2):
+                raise ValueError(f"{name}_param must be [pages][heads][page_size][D / 64][2]")
+        if self.k.shape != self.v.shape:
+            raise ValueError("k and v must have the same shape")
+        if self.k.shape[2] % 16 or 0 in self.k.shape:
+            raise ValueError("page_size must be a multiple of 16, and no size zero")
+        for t in (self.k_param, self.v, self.v_param):
+            if t.device != self.k.device:
+                raise ValueError(f"the cache is on {self.k.device} and {t.device}")
+
+    @classmethod
+    def empty(cls, pages: int, heads: int, page_size: int, head_dim: int, device="cuda"):
+        """A new cache; its memory holds what was there before."""
+        def part():
+            return (torch.empty((pages, heads, page_size, head_dim // 2), dtype=torch.uint8,
+                                device=device),
+                    torch.empty((pages, heads, page_size, head_dim // KV4_GROUP, 2),
+                                dtype=torch.float16, device=device))
+        return cls(*part(), *part())
+
+    @property
+    def head_dim(self) -> int:
+        return self.k.shape[3] * 2
+
+    @property
+    def heads(self) -> int:
+        return self.k.shape[1]
+
+    def _c(self):
+        pages, heads, page_size, half = self.k.shape
+        return _Kv4(self.k.data_ptr(), self.k_param.data_ptr(), self.v.data_ptr(),
+                    self.v_param.data_ptr(), pages, heads, page_size, 2 * half)
+
+
+def _need_places(cache: Kv4Cache, table, kv_len, cu, T: int):
+    """(B, table_width) of int32 tables on the cache's device."""
+    dev = cache.k.device
+    for t, name in ((table, "table"), (kv_len, "kv_len"), (cu, "cu")):
+        if t is not None:
+            _need_cuda(t, name, torch.int32)
+            if t.device != dev:
+                raise ValueError(f"{name} is on {t.device}, the cache on {dev}")
+    if table.dim() != 2 or 0 in table.shape:
+        raise ValueError("table must be [B][pages of a sequence]")
+    B, W = table.shape
+    if tuple(kv_len.shape) != (B,):
+        raise ValueError(f"kv_len must be [{B}]")
+    if cu is None:
+        if T != B:
+            raise ValueError(f"without cu there is a row for each of the {B} sequences, got {T}")
+    elif tuple(cu.shape) != (B + 1,):
+        raise ValueError(f"cu must be [{B + 1}]")
+    return B, W
+
+
+def _need_heads(t: torch.Tensor, name: str, cache: Kv4Cache, heads: int | None, dtype=None):
+    """Rows [T][heads][D], fp16 or bf16, each vector contiguous; returns the
+    distances (rows, heads) in elements."""
+    if not t.is_cuda or t.device != cache.k.device:
+        raise ValueError(f"{name} is on {t.device}, the cache on {cache.k.device}")
+    if t.dtype not in (torch.float16, torch.bfloat16) or (dtype is not None and t.dtype != dtype):
+        raise ValueError(f"{name} must be {dtype or 'float16 or bfloat16'}, got {t.dtype}")
+    D = cache.head_dim
+    if t.dim() != 3 or t.shape[2] != D or (heads is not None and t.shape[1] != heads):
+        raise ValueError(f"{name} must be [T][{'heads' if heads is None else heads}][{D}], "
+                         f"got {list(t.shape)}")
+    ld, hd = t.stride(0), t.stride(1)
+    if t.shape[0] <= 1:
+        ld = 0
+    if t.shape[1] <= 1:
+        hd = 0
+    if t.stride(2) != 1 or ld % 8 or hd % 8 or t.data_ptr() % 16:
+        raise ValueError(f"{name}'s vectors must be contiguous and start on multiples of 16 bytes")
+    return ld, hd
+
+
+def kv4_append(cache: Kv4Cache, k: torch.Tensor, v: torch.Tensor, table: torch.Tensor,
+               kv_len: torch.Tensor, cu: torch.Tensor | None = None, stream=None) -> None:
+    """Write rows of K and V (fp16 or bf16 [T][heads][D], any row and head
+    distance) into the cache (bcq_kv4_append).  kv_len [B] counts the new
+    tokens in: row i of a sequence's n rows cu[b]..cu[b + 1] - 1 goes to
+    position kv_len - n + i.  Without cu each sequence has one row."""
+    T = k.shape[0]
+    ldk, hdk = _need_heads(k, "k", cache, cache.heads)
+    ldv, hdv = _need_heads(v, "v", cache, cache.heads, k.dtype)
+    if v.shape[0] != T:
+        raise ValueError("k and v must have as many rows")
+    B, W = _need_places(cache, table, kv_len, cu, T)
+    dev = cache.k.device
+    with _on(dev):
+        _check(lib().bcq_kv4_append(ctypes.byref(cache._c()), _ptr(k), ldk, hdk, _ptr(v), ldv, hdv,
+                                    _DTYPES[k.dtype], T, _ptr(table), W, _ptr(kv_len), _ptr(cu), B,
+                                    _stream(stream, dev)), "bcq_kv4_append")
+
+
+def kv4_read(cache: Kv4Cache, table: torch.Tensor, kv_len: torch.Tensor,
+             cu: torch.Tensor | None = None, tokens: int | None = None, dtype=torch.float16,
+             k: torch.Tensor | None = None, v: torch.Tensor | None = None, stream=None):
+    """What the cache holds of the last n tokens of each sequence
+    (bcq_kv4_read), the reverse of kv4_append: (k, v) [T][heads][D] of `dtype`
+    (fp16, bf16, fp32), T = tokens (or k's rows; without cu, one of each
+    sequence).  Rows that cu gives to no sequence are left as they were."""
+    if dtype not in _DTYPES:
+        raise ValueError("dtype must be float16, bfloat16 or float32")
+    if (k is None) != (v is None):
+        raise ValueError("give both k and v or neither")
+    T = k.shape[0] if k is not None else table.shape[0] if tokens is None and cu is None else tokens
+    if T is None:
+        raise ValueError("with cu, give tokens (or k and v)")
+    T = int(T)
+    B, W = _need_places(cache, table, kv_len, cu, T)
+    dev = cache.k.device
+    shape = (T, cache.heads, cache.head_dim)
+    if k is None:
+        k, v = _empty_on(shape, dtype, dev, stream), _empty_on(shape, dtype, dev, stream)
+    else:
+        for t, name in ((k, "k"), (v, "v")):
+            _need_cuda(t, name, dtype)
+            if tuple(t.shape) != shape or t.device != dev or t.data_ptr() % 16:
+                raise ValueError(f"{name} must be {list(shape)} on {dev}, 16-byte aligned")
+    with _on(dev):
+        _check(lib().bcq_kv4_read(ctypes.byref(cache._c()), _ptr(k), _ptr(v), _DTYPES[dtype], T,
+                                  _ptr(table), W, _ptr(kv_len), _ptr(cu), B, _stream(stream, dev)),
+               "bcq_kv4_read")
+    return k, v
+
+
+def kv4_attention(q: torch.Tensor, cache: Kv4Cache, table: torch.Tensor, kv_len: torch.Tensor,
+                  cu: torch.Tensor | None = None, max_q: int | None = None,
+                  max_kv: int | None = None, causal: bool = True, window: int = 0,
+                  scale: float | None = None, out: torch.Tensor | None = None,
+                  return_lse: bool = False, stream=None):
+    """Attention of rows q (fp16 or bf16 [T][q_heads][D], any row and head
+    distance) over the cache (bcq_kv4_attention): out [T][q_heads][D] of q's
+    type, with return_lse also the logarithm of each row's sum of exponentials,
+    fp32 [T][q_heads].  The new tokens' own K and V are appended first.
+
+    cu gives each sequence its rows (without it, one each); max_q is the most
+    rows that a sequence has (T when not given), max_kv the plan's guess at the
+    longest kv_len (the table's width when not given; any value is right, a
+    near one fast); window > 0 lets a row see that many positions, its own the
+    last; scale is 1 / sqrt(D) when not given.  A row that sees nothing gives
+    zeros and -inf; rows that cu gives to no sequence are left as they were."""
+    D = cache.head_dim
+    ldq, hdq = _need_heads(q, "q", cache, None)
+    T, H = q.shape[0], q.shape[1]
+    if H == 0 or H % cache.heads:
+        raise ValueError(f"q's heads must be a multiple of the cache's {cache.heads}, got {H}")
+    B, W = _need_places(cache, table, kv_len, cu, T)
+    dev = cache.k.device
+    if out is None:
+        out = _empty_on((T, H, D), q.dtype, dev, stream)
+        ldo, hdo = H * D, D
+    else:
+        ldo, hdo = _need_heads(out, "out", cache, H, q.dtype)
+        if out.shape[0] != T:
+            raise ValueError(f"out must have {T} rows")
+        if (T > 1 and ldo < D) or (H > 1 and hdo < D) or (
+                T > 1 and H > 1 and ldo < (H - 1) * hdo + D and hdo < (T - 1) * ldo + D):
+            raise ValueError("out's vectors overlap")
+    lse = _empty_on((T, H), torch.float32, dev, stream) if return_lse else None
+    if max_q is None:
+        max_q = 1 if cu is None else max(T, 1)
+    if max_kv is None:
+        max_kv = W * cache.k.shape[2]
+    c = ctypes.byref(cache._c())
+    need = int(lib().bcq_kv4_attention_workspace_bytes(c, T, H, B, int(max_q), int(max_kv)))
+    ws = _empty_on((need,), torch.uint8, dev, stream) if need else None
+    with _on(dev):
+        _check(lib().bcq_kv4_attention(
+            c, _ptr(q), ldq, hdq, _DTYPES[q.dtype], T, H, _ptr(table), W, _ptr(kv_len), _ptr(cu), B,
+            int(max_q), int(max_kv), int(bool(causal)), int(window),
+            D ** -0.5 if scale is None else float(scale), _ptr(out), ldo, hdo, _ptr(lse), _ptr(ws),
+            need, _stream(stream, dev)), "bcq_kv4_attention")
+    return (out, lse) if return_lse else out
 
 
 def build_lut(x: torch.Tensor, stream=None):

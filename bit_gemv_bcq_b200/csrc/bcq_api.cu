@@ -471,6 +471,7 @@ const char* bcq_status_string(int status) {
     case BCQ_ERR_TIMEOUT: return "BCQ_ERR_TIMEOUT: a bounded wait in a kernel ran out";
     case BCQ_ERR_UNSUPPORTED: return "BCQ_ERR_UNSUPPORTED: request not handled by this build";
     case BCQ_ERR_SCRATCH: return "BCQ_ERR_SCRATCH: the call needs more than the built-in scratch";
+    case BCQ_ERR_PAGE: return "BCQ_ERR_PAGE: a page or length outside the cache";
     default: return "BCQ_ERR_UNKNOWN";
   }
 }
@@ -646,6 +647,12 @@ bcq_status bcq_build_lut(const uint16_t* x, int M, int K, float* lut, float* gro
 bcq_status bcq_device_error(void* stream) {
   int code = 0;
   if (read_and_clear_device_error((cudaStream_t)stream, &code) != cudaSuccess) return BCQ_ERR_CUDA;
+  // the words of the other translation units: all are cleared, the first set one is reported
+  for (auto read : {read_and_clear_i8_error, read_and_clear_kv4_error}) {
+    int more = 0;
+    if (read(&more) != cudaSuccess) return BCQ_ERR_CUDA;
+    if (code == 0) code = more;
+  }
   return (bcq_status)code;
 }
 

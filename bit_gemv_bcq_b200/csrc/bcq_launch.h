@@ -52,6 +52,11 @@ cudaError_t launch_wait_probe(unsigned long long limit_ns, cudaStream_t st);
 // Synchronises st, returns the device error word in *code and clears it.
 cudaError_t read_and_clear_device_error(cudaStream_t st, int* code);
 
+// As read_and_clear_device_error, for the kernels of bcq_i8.cu and of
+// bcq_kv4.cu, after the stream's synchronisation.
+cudaError_t read_and_clear_i8_error(int* code);
+cudaError_t read_and_clear_kv4_error(int* code);
+
 // The argument checks of bcq_gemm (defined in bcq_api.cu).
 bcq_status check_gemm_args(const uint16_t* x, const uint32_t* planes,
                            const uint16_t* const alpha[4], const uint16_t* z, int p,

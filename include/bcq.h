@@ -58,7 +58,8 @@ typedef enum bcq_status {
   BCQ_ERR_CUDA = 5,         /* a CUDA runtime call or launch failed            */
   BCQ_ERR_TIMEOUT = 6,      /* a bounded wait inside a kernel ran out          */
   BCQ_ERR_UNSUPPORTED = 7,  /* valid request this build does not handle (e.g. group != 128) */
-  BCQ_ERR_SCRATCH = 8       /* bcq_gemm_noalloc: the call needs more scratch than it has */
+  BCQ_ERR_SCRATCH = 8,      /* bcq_gemm_noalloc: the call needs more scratch than it has */
+  BCQ_ERR_PAGE = 9          /* a kernel met a page or a length that the cache does not have */
 } bcq_status;
 
 #define BCQ_GROUP 128       /* columns per scale group                          */
@@ -367,6 +368,202 @@ bcq_status bcq_quantize(const uint16_t* w, int N, int K, int p_L, int p_H, int r
 bcq_status bcq_quantize_zp(const uint16_t* w, int N, int K, int p_L, int p_H, int rounds,
                            uint32_t* planes, uint16_t* const alpha[4], uint16_t* const z[4],
                            double* sse, void* stream);
+
+/* ------------------------------------------------ the 8-bit integer product
+ *
+ * For layers that are kept at 8 bits next to the binary-coded ones, and for
+ * prompts of more rows than BCQ_MAX_M:
+ *   y[m][n] = sx[m] * sw[n] * sum_k x[m][k] * w[n][k]
+ * with signed 8-bit codes, a scale for each row of x (token) and of w (output
+ * channel), and an exact 32-bit sum.
+ */
+
+/* Element types of the entry points that take one. */
+enum { BCQ_F16 = 0, BCQ_BF16 = 1, BCQ_F32 = 2 };
+
+#define BCQ_I8_MAX_K 65536  /* |sum| <= 2^14 * 2^16 stays below 2^31 */
+
+/*
+ * Rows to 8-bit codes: with a = max_k |x[m][k]|,
+ *   scale[m] = a / 127 (fp32),  q[m][k] = 127 x[m][k] / a rounded to the
+ * nearest integer, halves to the even one -- decided exactly, so the codes do
+ * not depend on the order of any operation.  A row of zeros gets scale 0 and
+ * codes 0; a row that holds an infinity or a NaN gets scale NaN and codes 0
+ * (its products are then NaN).  For activations (a row per token) and, once,
+ * for weights (a row per output channel).
+ *
+ *   x      device, [M][K] of `dtype` (BCQ_F16 or BCQ_BF16), rows ldx elements
+ *          apart; 2-byte aligned.
+ *   q      device, int8, rows ldq bytes apart, overwritten in columns 0..K-1;
+ *          base 16-byte aligned, ldq a multiple of 16.
+ *   scale  device, fp32 [M], overwritten.
+ *   M      0.. (0 = nothing to do);  K  1..BCQ_I8_MAX_K.
+ *   ldx, ldq >= K.
+ * Errors: NULL -> BCQ_ERR_NULL; sizes or row distances -> BCQ_ERR_SHAPE;
+ * misaligned -> BCQ_ERR_ALIGN; another dtype -> BCQ_ERR_UNSUPPORTED.
+ */
+bcq_status bcq_quantize_i8(const void* x, int dtype, int M, int K, int64_t ldx, int8_t* q,
+                           int64_t ldq, float* scale, void* stream);
+
+/*
+ * The product from codes and scales.
+ *
+ *   x, w   device, int8 [M][K] and [N][K], rows ldx / ldw bytes apart; bases
+ *          16-byte aligned, row distances multiples of 16 and >= K.  Bytes
+ *          between K and the row distance are not read as data.
+ *   sx, sw device, fp32 [M] and [N], 4-byte aligned.
+ *   y      device, [M][N] of `dtype` (BCQ_F16, BCQ_BF16, BCQ_F32), rows ldy
+ *          >= N elements apart, aligned to its element; overwritten in columns
+ *          0..N-1.
+ *   M      0.. (0 = nothing to do);  N  1..;  K  1..BCQ_I8_MAX_K.
+ * The sum is exact; y = (float)sum * sx[m] * sw[n] in fp32, rounded once to
+ * `dtype` (nearest even; fp16 overflow becomes an infinity).
+ * Errors as for bcq_quantize_i8.
+ */
+bcq_status bcq_gemm_i8(const int8_t* x, int64_t ldx, const float* sx, const int8_t* w,
+                       int64_t ldw, const float* sw, int M, int N, int K, void* y, int dtype,
+                       int64_t ldy, void* stream);
+
+/* Bytes of workspace bcq_linear_i8 needs: the codes and scales of M rows of K
+ * columns.  0 for invalid sizes. */
+size_t bcq_linear_i8_workspace_bytes(int M, int K);
+
+/*
+ * bcq_quantize_i8 of x followed by bcq_gemm_i8, in one call: y = x . W^T for
+ * 16-bit activations and an 8-bit weight; y has x's type.  The product's
+ * weight tiles are on their way while x is quantised.
+ *
+ *   workspace  device, bcq_linear_i8_workspace_bytes(M, K) bytes, 16-byte
+ *              aligned; needs no initial value and keeps none.  Calls that
+ *              may run at the same time need workspaces of their own.
+ * Every other argument and error as above (workspace too small or NULL ->
+ * BCQ_ERR_NULL).
+ */
+bcq_status bcq_linear_i8(const void* x, int dtype, int64_t ldx, const int8_t* w, int64_t ldw,
+                         const float* sw, int M, int N, int K, void* y, int64_t ldy,
+                         void* workspace, size_t workspace_bytes, void* stream);
+
+/* --------------------------------------------- a key/value cache in 4 bits
+ *
+ * K and V of past tokens, paged, in the asymmetric group-wise form that the
+ * weights have (AnyBCQ page, "训练策略"): a group of BCQ_KV4_GROUP values of a
+ * head's vector is 4-bit codes c with a scale a and an offset z, each code
+ * standing for a c + z.  Attention contracts the codes and applies scales and
+ * offsets to the results.
+ *
+ *   k, v              device, uint8 [pages][heads][page_size][D / 2]: byte b
+ *                     of a vector holds value 2b in its low four bits and
+ *                     value 2b + 1 in its high four; 16-byte aligned.
+ *   k_param, v_param  device, fp16 [pages][heads][page_size][D / 64][2]: (a, z)
+ *                     of each group; 16-byte aligned.
+ *   table             device, int32 [B][table_width]: position j of sequence b
+ *                     is at page table[b][j / page_size], offset j %
+ *                     page_size.
+ *   kv_len            device, int32 [B]: tokens of each sequence in the cache,
+ *                     the ones of this call among them; at most table_width *
+ *                     page_size.  May be 0.
+ *   cu                device, int32 [B + 1]: this call's rows cu[b]..cu[b+1]-1
+ *                     belong to sequence b, ascending from cu[0] >= 0 to cu[B]
+ *                     <= T.  Row i of the n rows of a sequence is its position
+ *                     kv_len - n + i.  Rows outside cu[0]..cu[B]-1 are neither
+ *                     read nor written.  NULL: a row for each sequence, in
+ *                     order (T must be B).
+ * Lengths and tables are read on the device, when the kernels run (a captured
+ * call may be replayed with others).  A kernel that meets a page outside
+ * 0..pages-1, a position below 0 or a length above the table touches nothing
+ * there and records BCQ_ERR_PAGE (bcq_device_error).
+ */
+#define BCQ_KV4_GROUP 64
+
+typedef struct bcq_kv4 {
+  uint8_t* k;
+  uint16_t* k_param;
+  uint8_t* v;
+  uint16_t* v_param;
+  int pages;      /* 1..                                                        */
+  int heads;      /* key/value heads, 1..                                       */
+  int page_size;  /* tokens of a page: a multiple of 16                         */
+  int head_dim;   /* D: 64, 128 or 256                                          */
+} bcq_kv4;
+
+/*
+ * Quantises this call's rows of K and V into the cache.  For each group: lo,
+ * hi = its least and greatest value, z = fp16(lo), a = fp16((hi - lo) / 15,
+ * each operation rounded to fp32), c = (x - z) / a rounded to the nearest
+ * integer (halves to the even one, decided exactly) and clamped to 0..15; a =
+ * 0 gives c = 0.  A group with a value that is not finite, or beyond
+ * +-60000 (the cache's range), gets a = z = NaN: what reads it becomes NaN.
+ *
+ *   k, v   device, [T][heads][D] of `dtype` (BCQ_F16 or BCQ_BF16): rows
+ *          ld_k / ld_v and heads hd_k / hd_v elements apart, a vector's D
+ *          values contiguous; bases 16-byte aligned, distances multiples of 8.
+ *   T      rows of k and v; rows cu[B].. are not read.  cu[B] <= T.
+ * A position must not be written by two rows of one call (two sequences may
+ * share pages that neither appends to).
+ * Errors: NULL -> BCQ_ERR_NULL; sizes -> BCQ_ERR_SHAPE; misaligned ->
+ * BCQ_ERR_ALIGN; head_dim or dtype -> BCQ_ERR_UNSUPPORTED.
+ */
+bcq_status bcq_kv4_append(const bcq_kv4* cache, const void* k, int64_t ld_k, int64_t hd_k,
+                          const void* v, int64_t ld_v, int64_t hd_v, int dtype, int T,
+                          const int32_t* table, int table_width, const int32_t* kv_len,
+                          const int32_t* cu, int B, void* stream);
+
+/*
+ * The reverse: the values a c + z that the cache holds for the last n tokens
+ * of each sequence, in rows cu[b]..cu[b+1]-1 of k and v.
+ *
+ *   k, v   device, [T][heads][D] of `dtype` (BCQ_F16, BCQ_BF16, BCQ_F32),
+ *          contiguous, 16-byte aligned; a c + z in fp32, rounded once.  Rows
+ *          that belong to no sequence are left as they were; a position that
+ *          cannot be read (see above) gives zeros.
+ */
+bcq_status bcq_kv4_read(const bcq_kv4* cache, void* k, void* v, int dtype, int T,
+                        const int32_t* table, int table_width, const int32_t* kv_len,
+                        const int32_t* cu, int B, void* stream);
+
+/*
+ * Bytes of workspace for bcq_kv4_attention with these sizes (0 for invalid
+ * ones).  It depends on the host's bounds only, never on the lengths.
+ */
+size_t bcq_kv4_attention_workspace_bytes(const bcq_kv4* cache, int T, int q_heads, int B,
+                                         int max_q, int max_kv);
+
+/*
+ * Attention of this call's rows over the cache (which holds their own K and V
+ * already, where they are to be seen):
+ *   out[t][h] = sum_j p_j V_j,  p = softmax_j(scale * q[t][h] . K_j),
+ * with the key/value head h / (q_heads / heads) and j over the positions
+ * 0..kv_len-1 of t's sequence, those that the masks leave: with causal != 0 j
+ * <= pos(t) = kv_len - n + i, and with window > 0 j > pos(t) - window.  A row
+ * that nothing is left for gives zeros (and lse -infinity).
+ *
+ *   q       device, [T][q_heads][D] of `dtype` (BCQ_F16 or BCQ_BF16), rows
+ *           ld_q and heads hd_q elements apart; base 16-byte aligned,
+ *           distances multiples of 8.
+ *   out     device, the same type, rows ld_o and heads hd_o elements apart;
+ *           same alignment.
+ *   lse     device, fp32 [T][q_heads], or NULL: log sum_j exp(scale * q . K_j).
+ *   q_heads a multiple of heads, at most 128 times as many.
+ *   max_q   no sequence has more rows than this in the call (rows behind it
+ *           are left as they were, and BCQ_ERR_SHAPE is recorded).
+ *   max_kv  the plan's guess at the longest kv_len, 1..; longer ones are
+ *           computed all the same.
+ *   scale   a finite factor.
+ *   workspace, workspace_bytes
+ *           device, bcq_kv4_attention_workspace_bytes(..) bytes, 16-byte
+ *           aligned (NULL allowed when that is 0); needs no initial value and
+ *           keeps none.  Calls that may run at the same time need workspaces
+ *           of their own.
+ * Scores, sums and outputs are fp32 until the last rounding.  Results do not
+ * depend on scheduling.
+ * Errors as for bcq_kv4_append; a scale that is not finite -> BCQ_ERR_SHAPE.
+ */
+bcq_status bcq_kv4_attention(const bcq_kv4* cache, const void* q, int64_t ld_q, int64_t hd_q,
+                             int dtype, int T, int q_heads, const int32_t* table,
+                             int table_width, const int32_t* kv_len, const int32_t* cu, int B,
+                             int max_q, int max_kv, int causal, int window, float scale,
+                             void* out, int64_t ld_o, int64_t hd_o, float* lse, void* workspace,
+                             size_t workspace_bytes, void* stream);
 
 /*
  * The lookup table and group sums exactly as the GEMV kernel builds them in

@@ -1,0 +1,549 @@
+"""The 4-bit key/value cache on the GPU against the fp64 oracle (oracle/kv4.py).
+
+Codes, scales and offsets have to be the oracle's, bit for bit, and what is
+read back is a c + z in fp32 (one rounding) rounded to its type.
+
+Attention's tolerance counts its roundings, each at most half a step of its
+type, u = 2^-11 for fp16 and e = 2^-24 for fp32.  A value of K or V may be
+rounded to fp16 once (u of its magnitude a c + |z|), and p or p a once (u):
+  scores    ds <= S (u + 4 D e) with S = |scale| sum |q| (a c + |z|), the sums
+            over D and the two scalings in fp32; exp2's argument, up to
+            |s| log2 e < 2 S, is rounded to fp32 and its result is good to a
+            few steps: 16 e (1 + S) more;
+  weights   p is off by at most 2 ds of itself (numerator and sum), and by u;
+  output    A (2 ds + 2 u + n 4 e) with A = sum p (a c + |z|), n positions
+            summed in fp32, and half a step of the output's type;
+  lse       ds, n 4 e and fp32's own step.
+"""
+import numpy as np
+import pytest
+import torch
+
+from bit_gemv_bcq_b200 import api
+from oracle import kv4
+
+pytestmark = pytest.mark.gpu
+
+F16, BF16, F32 = torch.float16, torch.bfloat16, torch.float32
+
+
+@pytest.fixture(scope="module", autouse=True)
+def _cuda():
+    if not torch.cuda.is_available():
+        pytest.skip("no CUDA device")
+    api.lib()
+    yield
+    assert api.device_error() == api.BCQ_OK
+
+
+def _i32(v):
+    return torch.tensor(v, dtype=torch.int32, device="cuda")
+
+
+def _f64(t):
+    return t.double().cpu().numpy()
+
+
+class Case:
+    """A cache of drawn codes behind a shuffled table; NaN wherever no token is."""
+
+    def __init__(self, lens, new, heads, D, page_size, seed=0, extra=0, spare=2):
+        self.lens, self.new = list(lens), list(new)
+        B = len(lens)
+        rng = np.random.default_rng(seed)
+        W = max(1, -(-max(max(lens), 1) // page_size)) + extra
+        pages = W * B + spare
+        self.table = rng.permutation(pages)[:W * B].reshape(B, W).astype(np.int32)
+        self.cu = np.concatenate([[0], np.cumsum(new)]).astype(np.int32)
+        shape = (pages, heads, page_size)
+        self.arrays = {}
+        for part in ("k", "v"):
+            a = rng.uniform(0.05, 0.4, (*shape, D // 64)).astype(np.float16)
+            z = (rng.normal(0, 0.5, a.shape) - 7.5 * a).astype(np.float16)
+            param = np.stack([a, z], -1)
+            live = np.zeros((pages, page_size), dtype=bool)
+            for b, n in enumerate(lens):
+                at = np.arange(n)
+                live[self.table[b][at // page_size], at % page_size] = True
+            param.transpose(0, 2, 1, 3, 4)[~live] = np.nan
+            self.arrays[part] = rng.integers(0, 256, (*shape, D // 2)).astype(np.uint8)
+            self.arrays[part + "_param"] = param
+        self.cache = api.Kv4Cache(*(torch.from_numpy(self.arrays[n]).cuda()
+                                    for n in ("k", "k_param", "v", "v_param")))
+        self.t_table, self.t_len, self.t_cu = (torch.from_numpy(x).cuda() for x in (
+            self.table, np.array(lens, dtype=np.int32), self.cu))
+
+    @property
+    def T(self):
+        return int(self.cu[-1])
+
+
+def _queries(T, H, D, dtype, seed=0, scale=1.0):
+    g = torch.Generator().manual_seed(seed)
+    return (torch.randn(T, H, D, generator=g) * scale).to(dtype).cuda()
+
+
+U, E = 2.0 ** -11, 2.0 ** -24
+
+
+def _tolerances(S, A, ref, n, D, dtype):
+    """(ds, the output's tolerance) of the header, S [...], A and ref [..., D]."""
+    ds = S * (U + 4 * D * E) + 16 * E * (1 + S)
+    tol = A * (2 * ds + 2 * U + 4 * n * E)[..., None]
+    return ds, tol + torch.finfo(dtype).eps / 2 * np.abs(ref) + 2.0 ** -25
+
+
+def _check_attention(c, q, out, lse, scale=None, causal=True, window=0, what=""):
+    D = q.shape[2]
+    scale = D ** -0.5 if scale is None else scale
+    scale32 = float(np.float32(scale))
+    ro, rl, mag = kv4.attention(_f64(q), c.arrays["k"], c.arrays["k_param"], c.arrays["v"],
+                                c.arrays["v_param"], c.table, c.lens, c.cu, scale32, causal, window)
+    n = max(c.lens)
+    ds, tol = _tolerances(mag["s"], mag["v"], ro, n, D, q.dtype)
+    err = np.abs(_f64(out) - ro)
+    assert np.isfinite(_f64(out)).all(), what
+    assert (err <= tol).all(), f"{what}: worst {err.max():.3e} of {tol.max():.3e}, {(err > tol).sum()} outside"
+    if lse is not None:
+        got = _f64(lse)
+        empty = np.isneginf(rl)
+        assert np.array_equal(np.isneginf(got), empty), what
+        d = np.abs(got[~empty] - rl[~empty])
+        t = (ds + 4 * n * E + 2 * E * np.abs(np.where(empty, 0, rl)))[~empty]
+        assert (d <= t).all(), f"{what}: lse off by {d.max():.3e}"
+
+
+def _run(c, q, **kw):
+    args = dict(max_q=max(c.new), max_kv=max(max(c.lens), 1), return_lse=True)
+    args.update(kw)
+    return api.kv4_attention(q, c.cache, c.t_table, c.t_len, c.t_cu, **args)
+
+
+# ------------------------------------------------------------------- append
+
+def _append_case(lens, new, heads, D, page_size, dtype, seed=0, scale=1.0):
+    c = Case(lens, new, heads, D, page_size, seed)
+    g = torch.Generator().manual_seed(seed)
+    row = torch.randn(c.T + 1, (4 + 2 * heads) * D + 8, generator=g) * scale  # a fused projection's rows
+    row = row.to(dtype).cuda()
+    k = row[:c.T, 4 * D:(4 + heads) * D].view(c.T, heads, D)
+    v = row[:c.T, (4 + heads) * D:(4 + 2 * heads) * D].view(c.T, heads, D)
+    return c, k, v
+
+
+def _expect_append(c, k, v):
+    page_size = c.arrays["k"].shape[2]
+    want = {n: x.copy() for n, x in c.arrays.items()}
+    for part, x in (("k", k), ("v", v)):
+        code, param = kv4.quantize(_f64(x))
+        for b, n in enumerate(c.lens):
+            for i in range(c.new[b]):
+                j = n - c.new[b] + i
+                if j < 0:
+                    continue
+                p, o = c.table[b, j // page_size], j % page_size
+                want[part][p, :, o] = kv4.pack(code[c.cu[b] + i])
+                want[part + "_param"][p, :, o] = param[c.cu[b] + i]
+    return want
+
+
+def _check_cache(c, want):
+    for n in ("k", "k_param", "v", "v_param"):
+        got = getattr(c.cache, n).cpu().numpy()
+        assert np.array_equal(got.view(np.uint8 if n in "kv" else np.uint16),
+                              want[n].view(np.uint8 if n in "kv" else np.uint16)) or \
+            np.array_equal(got, want[n], equal_nan=True), n
+
+
+@pytest.mark.parametrize("dtype", [F16, BF16])
+@pytest.mark.parametrize("lens,new,heads,D,page_size", [
+    ([1], [1], 1, 64, 16), ([5, 40], [5, 1], 2, 128, 16), ([33, 16, 100], [17, 0, 64], 3, 64, 32),
+    ([70, 3], [70, 2], 8, 128, 48), ([20], [20], 1, 256, 16), ([200, 1, 0], [129, 1, 0], 4, 128, 64)])
+def test_append_writes_the_oracles_codes_and_nothing_else(lens, new, heads, D, page_size, dtype):
+    c, k, v = _append_case(lens, new, heads, D, page_size, dtype)
+    api.kv4_append(c.cache, k, v, c.t_table, c.t_len, c.t_cu)
+    _check_cache(c, _expect_append(c, k, v))
+
+
+@pytest.mark.parametrize("dtype", [F16, BF16])
+def test_append_one_row_each_without_cu(dtype):
+    lens = [3, 17, 64, 1]
+    c, k, v = _append_case(lens, [1] * 4, 2, 128, 16, dtype)
+    api.kv4_append(c.cache, k, v, c.t_table, c.t_len)
+    _check_cache(c, _expect_append(c, k, v))
+    a = api.kv4_read(c.cache, c.t_table, c.t_len, dtype=dtype)
+    b = api.kv4_read(c.cache, c.t_table, c.t_len, c.t_cu, tokens=4, dtype=dtype)
+    assert torch.equal(a[0], b[0]) and torch.equal(a[1], b[1])
+
+
+@pytest.mark.parametrize("dtype", [F16, BF16])
+def test_groups_at_the_edge_of_the_format(dtype):
+    D, rows = 128, []
+    ramp = torch.linspace(-1, 1, 64, dtype=torch.float64)
+    half = torch.arange(64, dtype=torch.float64) / 2          # steps of a half: every quotient a half or whole
+    rows.append(torch.cat([torch.zeros(64), torch.full((64,), 3.25)]))           # constant: a = 0
+    rows.append(torch.cat([half.clamp(max=15), -half.clamp(max=15)]))           # a = 1: halves to even
+    rows.append(torch.cat([ramp * 59000, ramp * 60000]))
+    rows.append(torch.cat([ramp * 1e-7, ramp * 6e-5]))                          # a is subnormal or zero
+    rows.append(torch.cat([ramp * 61000, ramp]))                                # beyond the range: NaN
+    rows.append(torch.cat([ramp, torch.where(ramp == 1, float("nan"), ramp)]))
+    rows.append(torch.cat([torch.where(ramp == 1, float("inf"), ramp), ramp]))
+    rows.append(torch.cat([1000 + ramp, 1e-3 * ramp - 500]))                    # a small range far from zero
+    x = torch.stack([r.double() for r in rows]).to(dtype)
+    T = len(rows)
+    c = Case([T], [T], 1, D, 16)
+    k = x.view(T, 1, D).cuda()
+    v = k.flip(0).contiguous()
+    api.kv4_append(c.cache, k, v, c.t_table, c.t_len, c.t_cu)
+    _check_cache(c, _expect_append(c, k, v))
+
+
+@pytest.mark.parametrize("dtype", [F16, BF16])
+def test_halves_decided_exactly(dtype):
+    # offsets and steps for which (x - z) / a is a half, or next to one, all over the range
+    rng = np.random.default_rng(5)
+    T, D = 2000, 64
+    a = rng.uniform(0.01, 3, (T, 1)).astype(np.float16).astype(np.float64)
+    z = rng.normal(0, 2, (T, 1)).astype(np.float16).astype(np.float64)
+    c = np.concatenate([np.zeros((T, 1)), np.full((T, 1), 15.0),
+                        rng.integers(0, 15, (T, D - 2)) + 0.5], 1)
+    x = torch.from_numpy((z + a * c)[:, None, :]).to(dtype).cuda()
+    k = Case([T], [T], 1, D, 64)
+    api.kv4_append(k.cache, x, x, k.t_table, k.t_len, k.t_cu)
+    _check_cache(k, _expect_append(k, x, x))
+
+
+def test_rows_of_no_sequence_are_not_read_or_written():
+    c, k, v = _append_case([20, 9], [4, 9], 2, 128, 16, F16)
+    k2 = torch.cat([torch.full((3, 2, 128), float("nan"), dtype=F16, device="cuda"), k,
+                    torch.full((5, 2, 128), float("nan"), dtype=F16, device="cuda")])
+    v2 = torch.cat([k2[:3], v, k2[-5:]])
+    cu = c.t_cu + 3
+    api.kv4_append(c.cache, k2, v2, c.t_table, c.t_len, cu)
+    want = _expect_append(c, k, v)
+    _check_cache(c, want)
+    c.arrays = want
+    rk = torch.full((c.T + 8, 2, 128), 7.0, dtype=F16, device="cuda")
+    rv = rk.clone()
+    api.kv4_read(c.cache, c.t_table, c.t_len, cu, k=rk, v=rv)
+    assert (rk[:3] == 7).all() and (rk[-5:] == 7).all() and (rv[:3] == 7).all() and (rv[-5:] == 7).all()
+    wk, _ = api.kv4_read(c.cache, c.t_table, c.t_len, c.t_cu, tokens=c.T)
+    assert torch.equal(rk[3:-5], wk)
+    q = _queries(c.T + 8, 4, 128, F16)
+    out = torch.full_like(q, 7.0)
+    api.kv4_attention(q, c.cache, c.t_table, c.t_len, cu, max_q=9, out=out)
+    assert (out[:3] == 7).all() and (out[-5:] == 7).all()
+    _check_attention(c, q[3:-5], out[3:-5], None)
+
+
+# --------------------------------------------------------------------- read
+
+@pytest.mark.parametrize("dtype", [F16, BF16, F32])
+@pytest.mark.parametrize("D", [64, 128, 256])
+def test_read_gives_the_values(D, dtype):
+    c = Case([40, 7, 0, 129], [33, 7, 0, 50], 3, D, 32)
+    k, v = api.kv4_read(c.cache, c.t_table, c.t_len, c.t_cu, tokens=c.T, dtype=dtype)
+    for got, part in ((k, "k"), (v, "v")):
+        for b, n in enumerate(c.lens):
+            val = kv4.values(kv4.gather(c.arrays[part], c.table[b], n),
+                             kv4.gather(c.arrays[part + "_param"], c.table[b], n))[n - c.new[b]:]
+            # a c + z: its bits span less than fp64's, so fp32's rounding of it is the fused one
+            want = torch.from_numpy(val.astype(np.float32)).to(dtype)
+            assert torch.equal(got[c.cu[b]:c.cu[b + 1]].cpu(), want), (part, b)
+
+
+# ---------------------------------------------------------------- attention
+
+@pytest.mark.parametrize("dtype", [F16, BF16])
+@pytest.mark.parametrize("H,heads", [(1, 1), (4, 4), (8, 2), (8, 1), (7, 1), (12, 4), (32, 2), (20, 1)])
+@pytest.mark.parametrize("D", [64, 128, 256])
+def test_one_token_each(D, H, heads, dtype):
+    lens = [1, 2, 15, 16, 17, 63, 100, 0, 257]
+    c = Case(lens, [1] * len(lens), heads, D, 16, seed=H)
+    q = _queries(len(lens), H, D, dtype)
+    out, lse = _run(c, q)
+    _check_attention(c, q, out, lse, what=f"D={D} H={H}/{heads}")
+    o2 = api.kv4_attention(q, c.cache, c.t_table, c.t_len)       # no cu, no hints
+    _check_attention(c, q, o2, None)
+
+
+@pytest.mark.parametrize("dtype", [F16, BF16])
+@pytest.mark.parametrize("lens,new,H,heads,D,page_size", [
+    ([5], [5], 2, 1, 64, 16), ([40, 3, 77], [7, 3, 2], 8, 2, 128, 16), ([130, 64], [33, 64], 4, 4, 64, 32),
+    ([300], [150], 12, 3, 128, 48), ([70, 0, 71], [5, 0, 70], 6, 1, 256, 64), ([256], [256], 2, 2, 128, 128),
+    ([1000, 513], [3, 129], 4, 1, 128, 64), ([260, 259], [1, 140], 5, 1, 64, 16)])
+def test_several_rows(lens, new, H, heads, D, page_size, dtype):
+    c = Case(lens, new, heads, D, page_size, seed=sum(lens))
+    q = _queries(c.T, H, D, dtype, seed=1)
+    out, lse = _run(c, q)
+    _check_attention(c, q, out, lse)
+
+
+@pytest.mark.parametrize("causal,window", [(True, 1), (True, 5), (True, 16), (True, 64), (True, 1000),
+                                           (False, 0), (False, 9)])
+@pytest.mark.parametrize("lens,new", [([33, 100], [1, 1]), ([50, 20], [20, 20]), ([200], [140])])
+def test_masks(lens, new, causal, window):
+    c = Case(lens, new, 2, 128, 16, seed=window)
+    q = _queries(c.T, 8, 128, F16, seed=2)
+    out, lse = _run(c, q, causal=causal, window=window)
+    _check_attention(c, q, out, lse, causal=causal, window=window)
+
+
+@pytest.mark.parametrize("n,new,H", [(3, 8, 4), (0, 2, 8), (10, 200, 4), (0, 1, 1)])
+def test_rows_that_see_nothing(n, new, H):
+    """More rows than tokens: the first rows lie before position 0."""
+    c = Case([n, 40], [new, 1], 1, 128, 16)
+    q = _queries(c.T, H, 128, F16)
+    out, lse = _run(c, q)
+    _check_attention(c, q, out, lse)
+    empty = max(0, new - n)
+    assert (out[:empty] == 0).all() and torch.isneginf(lse[:empty]).all()
+
+
+@pytest.mark.parametrize("new", [1, 4, 160])
+@pytest.mark.parametrize("scale", [0.0, -0.3, 1.0, 4.0])
+def test_scales_of_the_scores(scale, new):
+    c = Case([200, 30], [new, 1], 2, 64, 16)
+    q = _queries(c.T, 4, 64, F16)
+    out, lse = _run(c, q, scale=scale)
+    _check_attention(c, q, out, lse, scale=scale)
+
+
+@pytest.mark.parametrize("new", [1, 150])
+@pytest.mark.parametrize("dtype,mag", [(F16, 1e-4), (F16, 300.0), (F16, 3e4), (BF16, 1e-12), (BF16, 1e6), (BF16, 1e30)])
+def test_queries_of_any_magnitude(dtype, mag, new):
+    """The factor keeps the scores where they are; fp16's and fp32's ranges must not matter in between."""
+    c = Case([180, 9], [new, 1], 2, 128, 16)
+    q = _queries(c.T, 4, 128, dtype).float().clamp(-2, 2).mul(mag).to(dtype)
+    scale = 128 ** -0.5 / mag
+    out, lse = _run(c, q, scale=scale)
+    _check_attention(c, q, out, lse, scale=scale)
+
+
+@pytest.mark.parametrize("new", [1, 6, 140])
+def test_nan_stays_where_it_belongs(new):
+    c = Case([160, 50], [new, 1], 2, 128, 16)
+    q = _queries(c.T, 8, 128, F16)
+    ref, _ = _run(c, q)
+    q2 = q.clone()
+    q2[0, 3, 5] = float("nan")
+    q2[-1, 6, 0] = float("inf")
+    out, _ = _run(c, q2)
+    assert torch.isnan(out[0, 3]).all() and torch.isnan(out[-1, 6]).all()
+    keep = torch.ones(c.T, 8, dtype=torch.bool)
+    keep[0, 3] = keep[-1, 6] = False
+    assert torch.equal(out[keep], ref[keep])
+    # a NaN group in the second sequence's key of head 1: that head's rows, nothing else
+    p = int(c.table[1, 0])
+    c.cache.k_param[p, 1, 3, 0] = float("nan")
+    out, _ = _run(c, q)
+    assert torch.isnan(out[-1, 4:]).all()
+    assert torch.equal(out[-1, :4], ref[-1, :4]) and torch.equal(out[:-1], ref[:-1])
+
+
+@pytest.mark.parametrize("new", [1, 5, 200])
+def test_strided_queries_and_outputs(new):
+    c = Case([300, 20], [new, 2], 2, 128, 32)
+    q = _queries(c.T, 8, 128, BF16)
+    ref, _ = _run(c, q)
+    fused = torch.full((c.T, 8 * 128 + 4 * 128 + 8), float("nan"), dtype=BF16, device="cuda")
+    qs = fused[:, :1024].view(c.T, 8, 128)
+    qs.copy_(q)
+    buf = torch.full((8, c.T + 1, 136), 3.0, dtype=BF16, device="cuda")   # head-major, padded
+    out = buf[:, :c.T, :128].transpose(0, 1)
+    got, _ = _run(c, qs, out=out)
+    assert got is out and torch.equal(out, ref)
+    buf[:, :c.T, :128] = 3.0
+    assert (buf == 3.0).all()
+
+
+def test_results_do_not_depend_on_the_hint_or_the_neighbours():
+    lens = [1000, 3, 517, 64]
+    c = Case(lens, [1] * 4, 2, 128, 16, extra=3)
+    q = _queries(4, 8, 128, F16)
+    ref, rl = _run(c, q)
+    _check_attention(c, q, ref, rl)
+    for hint in (1, 64, 100000):
+        out, lse = _run(c, q, max_kv=hint)
+        _check_attention(c, q, out, lse, what=f"hint {hint}")
+    again, _ = _run(c, q)
+    assert torch.equal(again, ref)
+
+
+def test_bad_pages_lengths_and_row_counts_are_recorded():
+    c = Case([40, 40], [1, 1], 1, 64, 16)
+    q = _queries(2, 2, 64, F16)
+    ref, _ = _run(c, q)
+    for bad in (-1, 10 ** 6):
+        t = c.t_table.clone()
+        t[1, 1] = bad
+        out = api.kv4_attention(q, c.cache, t, c.t_len, c.t_cu, max_q=1)
+        assert api.device_error() == api.BCQ_ERR_PAGE
+        assert torch.equal(out[0], ref[0]) and torch.isfinite(out[1]).all()
+        k = torch.ones(2, 1, 64, dtype=F16, device="cuda")
+        t[1, 1], t[1, 2] = c.t_table[1, 1], bad
+        before = c.cache.k.clone()
+        api.kv4_append(c.cache, k[:0], k[:0], t, c.t_len, torch.zeros_like(c.t_cu))
+        assert api.device_error() == api.BCQ_OK and torch.equal(before, c.cache.k)
+        api.kv4_append(c.cache, k[1:], k[1:], t, c.t_len, _i32([0, 0, 1]))
+        assert api.device_error() == api.BCQ_ERR_PAGE and torch.equal(before, c.cache.k)
+        rk, _ = api.kv4_read(c.cache, t, c.t_len, _i32([0, 0, 1]), tokens=1)
+        assert api.device_error() == api.BCQ_ERR_PAGE and (rk == 0).all()
+    long = _i32([40, 10 ** 6])
+    out = api.kv4_attention(q, c.cache, c.t_table, long, c.t_cu, max_q=1)
+    assert api.device_error() == api.BCQ_ERR_PAGE and torch.equal(out[0], ref[0])
+    out = api.kv4_attention(q, c.cache, c.t_table, _i32([40, -7]), c.t_cu, max_q=1)
+    assert api.device_error() == api.BCQ_ERR_PAGE
+    assert torch.equal(out[0], ref[0]) and (out[1] == 0).all()
+    out = torch.full_like(q, 5.0)
+    api.kv4_attention(q, c.cache, c.t_table, c.t_len, _i32([0, 2, 2]), max_q=1, out=out)
+    assert api.device_error() == api.BCQ_ERR_SHAPE and (out[1] == 5).all()
+
+
+def test_no_rows():
+    c = Case([40], [1], 1, 64, 16)
+    q = torch.empty(0, 2, 64, dtype=F16, device="cuda")
+    zero = _i32([0, 0])
+    assert api.kv4_attention(q, c.cache, c.t_table, c.t_len, zero).shape == (0, 2, 64)
+    k, v = api.kv4_read(c.cache, c.t_table, c.t_len, zero, tokens=0)
+    assert k.shape == (0, 1, 64)
+    api.kv4_append(c.cache, k, v, c.t_table, c.t_len, zero)
+
+
+@pytest.mark.parametrize("new", [1, 130])
+def test_a_long_cache(new):
+    """Offsets beyond 2^31 bytes: the sequence's pages are the last of a large cache."""
+    pages, heads, page_size, D = 18000, 8, 256, 128
+    free, _ = torch.cuda.mem_get_info()
+    if free < 8 << 30:
+        pytest.skip("needs 8 GB")
+    small = Case([700], [new], heads, D, page_size, seed=3)
+    cache = api.Kv4Cache.empty(pages, heads, page_size, D)
+    assert cache.k.numel() > 2 ** 31
+    W = small.table.shape[1]
+    far = torch.arange(pages - W, pages, dtype=torch.int32, device="cuda").flip(0)
+    src = torch.from_numpy(small.table[0].astype(np.int64)).cuda()
+    for n in ("k", "k_param", "v", "v_param"):
+        getattr(cache, n)[far.long()] = getattr(small.cache, n)[src]
+    q = _queries(new, 16, D, F16)
+    ref, rl = _run(small, q)
+    out, lse = api.kv4_attention(q, cache, far.view(1, W), small.t_len, small.t_cu, max_q=new, max_kv=700,
+                                 return_lse=True)
+    assert torch.equal(out, ref) and torch.equal(lse, rl)
+    k, v = api.kv4_read(cache, far.view(1, W), small.t_len, small.t_cu, tokens=new)
+    api.kv4_append(cache, k, v, far.view(1, W), small.t_len, small.t_cu)
+    k2, _ = api.kv4_read(small.cache, small.t_table, small.t_len, small.t_cu, tokens=new)
+    assert torch.equal(k, k2)
+
+
+@pytest.mark.parametrize("B,n,H,heads", [(1, 20000, 8, 1), (1, 5000, 32, 8), (40, 600, 8, 4), (300, 90, 4, 2)])
+def test_long_and_many(B, n, H, heads):
+    """Split sequences and full grids: some of the rows in fp64."""
+    D, page_size = 128, 64
+    rng = np.random.default_rng(B)
+    lens = [int(x) for x in rng.integers(n // 2, n + 1, B)]
+    c = Case(lens, [1] * B, heads, D, page_size, seed=B)
+    q = _queries(B, H, D, F16)
+    out, lse = _run(c, q)
+    pick = sorted(set(int(x) for x in rng.integers(0, B, 6)))
+    for b in pick:
+        at = [(kv4.gather(c.arrays[p], c.table[b], lens[b]),
+               kv4.gather(c.arrays[p + "_param"], c.table[b], lens[b])) for p in "kv"]
+        K, V = (kv4.values(*x) for x in at)
+        Km, Vm = (kv4.magnitudes(*x) for x in at)
+        g = np.arange(H) // (H // heads)
+        scale = float(np.float32(D ** -0.5))
+        s = np.einsum("hd,nhd->hn", _f64(q[b]), K[:, g]) * scale
+        S = (np.einsum("hd,nhd->hn", np.abs(_f64(q[b])), Km[:, g]) * scale).max(1)
+        p = np.exp(s - s.max(1, keepdims=True))
+        total = p.sum(1)
+        ref = np.einsum("hn,nhd->hd", p / total[:, None], V[:, g])
+        A = np.einsum("hn,nhd->hd", p / total[:, None], Vm[:, g])
+        ds, tol = _tolerances(S, A, ref, lens[b], D, F16)
+        assert (np.abs(_f64(lse[b]) - s.max(1) - np.log(total)) <= ds + 4 * lens[b] * E + 64 * E).all()
+        assert (np.abs(_f64(out[b]) - ref) <= tol).all()
+
+
+# ------------------------------------------------------------------ together
+
+def test_a_decode_layer_as_it_is_used():
+    """Projection in 8 bits, rows into the cache, attention, projection: prompt, then tokens."""
+    torch.manual_seed(0)
+    E, H, heads, D, page_size = 512, 4, 2, 128, 16
+    wq, sq = api.quantize_i8((torch.randn((H + 2 * heads) * D, E) * E ** -0.5).half().cuda())
+    wo, so = api.quantize_i8((torch.randn(E, H * D) * (H * D) ** -0.5).half().cuda())
+    cache = api.Kv4Cache.empty(24, heads, page_size, D)
+    table = torch.randperm(24, dtype=torch.int32).cuda()[:16].view(2, 8)
+    lens = np.array([0, 0])
+    seen = [[], []]
+    for new in ([37, 20], [1, 1], [1, 1], [5, 3]):
+        cu = np.concatenate([[0], np.cumsum(new)])
+        T = int(cu[-1])
+        lens = lens + np.array(new)
+        x = torch.randn(T, E).half().cuda()
+        qkv = api.linear_i8(x, wq, sq)
+        q = qkv[:, :H * D].view(T, H, D)
+        k = qkv[:, H * D:(H + heads) * D].view(T, heads, D)
+        v = qkv[:, (H + heads) * D:].view(T, heads, D)
+        t_len, t_cu = _i32(lens.tolist()), _i32(cu.tolist())
+        api.kv4_append(cache, k, v, table, t_len, t_cu)
+        o = api.kv4_attention(q, cache, table, t_len, t_cu, max_q=max(new))
+        y = api.linear_i8(o.view(T, H * D), wo, so)
+        assert torch.isfinite(y).all() and y.shape == (T, E)
+        for b in range(2):
+            held = [(kv4.pack(code), param) for code, param in (
+                kv4.quantize(_f64(x[cu[b]:cu[b + 1]])) for x in (k, v))]
+            seen[b].append([f(*h) for h in held for f in (kv4.values, kv4.magnitudes)])
+            Kb, Km, Vb, Vm = (np.concatenate([s[i] for s in seen[b]]) for i in range(4))
+            for i in range(new[b]):
+                n = int(lens[b]) - new[b] + i + 1
+                for h in range(H):
+                    row = _f64(q[cu[b] + i, h])
+                    s = Kb[:n, h // 2] @ row * D ** -0.5
+                    S = (Km[:n, h // 2] @ np.abs(row) * D ** -0.5).max()
+                    p = np.exp(s - s.max())
+                    p /= p.sum()
+                    ref = p @ Vb[:n, h // 2]
+                    _, tol = _tolerances(S, p @ Vm[:n, h // 2], ref, n, D, F16)
+                    assert (np.abs(_f64(o[cu[b] + i, h]) - ref) <= tol).all()
+
+
+def test_captured_and_replayed_with_other_lengths():
+    """One graph, replayed as the sequences grow; two graphs of the same stream replayed at once."""
+    lens = [30, 5]
+    c = Case([64, 64], [1, 1], 2, 128, 16)
+    q = _queries(2, 8, 128, F16)
+    kv_len = _i32(lens)
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        api.kv4_attention(q, c.cache, c.t_table, kv_len, max_kv=64)
+    side.synchronize()
+    graphs = []
+    for _ in range(2):
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g):
+            out = api.kv4_attention(q, c.cache, c.t_table, kv_len, max_kv=64)
+        graphs.append((g, out))
+    for lens in ([30, 5], [33, 48], [64, 1], [0, 64]):
+        kv_len.copy_(_i32(lens))
+        torch.cuda.synchronize()
+        streams = [torch.cuda.Stream(), torch.cuda.Stream()]
+        for (g, _), st in zip(graphs, streams):
+            with torch.cuda.stream(st):
+                g.replay()
+        torch.cuda.synchronize()
+        c.lens = lens
+        for _, out in graphs:
+            _check_attention(c, q, out, None, what=str(lens))
+
+
+def test_side_stream():
+    c = Case([500, 30], [1, 1], 2, 128, 16)
+    q = _queries(2, 8, 128, F16)
+    ref, _ = _run(c, q)
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    out, _ = _run(c, q, stream=side)
+    side.synchronize()
+    assert torch.equal(out, ref)
