@@ -5,11 +5,13 @@
 #include <cuda_runtime.h>
 
 #include <algorithm>
+#include <atomic>
 #include <cstdint>
 
 #include "bcq.h"
 #include "bcq_device.cuh"
 #include "bcq_launch.h"
+#include "bcq_tcgen05.cuh"
 
 namespace bcq {
 namespace {
@@ -37,86 +39,368 @@ __device__ __forceinline__ void store_out(__nv_bfloat16* p, float v) { *p = __fl
 
 // ----------------------------------------------------------- rows to codes
 
-// One block a row.  |x| is compared by its bits, which order like the values
-// (an infinity or a NaN is the largest of all).  The code is 127 x / a to the
-// nearest integer: x times 127 / a first; where that lies within 1e-4 of a
-// half (its error is below 127 * 3 * 2^-24 < 3e-5) the quotient itself
-// decides.  With the mantissas X and A (at most 11 bits) the quotient is 127 X
-// / A times a power of two that is at most 1, so one that is no half is at
-// least 1 / (254 X) > 2^-19 of itself away from it, more than the division's
-// rounding (2^-24): the rounded quotient is on the right side of the half.
-// 127 X is exact, and so is a quotient that is a half.
-// Rows of very large or very small values are scaled by a power of two first,
-// exactly, so that neither 127 x nor 127 / a leaves fp32.
+// The code of x: 127 x / a to the nearest integer, x times 127 / a first;
+// where that lies within 1e-4 of a half (its error is below 127 * 3 * 2^-24 <
+// 3e-5) the quotient itself decides.  With the mantissas X and A (at most 11
+// bits) the quotient is 127 X / A times a power of two that is at most 1, so
+// one that is no half is at least 1 / (254 X) > 2^-19 of itself away from it,
+// more than the division's rounding (2^-24): the rounded quotient is on the
+// right side of the half.  127 X is exact, and so is a quotient that is a
+// half.  Rows of very large or very small values are scaled by a power of two
+// first, exactly, so that neither 127 x nor 127 / a leaves fp32.
+struct RowScale {
+  float pre, as, inv;  // power of two, a * pre, 127 / as
+  bool any;            // finite and not all zeros
+};
+
 template <typename T>
-__global__ void __launch_bounds__(256) quantize_i8_kernel(const uint16_t* __restrict__ x,
-                                                          int64_t ldx, int K, int8_t* q,
-                                                          int64_t ldq, float* scale) {
-  __shared__ uint32_t s_max[8];
+__device__ __forceinline__ RowScale row_scale(uint32_t top) {
+  const float a = Bits16<T>::to_float(top);
+  const float pre = a > 0x1p64f ? 0x1p-64f : a < 0x1p-64f ? 0x1p64f : 1.f;
+  return {pre, a * pre, __fdiv_rn(127.f, a * pre), top != 0 && top < Bits16<T>::kInf};
+}
+
+template <typename T>
+__device__ __forceinline__ int code_of(uint32_t bits, const RowScale& s) {
+  const float x = Bits16<T>::to_float(bits) * s.pre;
+  const float v = x * s.inv;
+  float r = rintf(v);
+  if (fabsf(v - r) > 0.4999f) r = rintf(__fdiv_rn(x * 127.f, s.as));
+  return (int)r;
+}
+
+__device__ __forceinline__ float4 lds_f32x4(uint32_t addr) {
+  float4 v;
+  asm volatile("ld.shared.v4.f32 {%0, %1, %2, %3}, [%4];" : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w) : "r"(addr));
+  return v;
+}
+
+// Two signed bytes below the ones of `next`.
+__device__ __forceinline__ uint32_t pack_s8(int hi, int lo, uint32_t next) {
+  uint32_t d;
+  asm("cvt.pack.sat.s8.s32.b32 %0, %1, %2, %3;" : "=r"(d) : "r"(hi), "r"(lo), "r"(next));
+  return d;
+}
+
+// One block a row, which it holds in registers between the two looks at it
+// (NV vectors of eight a thread): a row is read once.  |x| is compared by its
+// bits, two at a time, which order like the values (an infinity or a NaN is
+// the largest of all).  VEC: rows start on 16 bytes; else element by element,
+// the row read twice.
+template <typename T, int NV, bool VEC>
+__global__ void __launch_bounds__(1024) quantize_i8_kernel(const uint16_t* __restrict__ x,
+                                                           int64_t ldx, int K, int8_t* q,
+                                                           int64_t ldq, float* scale) {
+  __shared__ uint32_t s_max[32];
+  launch_dependents();  // the product may fetch its weights meanwhile
   const int64_t m = blockIdx.x;
   const uint16_t* row = x + m * ldx;
-  uint32_t top = 0;
-  for (int k = threadIdx.x; k < K; k += blockDim.x) top = max(top, (uint32_t)row[k] & 0x7FFFu);
-  top = __reduce_max_sync(0xFFFFFFFFu, top);
-  if ((threadIdx.x & 31) == 0) s_max[threadIdx.x >> 5] = top;
-  __syncthreads();
-  top = 0;
-  for (int i = 0; i < 8; ++i) top = max(top, s_max[i]);
-  const bool finite = top < Bits16<T>::kInf;
-  const float a = Bits16<T>::to_float(top);
-  if (threadIdx.x == 0) scale[m] = finite ? __fdiv_rn(a, 127.f) : __uint_as_float(0x7FC00000u);
-  const float pre = a > 0x1p64f ? 0x1p-64f : a < 0x1p-64f ? 0x1p64f : 1.f;
-  const float as = a * pre;
-  const float inv = __fdiv_rn(127.f, as);
-  for (int k = threadIdx.x; k < K; k += blockDim.x) {
-    int c = 0;
-    if (finite && top) {
-      const float xs = Bits16<T>::to_float(row[k]) * pre;
-      const float v = xs * inv;
-      float r = rintf(v);
-      if (fabsf(v - r) > 0.4999f) r = rintf(__fdiv_rn(xs * 127.f, as));
-      c = (int)r;
-    }
-    q[m * ldq + k] = (int8_t)c;
+  int8_t* to = q + m * ldq;
+  const int tid = threadIdx.x, threads = blockDim.x;
+  const int vecs = VEC ? K / 8 : 0;
+  uint4 v[NV];
+  uint32_t top2 = 0;
+#pragma unroll
+  for (int i = 0; i < NV; ++i) {
+    v[i] = make_uint4(0, 0, 0, 0);
+    if (tid + i * threads < vecs) v[i] = ldg_nc_v4(row + (int64_t)(tid + i * threads) * 8);
   }
+#pragma unroll
+  for (int i = 0; i < NV; ++i) {
+    top2 = __vmaxu2(top2, v[i].x & 0x7FFF7FFFu);
+    top2 = __vmaxu2(top2, v[i].y & 0x7FFF7FFFu);
+    top2 = __vmaxu2(top2, v[i].z & 0x7FFF7FFFu);
+    top2 = __vmaxu2(top2, v[i].w & 0x7FFF7FFFu);
+  }
+  uint32_t top = max(top2 & 0xFFFFu, top2 >> 16);
+  for (int k = vecs * 8 + tid; k < K; k += threads) top = max(top, (uint32_t)row[k] & 0x7FFFu);
+  top = __reduce_max_sync(0xFFFFFFFFu, top);
+  if ((tid & 31) == 0) s_max[tid >> 5] = top;
+  __syncthreads();
+  top = __reduce_max_sync(0xFFFFFFFFu, (tid & 31) < threads / 32 ? s_max[tid & 31] : 0u);
+  const RowScale rs = row_scale<T>(top);
+  if (tid == 0)
+    scale[m] = top < Bits16<T>::kInf ? __fdiv_rn(Bits16<T>::to_float(top), 127.f)
+                                     : __uint_as_float(0x7FC00000u);
+#pragma unroll
+  for (int i = 0; i < NV; ++i) {
+    if (tid + i * threads >= vecs) continue;
+    uint2 out = make_uint2(0, 0);
+    if (rs.any) {
+      const uint32_t w[4] = {v[i].x, v[i].y, v[i].z, v[i].w};
+      int c[8];
+#pragma unroll
+      for (int e = 0; e < 8; ++e) c[e] = code_of<T>((w[e >> 1] >> (16 * (e & 1))) & 0xFFFFu, rs);
+      out.x = pack_s8(c[1], c[0], pack_s8(c[3], c[2], 0));
+      out.y = pack_s8(c[5], c[4], pack_s8(c[7], c[6], 0));
+    }
+    *reinterpret_cast<uint2*>(to + (int64_t)(tid + i * threads) * 8) = out;
+  }
+  for (int k = vecs * 8 + tid; k < K; k += threads)
+    to[k] = (int8_t)(rs.any ? code_of<T>(row[k], rs) : 0);
 }
 
 // ------------------------------------------------------------- the product
 
-// 64 x 64 outputs a block, 64 columns of K at a time through shared memory.
-template <typename TO>
-__global__ void __launch_bounds__(256) gemm_i8_kernel(const int8_t* __restrict__ x, int64_t ldx,
-                                                      const float* __restrict__ sx,
-                                                      const int8_t* __restrict__ w, int64_t ldw,
-                                                      const float* __restrict__ sw, int M, int N,
-                                                      int K, TO* y, int64_t ldy) {
-  __shared__ int xs[64][17], ws[64][17];
-  const int tx = threadIdx.x & 15, ty = threadIdx.x >> 4;
-  const int64_t m0 = (int64_t)blockIdx.y * 64, n0 = (int64_t)blockIdx.x * 64;
-  int acc[4][4] = {};
-  for (int k0 = 0; k0 < K; k0 += 64) {
-    for (int i = threadIdx.x; i < 64 * 16; i += 256) {
-      const int r = i >> 4, c = i & 15;
-      int a = 0, b = 0;
-      for (int j = 0; j < 4; ++j) {
-        const int k = k0 + 4 * c + j;
-        if (k < K && m0 + r < M) a |= (int)(uint8_t)x[(m0 + r) * ldx + k] << (8 * j);
-        if (k < K && n0 + r < N) b |= (int)(uint8_t)w[(n0 + r) * ldw + k] << (8 * j);
-      }
-      xs[r][c] = a;
-      ws[r][c] = b;
-    }
-    __syncthreads();
-    for (int c = 0; c < 16; ++c)
-      for (int i = 0; i < 4; ++i)
-        for (int j = 0; j < 4; ++j) acc[i][j] = __dp4a(xs[ty + 16 * i][c], ws[tx + 16 * j][c], acc[i][j]);
-    __syncthreads();
+// y^T in tiles of R <= 128 rows of w by BT <= 256 rows of x: the weight's rows
+// are the tensor core's M (its lanes of tensor memory), the tokens its N, so a
+// single token costs no more than the 16 columns that an instruction has at
+// least, and y's rows are written along the lanes.  Both operands come in
+// blocks of 128 columns of K through TMA (128-byte swizzle, zeros beyond the
+// matrices' edges) into a ring of stages of G blocks, each operand from a warp
+// of its own; tcgen05 (kind::i8) adds them into int32 accumulators in tensor
+// memory, two sets of them, so that a tile's output is written while the next
+// one is summed.  A wait and four instructions of few columns keep a warp for
+// longer than the tensor core (about 450 cycles against 160), so up to four
+// warps take stages in turn, each into an accumulator of its own; the output
+// adds them up.  A ring slot always belongs to the same warp (the ring's depth
+// is a multiple of theirs): a warp that took a slot's next round could wait
+// for it before the round in progress is full, and a wait by parity would take
+// the round before that one for it.  R needs no alignment: the tensor core reads 64 or 128 rows of
+// the stage whatever they hold, and what they give for rows beyond R is not
+// looked at.
+struct GemmParams {
+  const float* sx;
+  const float* sw;
+  void* y;
+  int64_t ldy;
+  int M, N, K;
+  int R, BT, rows;      // tile; rows the tensor core takes of w (64 or 128)
+  int mt, tiles;        // tiles along M, in all
+  int KB, G, KG;        // blocks of K, blocks a stage, stages' worth of K
+  int stages;           // ring depth
+  int bufs;             // sets of accumulators (1 or 2)
+  int issuers;          // warps that issue MMAs, accumulators of a set (1, 2 or 4)
+  int tiles_each, tiles_more;  // tiles of every CTA, CTAs that have one more
+  uint32_t kg_step;     // 2^16 KG / CTAs: where a CTA starts along K
+  int overlap;          // the kernel before makes x's codes and may still run
+  uint32_t a_block, b_block, b_off, bar_off, tmem_cols;
+  unsigned long long timeout_ns;
+};
+
+constexpr int kGemmThreads = 320;  // w, x, MMA, MMA, four output warps, MMA, MMA
+constexpr int kMaxGemmStages = 32;
+constexpr uint32_t kKBlock = 128;
+
+// Where a CTA is on its way through its tiles and, within each, K.
+struct GemmCursor {
+  int tile, kg, left, slot;  // left: stages left of the tile
+  uint32_t phase;            // of the ring slot
+  __device__ __forceinline__ void start(int kg_first, int KG) {
+    tile = (int)blockIdx.x;
+    kg = kg_first;
+    left = KG;
+    slot = 0;
+    phase = 0;
   }
-  for (int i = 0; i < 4; ++i)
-    for (int j = 0; j < 4; ++j) {
-      const int64_t m = m0 + ty + 16 * i, n = n0 + tx + 16 * j;
-      if (m < M && n < N) store_out(y + m * ldy + n, (float)acc[i][j] * sx[m] * sw[n]);
+  // returns whether the next stage belongs to another tile
+  __device__ __forceinline__ bool step(int KG, int S) {
+    if (++slot == S) {
+      slot = 0;
+      phase ^= 1u;
     }
+    if (++kg == KG) kg = 0;
+    if (--left > 0) return false;
+    left = KG;
+    tile += (int)gridDim.x;
+    return true;
+  }
+};
+
+template <typename TO>
+__global__ void __launch_bounds__(kGemmThreads, 1)
+    gemm_i8_kernel(const __grid_constant__ CUtensorMap wmap, const __grid_constant__ CUtensorMap xmap,
+                   const GemmParams p) {
+  extern __shared__ unsigned char smem_raw[];
+  const uint32_t sbase = (smem_u32(smem_raw) + 1023u) & ~1023u;
+  // warp roles, waits and loops are uniform by construction, so that
+  // descriptors and addresses stay in uniform registers (moved there for each
+  // instruction, they cost 107 cycles an MMA against 39)
+  const int warp = __shfl_sync(0xFFFFFFFFu, (int)threadIdx.x >> 5, 0), lane = threadIdx.x & 31;
+  const int S = p.stages;
+  const uint32_t full = sbase + p.bar_off, empty = full + 8u * S, accfull = empty + 8u * S,
+                 accempty = accfull + 16u, drain = accempty + 16u, slot = drain + 32u,
+                 sx_off = slot + 16u;
+  if (warp == 0) {
+    for (int i = lane; i < S; i += 32) {
+      mbar_init(full + 8u * i, 2);
+      mbar_init(empty + 8u * i, 1);
+    }
+    if (lane < 2) {
+      mbar_init(accfull + 8u * lane, (uint32_t)p.issuers);
+      mbar_init(accempty + 8u * lane, 4);
+    }
+    if (lane < 4) mbar_init(drain + 8u * lane, 1);
+    fence_mbar_init();
+  } else if (warp == 2) {
+    tmem_alloc(slot, p.tmem_cols);
+  }
+  umma_fence_before();
+  // the weights' warp goes ahead: its first loads need nothing of the others
+  if (warp == 0) asm volatile("bar.arrive 2, %0;" ::"n"(kGemmThreads) : "memory");
+  else named_barrier_sync(2, kGemmThreads);
+  umma_fence_after();
+  const uint32_t tmem = warp == 0 ? 0u : lds_u32v(slot);
+  const int mine = p.tiles_each + ((int)blockIdx.x < p.tiles_more ? 1 : 0);
+  const int total = mine * p.KG;
+  // Stages of K in turn from a first one of this CTA's own (the sum is exact in
+  // any order): CTAs that read the same rows of x do not ask for the same lines
+  // of L2 at the same time.
+  const int kg_first = (int)((blockIdx.x * p.kg_step) >> 16);
+  auto wait = [&](uint32_t bar, uint32_t parity) {
+    return __all_sync(0xFFFFFFFFu, mbar_wait_bounded(bar, parity, p.timeout_ns)) != 0;
+  };
+
+  if (warp <= 1) {
+    // ---------------------------------------------------------- the operands
+    const bool one = elect_one(), is_w = warp == 0;
+    const CUtensorMap* map = is_w ? &wmap : &xmap;
+    const uint32_t block = is_w ? p.a_block : p.b_block, base = sbase + (is_w ? 0u : p.b_off);
+    const uint32_t bytes = (uint32_t)(is_w ? p.R : p.BT) * kKBlock;
+    // x's codes come from the kernel before; the first weights need not wait for it
+    if (!is_w && p.overlap) grid_dependency_wait();
+    GemmCursor c;
+    c.start(kg_first, p.KG);
+    auto first_row = [&]() {
+      const int nt = p.mt == 1 ? c.tile : c.tile / p.mt;
+      return is_w ? nt * p.R : (c.tile - nt * p.mt) * p.BT;
+    };
+    int row = first_row();
+    for (int i = 0; i < total; ++i) {
+      if (i >= S && !wait(empty + 8u * c.slot, c.phase ^ 1u)) {
+        if (one) record_error(&g_i8_error, BCQ_ERR_TIMEOUT);
+        for (int j = i - S; j < i; ++j)  // the copies in flight
+          mbar_wait_bounded(full + 8u * (j % S), (uint32_t)(j / S) & 1u, p.timeout_ns);
+        break;
+      }
+      const int kb = c.kg * p.G, n = min(p.G, p.KB - kb);
+      if (one) {
+        mbar_arrive_expect_tx(full + 8u * c.slot, bytes * (uint32_t)n);
+        uint32_t to = base + (uint32_t)(c.slot * p.G) * block;
+        for (int j = 0; j < n; ++j, to += block)
+          tma_load_2d(to, map, (kb + j) * (int)kKBlock, row, full + 8u * c.slot);
+      }
+      if (c.step(p.KG, S)) row = first_row();
+    }
+  } else if (warp < 4 || warp >= 8) {
+    // --------------------------------------------------------------- the sums
+    const int issuer = warp < 4 ? warp - 2 : warp - 6;
+    const bool one = elect_one();
+    // kind::i8: int32 D, signed A and B, both K-major, N = BT, M = rows
+    const uint32_t idesc = (2u << 4) | (1u << 7) | (1u << 10) | ((uint32_t)(p.BT >> 3) << 17) |
+                           ((uint32_t)(p.rows >> 4) << 24);
+    const uint64_t ad0 = umma_desc_sw128(sbase), bd0 = umma_desc_sw128(sbase + p.b_off);
+    const uint32_t a_units = p.a_block >> 4, b_units = p.b_block >> 4;  // never carry out of the address
+    bool ok = true;
+    GemmCursor c;
+    c.start(kg_first, p.KG);
+    for (int t = 0; t < mine && ok && issuer < p.issuers; ++t) {
+      const int buf = p.bufs == 2 ? t & 1 : 0, round = p.bufs == 2 ? t >> 1 : t;
+      if (round > 0) ok = wait(accempty + 8u * buf, (uint32_t)(round - 1) & 1u);
+      umma_fence_after();
+      const uint32_t d = tmem + (uint32_t)((buf * p.issuers + issuer) * p.BT);
+      uint32_t more = 0;  // whether the accumulator holds something
+      for (int g = 0; g < p.KG && ok; ++g) {
+        if ((c.slot & (p.issuers - 1)) == issuer) {
+          ok = wait(full + 8u * c.slot, c.phase);
+          if (!ok) break;
+          umma_fence_after();
+          const int kb = c.kg * p.G, n = min(p.G, p.KB - kb);
+          uint64_t ad = ad0 + (uint32_t)(c.slot * p.G) * a_units, bd = bd0 + (uint32_t)(c.slot * p.G) * b_units;
+          if (one) {
+            for (int j = 0; j < n; ++j, ad += a_units, bd += b_units) {
+              // 32-byte slices of K: all four, or those that hold some of it
+              const int rest = p.K - (kb + j) * (int)kKBlock;
+              umma_i8_ss(d, ad, bd, idesc, more);
+              if (rest > 32) umma_i8_ss(d, ad + 2, bd + 2, idesc, 1);
+              if (rest > 64) umma_i8_ss(d, ad + 4, bd + 4, idesc, 1);
+              if (rest > 96) umma_i8_ss(d, ad + 6, bd + 6, idesc, 1);
+              more = 1;
+            }
+            umma_commit(empty + 8u * c.slot);
+          }
+          more = 1;
+        }
+        c.step(p.KG, S);
+      }
+      if (ok && one) umma_commit(accfull + 8u * buf);
+    }
+    if (!ok) {
+      if (one) {
+        record_error(&g_i8_error, BCQ_ERR_TIMEOUT);
+        umma_commit(drain + 8u * issuer);
+      }
+      mbar_wait_bounded(drain + 8u * issuer, 0, p.timeout_ns);
+    }
+  } else {
+    // ------------------------------------------------------------ the outputs
+    // 64 rows lie in the first 16 lanes of each quarter, 128 in all 32
+    const int quarter = warp & 3, each = p.rows >> 2;
+    const int r = lane < each ? quarter * each + lane : 1 << 20;
+    if (p.overlap) grid_dependency_wait();  // sx
+    for (int t = 0; t < mine; ++t) {
+      const int tile = (int)blockIdx.x + t * (int)gridDim.x;
+      const int nt = p.mt == 1 ? tile : tile / p.mt;
+      const int n = nt * p.R + r, m0 = (tile - nt * p.mt) * p.BT;
+      const int buf = p.bufs == 2 ? t & 1 : 0, cols = min(p.BT, p.M - m0);
+      const bool row = r < p.R && n < p.N;
+      const float swn = row ? p.sw[n] : 0.f;
+      // the tile's sx, fetched while it is summed; two buffers, and the barrier
+      // of the next tile parts their uses
+      const uint32_t sxs = sx_off + (uint32_t)(t & 1) * 1024u;
+      for (int c = (int)threadIdx.x - 128; c < p.BT; c += 128)
+        sts_f32(sxs + 4u * c, c < cols ? p.sx[m0 + c] : 0.f);
+      named_barrier_sync(1, 128);
+      if (!wait(accfull + 8u * buf, (uint32_t)(p.bufs == 2 ? t >> 1 : t) & 1u)) {
+        if (lane == 0) record_error(&g_i8_error, BCQ_ERR_TIMEOUT);
+        break;
+      }
+      umma_fence_after();
+      if (quarter * each < p.R) {
+        TO* y = static_cast<TO*>(p.y) + (int64_t)m0 * p.ldy + n;
+        const uint32_t acc = tmem + (uint32_t)(buf * p.issuers * p.BT) + ((uint32_t)(quarter * 32) << 16);
+        for (int c = 0; c < cols; c += 16) {
+          uint32_t v[16];
+          tmem_ld16(acc + (uint32_t)c, v);
+          float4 sx4[4];
+#pragma unroll
+          for (int j = 0; j < 4; ++j) sx4[j] = lds_f32x4(sxs + 4u * (c + 4 * j));
+          tmem_wait_ld();
+          for (int i = 1; i < p.issuers; ++i) {
+            uint32_t w[16];
+            tmem_ld16(acc + (uint32_t)(i * p.BT + c), w);
+            tmem_wait_ld();
+#pragma unroll
+            for (int j = 0; j < 16; ++j) v[j] += w[j];
+          }
+          float f[16];
+#pragma unroll
+          for (int j = 0; j < 16; ++j) {
+            const float4 q = sx4[j >> 2];
+            f[j] = (float)(int)v[j] * ((j & 3) == 0 ? q.x : (j & 3) == 1 ? q.y : (j & 3) == 2 ? q.z : q.w) * swn;
+          }
+          if (row && c + 16 <= cols) {
+#pragma unroll
+            for (int j = 0; j < 16; ++j, y += p.ldy) store_out(y, f[j]);
+          } else if (row) {
+#pragma unroll
+            for (int j = 0; j < 16; ++j, y += p.ldy)
+              if (c + j < cols) store_out(y, f[j]);
+          }
+        }
+      }
+      umma_fence_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive_cta(accempty + 8u * buf);
+    }
+  }
+  __syncwarp();
+  umma_fence_before();
+  __syncthreads();
+  if (warp == 2) {
+    umma_fence_after();
+    tmem_dealloc(tmem, p.tmem_cols);
+  }
 }
 
 // -------------------------------------------------------------------- host
@@ -129,27 +413,181 @@ bool sizes_ok(int M, int K) { return M >= 0 && K >= 1 && K <= BCQ_I8_MAX_K; }
 
 bool is16(int dtype) { return dtype == BCQ_F16 || dtype == BCQ_BF16; }
 
-cudaError_t launch_quantize(const void* x, int dtype, int M, int K, int64_t ldx, int8_t* q,
-                            int64_t ldq, float* scale, cudaStream_t st) {
-  const uint16_t* p = static_cast<const uint16_t*>(x);
-  if (dtype == BCQ_F16)
-    quantize_i8_kernel<__half><<<M, 256, 0, st>>>(p, ldx, K, q, ldq, scale);
-  else
-    quantize_i8_kernel<__nv_bfloat16><<<M, 256, 0, st>>>(p, ldx, K, q, ldq, scale);
+constexpr size_t kMaxSmem = 232448;                          // 227 KiB per CTA on sm_100
+constexpr unsigned long long kWaitNs = 2000000000ull;         // 2 s
+
+template <typename T>
+cudaError_t launch_quantize_t(const uint16_t* x, int M, int K, int64_t ldx, int8_t* q, int64_t ldq,
+                              float* scale, cudaStream_t st) {
+  if (aligned(x, 16) && (ldx % 8 == 0 || M == 1)) {
+    if (K <= 4096) quantize_i8_kernel<T, 2, true><<<M, 256, 0, st>>>(x, ldx, K, q, ldq, scale);
+    else if (K <= 16384) quantize_i8_kernel<T, 4, true><<<M, 512, 0, st>>>(x, ldx, K, q, ldq, scale);
+    else quantize_i8_kernel<T, 8, true><<<M, 1024, 0, st>>>(x, ldx, K, q, ldq, scale);
+  } else {
+    quantize_i8_kernel<T, 1, false><<<M, 256, 0, st>>>(x, ldx, K, q, ldq, scale);
+  }
   return cudaGetLastError();
 }
 
+cudaError_t launch_quantize(const void* x, int dtype, int M, int K, int64_t ldx, int8_t* q,
+                            int64_t ldq, float* scale, cudaStream_t st) {
+  const uint16_t* p = static_cast<const uint16_t*>(x);
+  return dtype == BCQ_F16 ? launch_quantize_t<__half>(p, M, K, ldx, q, ldq, scale, st)
+                          : launch_quantize_t<__nv_bfloat16>(p, M, K, ldx, q, ldq, scale, st);
+}
+
+using EncodeTiled = CUresult (*)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*,
+                                 const cuuint64_t*, const cuuint64_t*, const cuuint32_t*,
+                                 const cuuint32_t*, CUtensorMapInterleave, CUtensorMapSwizzle,
+                                 CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
+
+// The driver's encoder (no link-time dependency on the driver library).
+EncodeTiled encode_tiled() {
+  static std::atomic<void*> found{nullptr};
+  void* f = found.load(std::memory_order_acquire);
+  if (!f) {
+    cudaDriverEntryPointQueryResult r;
+    if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &f, 12000, cudaEnableDefault,
+                                         &r) != cudaSuccess ||
+        r != cudaDriverEntryPointSuccess)
+      return nullptr;
+    found.store(f, std::memory_order_release);
+  }
+  return reinterpret_cast<EncodeTiled>(f);
+}
+
+// Codes [rows][K] in boxes of box_rows rows by 128 columns.
+bool encode_codes(CUtensorMap* map, const int8_t* p, int64_t rows, int64_t K, int64_t ld,
+                  uint32_t box_rows) {
+  const EncodeTiled f = encode_tiled();
+  if (!f) return false;
+  const cuuint64_t dims[2] = {(cuuint64_t)K, (cuuint64_t)rows};
+  const cuuint64_t strides[1] = {(cuuint64_t)ld};
+  const cuuint32_t box[2] = {kKBlock, box_rows}, step[2] = {1, 1};
+  return f(map, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, const_cast<int8_t*>(p), dims, strides, box, step,
+           CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+           CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+int round_up(int v, int to) { return (v + to - 1) / to * to; }
+
+// The tile that a model of one SM's time likes best.  A block of K takes the
+// longest of: the tensor core (BT / 2 cycles for each of its four
+// instructions), shared memory's reads by it (128 rows of w and BT of x at 128
+// bytes a cycle), the operands' way from L2 (about 50 bytes a cycle an SM),
+// and, where w is read by one tile only, its share of the memory's rate (about
+// 24 bytes a cycle an SM).  Rounds of tiles count whole; a tile's output costs
+// about 8 cycles a column when nothing hides it.
+void plan_gemm(int M, int N, int K, int sms, GemmParams* p, size_t* smem, int* grid) {
+  const int KB = (K + (int)kKBlock - 1) / (int)kKBlock;
+  double best = 0;
+  const int mt0 = (M + 255) / 256;
+  for (int mt = mt0; mt <= mt0 + 4; ++mt) {
+    const int BT = round_up((M + mt - 1) / mt, 16);
+    if ((int64_t)BT * (mt - 1) >= M) continue;
+    const int64_t least = ((int64_t)(N + 127) / 128 * mt + sms - 1) / sms;  // rounds with R = 128
+    for (int64_t rounds = least; rounds <= least + 2; ++rounds) {
+      const int64_t nt_most = std::max<int64_t>(1, rounds * sms / mt);
+      const int R = (int)std::min<int64_t>(128, std::max<int64_t>(8, (N + nt_most - 1) / nt_most));
+      const int64_t nt = (N + R - 1) / R, tiles = nt * mt, full_rounds = (tiles + sms - 1) / sms;
+      const double core = 4.0 * std::max(BT / 2.0, 32.0 + BT / 4.0);
+      const double l2 = 128.0 * (R + BT) / 50.0, dram = mt == 1 ? 128.0 * R / 24.0 : 0;
+      const double cost = full_rounds * KB * std::max(core, std::max(l2, dram)) + 8.0 * BT + 20.0 * full_rounds;
+      if (best == 0 || cost < best) {
+        best = cost;
+        p->R = std::min(R, N);
+        p->BT = BT;
+        p->mt = mt;
+        p->tiles = (int)tiles;
+      }
+    }
+  }
+  p->KB = KB;
+  p->bufs = p->tiles > sms ? 2 : 1;
+  p->rows = p->R <= 64 ? 64 : 128;
+  p->a_block = (uint32_t)round_up(p->R, 8) * kKBlock;
+  p->b_block = (uint32_t)p->BT * kKBlock;
+  const uint32_t block = p->a_block + p->b_block;
+  // about 24 KB a stage: a wait costs the MMA warp about 100 cycles, as long
+  // as the four instructions of a small block of K take
+  p->G = std::max(1, std::min({8, KB, (int)(24576 / block)}));
+  p->KG = (KB + p->G - 1) / p->G;
+  const size_t room = kMaxSmem - 1024 /* alignment */ - 16 * kMaxGemmStages - 96 - 2048 /* sx */;
+  const uint32_t overrun = (uint32_t)p->rows * kKBlock;  // read of the last block of w, beyond R
+  int S = (int)std::min<size_t>(kMaxGemmStages, room / (block * (uint32_t)p->G));
+  while (S > 1 && (size_t)S * p->G * p->a_block + overrun > room) --S;
+  // accumulators fit tensor memory, every issuer has a stage of every tile, and
+  // the ring is a multiple of the issuers
+  p->issuers = p->bufs * p->BT <= 128 ? 4 : p->bufs * p->BT <= 256 ? 2 : 1;
+  while (p->issuers > p->KG || p->issuers > S) p->issuers /= 2;
+  S -= S % p->issuers;
+  p->stages = S;
+  p->b_off = (uint32_t)(S * p->G) * p->a_block;
+  p->bar_off = p->b_off + std::max((uint32_t)(S * p->G) * p->b_block, overrun);
+  uint32_t cols = 32;
+  while (cols < (uint32_t)(p->bufs * p->issuers * p->BT)) cols *= 2;
+  p->tmem_cols = cols;
+  *smem = 1024 + p->bar_off + 16 * (size_t)S + 96 + 2048;
+  *grid = std::min(p->tiles, sms);
+  p->tiles_each = p->tiles / *grid;
+  p->tiles_more = p->tiles % *grid;
+  p->kg_step = ((uint32_t)p->KG << 16) / (uint32_t)*grid;
+}
+
+int sm_count() {
+  int dev = 0, n = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess ||
+      cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess || n < 1)
+    return 0;
+  return n;
+}
+
+template <typename TO>
+cudaError_t launch_gemm_t(const CUtensorMap& wmap, const CUtensorMap& xmap, const GemmParams& p,
+                          size_t smem, int grid, bool overlap, cudaStream_t st) {
+  cudaError_t e = cudaFuncSetAttribute(gemm_i8_kernel<TO>,
+                                       cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kMaxSmem);
+  if (e != cudaSuccess) return e;
+  cudaLaunchAttribute attr = {};
+  attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr.val.programmaticStreamSerializationAllowed = 1;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3((unsigned)grid);
+  cfg.blockDim = dim3(kGemmThreads);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = st;
+  cfg.attrs = &attr;
+  cfg.numAttrs = overlap ? 1 : 0;
+  return cudaLaunchKernelEx(&cfg, gemm_i8_kernel<TO>, wmap, xmap, p);
+}
+
+// overlap: the kernel before in the stream is the quantiser, whose codes and
+// scales are waited for; it writes nothing of w.
 cudaError_t launch_gemm(const int8_t* x, int64_t ldx, const float* sx, const int8_t* w,
                         int64_t ldw, const float* sw, int M, int N, int K, void* y, int dtype,
-                        int64_t ldy, cudaStream_t st) {
-  const dim3 grid((unsigned)((N + 63) / 64), (unsigned)((M + 63) / 64));
-  if (dtype == BCQ_F32)
-    gemm_i8_kernel<<<grid, 256, 0, st>>>(x, ldx, sx, w, ldw, sw, M, N, K, (float*)y, ldy);
-  else if (dtype == BCQ_F16)
-    gemm_i8_kernel<<<grid, 256, 0, st>>>(x, ldx, sx, w, ldw, sw, M, N, K, (__half*)y, ldy);
-  else
-    gemm_i8_kernel<<<grid, 256, 0, st>>>(x, ldx, sx, w, ldw, sw, M, N, K, (__nv_bfloat16*)y, ldy);
-  return cudaGetLastError();
+                        int64_t ldy, bool overlap, cudaStream_t st) {
+  const int sms = sm_count();
+  if (sms == 0) return cudaErrorInvalidDevice;
+  GemmParams p = {};
+  p.sx = sx;
+  p.sw = sw;
+  p.y = y;
+  p.ldy = ldy;
+  p.M = M;
+  p.N = N;
+  p.K = K;
+  p.timeout_ns = kWaitNs;
+  p.overlap = overlap;
+  size_t smem = 0;
+  int grid = 0;
+  plan_gemm(M, N, K, sms, &p, &smem, &grid);
+  CUtensorMap wmap, xmap;
+  if (!encode_codes(&wmap, w, N, K, ldw, (uint32_t)p.R) ||
+      !encode_codes(&xmap, x, M, K, ldx, (uint32_t)p.BT))
+    return cudaErrorInvalidValue;
+  if (dtype == BCQ_F32) return launch_gemm_t<float>(wmap, xmap, p, smem, grid, overlap, st);
+  if (dtype == BCQ_F16) return launch_gemm_t<__half>(wmap, xmap, p, smem, grid, overlap, st);
+  return launch_gemm_t<__nv_bfloat16>(wmap, xmap, p, smem, grid, overlap, st);
 }
 
 // The weight's and the output's arguments, shared by bcq_gemm_i8 and bcq_linear_i8.
@@ -201,7 +639,7 @@ bcq_status bcq_gemm_i8(const int8_t* x, int64_t ldx, const float* sx, const int8
   if (s != BCQ_OK) return s;
   if (ldx < K) return BCQ_ERR_SHAPE;
   if (!aligned(x, 16) || ldx % 16 || !aligned(sx, 4)) return BCQ_ERR_ALIGN;
-  return launch_gemm(x, ldx, sx, w, ldw, sw, M, N, K, y, dtype, ldy, (cudaStream_t)stream) ==
+  return launch_gemm(x, ldx, sx, w, ldw, sw, M, N, K, y, dtype, ldy, false, (cudaStream_t)stream) ==
                  cudaSuccess
              ? BCQ_OK
              : BCQ_ERR_CUDA;
@@ -228,7 +666,7 @@ bcq_status bcq_linear_i8(const void* x, int dtype, int64_t ldx, const int8_t* w,
   float* sx = reinterpret_cast<float*>(q + (size_t)M * (size_t)ldq);
   cudaStream_t st = (cudaStream_t)stream;
   if (launch_quantize(x, dtype, M, K, ldx, q, ldq, sx, st) != cudaSuccess) return BCQ_ERR_CUDA;
-  return launch_gemm(q, ldq, sx, w, ldw, sw, M, N, K, y, dtype, ldy, st) == cudaSuccess
+  return launch_gemm(q, ldq, sx, w, ldw, sw, M, N, K, y, dtype, ldy, true, st) == cudaSuccess
              ? BCQ_OK
              : BCQ_ERR_CUDA;
 }

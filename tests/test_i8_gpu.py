@@ -143,6 +143,20 @@ def test_product_matches_the_oracle(M, N, K, dtype):
                    f"M={M} N={N} K={K} {dtype}")
 
 
+@pytest.mark.parametrize("M,N,K", [(1, 14336, 4096), (16, 14336, 4096), (16, 4096, 14336), (48, 4096, 4096),
+                                   (64, 14336, 4096), (100, 5000, 8192), (128, 14336, 2048), (144, 4096, 3000),
+                                   (250, 9000, 4096), (333, 6000, 4000), (600, 8192, 4096), (1500, 4096, 1100)])
+def test_long_sums_and_many_tiles(M, N, K):
+    """Rings that wrap, tiles in several rounds: against fp64 on the GPU, three calls in a row."""
+    x, sx = _codes(M, K, 3 * M + K)
+    ws = [_codes(N, K, 7 * N + i) for i in range(3)]
+    ys = [api.gemm_i8(x, sx, w, sw, dtype=F32) for w, sw in ws]
+    for y, (w, sw) in zip(ys, ws):
+        acc = x.double() @ w.double().t()          # exact: below 2^53
+        ref = acc * sx.double()[:, None] * sw.double()[None]
+        assert bool(((y.double() - ref).abs() <= 3.01 * 2.0 ** -24 * (1 + 2.0 ** -10) * ref.abs()).all())
+
+
 @pytest.mark.parametrize("M", [1, 20, 300])
 def test_largest_sums_do_not_wrap(M):
     K, N = 65536, 40
