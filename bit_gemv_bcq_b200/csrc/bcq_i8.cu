@@ -7,6 +7,7 @@
 #include <algorithm>
 #include <atomic>
 #include <cstdint>
+#include <type_traits>
 
 #include "bcq.h"
 #include "bcq_device.cuh"
@@ -159,26 +160,34 @@ __global__ void __launch_bounds__(1024) quantize_i8_kernel(const uint16_t* __res
 // the round before that one for it.  R needs no alignment: the tensor core reads 64 or 128 rows of
 // the stage whatever they hold, and what they give for rows beyond R is not
 // looked at.
+//
+// PAIR: two CTAs of a cluster share an instruction (cta_group::2, M = 256).
+// Each holds R rows of w, half of the tile's rows of x, and the outputs of its
+// own R rows, so a CTA fetches BT / 2 rows of x instead of BT.  The CTA of rank
+// 0 issues for both; its `full` barriers count the copies of both, and
+// consumed stages and finished sums are told to both.
 struct GemmParams {
   const float* sx;
   const float* sw;
   void* y;
   int64_t ldy;
   int M, N, K;
-  int R, BT, rows;      // tile; rows the tensor core takes of w (64 or 128)
+  int R, BT, rows;      // tile (PAIR: R rows for each CTA); rows the tensor core takes of w, 64 or 128
+  int BX;               // rows of x that a CTA holds (BT, or half of it)
   int mt, tiles;        // tiles along M, in all
   int KB, G, KG;        // blocks of K, blocks a stage, stages' worth of K
   int stages;           // ring depth
   int bufs;             // sets of accumulators (1 or 2)
   int issuers;          // warps that issue MMAs, accumulators of a set (1, 2 or 4)
-  int tiles_each, tiles_more;  // tiles of every CTA, CTAs that have one more
-  uint32_t kg_step;     // 2^16 KG / CTAs: where a CTA starts along K
+  int workers;          // CTAs, or pairs
+  int tiles_each, tiles_more;  // tiles of every worker, workers that have one more
+  uint32_t kg_step;     // 2^16 KG / workers: where a worker starts along K
   int overlap;          // the kernel before makes x's codes and may still run
   uint32_t a_block, b_block, b_off, bar_off, tmem_cols;
   unsigned long long timeout_ns;
 };
 
-constexpr int kGemmThreads = 320;  // w, x, MMA, MMA, four output warps, MMA, MMA
+constexpr int kGemmThreads = 448;  // w, x, MMA, MMA, eight output warps, MMA, MMA
 constexpr int kMaxGemmStages = 32;
 constexpr uint32_t kKBlock = 128;
 
@@ -186,15 +195,15 @@ constexpr uint32_t kKBlock = 128;
 struct GemmCursor {
   int tile, kg, left, slot;  // left: stages left of the tile
   uint32_t phase;            // of the ring slot
-  __device__ __forceinline__ void start(int kg_first, int KG) {
-    tile = (int)blockIdx.x;
+  __device__ __forceinline__ void start(int worker, int kg_first, int KG) {
+    tile = worker;
     kg = kg_first;
     left = KG;
     slot = 0;
     phase = 0;
   }
   // returns whether the next stage belongs to another tile
-  __device__ __forceinline__ bool step(int KG, int S) {
+  __device__ __forceinline__ bool step(int KG, int S, int workers) {
     if (++slot == S) {
       slot = 0;
       phase ^= 1u;
@@ -202,12 +211,12 @@ struct GemmCursor {
     if (++kg == KG) kg = 0;
     if (--left > 0) return false;
     left = KG;
-    tile += (int)gridDim.x;
+    tile += workers;
     return true;
   }
 };
 
-template <typename TO>
+template <typename TO, bool PAIR>
 __global__ void __launch_bounds__(kGemmThreads, 1)
     gemm_i8_kernel(const __grid_constant__ CUtensorMap wmap, const __grid_constant__ CUtensorMap xmap,
                    const GemmParams p) {
@@ -218,6 +227,8 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
   // instruction, they cost 107 cycles an MMA against 39)
   const int warp = __shfl_sync(0xFFFFFFFFu, (int)threadIdx.x >> 5, 0), lane = threadIdx.x & 31;
   const int S = p.stages;
+  const int rank = PAIR ? (int)cluster_rank() : 0;
+  const int worker = PAIR ? (int)blockIdx.x >> 1 : (int)blockIdx.x;
   const uint32_t full = sbase + p.bar_off, empty = full + 8u * S, accfull = empty + 8u * S,
                  accempty = accfull + 16u, drain = accempty + 16u, slot = drain + 32u,
                  sx_off = slot + 16u;
@@ -228,25 +239,32 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
     }
     if (lane < 2) {
       mbar_init(accfull + 8u * lane, (uint32_t)p.issuers);
-      mbar_init(accempty + 8u * lane, 4);
+      mbar_init(accempty + 8u * lane, PAIR ? 16 : 8);
     }
     if (lane < 4) mbar_init(drain + 8u * lane, 1);
     fence_mbar_init();
   } else if (warp == 2) {
-    tmem_alloc(slot, p.tmem_cols);
+    if (PAIR) tmem_alloc_pair(slot, p.tmem_cols);
+    else tmem_alloc(slot, p.tmem_cols);
   }
   umma_fence_before();
-  // the weights' warp goes ahead: its first loads need nothing of the others
-  if (warp == 0) asm volatile("bar.arrive 2, %0;" ::"n"(kGemmThreads) : "memory");
-  else named_barrier_sync(2, kGemmThreads);
+  if (PAIR) {
+    __syncthreads();
+    cluster_sync();
+  } else if (warp == 0) {
+    // the weights' warp goes ahead: its first loads need nothing of the others
+    asm volatile("bar.arrive 2, %0;" ::"n"(kGemmThreads) : "memory");
+  } else {
+    named_barrier_sync(2, kGemmThreads);
+  }
   umma_fence_after();
-  const uint32_t tmem = warp == 0 ? 0u : lds_u32v(slot);
-  const int mine = p.tiles_each + ((int)blockIdx.x < p.tiles_more ? 1 : 0);
+  const uint32_t tmem = !PAIR && warp == 0 ? 0u : lds_u32v(slot);
+  const int mine = p.tiles_each + (worker < p.tiles_more ? 1 : 0);
   const int total = mine * p.KG;
-  // Stages of K in turn from a first one of this CTA's own (the sum is exact in
+  // Stages of K in turn from a first one of this worker's own (the sum is exact in
   // any order): CTAs that read the same rows of x do not ask for the same lines
   // of L2 at the same time.
-  const int kg_first = (int)((blockIdx.x * p.kg_step) >> 16);
+  const int kg_first = (int)(((uint32_t)worker * p.kg_step) >> 16);
   auto wait = [&](uint32_t bar, uint32_t parity) {
     return __all_sync(0xFFFFFFFFu, mbar_wait_bounded(bar, parity, p.timeout_ns)) != 0;
   };
@@ -256,45 +274,62 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
     const bool one = elect_one(), is_w = warp == 0;
     const CUtensorMap* map = is_w ? &wmap : &xmap;
     const uint32_t block = is_w ? p.a_block : p.b_block, base = sbase + (is_w ? 0u : p.b_off);
-    const uint32_t bytes = (uint32_t)(is_w ? p.R : p.BT) * kKBlock;
+    const uint32_t bytes = (uint32_t)(is_w ? p.R : p.BX) * kKBlock * (PAIR ? 2u : 1u);  // of both CTAs
     // x's codes come from the kernel before; the first weights need not wait for it
     if (!is_w && p.overlap) grid_dependency_wait();
     GemmCursor c;
-    c.start(kg_first, p.KG);
+    c.start(worker, kg_first, p.KG);
     auto first_row = [&]() {
       const int nt = p.mt == 1 ? c.tile : c.tile / p.mt;
-      return is_w ? nt * p.R : (c.tile - nt * p.mt) * p.BT;
+      return is_w ? (PAIR ? 2 * nt + rank : nt) * p.R : (c.tile - nt * p.mt) * p.BT + rank * p.BX;
     };
     int row = first_row();
     for (int i = 0; i < total; ++i) {
       if (i >= S && !wait(empty + 8u * c.slot, c.phase ^ 1u)) {
         if (one) record_error(&g_i8_error, BCQ_ERR_TIMEOUT);
-        for (int j = i - S; j < i; ++j)  // the copies in flight
+        // the copies in flight (a pair's are all told to rank 0, which the
+        // other CTA waits for at the end)
+        for (int j = rank == 0 ? i - S : i; j < i; ++j)
           mbar_wait_bounded(full + 8u * (j % S), (uint32_t)(j / S) & 1u, p.timeout_ns);
         break;
       }
       const int kb = c.kg * p.G, n = min(p.G, p.KB - kb);
       if (one) {
-        mbar_arrive_expect_tx(full + 8u * c.slot, bytes * (uint32_t)n);
+        const uint32_t bar = full + 8u * c.slot;
         uint32_t to = base + (uint32_t)(c.slot * p.G) * block;
-        for (int j = 0; j < n; ++j, to += block)
-          tma_load_2d(to, map, (kb + j) * (int)kKBlock, row, full + 8u * c.slot);
+        if (rank == 0) mbar_arrive_expect_tx(bar, bytes * (uint32_t)n);
+        if (PAIR) {
+          const uint32_t leader = map_rank(bar, 0);
+          for (int j = 0; j < n; ++j, to += block)
+            tma_load_2d_pair(to, map, (kb + j) * (int)kKBlock, row, leader);
+        } else {
+          for (int j = 0; j < n; ++j, to += block)
+            tma_load_2d(to, map, (kb + j) * (int)kKBlock, row, bar);
+        }
       }
-      if (c.step(p.KG, S)) row = first_row();
+      if (c.step(p.KG, S, p.workers)) row = first_row();
     }
-  } else if (warp < 4 || warp >= 8) {
+  } else if (warp < 4 || warp >= 12) {
     // --------------------------------------------------------------- the sums
-    const int issuer = warp < 4 ? warp - 2 : warp - 6;
+    const int issuer = warp < 4 ? warp - 2 : warp - 10;
     const bool one = elect_one();
     // kind::i8: int32 D, signed A and B, both K-major, N = BT, M = rows
     const uint32_t idesc = (2u << 4) | (1u << 7) | (1u << 10) | ((uint32_t)(p.BT >> 3) << 17) |
-                           ((uint32_t)(p.rows >> 4) << 24);
+                           ((uint32_t)((PAIR ? 256 : p.rows) >> 4) << 24);
     const uint64_t ad0 = umma_desc_sw128(sbase), bd0 = umma_desc_sw128(sbase + p.b_off);
     const uint32_t a_units = p.a_block >> 4, b_units = p.b_block >> 4;  // never carry out of the address
+    auto mma = [](uint32_t d, uint64_t a, uint64_t b, uint32_t id, uint32_t acc) {
+      if (PAIR) umma_i8_ss_pair(d, a, b, id, acc);
+      else umma_i8_ss(d, a, b, id, acc);
+    };
+    auto commit = [](uint32_t bar) {
+      if (PAIR) umma_commit_pair(bar);
+      else umma_commit(bar);
+    };
     bool ok = true;
     GemmCursor c;
-    c.start(kg_first, p.KG);
-    for (int t = 0; t < mine && ok && issuer < p.issuers; ++t) {
+    c.start(worker, kg_first, p.KG);
+    for (int t = 0; t < mine && ok && issuer < p.issuers && rank == 0; ++t) {
       const int buf = p.bufs == 2 ? t & 1 : 0, round = p.bufs == 2 ? t >> 1 : t;
       if (round > 0) ok = wait(accempty + 8u * buf, (uint32_t)(round - 1) & 1u);
       umma_fence_after();
@@ -311,55 +346,58 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
             for (int j = 0; j < n; ++j, ad += a_units, bd += b_units) {
               // 32-byte slices of K: all four, or those that hold some of it
               const int rest = p.K - (kb + j) * (int)kKBlock;
-              umma_i8_ss(d, ad, bd, idesc, more);
-              if (rest > 32) umma_i8_ss(d, ad + 2, bd + 2, idesc, 1);
-              if (rest > 64) umma_i8_ss(d, ad + 4, bd + 4, idesc, 1);
-              if (rest > 96) umma_i8_ss(d, ad + 6, bd + 6, idesc, 1);
+              mma(d, ad, bd, idesc, more);
+              if (rest > 32) mma(d, ad + 2, bd + 2, idesc, 1u);
+              if (rest > 64) mma(d, ad + 4, bd + 4, idesc, 1u);
+              if (rest > 96) mma(d, ad + 6, bd + 6, idesc, 1u);
               more = 1;
             }
-            umma_commit(empty + 8u * c.slot);
+            commit(empty + 8u * c.slot);
           }
           more = 1;
         }
-        c.step(p.KG, S);
+        c.step(p.KG, S, p.workers);
       }
-      if (ok && one) umma_commit(accfull + 8u * buf);
+      if (ok && one) commit(accfull + 8u * buf);
     }
     if (!ok) {
       if (one) {
         record_error(&g_i8_error, BCQ_ERR_TIMEOUT);
-        umma_commit(drain + 8u * issuer);
+        commit(drain + 8u * issuer);
       }
       mbar_wait_bounded(drain + 8u * issuer, 0, p.timeout_ns);
     }
   } else {
     // ------------------------------------------------------------ the outputs
     // 64 rows lie in the first 16 lanes of each quarter, 128 in all 32
-    const int quarter = warp & 3, each = p.rows >> 2;
+    // two warps a quarter, each half of the columns
+    const int quarter = warp & 3, each = p.rows >> 2, half = (warp - 4) >> 2;
+    const int split = ((p.BT >> 4) + 1) / 2 * 16;
     const int r = lane < each ? quarter * each + lane : 1 << 20;
     if (p.overlap) grid_dependency_wait();  // sx
     for (int t = 0; t < mine; ++t) {
-      const int tile = (int)blockIdx.x + t * (int)gridDim.x;
+      const int tile = worker + t * p.workers;
       const int nt = p.mt == 1 ? tile : tile / p.mt;
-      const int n = nt * p.R + r, m0 = (tile - nt * p.mt) * p.BT;
+      const int n = (PAIR ? 2 * nt + rank : nt) * p.R + r, m0 = (tile - nt * p.mt) * p.BT;
       const int buf = p.bufs == 2 ? t & 1 : 0, cols = min(p.BT, p.M - m0);
       const bool row = r < p.R && n < p.N;
       const float swn = row ? p.sw[n] : 0.f;
       // the tile's sx, fetched while it is summed; two buffers, and the barrier
       // of the next tile parts their uses
       const uint32_t sxs = sx_off + (uint32_t)(t & 1) * 1024u;
-      for (int c = (int)threadIdx.x - 128; c < p.BT; c += 128)
+      for (int c = (int)threadIdx.x - 128; c < p.BT; c += 256)
         sts_f32(sxs + 4u * c, c < cols ? p.sx[m0 + c] : 0.f);
-      named_barrier_sync(1, 128);
+      named_barrier_sync(1, 256);
       if (!wait(accfull + 8u * buf, (uint32_t)(p.bufs == 2 ? t >> 1 : t) & 1u)) {
         if (lane == 0) record_error(&g_i8_error, BCQ_ERR_TIMEOUT);
         break;
       }
       umma_fence_after();
       if (quarter * each < p.R) {
-        TO* y = static_cast<TO*>(p.y) + (int64_t)m0 * p.ldy + n;
+        const int c_first = half * split, c_end = half ? cols : min(cols, split);
+        TO* y = static_cast<TO*>(p.y) + (int64_t)(m0 + c_first) * p.ldy + n;
         const uint32_t acc = tmem + (uint32_t)(buf * p.issuers * p.BT) + ((uint32_t)(quarter * 32) << 16);
-        for (int c = 0; c < cols; c += 16) {
+        for (int c = c_first; c < c_end; c += 16) {
           uint32_t v[16];
           tmem_ld16(acc + (uint32_t)c, v);
           float4 sx4[4];
@@ -379,27 +417,32 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
             const float4 q = sx4[j >> 2];
             f[j] = (float)(int)v[j] * ((j & 3) == 0 ? q.x : (j & 3) == 1 ? q.y : (j & 3) == 2 ? q.z : q.w) * swn;
           }
-          if (row && c + 16 <= cols) {
+          if (row && c + 16 <= c_end) {
 #pragma unroll
             for (int j = 0; j < 16; ++j, y += p.ldy) store_out(y, f[j]);
           } else if (row) {
 #pragma unroll
             for (int j = 0; j < 16; ++j, y += p.ldy)
-              if (c + j < cols) store_out(y, f[j]);
+              if (c + j < c_end) store_out(y, f[j]);
           }
         }
       }
       umma_fence_before();
       __syncwarp();
-      if (lane == 0) mbar_arrive_cta(accempty + 8u * buf);
+      if (lane == 0) {
+        if (PAIR) mbar_arrive_cluster(map_rank(accempty + 8u * buf, 0));
+        else mbar_arrive_cta(accempty + 8u * buf);
+      }
     }
   }
   __syncwarp();
   umma_fence_before();
   __syncthreads();
+  if (PAIR) cluster_sync();  // neither CTA leaves while the other uses its memory
   if (warp == 2) {
     umma_fence_after();
-    tmem_dealloc(tmem, p.tmem_cols);
+    if (PAIR) tmem_dealloc_pair(tmem, p.tmem_cols);
+    else tmem_dealloc(tmem, p.tmem_cols);
   }
 }
 
@@ -471,42 +514,53 @@ bool encode_codes(CUtensorMap* map, const int8_t* p, int64_t rows, int64_t K, in
 
 int round_up(int v, int to) { return (v + to - 1) / to * to; }
 
-// The tile that a model of one SM's time likes best.  A block of K takes the
-// longest of: the tensor core (BT / 2 cycles for each of its four
-// instructions), shared memory's reads by it (128 rows of w and BT of x at 128
-// bytes a cycle), the operands' way from L2 (about 50 bytes a cycle an SM),
-// and, where w is read by one tile only, its share of the memory's rate (about
-// 24 bytes a cycle an SM).  Rounds of tiles count whole; a tile's output costs
-// about 8 cycles a column when nothing hides it.
-void plan_gemm(int M, int N, int K, int sms, GemmParams* p, size_t* smem, int* grid) {
+// The tile, and whether CTAs work in pairs, that a model of one SM's time likes
+// best.  A block of K takes the longest of: the tensor core (BT / 2 cycles for
+// each of its four instructions), shared memory's reads by it (128 rows of w
+// and those of x at 128 bytes a cycle), the operands' way from L2 (about 50
+// bytes a cycle an SM), and, where w is read by one tile only, its share of
+// the memory's rate (about 24 bytes a cycle an SM).  Rounds of tiles count
+// whole; a tile's output costs about 15 cycles a column when nothing hides it,
+// a pair's start some 1000 cycles.
+void plan_gemm(int M, int N, int K, int sms, GemmParams* p, size_t* smem, int* grid, bool* pair) {
   const int KB = (K + (int)kKBlock - 1) / (int)kKBlock;
   double best = 0;
   const int mt0 = (M + 255) / 256;
-  for (int mt = mt0; mt <= mt0 + 4; ++mt) {
-    const int BT = round_up((M + mt - 1) / mt, 16);
-    if ((int64_t)BT * (mt - 1) >= M) continue;
-    const int64_t least = ((int64_t)(N + 127) / 128 * mt + sms - 1) / sms;  // rounds with R = 128
-    for (int64_t rounds = least; rounds <= least + 2; ++rounds) {
-      const int64_t nt_most = std::max<int64_t>(1, rounds * sms / mt);
-      const int R = (int)std::min<int64_t>(128, std::max<int64_t>(8, (N + nt_most - 1) / nt_most));
-      const int64_t nt = (N + R - 1) / R, tiles = nt * mt, full_rounds = (tiles + sms - 1) / sms;
-      const double core = 4.0 * std::max(BT / 2.0, 32.0 + BT / 4.0);
-      const double l2 = 128.0 * (R + BT) / 50.0, dram = mt == 1 ? 128.0 * R / 24.0 : 0;
-      const double cost = full_rounds * KB * std::max(core, std::max(l2, dram)) + 8.0 * BT + 20.0 * full_rounds;
-      if (best == 0 || cost < best) {
-        best = cost;
-        p->R = std::min(R, N);
-        p->BT = BT;
-        p->mt = mt;
-        p->tiles = (int)tiles;
+  for (int two = 0; two < 2; ++two) {
+    const int workers = two ? sms / 2 : sms;
+    for (int mt = mt0; mt <= mt0 + 4; ++mt) {
+      const int BT = round_up((M + mt - 1) / mt, two ? 32 : 16);
+      if ((int64_t)BT * (mt - 1) >= M || (two && BT < 64)) continue;
+      const int rows_most = two ? 256 : 128;
+      const int64_t least = ((int64_t)(N + rows_most - 1) / rows_most * mt + workers - 1) / workers;
+      for (int64_t rounds = least; rounds <= least + 2; ++rounds) {
+        const int64_t nt_most = std::max<int64_t>(1, rounds * workers / mt);
+        int64_t rows = std::min<int64_t>(rows_most, std::max<int64_t>(8, (N + nt_most - 1) / nt_most));
+        if (two) rows = (rows + 1) / 2 * 2;
+        const int R = (int)(two ? rows / 2 : rows);
+        const int64_t nt = (N + rows - 1) / rows, tiles = nt * mt, whole = (tiles + workers - 1) / workers;
+        const int BX = two ? BT / 2 : BT;
+        const double core = 4.0 * std::max(BT / 2.0, 32.0 + BX / 4.0);
+        const double l2 = 128.0 * (R + BX) / 50.0, dram = mt == 1 ? 128.0 * R / 24.0 : 0;
+        const double cost = whole * KB * std::max(core, std::max(l2, dram)) + 15.0 * BT + 20.0 * whole + (two ? 1000.0 : 0.0);
+        if (best == 0 || cost < best) {
+          best = cost;
+          p->R = std::min(R, N);
+          p->BT = BT;
+          p->BX = BX;
+          p->mt = mt;
+          p->tiles = (int)tiles;
+          p->workers = (int)std::min<int64_t>(workers, tiles);
+          *pair = two != 0;
+        }
       }
     }
   }
   p->KB = KB;
-  p->bufs = p->tiles > sms ? 2 : 1;
-  p->rows = p->R <= 64 ? 64 : 128;
+  p->bufs = p->tiles > p->workers ? 2 : 1;
+  p->rows = p->R <= 64 && !*pair ? 64 : 128;
   p->a_block = (uint32_t)round_up(p->R, 8) * kKBlock;
-  p->b_block = (uint32_t)p->BT * kKBlock;
+  p->b_block = (uint32_t)p->BX * kKBlock;
   const uint32_t block = p->a_block + p->b_block;
   // about 24 KB a stage: a wait costs the MMA warp about 100 cycles, as long
   // as the four instructions of a small block of K take
@@ -528,10 +582,10 @@ void plan_gemm(int M, int N, int K, int sms, GemmParams* p, size_t* smem, int* g
   while (cols < (uint32_t)(p->bufs * p->issuers * p->BT)) cols *= 2;
   p->tmem_cols = cols;
   *smem = 1024 + p->bar_off + 16 * (size_t)S + 96 + 2048;
-  *grid = std::min(p->tiles, sms);
-  p->tiles_each = p->tiles / *grid;
-  p->tiles_more = p->tiles % *grid;
-  p->kg_step = ((uint32_t)p->KG << 16) / (uint32_t)*grid;
+  *grid = *pair ? 2 * p->workers : p->workers;
+  p->tiles_each = p->tiles / p->workers;
+  p->tiles_more = p->tiles % p->workers;
+  p->kg_step = ((uint32_t)p->KG << 16) / (uint32_t)p->workers;
 }
 
 int sm_count() {
@@ -542,23 +596,32 @@ int sm_count() {
   return n;
 }
 
-template <typename TO>
+template <typename TO, bool PAIR>
 cudaError_t launch_gemm_t(const CUtensorMap& wmap, const CUtensorMap& xmap, const GemmParams& p,
-                          size_t smem, int grid, bool overlap, cudaStream_t st) {
-  cudaError_t e = cudaFuncSetAttribute(gemm_i8_kernel<TO>,
+                          size_t smem, int grid, cudaStream_t st) {
+  cudaError_t e = cudaFuncSetAttribute(gemm_i8_kernel<TO, PAIR>,
                                        cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kMaxSmem);
   if (e != cudaSuccess) return e;
-  cudaLaunchAttribute attr = {};
-  attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  attr.val.programmaticStreamSerializationAllowed = 1;
+  cudaLaunchAttribute attr[2] = {};
+  int n = 0;
+  if (PAIR) {
+    attr[n].id = cudaLaunchAttributeClusterDimension;
+    attr[n].val.clusterDim.x = 2;
+    attr[n].val.clusterDim.y = 1;
+    attr[n++].val.clusterDim.z = 1;
+  }
+  if (p.overlap) {
+    attr[n].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[n++].val.programmaticStreamSerializationAllowed = 1;
+  }
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3((unsigned)grid);
   cfg.blockDim = dim3(kGemmThreads);
   cfg.dynamicSmemBytes = smem;
   cfg.stream = st;
-  cfg.attrs = &attr;
-  cfg.numAttrs = overlap ? 1 : 0;
-  return cudaLaunchKernelEx(&cfg, gemm_i8_kernel<TO>, wmap, xmap, p);
+  cfg.attrs = attr;
+  cfg.numAttrs = (unsigned)n;
+  return cudaLaunchKernelEx(&cfg, gemm_i8_kernel<TO, PAIR>, wmap, xmap, p);
 }
 
 // overlap: the kernel before in the stream is the quantiser, whose codes and
@@ -580,14 +643,20 @@ cudaError_t launch_gemm(const int8_t* x, int64_t ldx, const float* sx, const int
   p.overlap = overlap;
   size_t smem = 0;
   int grid = 0;
-  plan_gemm(M, N, K, sms, &p, &smem, &grid);
+  bool pair = false;
+  plan_gemm(M, N, K, sms, &p, &smem, &grid, &pair);
   CUtensorMap wmap, xmap;
   if (!encode_codes(&wmap, w, N, K, ldw, (uint32_t)p.R) ||
-      !encode_codes(&xmap, x, M, K, ldx, (uint32_t)p.BT))
+      !encode_codes(&xmap, x, M, K, ldx, (uint32_t)p.BX))
     return cudaErrorInvalidValue;
-  if (dtype == BCQ_F32) return launch_gemm_t<float>(wmap, xmap, p, smem, grid, overlap, st);
-  if (dtype == BCQ_F16) return launch_gemm_t<__half>(wmap, xmap, p, smem, grid, overlap, st);
-  return launch_gemm_t<__nv_bfloat16>(wmap, xmap, p, smem, grid, overlap, st);
+  auto launch = [&](auto* type) {
+    using TO = std::remove_pointer_t<decltype(type)>;
+    return pair ? launch_gemm_t<TO, true>(wmap, xmap, p, smem, grid, st)
+                : launch_gemm_t<TO, false>(wmap, xmap, p, smem, grid, st);
+  };
+  if (dtype == BCQ_F32) return launch((float*)nullptr);
+  if (dtype == BCQ_F16) return launch((__half*)nullptr);
+  return launch((__nv_bfloat16*)nullptr);
 }
 
 // The weight's and the output's arguments, shared by bcq_gemm_i8 and bcq_linear_i8.
