@@ -203,6 +203,29 @@ __global__ void __launch_bounds__(256) kv4_read_kernel(ReadParams p) {
 
 // --------------------------------------------------------------- attention
 
+// Attention of few rows a key/value head: decode steps, drafts, short chunks.
+//
+// A warp takes 32 positions at a time, the codes as they lie in the cache.  A
+// nibble masked out of a word is the fp16 subnormal c 2^-24 (the high one of a
+// byte c 2^-20), which the tensor core multiplies exactly, so a code becomes
+// an operand by one AND, without a conversion, a scale or an offset: those are
+// applied to the results,
+//   q . K_t = sum_g  a_tg (sum_{d in g} q_d c_td) + z_tg (sum_{d in g} q_d)
+//   out_d   = sum_t (p_t a_tg) c_td + sum_t p_t z_tg,
+// a few operations a position instead of one a value.  Both products have the
+// codes as the first operand of mma.m16n8k16 (16 positions, or 16 values of a
+// vector; one 32-bit word of codes fills the four registers) and 8 rows as
+// the second, so 8 rows of a key/value head (the query heads that share it,
+// times the rows of the call) fill an instruction.  Queries are scaled by a
+// power of two to the top of fp16's range; p a is rounded to fp16 (half a step
+// 2^-11 of each weight), with p scaled by 4 so that neither the largest a (8000)
+// overflows nor small ones lose bits before 2^-26; scores, sums and outputs
+// are fp32.
+//
+// The codes' way: cp.async into a ring of three stages a warp (nobody else
+// reads them, so no barrier but the warp's own), 16-byte pieces placed so that
+// the fragment loads have no bank conflicts.  A long sequence is split over
+// CTAs, whose partial results a second kernel joins in order.
 struct AttentionParams {
   Places at;
   const uint8_t* k;
@@ -213,86 +236,549 @@ struct AttentionParams {
   uint16_t* out;
   float* lse;
   int64_t ld_q, hd_q, ld_o, hd_o;
-  int T, q_heads, D, max_q, causal, window;
+  int T, q_heads, max_q, causal, window;
   float scale;
+  int group;       // query heads a key/value head
+  int rows;        // rows (of a key/value head) a CTA
+  int row_blocks;  // CTAs along max_q * group rows
+  int splits;      // most CTAs along the positions
+  int chunk;       // positions of one, at least
+  float* part;     // [splits][T][q_heads][D], then (max, sum) [splits][T][q_heads]
 };
 
-// One block a (row, query head), 128 positions at a time: a thread a
-// position's score, then a thread two values of the output.
-template <typename T>
-__global__ void __launch_bounds__(128) kv4_attention_kernel(AttentionParams p) {
-  __shared__ float qs[256], ps[128], red[4];
-  const int t = blockIdx.x, h = blockIdx.y, tid = threadIdx.x, D = p.D;
+// The positions that a block of rows sees, and how they are split.
+struct Span {
+  int first_row, rows;   // of the sequence in the call
+  int len;               // tokens in the cache, within the table
+  int pos0;              // position of the sequence's first row
+  int begin, end;        // positions seen by some row of the block
+  int chunk, parts;      // positions a part, parts
+};
+
+__device__ __forceinline__ Span span_of(const AttentionParams& p, int b, int block) {
+  Span s;
+  const int2 r = rows_of(p.at, b);
+  s.first_row = r.x;
+  s.rows = r.x < 0 ? 0 : min(min(r.y, p.max_q), p.T - r.x);
+  const int len = p.at.kv_len[b];
+  s.len = (int)min((int64_t)max(len, 0), (int64_t)p.at.table_width * p.at.page_size);
+  s.pos0 = len - r.y;
+  const int i0 = block * p.rows / p.group;                                  // first and last row
+  const int i1 = min(s.rows - 1, ((block + 1) * p.rows - 1) / p.group);     // (of the sequence)
+  s.end = p.causal ? min(s.len, s.pos0 + i1 + 1) : s.len;
+  s.begin = p.window > 0 ? max(0, s.pos0 + i0 - p.window + 1) & ~31 : 0;
+  const int n = s.end - s.begin;
+  if (i0 >= s.rows || n <= 0) {
+    s.parts = i0 < s.rows ? 1 : 0;  // rows that see nothing are still written
+    s.chunk = 0;
+    s.end = s.begin;
+    return s;
+  }
+  const int even = (n + p.splits - 1) / p.splits;
+  s.chunk = max(p.chunk, (even + 127) & ~127);
+  s.parts = (n + s.chunk - 1) / s.chunk;
+  return s;
+}
+
+__device__ __forceinline__ void cp_async16(uint32_t dst, const void* src) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
+}
+__device__ __forceinline__ void cp_async_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int N>
+__device__ __forceinline__ void cp_async_wait() {
+  asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
+}
+
+// D (16 x 8, fp32) += A (16 x 16, fp16) x B (16 x 8, fp16).
+__device__ __forceinline__ void mma16816(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2,
+                                         uint32_t a3, uint32_t b0, uint32_t b1) {
+  asm volatile(
+      "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, "
+      "{%8, %9}, {%0, %1, %2, %3};"
+      : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+// Transpose of an 8 x 8 matrix of 16-bit values, two a lane.
+__device__ __forceinline__ uint32_t transpose8x8(uint32_t v) {
+  uint32_t d;
+  asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(d) : "r"(v));
+  return d;
+}
+__device__ __forceinline__ uint32_t pack_f16(float lo, float hi) {
+  uint32_t d;
+  asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(d) : "f"(hi), "f"(lo));
+  return d;
+}
+__device__ __forceinline__ float ex2(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+__device__ __forceinline__ float2 half2_at(uint32_t bits) {
+  return __half22float2(*reinterpret_cast<const __half2*>(&bits));
+}
+
+constexpr int kFewWarps = 4;    // of a CTA
+constexpr int kFewStages = 3;   // of a warp's ring
+constexpr int kFewTokens = 32;  // of a stage
+constexpr float kWeightBits = 2.f;  // p is held times 2^2
+
+template <int D>
+struct FewShape {
+  static constexpr int kGroups = D / kKvGroup;
+  static constexpr int kRow = D / 2;                         // bytes of a vector's codes
+  static constexpr int kPieces = kRow / 16;                  // 16-byte pieces of it
+  static constexpr uint32_t kCodes = 16 * kRow;              // of 16 positions, K or V
+  static constexpr uint32_t kParam = 16 * kGroups * 4;
+  static constexpr uint32_t kHalf = 2 * kCodes + 2 * kParam; // 16 positions: K, V, their params
+  static constexpr uint32_t kStage = 2 * kHalf;
+  static constexpr uint32_t kRing = kFewStages * kStage;     // of a warp
+  // where piece `piece` of row `row` of 16 lies: four rows in turn take four
+  // different 32-byte parts of the banks
+  static __device__ __forceinline__ uint32_t place(int row, int piece) {
+    const int f = kGroups == 1 ? 0 : kGroups == 2 ? (row >> 1) & 1 : row & 3;
+    return (uint32_t)(row * kRow + ((piece ^ (f << 1)) << 4));
+  }
+};
+
+template <typename T, int D, int NT>
+__global__ void __launch_bounds__(kFewWarps * 32) kv4_few_kernel(const AttentionParams p) {
+  using S = FewShape<D>;
+  constexpr int G = S::kGroups;
+  extern __shared__ __align__(128) unsigned char smem[];
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int r = lane >> 2, c = lane & 3;
+  const int block = blockIdx.x % p.row_blocks, kvh = blockIdx.x / p.row_blocks % p.at.heads;
+  const int b = blockIdx.x / p.row_blocks / p.at.heads, part = blockIdx.y;
+  const Span sp = span_of(p, b, block);
+  if (part == 0 && block == 0 && kvh == 0 && threadIdx.x == 0) {
+    if (rows_of(p.at, b).y > p.max_q) record_error(&g_kv4_error, BCQ_ERR_SHAPE);
+    if (p.at.kv_len[b] != sp.len) record_error(&g_kv4_error, BCQ_ERR_PAGE);
+  }
+  if (part >= sp.parts) return;
+  const int row0 = block * p.rows;                       // of the key/value head's rows
+  const int row_n = min(p.rows, sp.rows * p.group - row0);
+
+  // ---- queries: lane (r, c) holds row r's values that its codes will meet
+  uint32_t qf[NT][G][2][4];
+  float qs[NT][G][2], fs[NT][2];
+  int hi[NT][2], lo[NT][2];
+  int hi_all = sp.end, lo_all = sp.begin;
+#pragma unroll
+  for (int nt = 0; nt < NT; ++nt) {
+    const int row = nt * 8 + r;
+    const bool live = row < row_n;
+    const int i = live ? (row0 + row) / p.group : 0, h = live ? (row0 + row) % p.group : 0;
+    const uint16_t* src = p.q + (int64_t)(sp.first_row + i) * p.ld_q + (int64_t)(kvh * p.group + h) * p.hd_q;
+    float f[G][2][8];
+    float top = 0.f;
+#pragma unroll
+    for (int g = 0; g < G; ++g)
+#pragma unroll
+      for (int w = 0; w < 2; ++w) {
+        uint4 raw = make_uint4(0, 0, 0, 0);
+        if (live) raw = *reinterpret_cast<const uint4*>(src + g * kKvGroup + (2 * c + w) * 8);
+        const uint32_t words[4] = {raw.x, raw.y, raw.z, raw.w};
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+          f[g][w][e] = bits_to_float<T>((words[e >> 1] >> (16 * (e & 1))) & 0xFFFFu);
+          top = fmaxf(top, fabsf(f[g][w][e]));
+        }
+      }
+    top = fmaxf(top, __shfl_xor_sync(0xFFFFFFFFu, top, 1));
+    top = fmaxf(top, __shfl_xor_sync(0xFFFFFFFFu, top, 2));
+    // 2^14 <= top 2^up < 2^15
+    int up = 0;
+    if (top > 0.f && top < INFINITY) up = min(126, 14 - (int)floorf(log2f(top)));
+    const float sign = p.scale < 0.f ? -1.f : p.scale == 0.f ? 0.f : 1.f;
+    const float mul = ldexpf(sign, up);
+    // never zero, so that a hidden score stays at -infinity
+    const float back =
+        sign == 0.f ? 1.f : fmaxf(ldexpf(fabsf(p.scale) * 1.4426950408889634f, 24 - up), 1e-37f);
+    float sum[G];
+#pragma unroll
+    for (int g = 0; g < G; ++g) {
+      sum[g] = 0.f;
+#pragma unroll
+      for (int w = 0; w < 2; ++w) {
+        float* x = f[g][w];
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+          x[e] *= mul;
+          sum[g] += x[e];
+        }
+        // code order in a word: values (0, 4), (1, 5) / 16, (2, 6), (3, 7) / 16
+        qf[nt][g][w][0] = pack_f16(x[0], x[4]);
+        qf[nt][g][w][1] = pack_f16(x[1] * 0.0625f, x[5] * 0.0625f);
+        qf[nt][g][w][2] = pack_f16(x[2], x[6]);
+        qf[nt][g][w][3] = pack_f16(x[3] * 0.0625f, x[7] * 0.0625f);
+      }
+      sum[g] += __shfl_xor_sync(0xFFFFFFFFu, sum[g], 1);
+      sum[g] += __shfl_xor_sync(0xFFFFFFFFu, sum[g], 2);
+      sum[g] *= 0x1p-24f;
+    }
+    const int pos = sp.pos0 + i;
+    const int top_pos = live ? (p.causal ? min(sp.len, pos + 1) : sp.len) : 1 << 30;
+    const int low_pos = live && p.window > 0 ? max(0, pos - p.window + 1) : 0;
+    // the results have rows 2c and 2c + 1 in a lane
+#pragma unroll
+    for (int e = 0; e < 2; ++e) {
+      const int from = (2 * c + e) * 4;
+#pragma unroll
+      for (int g = 0; g < G; ++g) qs[nt][g][e] = __shfl_sync(0xFFFFFFFFu, sum[g], from);
+      fs[nt][e] = __shfl_sync(0xFFFFFFFFu, back, from);
+      hi[nt][e] = __shfl_sync(0xFFFFFFFFu, top_pos, from);
+      lo[nt][e] = __shfl_sync(0xFFFFFFFFu, low_pos, from);
+    }
+    hi_all = min(hi_all, (int)__reduce_min_sync(0xFFFFFFFFu, top_pos));
+    lo_all = max(lo_all, (int)__reduce_max_sync(0xFFFFFFFFu, low_pos));
+  }
+
+  // ---- the positions
+  const int begin = sp.begin + part * sp.chunk, end = min(sp.end, begin + sp.chunk);
+  const int stages = (end - begin + kFewTokens - 1) / kFewTokens;
+  const int mine = stages > warp ? (stages - warp + kFewWarps - 1) / kFewWarps : 0;
+  const uint32_t ring = smem_u32(smem) + (uint32_t)warp * S::kRing;
+  uint32_t vecs = 0xFFFFFFFFu;  // lane l: first vector of half l & 1 of stage (l >> 1) of the next 16
+  auto look_up = [&](int s) {   // page table entries of stages s .. s + 15
+    const int j = begin + ((s + (lane >> 1)) * kFewWarps + warp) * kFewTokens + (lane & 1) * 16;
+    vecs = 0xFFFFFFFFu;
+    if (j < end) {
+      const int64_t slot = slot_of(p.at, b, j);
+      if (slot >= 0) vecs = (uint32_t)vector_of(p.at, slot, kvh);
+      else record_error(&g_kv4_error, BCQ_ERR_PAGE);
+    }
+  };
+  uint32_t bad = 0;  // two bits a stage of the ring: halves that have no page
+  auto fetch = [&](int s) {
+    if (s < mine) {
+      if ((s & 15) == 0) look_up(s);
+      const int slot = s % kFewStages;
+      const uint32_t to = ring + (uint32_t)slot * S::kStage;
+      bad &= ~(3u << (2 * slot));
+#pragma unroll
+      for (int half = 0; half < 2; ++half) {
+        const uint32_t vec = __shfl_sync(0xFFFFFFFFu, vecs, 2 * (s & 15) + half);
+        if (vec == 0xFFFFFFFFu) {
+          bad |= 1u << (2 * slot + half);
+          continue;
+        }
+        const uint8_t* k = p.k + (int64_t)vec * S::kRow;
+        const uint8_t* v = p.v + (int64_t)vec * S::kRow;
+        const uint32_t at = to + (uint32_t)half * S::kHalf;
+#pragma unroll
+        for (int i = 0; i < S::kPieces / 2; ++i) {
+          const int id = i * 32 + lane, row = id / S::kPieces, piece = id % S::kPieces;
+          // V's rows in the order 0, 2, 4, 6, 1, 3, 5, 7 (and so the next 8)
+          const int vrow = (row & 8) | ((row & 1) << 2) | ((row >> 1) & 3);
+          cp_async16(at + S::place(row, piece), k + id * 16);
+          cp_async16(at + S::kCodes + S::place(vrow, piece), v + id * 16);
+        }
+        if (lane < 8 * G) {
+          const int kv = lane >= 4 * G, piece = lane & (4 * G - 1);
+          const __half2* src = (kv ? p.v_param : p.k_param) + (int64_t)vec * G;
+          cp_async16(at + 2 * S::kCodes + (uint32_t)kv * S::kParam + piece * 16,
+                     reinterpret_cast<const uint8_t*>(src) + piece * 16);
+        }
+      }
+    }
+    cp_async_commit();
+  };
+
+  float o[NT][G][4][4] = {}, zo[NT][G][2] = {}, m[NT][2], l[NT][2] = {};
+#pragma unroll
+  for (int nt = 0; nt < NT; ++nt) m[nt][0] = m[nt][1] = -INFINITY;
+  for (int s = 0; s < kFewStages - 1; ++s) fetch(s);
+  for (int s = 0; s < mine; ++s) {
+    cp_async_wait<kFewStages - 2>();
+    __syncwarp();
+    fetch(s + kFewStages - 1);
+    const int slot = s % kFewStages;
+    const uint32_t at0 = ring + (uint32_t)slot * S::kStage;
+    const int j0 = begin + (s * kFewWarps + warp) * kFewTokens;
+
+    // scores u[..]: positions r and r + 8 of each half, rows 2c and 2c + 1
+    float u[2][NT][4];
+#pragma unroll
+    for (int half = 0; half < 2; ++half) {
+      const uint32_t at = at0 + (uint32_t)half * S::kHalf;
+      float acc[NT][G][4] = {};
+#pragma unroll
+      for (int g = 0; g < G; ++g) {
+        // words 2c and 2c + 1 of the group, of positions r and r + 8
+        const uint32_t in = (uint32_t)(c & 1) * 8u;
+        const uint2 wa = lds_v2u(at + S::place(r, 2 * g + (c >> 1)) + in);
+        const uint2 wb = lds_v2u(at + S::place(r + 8, 2 * g + (c >> 1)) + in);
+#pragma unroll
+        for (int w = 0; w < 2; ++w) {
+          const uint32_t x = w ? wa.y : wa.x, y = w ? wb.y : wb.x;
+#pragma unroll
+          for (int nt = 0; nt < NT; ++nt)
+            mma16816(acc[nt][g], x & 0x000F000Fu, y & 0x000F000Fu, x & 0x00F000F0u, y & 0x00F000F0u,
+                     qf[nt][g][w][0], qf[nt][g][w][1]);
+          const uint32_t x2 = x >> 8, y2 = y >> 8;
+#pragma unroll
+          for (int nt = 0; nt < NT; ++nt)
+            mma16816(acc[nt][g], x2 & 0x000F000Fu, y2 & 0x000F000Fu, x2 & 0x00F000F0u,
+                     y2 & 0x00F000F0u, qf[nt][g][w][2], qf[nt][g][w][3]);
+        }
+      }
+      const uint32_t pa = at + 2 * S::kCodes + (uint32_t)(r * G * 4);
+#pragma unroll
+      for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) u[half][nt][e] = 0.f;
+#pragma unroll
+      for (int g = 0; g < G; ++g)
+#pragma unroll
+        for (int e8 = 0; e8 < 2; ++e8) {
+          const float2 az = half2_at(lds_u32v(pa + (uint32_t)(e8 * 8 * G * 4 + g * 4)));
+#pragma unroll
+          for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+            for (int e = 0; e < 2; ++e)
+              u[half][nt][2 * e8 + e] = fmaf(az.x, acc[nt][g][2 * e8 + e],
+                                             fmaf(az.y, qs[nt][g][e], u[half][nt][2 * e8 + e]));
+        }
+    }
+
+    // masks, where the 32 positions are not seen by all rows
+    const uint32_t gone = (bad >> (2 * slot)) & 3u;
+    const bool whole = j0 >= lo_all && j0 + kFewTokens <= min(hi_all, end) && gone == 0;
+    uint32_t seen = 0xFFFFFFFFu;  // bit half * 8 NT + nt * 4 + e
+    if (!whole) {
+      seen = 0;
+#pragma unroll
+      for (int half = 0; half < 2; ++half)
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            const int j = j0 + half * 16 + r + (e >> 1) * 8;
+            const bool ok = j < min(hi[nt][e & 1], end) && j >= lo[nt][e & 1] && !((gone >> half) & 1u);
+            if (ok) seen |= 1u << (half * 4 * NT + nt * 4 + e);
+            else u[half][nt][e] = -INFINITY;
+          }
+    }
+
+    // running maximum (a factor fs >= 0 makes it the scores')
+    float fix[NT][2];
+    bool moved = false;
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+      for (int e = 0; e < 2; ++e) {
+        float t = fmaxf(fmaxf(u[0][nt][e], u[0][nt][e + 2]), fmaxf(u[1][nt][e], u[1][nt][e + 2]));
+        t = fmaxf(t, __shfl_xor_sync(0xFFFFFFFFu, t, 4));
+        t = fmaxf(t, __shfl_xor_sync(0xFFFFFFFFu, t, 8));
+        t = fmaxf(t, __shfl_xor_sync(0xFFFFFFFFu, t, 16));
+        const float now = fmaxf(m[nt][e], t * fs[nt][e]);
+        fix[nt][e] = now == -INFINITY ? 1.f : ex2(m[nt][e] - now);
+        moved |= now != m[nt][e];
+        m[nt][e] = now;
+      }
+    if (__any_sync(0xFFFFFFFFu, moved)) {
+#pragma unroll
+      for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+          l[nt][e] *= fix[nt][e];
+#pragma unroll
+          for (int g = 0; g < G; ++g) {
+            zo[nt][g][e] *= fix[nt][e];
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+              o[nt][g][j][e] *= fix[nt][e];
+              o[nt][g][j][e + 2] *= fix[nt][e];
+            }
+          }
+        }
+    }
+
+    // weights, and the second product
+#pragma unroll
+    for (int half = 0; half < 2; ++half) {
+      const uint32_t at = at0 + (uint32_t)half * S::kHalf;
+#pragma unroll
+      for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          const float base = m[nt][e & 1] == -INFINITY ? 0.f : m[nt][e & 1];
+          const float w = ex2(fmaf(u[half][nt][e], fs[nt][e & 1], kWeightBits - base));
+          u[half][nt][e] = w;
+          l[nt][e & 1] += w;
+        }
+      const uint32_t pa = at + 2 * S::kCodes + S::kParam + (uint32_t)(r * G * 4);
+#pragma unroll
+      for (int g = 0; g < G; ++g) {
+        const float2 az0 = half2_at(lds_u32v(pa + (uint32_t)(g * 4)));
+        const float2 az1 = half2_at(lds_u32v(pa + (uint32_t)(8 * G * 4 + g * 4)));
+        uint32_t b0[NT], b1[NT];
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt) {
+          float w[4], z[4];
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            w[e] = u[half][nt][e] * (e < 2 ? az0.x : az1.x);
+            z[e] = u[half][nt][e] * (e < 2 ? az0.y : az1.y);
+            // what a mask hides may be no number
+            if (!whole && !((seen >> (half * 4 * NT + nt * 4 + e)) & 1u)) w[e] = z[e] = 0.f;
+          }
+          zo[nt][g][0] += z[0] + z[2];
+          zo[nt][g][1] += z[1] + z[3];
+          b0[nt] = transpose8x8(pack_f16(w[0], w[1]));
+          b1[nt] = transpose8x8(pack_f16(w[2], w[3]));
+        }
+        // word r of the group, of positions 2c, 2c + 1, 2c + 8, 2c + 9
+        const uint32_t in = (uint32_t)(r & 3) * 4u;
+        const int piece = 2 * g + (r >> 2);
+        const uint32_t va = at + S::kCodes;
+        const uint32_t v0 = lds_u32v(va + S::place(c, piece) + in);
+        const uint32_t v1 = lds_u32v(va + S::place(c + 4, piece) + in);
+        const uint32_t v2 = lds_u32v(va + S::place(c + 8, piece) + in);
+        const uint32_t v3 = lds_u32v(va + S::place(c + 12, piece) + in);
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {  // byte j: values 8r + 2j and 8r + 2j + 1
+          const uint32_t x = prmt(v0, v1, (uint32_t)(j | (4 + j) << 8));
+          const uint32_t y = prmt(v2, v3, (uint32_t)(j | (4 + j) << 8));
+#pragma unroll
+          for (int nt = 0; nt < NT; ++nt)
+            mma16816(o[nt][g][j], x & 0x000F000Fu, x & 0x00F000F0u, y & 0x000F000Fu, y & 0x00F000F0u,
+                     b0[nt], b1[nt]);
+        }
+      }
+    }
+  }
+  launch_dependents();  // the joining kernel may be set up
+  cp_async_wait<0>();
+  __syncthreads();  // the rings are free: they take the warps' results
+
+  // ---- join the warps: [warp][row][D] and (max, sum) behind them
+  constexpr int kRows = 8 * NT;
+  float* so = reinterpret_cast<float*>(smem);
+  float* sm = so + kFewWarps * kRows * D;
+#pragma unroll
+  for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+    for (int e = 0; e < 2; ++e) {
+#pragma unroll
+      for (int step = 4; step < 32; step *= 2) {
+        l[nt][e] += __shfl_xor_sync(0xFFFFFFFFu, l[nt][e], step);
+#pragma unroll
+        for (int g = 0; g < G; ++g) zo[nt][g][e] += __shfl_xor_sync(0xFFFFFFFFu, zo[nt][g][e], step);
+      }
+      const int row = warp * kRows + nt * 8 + 2 * c + e;
+      if (r == 0) {
+        sm[2 * row] = m[nt][e];
+        sm[2 * row + 1] = l[nt][e];
+      }
+#pragma unroll
+      for (int g = 0; g < G; ++g)
+#pragma unroll
+        for (int j = 0; j < 4; ++j)
+          *reinterpret_cast<float2*>(so + row * D + g * kKvGroup + 8 * r + 2 * j) =
+              make_float2(fmaf(o[nt][g][j][e], 0x1p24f, zo[nt][g][e]),
+                          fmaf(o[nt][g][j][e + 2], 0x1p20f, zo[nt][g][e]));
+    }
+  __syncthreads();
+  for (int id = threadIdx.x; id < row_n * (D / 4); id += kFewWarps * 32) {
+    const int row = id / (D / 4), d = id % (D / 4) * 4;
+    float top = -INFINITY, sum = 0.f;
+#pragma unroll
+    for (int w = 0; w < kFewWarps; ++w) top = fmaxf(top, sm[2 * (w * kRows + row)]);
+    float4 x = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+    for (int w = 0; w < kFewWarps; ++w) {
+      const float mw = sm[2 * (w * kRows + row)];
+      const float lw = sm[2 * (w * kRows + row) + 1];
+      if (mw == -INFINITY && lw == 0.f) continue;  // this warp saw nothing of the row
+      const float f = ex2(mw - top);
+      sum = fmaf(lw, f, sum);
+      const float4 y = *reinterpret_cast<const float4*>(so + (w * kRows + row) * D + d);
+      x.x = fmaf(y.x, f, x.x);
+      x.y = fmaf(y.y, f, x.y);
+      x.z = fmaf(y.z, f, x.z);
+      x.w = fmaf(y.w, f, x.w);
+    }
+    const int i = (row0 + row) / p.group, h = kvh * p.group + (row0 + row) % p.group;
+    const int64_t t = sp.first_row + i;
+    if (sp.parts > 1) {
+      const int64_t at = ((int64_t)part * p.T + t) * p.q_heads + h;
+      *reinterpret_cast<float4*>(p.part + at * D + d) = x;
+      if (d == 0) {
+        float* ml = p.part + (int64_t)p.splits * p.T * p.q_heads * D + at * 2;
+        ml[0] = top;
+        ml[1] = sum;
+      }
+      continue;
+    }
+    const bool none = top == -INFINITY && sum == 0.f;
+    const float inv = none ? 0.f : 1.f / sum;
+    const T y[4] = {from_float<T>(x.x * inv), from_float<T>(x.y * inv), from_float<T>(x.z * inv),
+                    from_float<T>(x.w * inv)};
+    *reinterpret_cast<uint2*>(p.out + t * p.ld_o + (int64_t)h * p.hd_o + d) =
+        *reinterpret_cast<const uint2*>(y);
+    if (p.lse && d == 0)
+      p.lse[t * p.q_heads + h] =
+          none ? -INFINITY : (top + log2f(sum) - kWeightBits) * 0.69314718055994531f;
+  }
+}
+
+// Joins the parts of the rows that were split, each in the same order whenever
+// it runs: a CTA a row and head, D / 4 threads a part, 512 / D parts at a time.
+template <typename T, int D>
+__global__ void __launch_bounds__(128) kv4_join_kernel(const AttentionParams p) {
+  constexpr int kLanes = D / 4, kSets = 128 / kLanes;
+  __shared__ float4 so[kSets][kLanes];
+  __shared__ float sm[kSets][2];
+  const int64_t id = blockIdx.x;
+  const int t = (int)(id / p.q_heads), h = (int)(id % p.q_heads);
+  const int set = threadIdx.x / kLanes, lane = threadIdx.x % kLanes;
   const int b = sequence_of(p.at, t);
   if (b < 0) return;
-  const int2 rows = rows_of(p.at, b);
-  if (t - rows.x >= p.max_q) {
-    if (tid == 0) record_error(&g_kv4_error, BCQ_ERR_SHAPE);
-    return;
+  const int row = (t - rows_of(p.at, b).x) * p.group + h % p.group;
+  const Span sp = span_of(p, b, row / p.rows);
+  grid_dependency_wait();
+  if (sp.parts <= 1 || t - sp.first_row >= sp.rows) return;
+  const int64_t step = (int64_t)p.T * p.q_heads;
+  const float* ml = p.part + (int64_t)p.splits * step * D + id * 2;
+  const float* src = p.part + id * D + lane * 4;
+  float top = -INFINITY, sum = 0.f;
+  float4 x = make_float4(0.f, 0.f, 0.f, 0.f);
+  auto add = [](float& top, float& sum, float4& x, float m, float l, const float4& y) {
+    if (m == -INFINITY && l == 0.f) return;  // nothing seen
+    const float now = fmaxf(top, m);
+    const float f = sum == 0.f && top == -INFINITY ? 0.f : ex2(top - now), g = ex2(m - now);
+    sum = sum * f + l * g;
+    x.x = x.x * f + y.x * g;
+    x.y = x.y * f + y.y * g;
+    x.z = x.z * f + y.z * g;
+    x.w = x.w * f + y.w * g;
+    top = now;
+  };
+#pragma unroll 4
+  for (int i = set; i < sp.parts; i += kSets) {
+    const float2 s = *reinterpret_cast<const float2*>(ml + i * step * 2);
+    const float4 y = *reinterpret_cast<const float4*>(src + i * step * D);
+    add(top, sum, x, s.x, s.y, y);
   }
-  int len = p.at.kv_len[b];
-  if (len < 0 || len > (int64_t)p.at.table_width * p.at.page_size) {
-    if (tid == 0) record_error(&g_kv4_error, BCQ_ERR_PAGE);
-    len = len < 0 ? 0 : p.at.table_width * p.at.page_size;
+  so[set][lane] = x;
+  if (lane == 0) {
+    sm[set][0] = top;
+    sm[set][1] = sum;
   }
-  const int pos = p.at.kv_len[b] - rows.y + (t - rows.x);
-  const int hi = p.causal ? min(len, pos + 1) : len;
-  const int lo = p.window > 0 ? max(0, pos - p.window + 1) : 0;
-  const int kvh = h / (p.q_heads / p.at.heads);
-  for (int d = tid; d < D; d += 128)
-    qs[d] = bits_to_float<T>(p.q[(int64_t)t * p.ld_q + (int64_t)h * p.hd_q + d]) * p.scale;
-  float top = -INFINITY, sum = 0.f, acc[2] = {0.f, 0.f};
-  for (int j0 = lo; j0 < hi; j0 += 128) {
-    __syncthreads();
-    const int j = j0 + tid;
-    const int64_t slot = j < hi ? slot_of(p.at, b, j) : -1;
-    if (j < hi && slot < 0) record_error(&g_kv4_error, BCQ_ERR_PAGE);
-    float s = -INFINITY;
-    if (slot >= 0) {
-      const int64_t vec = vector_of(p.at, slot, kvh);
-      s = 0.f;
-      for (int d = 0; d < D; ++d) {
-        const float2 az = __half22float2(p.k_param[vec * (D / kKvGroup) + d / kKvGroup]);
-        const uint32_t c = p.k[vec * (D / 2) + d / 2] >> (4 * (d & 1)) & 15u;
-        s = fmaf(qs[d], fmaf((float)c, az.x, az.y), s);
-      }
-    }
-    float m = s;
-    for (int o = 1; o < 32; o <<= 1) m = fmaxf(m, __shfl_xor_sync(0xFFFFFFFFu, m, o));
-    if ((tid & 31) == 0) red[tid >> 5] = m;
-    __syncthreads();
-    m = fmaxf(top, fmaxf(fmaxf(red[0], red[1]), fmaxf(red[2], red[3])));
-    const float base = m == -INFINITY ? 0.f : m;
-    const float fix = expf(top - base);
-    ps[tid] = expf(s - base);
-    __syncthreads();
-    sum *= fix;
-    acc[0] *= fix;
-    acc[1] *= fix;
-    for (int i = 0; i < 128 && j0 + i < hi; ++i) {
-      const float w = ps[i];
-      sum += w;
-      const int64_t sl = slot_of(p.at, b, j0 + i);
-      if (sl < 0) continue;
-      const int64_t vec = vector_of(p.at, sl, kvh);
-      for (int e = 0; e < 2; ++e) {
-        const int d = tid + 128 * e;
-        if (d >= D) continue;
-        const float2 az = __half22float2(p.v_param[vec * (D / kKvGroup) + d / kKvGroup]);
-        const uint32_t c = p.v[vec * (D / 2) + d / 2] >> (4 * (d & 1)) & 15u;
-        acc[e] = fmaf(w, fmaf((float)c, az.x, az.y), acc[e]);
-      }
-    }
-    top = m;
-  }
-  for (int e = 0; e < 2; ++e) {
-    const int d = tid + 128 * e;
-    if (d < D) {
-      const T r = from_float<T>(sum > 0.f || sum != sum ? acc[e] / sum : 0.f);
-      p.out[(int64_t)t * p.ld_o + (int64_t)h * p.hd_o + d] = *reinterpret_cast<const uint16_t*>(&r);
-    }
-  }
-  if (p.lse && tid == 0) p.lse[(int64_t)t * p.q_heads + h] = sum > 0.f || sum != sum ? top + logf(sum) : -INFINITY;
+  __syncthreads();
+  if (set != 0) return;
+#pragma unroll
+  for (int i = 1; i < kSets; ++i) add(top, sum, x, sm[i][0], sm[i][1], so[i][lane]);
+  const bool none = top == -INFINITY && sum == 0.f;
+  const float inv = none ? 0.f : 1.f / sum;
+  const T y[4] = {from_float<T>(x.x * inv), from_float<T>(x.y * inv), from_float<T>(x.z * inv),
+                  from_float<T>(x.w * inv)};
+  *reinterpret_cast<uint2*>(p.out + (int64_t)t * p.ld_o + (int64_t)h * p.hd_o + lane * 4) =
+      *reinterpret_cast<const uint2*>(y);
+  if (p.lse && lane == 0)
+    p.lse[id] = none ? -INFINITY : (top + log2f(sum) - kWeightBits) * 0.69314718055994531f;
 }
 
 // -------------------------------------------------------------------- host
@@ -332,6 +818,62 @@ bcq_status check_rows(const void* x, int64_t ld, int64_t hd, int dtype) {
 Places places_of(const bcq_kv4* c, const int32_t* table, int table_width, const int32_t* kv_len,
                  const int32_t* cu, int B) {
   return {table, kv_len, cu, table_width, B, c->pages, c->page_size, c->heads};
+}
+
+// Rows of a CTA (8 nt of a key/value head's) and parts of the positions.
+struct FewPlan {
+  int nt, row_blocks, splits, chunk;
+};
+
+// Parts: a wave is 3 CTAs on each of 148 SMs; CTAs beyond one start as others
+// end, the last of them alone on average for half of one's time.  A CTA costs
+// about as much as 160 positions before and after its positions.
+FewPlan plan_few(const bcq_kv4* c, int q_heads, int B, int max_q, int max_kv) {
+  FewPlan f;
+  const int64_t rows = (int64_t)max_q * (q_heads / c->heads);
+  f.nt = rows <= 8 || c->head_dim == 256 ? 1 : 2;
+  f.row_blocks = (int)std::min<int64_t>((rows + 8 * f.nt - 1) / (8 * f.nt), INT32_MAX);
+  const double units = (double)f.row_blocks * c->heads * B;
+  double best = 0;
+  for (int s = 1; s <= 256 && (s == 1 || (int64_t)(s - 1) * 128 < max_kv); ++s) {
+    const int chunk = (int)std::min<int64_t>((((int64_t)max_kv + s - 1) / s + 127) / 128 * 128, 1 << 30);
+    const double waves = units * s / 444.0;
+    const double cost = (waves <= 1 ? 1.0 : waves + 0.5) * (chunk + 160.0) + s;
+    if (best == 0 || cost < best) {
+      best = cost;
+      f.splits = s;
+      f.chunk = chunk;
+    }
+  }
+  return f;
+}
+
+template <typename T, int D, int NT>
+cudaError_t launch_few_t(const AttentionParams& p, cudaStream_t st) {
+  constexpr int smem = (int)(kFewWarps * FewShape<D>::kRing);
+  cudaError_t e = cudaFuncSetAttribute(kv4_few_kernel<T, D, NT>,
+                                       cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+  if (e != cudaSuccess) return e;
+  const dim3 grid((unsigned)((int64_t)p.row_blocks * p.at.heads * p.at.B), (unsigned)p.splits);
+  kv4_few_kernel<T, D, NT><<<grid, kFewWarps * 32, smem, st>>>(p);
+  if ((e = cudaGetLastError()) != cudaSuccess || p.splits == 1) return e;
+  cudaLaunchAttribute attr = {};
+  attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr.val.programmaticStreamSerializationAllowed = 1;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3((unsigned)((int64_t)p.T * p.q_heads));
+  cfg.blockDim = dim3(128);
+  cfg.stream = st;
+  cfg.attrs = &attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, kv4_join_kernel<T, D>, p);
+}
+
+template <typename T>
+cudaError_t launch_few(const AttentionParams& p, int D, int nt, cudaStream_t st) {
+  if (D == 256) return launch_few_t<T, 256, 1>(p, st);
+  if (D == 128) return nt == 1 ? launch_few_t<T, 128, 1>(p, st) : launch_few_t<T, 128, 2>(p, st);
+  return nt == 1 ? launch_few_t<T, 64, 1>(p, st) : launch_few_t<T, 64, 2>(p, st);
 }
 
 bcq_status launched() { return cudaGetLastError() == cudaSuccess ? BCQ_OK : BCQ_ERR_CUDA; }
@@ -404,9 +946,11 @@ bcq_status bcq_kv4_read(const bcq_kv4* cache, void* k, void* v, int dtype, int T
 size_t bcq_kv4_attention_workspace_bytes(const bcq_kv4* cache, int T, int q_heads, int B,
                                          int max_q, int max_kv) {
   if (!cache || !cache_sizes_ok(cache) || !head_dim_ok(cache->head_dim) || T < 0 || B < 1 ||
-      max_q < 1 || max_kv < 1 || q_heads < 1)
+      max_q < 1 || max_kv < 1 || q_heads < 1 || q_heads % cache->heads)
     return 0;
-  return 0;
+  const FewPlan f = plan_few(cache, q_heads, B, max_q, max_kv);
+  if (f.splits == 1) return 0;
+  return (size_t)f.splits * (size_t)T * (size_t)q_heads * (size_t)(cache->head_dim + 2) * 4;
 }
 
 bcq_status bcq_kv4_attention(const bcq_kv4* cache, const void* q, int64_t ld_q, int64_t hd_q,
@@ -443,16 +987,23 @@ bcq_status bcq_kv4_attention(const bcq_kv4* cache, const void* q, int64_t ld_q, 
                        hd_o,
                        T,
                        q_heads,
-                       cache->head_dim,
                        max_q,
                        causal,
                        window,
                        scale};
+  const FewPlan f = plan_few(cache, q_heads, B, max_q, max_kv);
+  p.group = q_heads / cache->heads;
+  p.rows = 8 * f.nt;
+  p.row_blocks = f.row_blocks;
+  p.splits = f.splits;
+  p.chunk = f.chunk;
+  p.part = static_cast<float*>(workspace);
+  if ((int64_t)f.row_blocks * cache->heads * B > INT32_MAX || (int64_t)T * q_heads > INT32_MAX)
+    return BCQ_ERR_SHAPE;
   cudaStream_t st = (cudaStream_t)stream;
-  const dim3 grid((unsigned)T, (unsigned)q_heads);
-  if (dtype == BCQ_F16) kv4_attention_kernel<__half><<<grid, 128, 0, st>>>(p);
-  else kv4_attention_kernel<__nv_bfloat16><<<grid, 128, 0, st>>>(p);
-  return launched();
+  const cudaError_t e = dtype == BCQ_F16 ? launch_few<__half>(p, cache->head_dim, f.nt, st)
+                                         : launch_few<__nv_bfloat16>(p, cache->head_dim, f.nt, st);
+  return e == cudaSuccess ? BCQ_OK : BCQ_ERR_CUDA;
 }
 
 }  // extern "C"
