@@ -590,63 +590,94 @@ def gemm_host(x_host: torch.Tensor, w: BcqWeights, y_host: torch.Tensor,
 # ------------------------------------------------------- the 8-bit product
 
 _DTYPES = {torch.float16: 0, torch.bfloat16: 1, torch.float32: 2}   # BCQ_F16, BCQ_BF16, BCQ_F32
+_HALVES = (torch.float16, torch.bfloat16)
 I8_MAX_K = 65536
 
+# The calls below take a few microseconds on the GPU at their smallest, so the
+# checks read each property of a tensor once and streams and devices are
+# compared by number.
 
-def _empty_on(shape, dtype, device, stream):
-    """torch.empty for work on `stream` (the current one when None): memory
-    that the allocator hands out in that stream's order."""
+
+def _raw_stream(stream, index: int) -> int:
+    """The CUDA stream handle of `stream`, else of device `index`'s current one."""
     if stream is None:
-        return torch.empty(shape, dtype=dtype, device=device)
+        return torch._C._cuda_getCurrentRawStream(index)
+    if stream.device_index != index:
+        raise ValueError(f"stream is on {stream.device}, the data on cuda:{index}")
+    return stream.cuda_stream
+
+
+def _run(name: str, index: int, *args) -> None:
+    """Call the entry point with device `index` current."""
+    f = getattr(lib(), name)
+    if index == torch.cuda.current_device():
+        status = f(*args)
+    else:
+        with torch.cuda.device(index):
+            status = f(*args)
+    if status != BCQ_OK:
+        raise BcqError(status, name)
+
+
+def _new(like: torch.Tensor, shape, dtype, stream) -> torch.Tensor:
+    """An uninitialised tensor on like's device for work on `stream` (the
+    current one when None): memory that the allocator hands out in that
+    stream's order."""
+    if stream is None:
+        return like.new_empty(shape, dtype=dtype)
     with torch.cuda.stream(stream):
-        t = torch.empty(shape, dtype=dtype, device=device)
-    t.record_stream(torch.cuda.current_stream(device))
+        t = like.new_empty(shape, dtype=dtype)
+    t.record_stream(torch.cuda.current_stream(like.device))
     return t
 
 
-def _need_matrix(t: torch.Tensor, name: str, dtypes, device=None) -> int:
-    """A CUDA matrix of one of `dtypes` whose rows are contiguous; returns the
-    distance of its rows in elements."""
+def _need_matrix(t: torch.Tensor, name: str, dtypes, index=None) -> int:
+    """A CUDA matrix of one of `dtypes` (on device `index`) whose rows are
+    contiguous; returns the distance of its rows in elements."""
     if not t.is_cuda:
         raise ValueError(f"{name} must be a CUDA tensor")
     if t.dtype not in dtypes:
         raise ValueError(f"{name} must be one of {[str(d) for d in dtypes]}, got {t.dtype}")
-    if device is not None and t.device != device:
-        raise ValueError(f"{name} is on {t.device}, x on {device}")
+    if index is not None and t.get_device() != index:
+        raise ValueError(f"{name} is on {t.device}, x on cuda:{index}")
     if t.dim() != 2:
         raise ValueError(f"{name} must be a matrix")
     rows, cols = t.shape
-    if cols > 1 and t.stride(1) != 1:
+    ld, step = t.stride()
+    if cols > 1 and step != 1:
         raise ValueError(f"{name} must have contiguous rows")
     if rows <= 1:
         return -(-cols // 16) * 16     # one row: its distance to the next is never used
-    if t.stride(0) < cols:
+    if ld < cols:
         raise ValueError(f"{name}'s rows overlap")
-    return t.stride(0)
+    return ld
 
 
-def _need_codes(t: torch.Tensor, name: str, device=None) -> int:
-    ld = _need_matrix(t, name, (torch.int8,), device)
+def _need_codes(t: torch.Tensor, name: str, index=None) -> int:
+    ld = _need_matrix(t, name, (torch.int8,), index)
     if ld % 16 or t.data_ptr() % 16:
         raise ValueError(f"{name}'s rows must start on multiples of 16 bytes (as quantize_i8's do)")
     return ld
 
 
-def _need_scale(t: torch.Tensor, name: str, rows: int, device) -> None:
-    _need_cuda(t, name, torch.float32)
-    _need_on(t, name, device)
-    if tuple(t.shape) != (rows,):
-        raise ValueError(f"{name} must be [{rows}], got {list(t.shape)}")
+def _need_vector(t: torch.Tensor, name: str, dtype, size: int, index: int, other: str) -> None:
+    """A contiguous vector of `size` values of `dtype` on device `index`."""
+    if not t.is_cuda or not t.is_contiguous() or t.dtype is not dtype:
+        _need_cuda(t, name, dtype)
+    if t.get_device() != index:
+        raise ValueError(f"{name} is on {t.device}, {other} on cuda:{index}")
+    if t.dim() != 1 or t.numel() != size:
+        raise ValueError(f"{name} must be [{size}], got {list(t.shape)}")
 
 
-def _need_product_out(out, M: int, N: int, dtype, device, stream):
+def _need_product_out(out, M: int, N: int, dtype, like, index: int, stream):
     """(out [M][N] of `dtype`, its row distance): allocated when None."""
     if out is None:
-        return _empty_on((M, N), dtype, device, stream), N
-    ld = _need_matrix(out, "out", (dtype,), device)
-    if tuple(out.shape) != (M, N):
+        return _new(like, (M, N), dtype, stream), N
+    ld = _need_matrix(out, "out", (dtype,), index)
+    if out.shape[0] != M or out.shape[1] != N:
         raise ValueError(f"out must be [{M}][{N}], got {list(out.shape)}")
-    return out, ld
+    return out, max(ld, N)
 
 
 def quantize_i8(x: torch.Tensor, stream=None):
@@ -654,16 +685,16 @@ def quantize_i8(x: torch.Tensor, stream=None):
     (bcq_quantize_i8): (codes int8 [M][K] whose rows start on multiples of 16
     bytes, scale fp32 [M]); codes * scale is x to half a step.  Activations: a
     row per token; weights, once: a row per output channel."""
-    ldx = _need_matrix(x, "x", (torch.float16, torch.bfloat16))
+    ldx = _need_matrix(x, "x", _HALVES)
     M, K = x.shape
-    dev = x.device
+    index = x.get_device()
+    st = _raw_stream(stream, index)
     ldq = -(-K // 16) * 16
-    q = _empty_on((M, ldq), torch.int8, dev, stream)
-    scale = _empty_on((M,), torch.float32, dev, stream)
-    with _on(dev):
-        _check(lib().bcq_quantize_i8(_ptr(x), _DTYPES[x.dtype], M, K, ldx, _ptr(q), ldq,
-                                     _ptr(scale), _stream(stream, dev)), "bcq_quantize_i8")
-    return q[:, :K], scale
+    q = _new(x, (M, ldq), torch.int8, stream)
+    scale = _new(x, (M,), torch.float32, stream)
+    _run("bcq_quantize_i8", index, x.data_ptr(), _DTYPES[x.dtype], M, K, ldx, q.data_ptr(), ldq,
+         scale.data_ptr(), st)
+    return (q if ldq == K else q[:, :K]), scale
 
 
 def gemm_i8(x: torch.Tensor, x_scale: torch.Tensor, w: torch.Tensor, w_scale: torch.Tensor,
@@ -674,19 +705,18 @@ def gemm_i8(x: torch.Tensor, x_scale: torch.Tensor, w: torch.Tensor, w_scale: to
     if dtype not in _DTYPES:
         raise ValueError("dtype must be float16, bfloat16 or float32")
     ldx = _need_codes(x, "x")
-    dev = x.device
-    ldw = _need_codes(w, "w", dev)
+    index = x.get_device()
+    ldw = _need_codes(w, "w", index)
     M, K = x.shape
-    N = w.shape[0]
-    if w.shape[1] != K:
+    N, KW = w.shape
+    if KW != K:
         raise ValueError(f"w must be [N][{K}], got {list(w.shape)}")
-    _need_scale(x_scale, "x_scale", M, dev)
-    _need_scale(w_scale, "w_scale", N, dev)
-    out, ldy = _need_product_out(out, M, N, dtype, dev, stream)
-    with _on(dev):
-        _check(lib().bcq_gemm_i8(_ptr(x), ldx, _ptr(x_scale), _ptr(w), ldw, _ptr(w_scale), M, N, K,
-                                 _ptr(out), _DTYPES[dtype], max(ldy, N), _stream(stream, dev)),
-               "bcq_gemm_i8")
+    _need_vector(x_scale, "x_scale", torch.float32, M, index, "x")
+    _need_vector(w_scale, "w_scale", torch.float32, N, index, "x")
+    out, ldy = _need_product_out(out, M, N, dtype, x, index, stream)
+    st = _raw_stream(stream, index)
+    _run("bcq_gemm_i8", index, x.data_ptr(), ldx, x_scale.data_ptr(), w.data_ptr(), ldw,
+         w_scale.data_ptr(), M, N, K, out.data_ptr(), _DTYPES[dtype], ldy, st)
     return out
 
 
@@ -695,21 +725,20 @@ def linear_i8(x: torch.Tensor, w: torch.Tensor, w_scale: torch.Tensor,
     """y = x W^T for fp16 or bf16 x [M][K] and an 8-bit weight (codes w [N][K],
     w_scale [N]): quantize_i8 of x's rows and gemm_i8 in one call
     (bcq_linear_i8); y [M][N] has x's type."""
-    ldx = _need_matrix(x, "x", (torch.float16, torch.bfloat16))
-    dev = x.device
-    ldw = _need_codes(w, "w", dev)
+    ldx = _need_matrix(x, "x", _HALVES)
+    index = x.get_device()
+    ldw = _need_codes(w, "w", index)
     M, K = x.shape
-    N = w.shape[0]
-    if w.shape[1] != K:
+    N, KW = w.shape
+    if KW != K:
         raise ValueError(f"w must be [N][{K}], got {list(w.shape)}")
-    _need_scale(w_scale, "w_scale", N, dev)
-    out, ldy = _need_product_out(out, M, N, x.dtype, dev, stream)
-    need = int(lib().bcq_linear_i8_workspace_bytes(M, K))
-    ws = _empty_on((max(need, 16),), torch.uint8, dev, stream)
-    with _on(dev):
-        _check(lib().bcq_linear_i8(_ptr(x), _DTYPES[x.dtype], ldx, _ptr(w), ldw, _ptr(w_scale),
-                                   M, N, K, _ptr(out), max(ldy, N), _ptr(ws), ws.numel(),
-                                   _stream(stream, dev)), "bcq_linear_i8")
+    _need_vector(w_scale, "w_scale", torch.float32, N, index, "x")
+    out, ldy = _need_product_out(out, M, N, x.dtype, x, index, stream)
+    st = _raw_stream(stream, index)
+    need = lib().bcq_linear_i8_workspace_bytes(M, K)
+    ws = _new(x, (need,), torch.uint8, stream)
+    _run("bcq_linear_i8", index, x.data_ptr(), _DTYPES[x.dtype], ldx, w.data_ptr(), ldw,
+         w_scale.data_ptr(), M, N, K, out.data_ptr(), ldy, ws.data_ptr(), need, st)
     return out
 
 
@@ -733,6 +762,8 @@ class Kv4Cache:
     k_param: torch.Tensor
     v: torch.Tensor
     v_param: torch.Tensor
+    # the tensors' addresses and the struct that the library takes: see _c
+    _marshal: list = field(default_factory=list, init=False, repr=False, compare=False)
 
     def __post_init__(self):
         for name in ("k", "v"):
@@ -770,51 +801,55 @@ class Kv4Cache:
         return self.k.shape[1]
 
     def _c(self):
-        pages, heads, page_size, half = self.k.shape
-        return _Kv4(self.k.data_ptr(), self.k_param.data_ptr(), self.v.data_ptr(),
-                    self.v_param.data_ptr(), pages, heads, page_size, 2 * half)
+        """(reference to the library's struct, heads, page_size, D); the
+        struct is kept while every tensor's address stays the same."""
+        at = (self.k.data_ptr(), self.k_param.data_ptr(), self.v.data_ptr(), self.v_param.data_ptr())
+        if not self._marshal or self._marshal[0] != at:
+            pages, heads, page_size, half = self.k.shape
+            c = _Kv4(*at, pages, heads, page_size, 2 * half)
+            self._marshal[:] = [at, (ctypes.byref(c), heads, page_size, 2 * half)]
+        return self._marshal[1]
 
 
-def _need_places(cache: Kv4Cache, table, kv_len, cu, T: int):
-    """(B, table_width) of int32 tables on the cache's device."""
-    dev = cache.k.device
-    for t, name in ((table, "table"), (kv_len, "kv_len"), (cu, "cu")):
-        if t is not None:
-            _need_cuda(t, name, torch.int32)
-            if t.device != dev:
-                raise ValueError(f"{name} is on {t.device}, the cache on {dev}")
-    if table.dim() != 2 or 0 in table.shape:
+def _need_places(table, kv_len, cu, T: int, index: int):
+    """(B, table_width, the three addresses) of int32 tables on the cache's device."""
+    if not table.is_cuda or not table.is_contiguous() or table.dtype is not torch.int32:
+        _need_cuda(table, "table", torch.int32)
+    if table.get_device() != index:
+        raise ValueError(f"table is on {table.device}, the cache on cuda:{index}")
+    if table.dim() != 2 or table.numel() == 0:
         raise ValueError("table must be [B][pages of a sequence]")
     B, W = table.shape
-    if tuple(kv_len.shape) != (B,):
-        raise ValueError(f"kv_len must be [{B}]")
+    _need_vector(kv_len, "kv_len", torch.int32, B, index, "the cache")
     if cu is None:
         if T != B:
             raise ValueError(f"without cu there is a row for each of the {B} sequences, got {T}")
-    elif tuple(cu.shape) != (B + 1,):
-        raise ValueError(f"cu must be [{B + 1}]")
-    return B, W
+        return B, W, table.data_ptr(), kv_len.data_ptr(), None
+    _need_vector(cu, "cu", torch.int32, B + 1, index, "the cache")
+    return B, W, table.data_ptr(), kv_len.data_ptr(), cu.data_ptr()
 
 
-def _need_heads(t: torch.Tensor, name: str, cache: Kv4Cache, heads: int | None, dtype=None):
-    """Rows [T][heads][D], fp16 or bf16, each vector contiguous; returns the
-    distances (rows, heads) in elements."""
-    if not t.is_cuda or t.device != cache.k.device:
-        raise ValueError(f"{name} is on {t.device}, the cache on {cache.k.device}")
-    if t.dtype not in (torch.float16, torch.bfloat16) or (dtype is not None and t.dtype != dtype):
+def _need_heads(t: torch.Tensor, name: str, heads: int | None, D: int, index: int, dtype=None):
+    """Rows [T][heads][D], fp16 or bf16, each vector contiguous: T, heads, and
+    the distances (rows, heads) in elements."""
+    if not t.is_cuda or t.get_device() != index:
+        raise ValueError(f"{name} is on {t.device}, the cache on cuda:{index}")
+    if t.dtype not in _HALVES or (dtype is not None and t.dtype != dtype):
         raise ValueError(f"{name} must be {dtype or 'float16 or bfloat16'}, got {t.dtype}")
-    D = cache.head_dim
-    if t.dim() != 3 or t.shape[2] != D or (heads is not None and t.shape[1] != heads):
+    if t.dim() != 3:
+        raise ValueError(f"{name} must be [T][heads][{D}]")
+    T, H, width = t.shape
+    if width != D or (heads is not None and H != heads):
         raise ValueError(f"{name} must be [T][{'heads' if heads is None else heads}][{D}], "
                          f"got {list(t.shape)}")
-    ld, hd = t.stride(0), t.stride(1)
-    if t.shape[0] <= 1:
+    ld, hd, step = t.stride()
+    if T <= 1:
         ld = 0
-    if t.shape[1] <= 1:
+    if H <= 1:
         hd = 0
-    if t.stride(2) != 1 or ld % 8 or hd % 8 or t.data_ptr() % 16:
+    if step != 1 or ld % 8 or hd % 8 or t.data_ptr() % 16:
         raise ValueError(f"{name}'s vectors must be contiguous and start on multiples of 16 bytes")
-    return ld, hd
+    return T, H, ld, hd
 
 
 def kv4_append(cache: Kv4Cache, k: torch.Tensor, v: torch.Tensor, table: torch.Tensor,
@@ -823,17 +858,15 @@ def kv4_append(cache: Kv4Cache, k: torch.Tensor, v: torch.Tensor, table: torch.T
     distance) into the cache (bcq_kv4_append).  kv_len [B] counts the new
     tokens in: row i of a sequence's n rows cu[b]..cu[b + 1] - 1 goes to
     position kv_len - n + i.  Without cu each sequence has one row."""
-    T = k.shape[0]
-    ldk, hdk = _need_heads(k, "k", cache, cache.heads)
-    ldv, hdv = _need_heads(v, "v", cache, cache.heads, k.dtype)
-    if v.shape[0] != T:
+    index = cache.k.get_device()
+    c, heads, _, D = cache._c()
+    T, _, ldk, hdk = _need_heads(k, "k", heads, D, index)
+    TV, _, ldv, hdv = _need_heads(v, "v", heads, D, index, k.dtype)
+    if TV != T:
         raise ValueError("k and v must have as many rows")
-    B, W = _need_places(cache, table, kv_len, cu, T)
-    dev = cache.k.device
-    with _on(dev):
-        _check(lib().bcq_kv4_append(ctypes.byref(cache._c()), _ptr(k), ldk, hdk, _ptr(v), ldv, hdv,
-                                    _DTYPES[k.dtype], T, _ptr(table), W, _ptr(kv_len), _ptr(cu), B,
-                                    _stream(stream, dev)), "bcq_kv4_append")
+    B, W, p_table, p_len, p_cu = _need_places(table, kv_len, cu, T, index)
+    _run("bcq_kv4_append", index, c, k.data_ptr(), ldk, hdk, v.data_ptr(), ldv, hdv,
+         _DTYPES[k.dtype], T, p_table, W, p_len, p_cu, B, _raw_stream(stream, index))
 
 
 def kv4_read(cache: Kv4Cache, table: torch.Tensor, kv_len: torch.Tensor,
@@ -851,20 +884,19 @@ def kv4_read(cache: Kv4Cache, table: torch.Tensor, kv_len: torch.Tensor,
     if T is None:
         raise ValueError("with cu, give tokens (or k and v)")
     T = int(T)
-    B, W = _need_places(cache, table, kv_len, cu, T)
-    dev = cache.k.device
-    shape = (T, cache.heads, cache.head_dim)
+    index = cache.k.get_device()
+    c, heads, _, D = cache._c()
+    B, W, p_table, p_len, p_cu = _need_places(table, kv_len, cu, T, index)
+    shape = (T, heads, D)
     if k is None:
-        k, v = _empty_on(shape, dtype, dev, stream), _empty_on(shape, dtype, dev, stream)
+        k, v = _new(cache.k, shape, dtype, stream), _new(cache.k, shape, dtype, stream)
     else:
         for t, name in ((k, "k"), (v, "v")):
             _need_cuda(t, name, dtype)
-            if tuple(t.shape) != shape or t.device != dev or t.data_ptr() % 16:
-                raise ValueError(f"{name} must be {list(shape)} on {dev}, 16-byte aligned")
-    with _on(dev):
-        _check(lib().bcq_kv4_read(ctypes.byref(cache._c()), _ptr(k), _ptr(v), _DTYPES[dtype], T,
-                                  _ptr(table), W, _ptr(kv_len), _ptr(cu), B, _stream(stream, dev)),
-               "bcq_kv4_read")
+            if tuple(t.shape) != shape or t.get_device() != index or t.data_ptr() % 16:
+                raise ValueError(f"{name} must be {list(shape)} on cuda:{index}, 16-byte aligned")
+    _run("bcq_kv4_read", index, c, k.data_ptr(), v.data_ptr(), _DTYPES[dtype], T, p_table, W, p_len,
+         p_cu, B, _raw_stream(stream, index))
     return k, v
 
 
@@ -884,37 +916,34 @@ def kv4_attention(q: torch.Tensor, cache: Kv4Cache, table: torch.Tensor, kv_len:
     near one fast); window > 0 lets a row see that many positions, its own the
     last; scale is 1 / sqrt(D) when not given.  A row that sees nothing gives
     zeros and -inf; rows that cu gives to no sequence are left as they were."""
-    D = cache.head_dim
-    ldq, hdq = _need_heads(q, "q", cache, None)
-    T, H = q.shape[0], q.shape[1]
-    if H == 0 or H % cache.heads:
-        raise ValueError(f"q's heads must be a multiple of the cache's {cache.heads}, got {H}")
-    B, W = _need_places(cache, table, kv_len, cu, T)
-    dev = cache.k.device
+    index = cache.k.get_device()
+    c, heads, page_size, D = cache._c()
+    T, H, ldq, hdq = _need_heads(q, "q", None, D, index)
+    if H == 0 or H % heads:
+        raise ValueError(f"q's heads must be a multiple of the cache's {heads}, got {H}")
+    B, W, p_table, p_len, p_cu = _need_places(table, kv_len, cu, T, index)
     if out is None:
-        out = _empty_on((T, H, D), q.dtype, dev, stream)
+        out = _new(q, (T, H, D), q.dtype, stream)
         ldo, hdo = H * D, D
     else:
-        ldo, hdo = _need_heads(out, "out", cache, H, q.dtype)
-        if out.shape[0] != T:
+        TO, _, ldo, hdo = _need_heads(out, "out", H, D, index, q.dtype)
+        if TO != T:
             raise ValueError(f"out must have {T} rows")
         if (T > 1 and ldo < D) or (H > 1 and hdo < D) or (
                 T > 1 and H > 1 and ldo < (H - 1) * hdo + D and hdo < (T - 1) * ldo + D):
             raise ValueError("out's vectors overlap")
-    lse = _empty_on((T, H), torch.float32, dev, stream) if return_lse else None
+    lse = _new(q, (T, H), torch.float32, stream) if return_lse else None
     if max_q is None:
         max_q = 1 if cu is None else max(T, 1)
     if max_kv is None:
-        max_kv = W * cache.k.shape[2]
-    c = ctypes.byref(cache._c())
-    need = int(lib().bcq_kv4_attention_workspace_bytes(c, T, H, B, int(max_q), int(max_kv)))
-    ws = _empty_on((need,), torch.uint8, dev, stream) if need else None
-    with _on(dev):
-        _check(lib().bcq_kv4_attention(
-            c, _ptr(q), ldq, hdq, _DTYPES[q.dtype], T, H, _ptr(table), W, _ptr(kv_len), _ptr(cu), B,
-            int(max_q), int(max_kv), int(bool(causal)), int(window),
-            D ** -0.5 if scale is None else float(scale), _ptr(out), ldo, hdo, _ptr(lse), _ptr(ws),
-            need, _stream(stream, dev)), "bcq_kv4_attention")
+        max_kv = W * page_size
+    need = lib().bcq_kv4_attention_workspace_bytes(c, T, H, B, max_q, max_kv)
+    ws = _new(q, (need,), torch.uint8, stream) if need else None
+    _run("bcq_kv4_attention", index, c, q.data_ptr(), ldq, hdq, _DTYPES[q.dtype], T, H, p_table, W,
+         p_len, p_cu, B, max_q, max_kv, 1 if causal else 0, window,
+         D ** -0.5 if scale is None else scale, out.data_ptr(), ldo, hdo,
+         None if lse is None else lse.data_ptr(), None if ws is None else ws.data_ptr(), need,
+         _raw_stream(stream, index))
     return (out, lse) if return_lse else out
 
 

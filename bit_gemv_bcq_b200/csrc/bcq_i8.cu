@@ -588,10 +588,11 @@ void plan_gemm(int M, int N, int K, int sms, GemmParams* p, size_t* smem, int* g
   p->kg_step = ((uint32_t)p->KG << 16) / (uint32_t)p->workers;
 }
 
+// SMs of the current device, 0 if it cannot be asked.
 int sm_count() {
   int dev = 0, n = 0;
   if (cudaGetDevice(&dev) != cudaSuccess ||
-      cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess || n < 1)
+      cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess || n < 2)
     return 0;
   return n;
 }
@@ -599,8 +600,8 @@ int sm_count() {
 template <typename TO, bool PAIR>
 cudaError_t launch_gemm_t(const CUtensorMap& wmap, const CUtensorMap& xmap, const GemmParams& p,
                           size_t smem, int grid, cudaStream_t st) {
-  cudaError_t e = cudaFuncSetAttribute(gemm_i8_kernel<TO, PAIR>,
-                                       cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kMaxSmem);
+  static std::atomic<uint64_t> done{0};
+  const cudaError_t e = allow_smem(gemm_i8_kernel<TO, PAIR>, kMaxSmem, done);
   if (e != cudaSuccess) return e;
   cudaLaunchAttribute attr[2] = {};
   int n = 0;

@@ -835,7 +835,7 @@ FewPlan plan_few(const bcq_kv4* c, int q_heads, int B, int max_q, int max_kv) {
   f.row_blocks = (int)std::min<int64_t>((rows + 8 * f.nt - 1) / (8 * f.nt), INT32_MAX);
   const double units = (double)f.row_blocks * c->heads * B;
   double best = 0;
-  for (int s = 1; s <= 256 && (s == 1 || (int64_t)(s - 1) * 128 < max_kv); ++s) {
+  for (int s = 1; s <= 512 && (s == 1 || (int64_t)(s - 1) * 128 < max_kv); s += 1 + s / 8) {
     const int chunk = (int)std::min<int64_t>((((int64_t)max_kv + s - 1) / s + 127) / 128 * 128, 1 << 30);
     const double waves = units * s / 444.0;
     const double cost = (waves <= 1 ? 1.0 : waves + 0.5) * (chunk + 160.0) + s;
@@ -851,8 +851,8 @@ FewPlan plan_few(const bcq_kv4* c, int q_heads, int B, int max_q, int max_kv) {
 template <typename T, int D, int NT>
 cudaError_t launch_few_t(const AttentionParams& p, cudaStream_t st) {
   constexpr int smem = (int)(kFewWarps * FewShape<D>::kRing);
-  cudaError_t e = cudaFuncSetAttribute(kv4_few_kernel<T, D, NT>,
-                                       cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+  static std::atomic<uint64_t> done{0};
+  cudaError_t e = allow_smem(kv4_few_kernel<T, D, NT>, smem, done);
   if (e != cudaSuccess) return e;
   const dim3 grid((unsigned)((int64_t)p.row_blocks * p.at.heads * p.at.B), (unsigned)p.splits);
   kv4_few_kernel<T, D, NT><<<grid, kFewWarps * 32, smem, st>>>(p);

@@ -3,6 +3,7 @@
 
 #include <cuda_runtime.h>
 
+#include <atomic>
 #include <cstdint>
 
 #include "bcq.h"
@@ -51,6 +52,20 @@ cudaError_t launch_wait_probe(unsigned long long limit_ns, cudaStream_t st);
 
 // Synchronises st, returns the device error word in *code and clears it.
 cudaError_t read_and_clear_device_error(cudaStream_t st, int* code);
+
+// Raises a kernel's dynamic shared-memory limit to `bytes` on the current
+// device, once a device (`done`: the devices that have it, of this kernel).
+template <typename Kernel>
+cudaError_t allow_smem(Kernel kernel, size_t bytes, std::atomic<uint64_t>& done) {
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return e;
+  const uint64_t bit = dev < 64 ? 1ull << dev : 0;
+  if (bit && (done.load(std::memory_order_relaxed) & bit)) return cudaSuccess;
+  e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)bytes);
+  if (e == cudaSuccess) done.fetch_or(bit, std::memory_order_relaxed);
+  return e;
+}
 
 // As read_and_clear_device_error, for the kernels of bcq_i8.cu and of
 // bcq_kv4.cu, after the stream's synchronisation.
