@@ -61,26 +61,21 @@ __device__ __forceinline__ RowScale row_scale(uint32_t top) {
   return {pre, a * pre, __fdiv_rn(127.f, a * pre), top != 0 && top < Bits16<T>::kInf};
 }
 
+// In the low byte; rounding by adding 1.5 2^23 (conversion instructions run at
+// an eighth of the rate).
 template <typename T>
-__device__ __forceinline__ int code_of(uint32_t bits, const RowScale& s) {
+__device__ __forceinline__ uint32_t code_of(uint32_t bits, const RowScale& s) {
   const float x = Bits16<T>::to_float(bits) * s.pre;
   const float v = x * s.inv;
-  float r = rintf(v);
-  if (fabsf(v - r) > 0.4999f) r = rintf(__fdiv_rn(x * 127.f, s.as));
-  return (int)r;
+  float up = v + 12582912.f;
+  if (fabsf(v - (up - 12582912.f)) > 0.4999f) up = __fdiv_rn(x * 127.f, s.as) + 12582912.f;
+  return __float_as_uint(up);
 }
 
 __device__ __forceinline__ float4 lds_f32x4(uint32_t addr) {
   float4 v;
   asm volatile("ld.shared.v4.f32 {%0, %1, %2, %3}, [%4];" : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w) : "r"(addr));
   return v;
-}
-
-// Two signed bytes below the ones of `next`.
-__device__ __forceinline__ uint32_t pack_s8(int hi, int lo, uint32_t next) {
-  uint32_t d;
-  asm("cvt.pack.sat.s8.s32.b32 %0, %1, %2, %3;" : "=r"(d) : "r"(hi), "r"(lo), "r"(next));
-  return d;
 }
 
 // One block a row, which it holds in registers between the two looks at it
@@ -129,16 +124,16 @@ __global__ void __launch_bounds__(1024) quantize_i8_kernel(const uint16_t* __res
     uint2 out = make_uint2(0, 0);
     if (rs.any) {
       const uint32_t w[4] = {v[i].x, v[i].y, v[i].z, v[i].w};
-      int c[8];
+      uint32_t c[8];
 #pragma unroll
       for (int e = 0; e < 8; ++e) c[e] = code_of<T>((w[e >> 1] >> (16 * (e & 1))) & 0xFFFFu, rs);
-      out.x = pack_s8(c[1], c[0], pack_s8(c[3], c[2], 0));
-      out.y = pack_s8(c[5], c[4], pack_s8(c[7], c[6], 0));
+      out.x = prmt(prmt(c[0], c[1], 0x0040), prmt(c[2], c[3], 0x0040), 0x5410);
+      out.y = prmt(prmt(c[4], c[5], 0x0040), prmt(c[6], c[7], 0x0040), 0x5410);
     }
     *reinterpret_cast<uint2*>(to + (int64_t)(tid + i * threads) * 8) = out;
   }
   for (int k = vecs * 8 + tid; k < K; k += threads)
-    to[k] = (int8_t)(rs.any ? code_of<T>(row[k], rs) : 0);
+    to[k] = (int8_t)(rs.any ? code_of<T>(row[k], rs) & 0xFFu : 0u);
 }
 
 // ------------------------------------------------------------- the product

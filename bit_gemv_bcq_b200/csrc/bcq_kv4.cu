@@ -7,6 +7,7 @@
 #include <algorithm>
 #include <cmath>
 #include <cstdint>
+#include <type_traits>
 
 #include "bcq.h"
 #include "bcq_device.cuh"
@@ -82,7 +83,45 @@ __device__ __forceinline__ int64_t vector_of(const Places& p, int64_t slot, int 
   return (slot / p.page_size * p.heads + h) * p.page_size + slot % p.page_size;
 }
 
-// ------------------------------------------------------------------ append
+// --------------------------------------------------- rows in, rows out
+
+constexpr int kRowThreads = 256;
+
+// Where kRows rows from t0 on go, found by the whole block: place[i] = index of
+// the vector of head 0 (the other heads' lie page_size apart), -1 for a
+// position that the cache does not have, -2 for a row of no sequence.
+template <int kRows>
+__device__ __forceinline__ void locate_rows(const Places& p, int t0, int T, int64_t* place,
+                                            int* count) {
+  const int tid = threadIdx.x;
+  if (p.cu) {
+    if (tid < kRows) count[tid] = 0;
+    __syncthreads();
+    // row t's sequence: how many of cu[1..B] are not above t
+    for (int b0 = 1; b0 <= p.B; b0 += kRowThreads) {
+      const int end = b0 + tid <= p.B ? p.cu[b0 + tid] : INT32_MAX;
+#pragma unroll
+      for (int i = 0; i < kRows; ++i) {
+        const int n = __popc(__ballot_sync(0xFFFFFFFFu, end <= t0 + i));
+        if ((tid & 31) == 0 && n) atomicAdd(&count[i], n);
+      }
+    }
+    __syncthreads();
+  }
+  if (tid < kRows) {
+    const int t = t0 + tid;
+    int64_t at = -2;
+    const int b = p.cu ? count[tid] : t;
+    if (t < T && b < p.B && (!p.cu || t >= p.cu[0])) {
+      const int2 rows = rows_of(p, b);
+      const int64_t slot = slot_of(p, b, p.kv_len[b] - rows.y + (t - rows.x));
+      at = slot < 0 ? -1 : vector_of(p, slot, 0);
+    }
+    if (at == -1) record_error(&g_kv4_error, BCQ_ERR_PAGE);
+    place[tid] = at;
+  }
+  __syncthreads();
+}
 
 struct AppendParams {
   Places at;
@@ -90,115 +129,144 @@ struct AppendParams {
   int64_t ld[2], hd[2];
   uint8_t* code[2];
   __half2* param[2];
-  int T, D;
+  int T;
 };
 
-// Eight lanes a group of 64: eight values a lane, one 32-bit word of codes.
-// The codes' quotient is taken in fp32 with a rounded reciprocal; where it
-// lies within 1e-4 of a half (its error is below 16 * 4 * 2^-24 < 4e-6, and
-// the difference's rounding adds less) the half decides in fp64, where x - z
-// and (c + 1/2) a are exact.
 template <typename T>
-__global__ void __launch_bounds__(256) kv4_append_kernel(AppendParams p) {
-  const int G = p.D / kKvGroup;
-  const int64_t units = (int64_t)p.T * p.at.heads * G * 2;
-  const int64_t u = ((int64_t)blockIdx.x * blockDim.x + threadIdx.x) >> 3;
-  const int sub = threadIdx.x & 7;
-  if (u >= units) return;  // whole groups of eight lanes leave
-  const uint32_t mask = 0xFFu << (threadIdx.x & 24);
-  const int g = (int)(u % G);
-  const int h = (int)(u / G % p.at.heads);
-  const int kv = (int)(u / G / p.at.heads % 2);
-  const int t = (int)(u / G / p.at.heads / 2);
-  const int b = sequence_of(p.at, t);
-  if (b < 0) return;
-  const int2 rows = rows_of(p.at, b);
-  const int j = p.at.kv_len[b] - rows.y + (t - rows.x);
-  const int64_t slot = slot_of(p.at, b, j);
-  if (slot < 0) {
-    if (sub == 0) record_error(&g_kv4_error, BCQ_ERR_PAGE);
-    return;
-  }
-  const uint4 raw = *reinterpret_cast<const uint4*>(p.x[kv] + (int64_t)t * p.ld[kv] +
-                                                    (int64_t)h * p.hd[kv] + g * kKvGroup + sub * 8);
-  const uint32_t w[4] = {raw.x, raw.y, raw.z, raw.w};
-  float f[8];
-  float lo = INFINITY, hi = -INFINITY;
-  bool ok = true;
-  for (int i = 0; i < 8; ++i) {
-    f[i] = bits_to_float<T>((w[i >> 1] >> (16 * (i & 1))) & 0xFFFFu);
-    ok = ok && fabsf(f[i]) <= kKvRange;  // false for a NaN
-    lo = fminf(lo, f[i]);
-    hi = fmaxf(hi, f[i]);
-  }
-  for (int o = 1; o < 8; o <<= 1) {
-    lo = fminf(lo, __shfl_xor_sync(mask, lo, o));
-    hi = fmaxf(hi, __shfl_xor_sync(mask, hi, o));
-  }
-  ok = __all_sync(mask, ok);
-  const __half a16 = __float2half_rn(__fdiv_rn(__fsub_rn(hi, lo), 15.f));
-  const __half z16 = __float2half_rn(lo);
-  const float a = __half2float(a16), z = __half2float(z16);
-  uint32_t word = 0;
-  if (ok && a > 0.f) {
-    const float inv = __fdiv_rn(1.f, a);
-    for (int i = 0; i < 8; ++i) {
-      const float v = (f[i] - z) * inv;
-      float r = rintf(v);
-      if (fabsf(v - r) > 0.4999f) {
-        const float c = floorf(v);  // the half in question is c + 1/2
-        const double d = (double)f[i] - (double)z, edge = ((double)c + 0.5) * (double)a;
-        r = d > edge ? c + 1.f : d < edge ? c : 2.f * rintf(0.5f * c + 0.25f);
+struct Pair16;  // two values of a 16-bit type
+template <>
+struct Pair16<__half> {
+  using V = __half2;
+};
+template <>
+struct Pair16<__nv_bfloat16> {
+  using V = __nv_bfloat162;
+};
+
+// A block takes kRows rows; eight lanes a group of 64, eight values a lane, one
+// 32-bit word of codes.  Least and greatest come from packed 16-bit compares
+// that keep a NaN.  The codes' quotient is taken in fp32 with a rounded
+// reciprocal and rounded by adding 1.5 2^23 (conversion instructions run at an
+// eighth of the rate); where it lies within 1e-4 of a half (its error is below
+// 16 * 4 * 2^-24 < 4e-6, and the difference's rounding adds less) the half
+// decides in fp64, where x - z and (c + 1/2) a are exact.
+template <typename T, int D, int kRows>
+__global__ void __launch_bounds__(kRowThreads) kv4_append_kernel(const AppendParams p) {
+  using V = typename Pair16<T>::V;
+  constexpr int G = D / kKvGroup, kWords = D / 8;
+  __shared__ int64_t place[kRows];
+  __shared__ int count[kRows];
+  const int t0 = (int)blockIdx.x * kRows, heads = p.at.heads;
+  locate_rows<kRows>(p.at, t0, p.T, place, count);
+  for (int i = threadIdx.x; i < 2 * heads * kWords; i += kRowThreads) {
+    const int kv = i >= heads * kWords;
+    const int in = kv ? i - heads * kWords : i;
+    const int h = in / kWords, word = in % kWords;
+    const uint16_t* x = p.x[kv] + (int64_t)h * p.hd[kv] + word * 8;
+    uint4 raw[kRows];
+#pragma unroll
+    for (int j = 0; j < kRows; ++j) {
+      raw[j] = make_uint4(0, 0, 0, 0);
+      if (place[j] >= 0) raw[j] = ldg_nc_v4(x + (int64_t)(t0 + j) * p.ld[kv]);
+    }
+    const uint32_t mask = 0xFFu << (threadIdx.x & 24);
+#pragma unroll
+    for (int j = 0; j < kRows; ++j) {
+      if (place[j] < 0) continue;
+      const uint32_t w[4] = {raw[j].x, raw[j].y, raw[j].z, raw[j].w};
+      const V* v2 = reinterpret_cast<const V*>(w);
+      V lo2 = __hmin2_nan(__hmin2_nan(v2[0], v2[1]), __hmin2_nan(v2[2], v2[3]));
+      V hi2 = __hmax2_nan(__hmax2_nan(v2[0], v2[1]), __hmax2_nan(v2[2], v2[3]));
+#pragma unroll
+      for (int o = 1; o < 8; o <<= 1) {
+        lo2 = __hmin2_nan(lo2, __shfl_xor_sync(mask, lo2, o));
+        hi2 = __hmax2_nan(hi2, __shfl_xor_sync(mask, hi2, o));
       }
-      word |= (uint32_t)fminf(fmaxf(r, 0.f), 15.f) << (4 * i);
+      const T lo16 = __hmin_nan(lo2.x, lo2.y), hi16 = __hmax_nan(hi2.x, hi2.y);
+      const float lo = (float)lo16, hi = (float)hi16;
+      const bool ok = lo >= -kKvRange && hi <= kKvRange;  // false for a NaN
+      const __half a16 = __float2half_rn(__fdiv_rn(__fsub_rn(hi, lo), 15.f));
+      const __half z16 = __float2half_rn(lo);
+      const float a = __half2float(a16), z = __half2float(z16);
+      uint32_t codes = 0;
+      if (ok && a > 0.f) {
+        const float inv = __fdiv_rn(1.f, a);
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+          const float f = bits_to_float<T>((w[e >> 1] >> (16 * (e & 1))) & 0xFFFFu);
+          const float q = fminf(fmaxf((f - z) * inv, 0.f), 15.f);
+          const float up = q + 12582912.f;  // 1.5 * 2^23: the nearest integer, halves to even
+          uint32_t c = __float_as_uint(up);
+          if (fabsf(q - (up - 12582912.f)) > 0.4999f) {
+            const float below = floorf(q);  // the half in question is below + 1/2
+            const double d = (double)f - (double)z, edge = ((double)below + 0.5) * (double)a;
+            c = (uint32_t)below;
+            c += d > edge || (d == edge && (c & 1u));
+          }
+          codes |= (c & 15u) << (4 * e);
+        }
+      }
+      const int64_t vec = place[j] + (int64_t)h * p.at.page_size;
+      *reinterpret_cast<uint32_t*>(p.code[kv] + vec * (D / 2) + word * 4) = codes;
+      if (word % 8 == 0) {
+        const __half nan = __ushort_as_half(0x7E00);
+        p.param[kv][vec * G + word / 8] = ok ? __halves2half2(a16, z16) : __halves2half2(nan, nan);
+      }
     }
   }
-  const int64_t vec = vector_of(p.at, slot, h);
-  *reinterpret_cast<uint32_t*>(p.code[kv] + vec * (p.D / 2) + g * (kKvGroup / 2) + sub * 4) = word;
-  if (sub == 0) {
-    const __half nan = __ushort_as_half(0x7E00);
-    p.param[kv][vec * G + g] = ok ? __halves2half2(a16, z16) : __halves2half2(nan, nan);
-  }
 }
-
-// -------------------------------------------------------------------- read
 
 struct ReadParams {
   Places at;
   const uint8_t* code[2];
   const __half2* param[2];
   void* y[2];
-  int T, D;
+  int T;
 };
 
-// Eight values (one word of codes) a thread.
-template <typename TO>
-__global__ void __launch_bounds__(256) kv4_read_kernel(ReadParams p) {
-  const int W = p.D / 8;
-  const int64_t u = (int64_t)blockIdx.x * blockDim.x + threadIdx.x;
-  if (u >= (int64_t)p.T * p.at.heads * W * 2) return;
-  const int i = (int)(u % W);
-  const int h = (int)(u / W % p.at.heads);
-  const int kv = (int)(u / W / p.at.heads % 2);
-  const int t = (int)(u / W / p.at.heads / 2);
-  const int b = sequence_of(p.at, t);
-  if (b < 0) return;
-  const int2 rows = rows_of(p.at, b);
-  const int64_t slot = slot_of(p.at, b, p.at.kv_len[b] - rows.y + (t - rows.x));
-  float f[8] = {};
-  if (slot >= 0) {
-    const int64_t vec = vector_of(p.at, slot, h);
-    const uint32_t word = *reinterpret_cast<const uint32_t*>(p.code[kv] + vec * (p.D / 2) + 4 * i);
-    const float2 az = __half22float2(p.param[kv][vec * (p.D / kKvGroup) + i / 8]);
-    for (int e = 0; e < 8; ++e) f[e] = fmaf((float)((word >> (4 * e)) & 15u), az.x, az.y);
-  } else if (i == 0) {
-    record_error(&g_kv4_error, BCQ_ERR_PAGE);
+// Eight values (one word of codes) a thread and row.
+template <typename TO, int D, int kRows>
+__global__ void __launch_bounds__(kRowThreads) kv4_read_kernel(const ReadParams p) {
+  constexpr int G = D / kKvGroup, kWords = D / 8;
+  __shared__ int64_t place[kRows];
+  __shared__ int count[kRows];
+  const int t0 = (int)blockIdx.x * kRows, heads = p.at.heads;
+  locate_rows<kRows>(p.at, t0, p.T, place, count);
+  for (int i = threadIdx.x; i < 2 * heads * kWords; i += kRowThreads) {
+    const int kv = i >= heads * kWords;
+    const int in = kv ? i - heads * kWords : i;
+    const int h = in / kWords, word = in % kWords;
+    uint32_t codes[kRows];
+    __half2 az[kRows];
+#pragma unroll
+    for (int j = 0; j < kRows; ++j) {
+      codes[j] = 0;
+      az[j] = __floats2half2_rn(0.f, 0.f);
+      if (place[j] >= 0) {
+        const int64_t vec = place[j] + (int64_t)h * p.at.page_size;
+        codes[j] = *reinterpret_cast<const uint32_t*>(p.code[kv] + vec * (D / 2) + 4 * word);
+        az[j] = p.param[kv][vec * G + word / 8];
+      }
+    }
+    TO* y = static_cast<TO*>(p.y[kv]) + ((int64_t)t0 * heads + h) * D + 8 * word;
+#pragma unroll
+    for (int j = 0; j < kRows; ++j, y += (int64_t)heads * D) {
+      if (place[j] == -2) continue;
+      const float2 f = __half22float2(az[j]);
+      union {
+        TO v[8];
+        uint4 q[8 * sizeof(TO) / 16];
+      } out;
+#pragma unroll
+      for (int e = 0; e < 8; ++e) {
+        // 2^23 + c by its bits, instead of a conversion
+        const float c = __uint_as_float(0x4B000000u | ((codes[j] >> (4 * e)) & 15u)) - 8388608.f;
+        out.v[e] = from_float<TO>(fmaf(c, f.x, f.y));
+      }
+#pragma unroll
+      for (int e = 0; e < (int)(8 * sizeof(TO) / 16); ++e) reinterpret_cast<uint4*>(y)[e] = out.q[e];
+    }
   }
-  TO out[8];
-  for (int e = 0; e < 8; ++e) out[e] = from_float<TO>(f[e]);
-  TO* y = static_cast<TO*>(p.y[kv]) + ((int64_t)t * p.at.heads + h) * p.D + 8 * i;
-  const uint4* src = reinterpret_cast<const uint4*>(out);
-  for (int e = 0; e < (int)(8 * sizeof(TO) / 16); ++e) reinterpret_cast<uint4*>(y)[e] = src[e];
 }
 
 // --------------------------------------------------------------- attention
@@ -820,6 +888,19 @@ Places places_of(const bcq_kv4* c, const int32_t* table, int table_width, const 
   return {table, kv_len, cu, table_width, B, c->pages, c->page_size, c->heads};
 }
 
+// f(D, rows a block) as compile-time numbers: one row while that leaves SMs
+// idle otherwise, else four, whose loads are in flight together.
+template <typename F>
+void by_shape(int D, int T, const F& f) {
+  auto rows = [&](auto d) {
+    if (T < 1184) f(d, std::integral_constant<int, 1>());
+    else f(d, std::integral_constant<int, 4>());
+  };
+  if (D == 64) rows(std::integral_constant<int, 64>());
+  else if (D == 128) rows(std::integral_constant<int, 128>());
+  else rows(std::integral_constant<int, 256>());
+}
+
 // Rows of a CTA (8 nt of a key/value head's) and parts of the positions.
 struct FewPlan {
   int nt, row_blocks, splits, chunk;
@@ -903,19 +984,21 @@ bcq_status bcq_kv4_append(const bcq_kv4* cache, const void* k, int64_t ld_k, int
   if (s != BCQ_OK || T == 0) return s;
   if ((s = check_rows(k, ld_k, hd_k, dtype)) != BCQ_OK) return s;
   if ((s = check_rows(v, ld_v, hd_v, dtype)) != BCQ_OK) return s;
-  AppendParams p = {places_of(cache, table, table_width, kv_len, cu, B),
-                    {static_cast<const uint16_t*>(k), static_cast<const uint16_t*>(v)},
-                    {ld_k, ld_v},
-                    {hd_k, hd_v},
-                    {cache->k, cache->v},
-                    {reinterpret_cast<__half2*>(cache->k_param), reinterpret_cast<__half2*>(cache->v_param)},
-                    T,
-                    cache->head_dim};
-  const int64_t blocks = ((int64_t)T * cache->heads * (cache->head_dim / kKvGroup) * 2 + 31) / 32;
-  if (blocks > INT32_MAX) return BCQ_ERR_SHAPE;
+  const AppendParams p = {places_of(cache, table, table_width, kv_len, cu, B),
+                          {static_cast<const uint16_t*>(k), static_cast<const uint16_t*>(v)},
+                          {ld_k, ld_v},
+                          {hd_k, hd_v},
+                          {cache->k, cache->v},
+                          {reinterpret_cast<__half2*>(cache->k_param),
+                           reinterpret_cast<__half2*>(cache->v_param)},
+                          T};
   cudaStream_t st = (cudaStream_t)stream;
-  if (dtype == BCQ_F16) kv4_append_kernel<__half><<<(unsigned)blocks, 256, 0, st>>>(p);
-  else kv4_append_kernel<__nv_bfloat16><<<(unsigned)blocks, 256, 0, st>>>(p);
+  by_shape(cache->head_dim, T, [&](auto d, auto rows) {
+    constexpr int D = decltype(d)::value, kRows = decltype(rows)::value;
+    const unsigned blocks = (unsigned)((T + kRows - 1) / kRows);
+    if (dtype == BCQ_F16) kv4_append_kernel<__half, D, kRows><<<blocks, kRowThreads, 0, st>>>(p);
+    else kv4_append_kernel<__nv_bfloat16, D, kRows><<<blocks, kRowThreads, 0, st>>>(p);
+  });
   return launched();
 }
 
@@ -927,19 +1010,20 @@ bcq_status bcq_kv4_read(const bcq_kv4* cache, void* k, void* v, int dtype, int T
   if (!k || !v) return BCQ_ERR_NULL;
   if (!is16(dtype) && dtype != BCQ_F32) return BCQ_ERR_UNSUPPORTED;
   if (!aligned(k, 16) || !aligned(v, 16)) return BCQ_ERR_ALIGN;
-  ReadParams p = {places_of(cache, table, table_width, kv_len, cu, B),
-                  {cache->k, cache->v},
-                  {reinterpret_cast<const __half2*>(cache->k_param),
-                   reinterpret_cast<const __half2*>(cache->v_param)},
-                  {k, v},
-                  T,
-                  cache->head_dim};
-  const int64_t blocks = ((int64_t)T * cache->heads * (cache->head_dim / 8) * 2 + 255) / 256;
-  if (blocks > INT32_MAX) return BCQ_ERR_SHAPE;
+  const ReadParams p = {places_of(cache, table, table_width, kv_len, cu, B),
+                        {cache->k, cache->v},
+                        {reinterpret_cast<const __half2*>(cache->k_param),
+                         reinterpret_cast<const __half2*>(cache->v_param)},
+                        {k, v},
+                        T};
   cudaStream_t st = (cudaStream_t)stream;
-  if (dtype == BCQ_F16) kv4_read_kernel<__half><<<(unsigned)blocks, 256, 0, st>>>(p);
-  else if (dtype == BCQ_BF16) kv4_read_kernel<__nv_bfloat16><<<(unsigned)blocks, 256, 0, st>>>(p);
-  else kv4_read_kernel<float><<<(unsigned)blocks, 256, 0, st>>>(p);
+  by_shape(cache->head_dim, T, [&](auto d, auto rows) {
+    constexpr int D = decltype(d)::value, kRows = decltype(rows)::value;
+    const unsigned blocks = (unsigned)((T + kRows - 1) / kRows);
+    if (dtype == BCQ_F16) kv4_read_kernel<__half, D, kRows><<<blocks, kRowThreads, 0, st>>>(p);
+    else if (dtype == BCQ_BF16) kv4_read_kernel<__nv_bfloat16, D, kRows><<<blocks, kRowThreads, 0, st>>>(p);
+    else kv4_read_kernel<float, D, kRows><<<blocks, kRowThreads, 0, st>>>(p);
+  });
   return launched();
 }
 
