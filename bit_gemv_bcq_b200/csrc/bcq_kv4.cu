@@ -849,6 +849,14 @@ __global__ void __launch_bounds__(128) kv4_join_kernel(const AttentionParams p) 
     p.lse[id] = none ? -INFINITY : (top + log2f(sum) - kWeightBits) * 0.69314718055994531f;
 }
 
+}  // namespace
+}  // namespace bcq
+
+#include "bcq_kv4_many.cuh"
+
+namespace bcq {
+namespace {
+
 // -------------------------------------------------------------------- host
 
 bool aligned(const void* p, size_t a) { return (reinterpret_cast<uintptr_t>(p) % a) == 0; }
@@ -901,31 +909,42 @@ void by_shape(int D, int T, const F& f) {
   else rows(std::integral_constant<int, 256>());
 }
 
-// Rows of a CTA (8 nt of a key/value head's) and parts of the positions.
-struct FewPlan {
-  int nt, row_blocks, splits, chunk;
+// How a call's rows and positions are shared out: the kernel (nt: row groups of
+// eight a CTA of the few-row kernel, 0 the many-row kernel), rows of a CTA,
+// and parts of the positions.
+struct AttentionPlan {
+  int nt, rows, row_blocks, splits, chunk;
 };
 
-// Parts: a wave is 3 CTAs on each of 148 SMs; CTAs beyond one start as others
-// end, the last of them alone on average for half of one's time.  A CTA costs
-// about as much as 160 positions before and after its positions.
-FewPlan plan_few(const bcq_kv4* c, int q_heads, int B, int max_q, int max_kv) {
-  FewPlan f;
-  const int64_t rows = (int64_t)max_q * (q_heads / c->heads);
-  f.nt = rows <= 8 || c->head_dim == 256 ? 1 : 2;
-  f.row_blocks = (int)std::min<int64_t>((rows + 8 * f.nt - 1) / (8 * f.nt), INT32_MAX);
-  const double units = (double)f.row_blocks * c->heads * B;
+// Parts: `room` CTAs run at once; those beyond start as others end, the last of
+// them alone on average for half of one's time.  A CTA costs about as much as
+// `start` positions before and after its positions.
+void plan_parts(AttentionPlan* f, double units, int max_kv, double room, double start) {
   double best = 0;
   for (int s = 1; s <= 512 && (s == 1 || (int64_t)(s - 1) * 128 < max_kv); s += 1 + s / 8) {
     const int chunk = (int)std::min<int64_t>((((int64_t)max_kv + s - 1) / s + 127) / 128 * 128, 1 << 30);
-    const double waves = units * s / 444.0;
-    const double cost = (waves <= 1 ? 1.0 : waves + 0.5) * (chunk + 160.0) + s;
+    const double waves = units * s / room;
+    const double cost = (waves <= 1 ? 1.0 : waves + 0.5) * (chunk + start) + s;
     if (best == 0 || cost < best) {
       best = cost;
-      f.splits = s;
-      f.chunk = chunk;
+      f->splits = s;
+      f->chunk = chunk;
     }
   }
+}
+
+// The few-row kernel passes over the positions once for every 16 rows, three
+// CTAs an SM; the many-row kernel once for every 256 (128 where D = 256).
+AttentionPlan plan_attention(const bcq_kv4* c, int q_heads, int B, int max_q, int max_kv) {
+  AttentionPlan f;
+  const int64_t rows = (int64_t)max_q * (q_heads / c->heads);
+  const bool many = rows > 48;
+  f.nt = many ? 0 : rows <= 8 || c->head_dim == 256 ? 1 : 2;
+  f.rows = !many ? 8 * f.nt : c->head_dim == 256 ? 128 : 256;
+  f.row_blocks = (int)std::min<int64_t>((rows + f.rows - 1) / f.rows, INT32_MAX);
+  const double units = (double)f.row_blocks * c->heads * B;
+  if (many) plan_parts(&f, units, max_kv, 148, 512);
+  else plan_parts(&f, units, max_kv, 444, 160);
   return f;
 }
 
@@ -937,7 +956,22 @@ cudaError_t launch_few_t(const AttentionParams& p, cudaStream_t st) {
   if (e != cudaSuccess) return e;
   const dim3 grid((unsigned)((int64_t)p.row_blocks * p.at.heads * p.at.B), (unsigned)p.splits);
   kv4_few_kernel<T, D, NT><<<grid, kFewWarps * 32, smem, st>>>(p);
-  if ((e = cudaGetLastError()) != cudaSuccess || p.splits == 1) return e;
+  return cudaGetLastError();
+}
+
+template <typename T, int D>
+cudaError_t launch_many_t(const AttentionParams& p, cudaStream_t st) {
+  constexpr size_t smem = ManyShape<D>::kSmem;
+  static std::atomic<uint64_t> done{0};
+  cudaError_t e = allow_smem(kv4_many_kernel<T, D>, smem, done);
+  if (e != cudaSuccess) return e;
+  const dim3 grid((unsigned)((int64_t)p.row_blocks * p.at.heads * p.at.B), (unsigned)p.splits);
+  kv4_many_kernel<T, D><<<grid, ManyShape<D>::kThreads, smem, st>>>(p);
+  return cudaGetLastError();
+}
+
+template <typename T, int D>
+cudaError_t launch_join_t(const AttentionParams& p, cudaStream_t st) {
   cudaLaunchAttribute attr = {};
   attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
   attr.val.programmaticStreamSerializationAllowed = 1;
@@ -950,11 +984,22 @@ cudaError_t launch_few_t(const AttentionParams& p, cudaStream_t st) {
   return cudaLaunchKernelEx(&cfg, kv4_join_kernel<T, D>, p);
 }
 
+template <typename T, int D>
+cudaError_t launch_attention_t(const AttentionParams& p, int nt, cudaStream_t st) {
+  cudaError_t e;
+  if constexpr (D == 256)
+    e = nt == 0 ? launch_many_t<T, D>(p, st) : launch_few_t<T, D, 1>(p, st);
+  else
+    e = nt == 0   ? launch_many_t<T, D>(p, st)
+        : nt == 1 ? launch_few_t<T, D, 1>(p, st)
+                  : launch_few_t<T, D, 2>(p, st);
+  return e == cudaSuccess && p.splits > 1 ? launch_join_t<T, D>(p, st) : e;
+}
+
 template <typename T>
-cudaError_t launch_few(const AttentionParams& p, int D, int nt, cudaStream_t st) {
-  if (D == 256) return launch_few_t<T, 256, 1>(p, st);
-  if (D == 128) return nt == 1 ? launch_few_t<T, 128, 1>(p, st) : launch_few_t<T, 128, 2>(p, st);
-  return nt == 1 ? launch_few_t<T, 64, 1>(p, st) : launch_few_t<T, 64, 2>(p, st);
+cudaError_t launch_attention(const AttentionParams& p, int D, int nt, cudaStream_t st) {
+  if (D == 256) return launch_attention_t<T, 256>(p, nt, st);
+  return D == 128 ? launch_attention_t<T, 128>(p, nt, st) : launch_attention_t<T, 64>(p, nt, st);
 }
 
 bcq_status launched() { return cudaGetLastError() == cudaSuccess ? BCQ_OK : BCQ_ERR_CUDA; }
@@ -1032,7 +1077,7 @@ size_t bcq_kv4_attention_workspace_bytes(const bcq_kv4* cache, int T, int q_head
   if (!cache || !cache_sizes_ok(cache) || !head_dim_ok(cache->head_dim) || T < 0 || B < 1 ||
       max_q < 1 || max_kv < 1 || q_heads < 1 || q_heads % cache->heads)
     return 0;
-  const FewPlan f = plan_few(cache, q_heads, B, max_q, max_kv);
+  const AttentionPlan f = plan_attention(cache, q_heads, B, max_q, max_kv);
   if (f.splits == 1) return 0;
   return (size_t)f.splits * (size_t)T * (size_t)q_heads * (size_t)(cache->head_dim + 2) * 4;
 }
@@ -1075,9 +1120,9 @@ bcq_status bcq_kv4_attention(const bcq_kv4* cache, const void* q, int64_t ld_q, 
                        causal,
                        window,
                        scale};
-  const FewPlan f = plan_few(cache, q_heads, B, max_q, max_kv);
+  const AttentionPlan f = plan_attention(cache, q_heads, B, max_q, max_kv);
   p.group = q_heads / cache->heads;
-  p.rows = 8 * f.nt;
+  p.rows = f.rows;
   p.row_blocks = f.row_blocks;
   p.splits = f.splits;
   p.chunk = f.chunk;
@@ -1085,8 +1130,8 @@ bcq_status bcq_kv4_attention(const bcq_kv4* cache, const void* q, int64_t ld_q, 
   if ((int64_t)f.row_blocks * cache->heads * B > INT32_MAX || (int64_t)T * q_heads > INT32_MAX)
     return BCQ_ERR_SHAPE;
   cudaStream_t st = (cudaStream_t)stream;
-  const cudaError_t e = dtype == BCQ_F16 ? launch_few<__half>(p, cache->head_dim, f.nt, st)
-                                         : launch_few<__nv_bfloat16>(p, cache->head_dim, f.nt, st);
+  const cudaError_t e = dtype == BCQ_F16 ? launch_attention<__half>(p, cache->head_dim, f.nt, st)
+                                         : launch_attention<__nv_bfloat16>(p, cache->head_dim, f.nt, st);
   return e == cudaSuccess ? BCQ_OK : BCQ_ERR_CUDA;
 }
 

@@ -1,0 +1,505 @@
+// bcq_kv4_many.cuh -- attention of many rows over the 4-bit cache (prompts and
+// their chunks), on the 5th-generation tensor core (included by bcq_kv4.cu
+// only, whose parameters, spans and helpers it uses).
+//
+//   S = Q K^T,  P = exp2(S fs - m),  O += P V  for 128 rows of a key/value head
+// (query heads that share it times rows of the call) a tile, two tiles a CTA
+// (one where D = 256 leaves tensor memory for no more), and 128 (64) positions
+// at a time.  Four warps turn the codes into fp16 operands in shared memory,
+// once for both tiles: c from its bits (1024 + c or 1024 + 16 c, exactly), then
+// a c + z with one rounding to fp16 (half a step, 2^-11).  One warp issues the
+// products; a tile's softmax (four warps, a thread a row) runs while the tensor
+// core works for the other tile.  P replaces S in tensor memory, in fp16 (the
+// second rounding of 2^-11); O stays there, and is scaled only when a row's
+// maximum has risen by more than 2^8 over the one in use, so p stays below 256.
+// Queries are scaled by a power of two a row to the top of fp16's range.
+// Within eight values of a vector both operands have the order 0 4 1 5 2 6 3 7,
+// in which masks yield them; outputs are put right as they are written.
+//
+// A value of V that is no number must not reach rows that do not see its
+// position (0 * NaN): such groups become zeros, and rows that see them are told
+// by a mask to write NaN.
+#pragma once
+
+#include "bcq_tcgen05.cuh"
+
+namespace bcq {
+namespace {
+
+template <int D>
+struct ManyShape {
+  static constexpr int kTiles = D == 256 ? 1 : 2;
+  static constexpr int kTokens = D == 256 ? 64 : 128;        // of a step
+  static constexpr int kBlocks = D / 64;                     // 128-byte column blocks of a vector
+  static constexpr uint32_t kQBlock = 128 * 128;             // bytes of 64 columns of 128 rows
+  static constexpr uint32_t kQTile = kBlocks * kQBlock;
+  static constexpr uint32_t kKvBlock = kTokens * 128;
+  static constexpr uint32_t kKvTile = kBlocks * kKvBlock;
+  static constexpr uint32_t kOffK = kTiles * kQTile;         // two buffers
+  static constexpr uint32_t kOffV = kOffK + 2 * kKvTile;     // two buffers
+  static constexpr uint32_t kOffBar = kOffV + 2 * kKvTile;
+  // per step (ring of four): words of the positions without a page, and of V's
+  // groups that are no numbers
+  static constexpr int kPieces = D / 32;                     // 16-byte pieces of a vector's codes
+  static constexpr int kPasses = kTokens * kPieces / 128;    // pieces a thread and step
+  static constexpr int kPerWarp = 32 / kPieces;              // positions a warp and pass
+  static constexpr int kWords = kPasses * 4;
+  static constexpr uint32_t kOffMask = kOffBar + 256;
+  static constexpr uint32_t kSmem = 1024 + kOffMask + 2 * 4 * kWords * 4;
+  static constexpr int kOCol = kTiles * kTokens;             // tensor memory: S tiles, then O tiles
+  static constexpr int kThreads = 32 * (4 * kTiles + 4 + 1); // softmax, codes, MMA
+};
+
+// Shared-memory descriptor, 128-byte swizzle: `lead` bytes between 64-element
+// blocks of a contiguous M or N (1 where K is contiguous), `stride` bytes
+// between groups of 8 rows.
+__device__ __forceinline__ uint64_t umma_desc_blocks(uint32_t addr, uint32_t lead, uint32_t stride) {
+  return (uint64_t)((addr >> 4) & 0x3FFFu) | ((uint64_t)(lead >> 4) << 16) |
+         ((uint64_t)(stride >> 4) << 32) | (1ull << 46) | (2ull << 61);
+}
+__device__ __forceinline__ void umma_f16_ss(uint32_t d, uint64_t adesc, uint64_t bdesc,
+                                            uint32_t idesc, uint32_t accumulate) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
+      "tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d),
+      "l"(adesc), "l"(bdesc), "r"(idesc), "r"(accumulate)
+      : "memory");
+}
+__device__ __forceinline__ void tmem_ld32(uint32_t taddr, uint32_t (&r)[32]) {
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x32.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, "
+      "%12, %13, %14, %15, %16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, "
+      "%30, %31}, [%32];"
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]),
+        "=r"(r[7]), "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]),
+        "=r"(r[14]), "=r"(r[15]), "=r"(r[16]), "=r"(r[17]), "=r"(r[18]), "=r"(r[19]), "=r"(r[20]),
+        "=r"(r[21]), "=r"(r[22]), "=r"(r[23]), "=r"(r[24]), "=r"(r[25]), "=r"(r[26]), "=r"(r[27]),
+        "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31])
+      : "r"(taddr)
+      : "memory");
+}
+
+// One word of codes as eight fp16 values a c + z, in the order 0 4 1 5 2 6 3 7.
+__device__ __forceinline__ uint4 word_values(uint32_t w, __half2 a, __half2 z) {
+  const __half2 k1024 = __float2half2_rn(1024.f), k16 = __float2half2_rn(0.0625f),
+                k64 = __float2half2_rn(-64.f);
+  auto low = [&](uint32_t x) {   // 1024 + c
+    const uint32_t h = (x & 0x000F000Fu) | 0x64006400u;
+    return __hfma2(a, __hsub2(*reinterpret_cast<const __half2*>(&h), k1024), z);
+  };
+  auto high = [&](uint32_t x) {  // 1024 + 16 c
+    const uint32_t h = (x & 0x00F000F0u) | 0x64006400u;
+    return __hfma2(a, __hfma2(*reinterpret_cast<const __half2*>(&h), k16, k64), z);
+  };
+  const __half2 v[4] = {low(w), high(w), low(w >> 8), high(w >> 8)};
+  return *reinterpret_cast<const uint4*>(v);
+}
+
+template <typename T, int D>
+__global__ void __launch_bounds__(ManyShape<D>::kThreads, 1) kv4_many_kernel(const AttentionParams p) {
+  using S = ManyShape<D>;
+  constexpr int G = D / kKvGroup;
+  extern __shared__ unsigned char smem_raw[];
+  const uint32_t sbase = (smem_u32(smem_raw) + 1023u) & ~1023u;
+  uint32_t* masks = reinterpret_cast<uint32_t*>(smem_raw + (sbase - smem_u32(smem_raw)) + S::kOffMask);
+  const int warp = __shfl_sync(0xFFFFFFFFu, (int)threadIdx.x >> 5, 0), lane = threadIdx.x & 31;
+
+  // the last blocks of rows see the most: they go first
+  const int block = p.row_blocks - 1 - (int)(blockIdx.x % p.row_blocks);
+  const int kvh = blockIdx.x / p.row_blocks % p.at.heads;
+  const int b = blockIdx.x / p.row_blocks / p.at.heads, part = blockIdx.y;
+  const Span sp = span_of(p, b, block);
+  if (part == 0 && block == 0 && kvh == 0 && threadIdx.x == 0) {
+    if (rows_of(p.at, b).y > p.max_q) record_error(&g_kv4_error, BCQ_ERR_SHAPE);
+    if (p.at.kv_len[b] != sp.len) record_error(&g_kv4_error, BCQ_ERR_PAGE);
+  }
+  if (part >= sp.parts) return;
+  const int row0 = block * p.rows, row_n = min(p.rows, sp.rows * p.group - row0);
+  const int begin = sp.begin + part * sp.chunk, end = min(sp.end, begin + sp.chunk);
+  const int steps = end > begin ? (end - begin + S::kTokens - 1) / S::kTokens : 0;
+  const int tiles = row_n > 128 ? 2 : 1;  // of this CTA
+
+  const uint32_t bar = sbase + S::kOffBar;
+  const uint32_t q_full = bar, k_full = bar + 8, k_empty = bar + 24, v_full = bar + 40,
+                 v_empty = bar + 56, s_full = bar + 72, p_full = bar + 88, o_done = bar + 104,
+                 drain = bar + 120, slot = bar + 128;
+  constexpr int kCodeWarp0 = 4 * S::kTiles, kMmaWarp = kCodeWarp0 + 4;
+  if (warp == kMmaWarp) {
+    if (lane == 0) {
+      mbar_init(q_full, (uint32_t)(4 * tiles));
+      mbar_init(drain, 1);
+      for (int i = 0; i < 2; ++i) {
+        mbar_init(k_full + 8 * i, 4);
+        mbar_init(k_empty + 8 * i, 1);
+        mbar_init(v_full + 8 * i, 4);
+        mbar_init(v_empty + 8 * i, 1);
+        mbar_init(s_full + 8 * i, 1);
+        mbar_init(p_full + 8 * i, 4);
+        mbar_init(o_done + 8 * i, 1);
+      }
+      fence_mbar_init();
+    }
+    __syncwarp();
+    tmem_alloc(slot, 512);
+  }
+  umma_fence_before();
+  __syncthreads();
+  umma_fence_after();
+  const uint32_t tmem = lds_u32v(slot);
+  constexpr unsigned long long kWaitNs = 2000000000ull;
+  auto wait = [&](uint32_t at, int round) {
+    return __all_sync(0xFFFFFFFFu, mbar_wait_bounded(at, (uint32_t)round & 1u, kWaitNs)) != 0;
+  };
+  auto give_up = [&]() {
+    if (lane == 0) record_error(&g_kv4_error, BCQ_ERR_TIMEOUT);
+  };
+
+  if (warp == kMmaWarp) {
+    // ------------------------------------------------------------ the products
+    const bool one = elect_one();
+    // fp16 A and B, fp32 D, M = 128; V has its values (N) contiguous
+    constexpr uint32_t kIdS = (1u << 4) | ((uint32_t)(S::kTokens >> 3) << 17) | (8u << 24);
+    constexpr uint32_t kIdO = (1u << 4) | (1u << 16) | ((uint32_t)(D >> 3) << 17) | (8u << 24);
+    const uint64_t qd = umma_desc_sw128(sbase), kd = umma_desc_sw128(sbase + S::kOffK);
+    const uint64_t vd = umma_desc_blocks(sbase + S::kOffV, S::kKvBlock, 1024);
+    bool ok = steps == 0 || wait(q_full, 0);
+    auto scores = [&](int t, int j) {
+      if (one) {
+#pragma unroll
+        for (int i = 0; i < D / 16; ++i)
+          umma_f16_ss(tmem + (uint32_t)(t * S::kTokens),
+                      qd + (uint32_t)((t * S::kQTile + (i >> 2) * S::kQBlock + (i & 3) * 32) >> 4),
+                      kd + (uint32_t)(((j & 1) * S::kKvTile + (i >> 2) * S::kKvBlock + (i & 3) * 32) >> 4),
+                      kIdS, i != 0);
+        umma_commit(s_full + 8u * t);
+        if (t == tiles - 1) umma_commit(k_empty + 8u * (j & 1));
+      }
+    };
+    for (int j = 0; j < steps && ok; ++j) {
+      if (j == 0) {
+        if (!(ok = wait(k_full, 0))) break;
+        umma_fence_after();
+        for (int t = 0; t < tiles; ++t) scores(t, 0);
+      }
+      for (int t = 0; t < tiles && ok; ++t) {
+        if (t == 0 && !(ok = wait(v_full + 8u * (j & 1), j >> 1))) break;
+        if (!(ok = wait(p_full + 8u * t, j))) break;
+        umma_fence_after();
+        if (one) {
+#pragma unroll
+          for (int i = 0; i < S::kTokens / 16; ++i)
+            umma_f16_ts(tmem + (uint32_t)(S::kOCol + t * D), tmem + (uint32_t)(t * S::kTokens + i * 8),
+                        vd + (uint32_t)(((j & 1) * S::kKvTile + i * 2048) >> 4), kIdO, (j | i) != 0);
+          umma_commit(o_done + 8u * t);
+          if (t == tiles - 1) umma_commit(v_empty + 8u * (j & 1));
+        }
+        if (j + 1 < steps) {
+          if (t == 0) {
+            if (!(ok = wait(k_full + 8u * ((j + 1) & 1), (j + 1) >> 1))) break;
+            umma_fence_after();
+          }
+          scores(t, j + 1);  // over P, after the product that reads it
+        }
+      }
+    }
+    if (!ok) {
+      give_up();
+      if (one) umma_commit(drain);
+      mbar_wait_bounded(drain, 0, kWaitNs);
+    }
+  } else if (warp >= kCodeWarp0) {
+    // --------------------------------------------------------------- the codes
+    const int w = warp - kCodeWarp0;
+    const int piece = lane % S::kPieces, sub = lane / S::kPieces;
+    // the order in which a thread writes its four words, and with it the banks
+    const int turn = D == 256 ? piece >> 1 : D == 128 ? (piece >> 1) << 1 : 0;
+    uint32_t vec[S::kPasses];
+    auto look_up = [&](int j) {  // this thread's positions of step j
+#pragma unroll
+      for (int i = 0; i < S::kPasses; ++i) {
+        const int at = begin + j * S::kTokens + (i * 4 + w) * S::kPerWarp + sub;
+        vec[i] = 0xFFFFFFFFu;
+        if (j < steps && at < end) {
+          const int64_t s = slot_of(p.at, b, at);
+          if (s >= 0) vec[i] = (uint32_t)vector_of(p.at, s, kvh);
+          else record_error(&g_kv4_error, BCQ_ERR_PAGE);
+        }
+      }
+    };
+    uint4 codes[S::kPasses];
+    uint32_t az[S::kPasses];
+    auto load = [&](const uint8_t* code, const __half2* param) {
+#pragma unroll
+      for (int i = 0; i < S::kPasses; ++i) {
+        codes[i] = make_uint4(0, 0, 0, 0);
+        az[i] = 0;
+        if (vec[i] != 0xFFFFFFFFu) {
+          codes[i] = *reinterpret_cast<const uint4*>(code + (int64_t)vec[i] * (D / 2) + piece * 16);
+          az[i] = *reinterpret_cast<const uint32_t*>(param + (int64_t)vec[i] * G + (piece >> 1));
+        }
+      }
+    };
+    // codes and params into a tile; for V what is no number becomes zero.  The
+    // mask word of a pass: lanes without a position's page (K), or with such a
+    // group (V)
+    auto store = [&](uint32_t tile, bool is_v, uint32_t* mask, const uint32_t (&at)[S::kPasses], int j) {
+#pragma unroll
+      for (int i = 0; i < S::kPasses; ++i) {
+        const int token = (i * 4 + w) * S::kPerWarp + sub;
+        __half2 f = *reinterpret_cast<const __half2*>(&az[i]);
+        const bool odd = (az[i] & 0x7C00u) == 0x7C00u || (az[i] & 0x7C000000u) == 0x7C000000u;
+        const bool gone = at[i] == 0xFFFFFFFFu && begin + j * S::kTokens + token < end;
+        if (is_v && odd) f = __floats2half2_rn(0.f, 0.f);
+        const uint32_t word = __ballot_sync(0xFFFFFFFFu, is_v ? odd : gone);
+        if (lane == 0) mask[i * 4 + w] = word;
+        uint4 c = codes[i];
+        if (turn & 2) c = make_uint4(c.z, c.w, c.x, c.y);
+        if (turn & 1) c = make_uint4(c.y, c.x, c.w, c.z);
+        const __half2 a = __low2half2(f), z = __high2half2(f);
+        const uint32_t row = tile + (uint32_t)((piece >> 1) * S::kKvBlock) + (uint32_t)token * 128u;
+        const uint32_t cs[4] = {c.x, c.y, c.z, c.w};
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          const uint32_t chunk = (uint32_t)((piece & 1) * 4 + (e ^ turn)) ^ (uint32_t)(token & 7);
+          const uint4 v = word_values(cs[e], a, z);
+          asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(row + (chunk << 4)), "r"(v.x),
+                       "r"(v.y), "r"(v.z), "r"(v.w)
+                       : "memory");
+        }
+      }
+      fence_proxy_async_smem();
+    };
+    bool ok = true;
+    look_up(0);
+    load(p.k, p.k_param);
+    for (int j = 0; j < steps; ++j) {
+      uint32_t now[S::kPasses];
+#pragma unroll
+      for (int i = 0; i < S::kPasses; ++i) now[i] = vec[i];
+      if (j >= 2 && !(ok = wait(k_empty + 8u * (j & 1), (j >> 1) - 1))) break;
+      store(sbase + S::kOffK + (uint32_t)(j & 1) * S::kKvTile, false, masks + (j & 3) * S::kWords, now, j);
+      load(p.v, p.v_param);
+      __syncwarp();
+      if (lane == 0) mbar_arrive_cta(k_full + 8u * (j & 1));
+      look_up(j + 1);
+      if (j >= 2 && !(ok = wait(v_empty + 8u * (j & 1), (j >> 1) - 1))) break;
+      store(sbase + S::kOffV + (uint32_t)(j & 1) * S::kKvTile, true, masks + (4 + (j & 3)) * S::kWords, now, j);
+      load(p.k, p.k_param);
+      __syncwarp();
+      if (lane == 0) mbar_arrive_cta(v_full + 8u * (j & 1));
+    }
+    if (!ok) give_up();
+  } else if (warp < 4 * tiles) {
+    // -------------------------------------------------------------- the softmax
+    const int t = warp >> 2, r = (warp & 3) * 32 + lane;  // tile, row of it
+    const int row = t * 128 + r;
+    const bool live = row < row_n;
+    const int i = live ? (row0 + row) / p.group : 0;
+    const int h = kvh * p.group + (live ? (row0 + row) % p.group : 0);
+    const int64_t token = sp.first_row + i;
+    const int pos = sp.pos0 + i;
+    const int hi = live ? (p.causal ? min(end, pos + 1) : end) : 1 << 30;
+    const int lo = live && p.window > 0 ? max(0, pos - p.window + 1) : 0;
+    const int hi_all = min(end, __reduce_min_sync(0xFFFFFFFFu, hi)), lo_all = __reduce_max_sync(0xFFFFFFFFu, lo);
+    float fs = 0.f, m = -INFINITY, l = 0.f;
+    uint32_t poison = 0;  // groups of the output that a seen position makes NaN
+    if (steps > 0) {
+      const uint16_t* src = p.q + token * p.ld_q + (int64_t)h * p.hd_q;
+      float top = 0.f;
+#pragma unroll 4
+      for (int c = 0; c < D / 8; ++c) {
+        uint4 raw = make_uint4(0, 0, 0, 0);
+        if (live) raw = *reinterpret_cast<const uint4*>(src + c * 8);
+        const uint32_t x[4] = {raw.x, raw.y, raw.z, raw.w};
+#pragma unroll
+        for (int e = 0; e < 8; ++e)
+          top = fmaxf(top, fabsf(bits_to_float<T>((x[e >> 1] >> (16 * (e & 1))) & 0xFFFFu)));
+      }
+      int up = 0;  // 2^14 <= top 2^up < 2^15
+      if (top > 0.f && top < INFINITY) up = min(126, 14 - (int)floorf(log2f(top)));
+      const float sign = p.scale < 0.f ? -1.f : p.scale == 0.f ? 0.f : 1.f;
+      const float mul = ldexpf(sign, up);
+      fs = sign == 0.f ? 1.f : fmaxf(ldexpf(fabsf(p.scale) * 1.4426950408889634f, -up), 1e-37f);
+      const uint32_t to = sbase + (uint32_t)t * S::kQTile + (uint32_t)r * 128u;
+#pragma unroll 4
+      for (int c = 0; c < D / 8; ++c) {
+        uint4 raw = make_uint4(0, 0, 0, 0);
+        if (live) raw = *reinterpret_cast<const uint4*>(src + c * 8);
+        const uint32_t x[4] = {raw.x, raw.y, raw.z, raw.w};
+        float f[8];
+#pragma unroll
+        for (int e = 0; e < 8; ++e) f[e] = bits_to_float<T>((x[e >> 1] >> (16 * (e & 1))) & 0xFFFFu) * mul;
+        const uint32_t at = to + (uint32_t)(c >> 3) * S::kQBlock + (uint32_t)(((c & 7) ^ (r & 7)) << 4);
+        asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(at), "r"(pack_f16(f[0], f[4])),
+                     "r"(pack_f16(f[1], f[5])), "r"(pack_f16(f[2], f[6])), "r"(pack_f16(f[3], f[7]))
+                     : "memory");
+      }
+      fence_proxy_async_smem();
+      __syncwarp();
+      if (lane == 0) mbar_arrive_cta(q_full);
+    }
+    const uint32_t lanes = (uint32_t)((warp & 3) * 32) << 16;
+    const uint32_t ts = tmem + lanes + (uint32_t)(t * S::kTokens), to = tmem + lanes + (uint32_t)(S::kOCol + t * D);
+    // whether position `token` of a step's mask words is marked, for piece q
+    auto marked = [&](const uint32_t* word, int token, int q) {
+      const int at = token / S::kPerWarp;
+      return (word[at] >> (token % S::kPerWarp * S::kPieces + q)) & 1u;
+    };
+    auto any_word = [&](const uint32_t* word) {
+      uint32_t all = 0;
+#pragma unroll
+      for (int i = 0; i < S::kWords; i += 4) {
+        const uint4 x = lds_v4(smem_u32(word + i));
+        all |= x.x | x.y | x.z | x.w;
+      }
+      return all != 0;
+    };
+    auto look_for_nan = [&](int j) {  // V's groups of step j, once its product is done
+      const uint32_t* word = masks + (4 + (j & 3)) * S::kWords;
+      if (!any_word(word)) return;
+      const uint32_t* gone = masks + (j & 3) * S::kWords;
+      for (int k = 0; k < S::kTokens; ++k) {
+        const int at = begin + j * S::kTokens + k;
+        if (at < lo || at >= min(hi, end) || marked(gone, k, 0)) continue;
+        for (int g = 0; g < G; ++g)
+          if (marked(word, k, 2 * g)) poison |= 1u << g;
+      }
+    };
+    bool ok = true;
+    for (int j = 0; j < steps; ++j) {
+      if (!(ok = wait(s_full + 8u * t, j))) break;
+      umma_fence_after();
+      if (j > 0) look_for_nan(j - 1);
+      const int j0 = begin + j * S::kTokens;
+      const uint32_t* gone = masks + (j & 3) * S::kWords;
+      const bool holes = any_word(gone);
+      const bool whole = j0 >= lo_all && j0 + S::kTokens <= hi_all && !holes;
+      auto hide = [&](uint32_t (&s)[32], int c) {
+#pragma unroll
+        for (int k = 0; k < 32; ++k) {
+          const int at = j0 + c + k;
+          if (at < lo || at >= min(hi, end) || (holes && marked(gone, c + k, 0))) s[k] = 0xFF800000u;
+        }
+      };
+      float top = -INFINITY;
+#pragma unroll 1
+      for (int c = 0; c < S::kTokens; c += 32) {
+        uint32_t s[32];
+        tmem_ld32(ts + (uint32_t)c, s);
+        tmem_wait_ld();
+        if (!whole) hide(s, c);
+        float x[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+#pragma unroll
+        for (int k = 0; k < 32; ++k) x[k & 3] = fmaxf(x[k & 3], __uint_as_float(s[k]));
+        top = fmaxf(top, fmaxf(fmaxf(x[0], x[1]), fmaxf(x[2], x[3])));
+      }
+      const float now = top * fs;
+      const bool moved = now > m + 8.f || (m == -INFINITY && now > -INFINITY);
+      if (__any_sync(0xFFFFFFFFu, moved)) {
+        const float f = moved ? (m == -INFINITY ? 0.f : ex2(m - now)) : 1.f;
+        if (j > 0) {
+          if (!(ok = wait(o_done + 8u * t, j - 1))) break;
+          umma_fence_after();
+#pragma unroll 1
+          for (int c = 0; c < D; c += 32) {
+            uint32_t o[32];
+            tmem_ld32(to + (uint32_t)c, o);
+            tmem_wait_ld();
+#pragma unroll
+            for (int k = 0; k < 32; ++k) o[k] = __float_as_uint(__uint_as_float(o[k]) * f);
+            tmem_st32(to + (uint32_t)c, o);
+          }
+        }
+        if (moved) {
+          l *= f;
+          m = now;
+        }
+      }
+      const float base = m == -INFINITY ? 0.f : m;
+      float sum[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll 1
+      for (int c = 0; c < S::kTokens; c += 32) {
+        uint32_t s[32], w[16];
+        tmem_ld32(ts + (uint32_t)c, s);
+        tmem_wait_ld();
+        if (!whole) hide(s, c);
+#pragma unroll
+        for (int k = 0; k < 16; ++k) {
+          const float x = ex2(fmaf(__uint_as_float(s[2 * k]), fs, -base));
+          const float y = ex2(fmaf(__uint_as_float(s[2 * k + 1]), fs, -base));
+          sum[k & 3] += x + y;
+          w[k] = pack_f16(x, y);
+        }
+        tmem_st16(ts + (uint32_t)(c / 2), w);  // over scores that this thread has read
+      }
+      l += (sum[0] + sum[1]) + (sum[2] + sum[3]);
+      tmem_wait_st();
+      umma_fence_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive_cta(p_full + 8u * t);
+    }
+    if (steps > 0 && ok) {
+      ok = wait(o_done + 8u * t, steps - 1);
+      umma_fence_after();
+      if (ok) look_for_nan(steps - 1);
+    }
+    if (!ok) {
+      give_up();
+    } else {
+      // ------------------------------------------------------------ the outputs
+      const bool none = m == -INFINITY && l == 0.f, split = sp.parts > 1;
+      const float inv = none ? 0.f : split ? 4.f : 1.f / l;  // parts are held times 2^kWeightBits
+      const int64_t at = ((int64_t)part * p.T + token) * p.q_heads + h;
+      for (int c = 0; c < D; c += 32) {
+        uint32_t o[32];
+        __syncwarp();
+        if (steps > 0) {
+          tmem_ld32(to + (uint32_t)c, o);
+          tmem_wait_ld();
+        }
+        const bool bad = (poison >> (c / kKvGroup)) & 1u;
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          float y[8];
+#pragma unroll
+          for (int k = 0; k < 8; ++k) {
+            const float x = none ? 0.f : __uint_as_float(o[8 * e + k]) * inv;
+            y[(k >> 1) + 4 * (k & 1)] = bad ? __uint_as_float(0x7FC00000u) : x;
+          }
+          if (!live) continue;
+          if (split) {
+            float4* to4 = reinterpret_cast<float4*>(p.part + at * D + c + 8 * e);
+            to4[0] = make_float4(y[0], y[1], y[2], y[3]);
+            to4[1] = make_float4(y[4], y[5], y[6], y[7]);
+          } else {
+            union {
+              T v[8];
+              uint4 q;
+            } u;
+#pragma unroll
+            for (int k = 0; k < 8; ++k) u.v[k] = from_float<T>(y[k]);
+            *reinterpret_cast<uint4*>(p.out + token * p.ld_o + (int64_t)h * p.hd_o + c + 8 * e) = u.q;
+          }
+        }
+      }
+      if (live && split) {
+        float* ml = p.part + (int64_t)p.splits * p.T * p.q_heads * D + at * 2;
+        ml[0] = m;
+        ml[1] = l * 4.f;
+      } else if (live && p.lse) {
+        p.lse[token * p.q_heads + h] = none ? -INFINITY : (m + log2f(l)) * 0.69314718055994531f;
+      }
+    }
+  }
+  launch_dependents();
+  __syncwarp();
+  umma_fence_before();
+  __syncthreads();
+  if (warp == kMmaWarp) {
+    umma_fence_after();
+    tmem_dealloc(tmem, 512);
+  }
+}
+
+}  // namespace
+}  // namespace bcq
