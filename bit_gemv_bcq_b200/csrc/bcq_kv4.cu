@@ -274,21 +274,31 @@ __global__ void __launch_bounds__(kRowThreads) kv4_read_kernel(const ReadParams 
 // Attention of few rows a key/value head: decode steps, drafts, short chunks.
 //
 // A warp takes 32 positions at a time, the codes as they lie in the cache.  A
-// nibble masked out of a word is the fp16 subnormal c 2^-24 (the high one of a
-// byte c 2^-20), which the tensor core multiplies exactly, so a code becomes
-// an operand by one AND, without a conversion, a scale or an offset: those are
-// applied to the results,
+// byte of two codes, low + 16 high, masked out of a word is the fp16 subnormal
+// (low + 16 high) 2^-24, and its low nibble low 2^-24; the tensor core
+// multiplies both exactly, so codes become operands by one AND or byte permute
+// each, without a conversion, a scale or an offset.  With the two as operands
+//   q_l low + q_h high = (q_l - q_h / 16) low + (q_h / 16) (low + 16 high),
+// the first factor rounded to fp16, and of V's sums over positions the one of
+// the high codes is the difference of the bytes' and the low ones' over 16.
+// Scales and offsets are applied to the results,
 //   q . K_t = sum_g  a_tg (sum_{d in g} q_d c_td) + z_tg (sum_{d in g} q_d)
 //   out_d   = sum_t (p_t a_tg) c_td + sum_t p_t z_tg,
-// a few operations a position instead of one a value.  Both products have the
-// codes as the first operand of mma.m16n8k16 (16 positions, or 16 values of a
-// vector; one 32-bit word of codes fills the four registers) and 8 rows as
-// the second, so 8 rows of a key/value head (the query heads that share it,
-// times the rows of the call) fill an instruction.  Queries are scaled by a
-// power of two to the top of fp16's range; p a is rounded to fp16 (half a step
-// 2^-11 of each weight), with p scaled by 4 so that neither the largest a (8000)
-// overflows nor small ones lose bits before 2^-26; scores, sums and outputs
-// are fp32.
+// a few operations a position instead of one a value; the two sums with the
+// offsets are one more instruction of the tensor core each (the sums of q as
+// two fp16 parts, so to 2^-22).  Both products have the codes as the first
+// operand of mma.m16n8k16 (16 positions, or 16 values of a vector; one 32-bit
+// word of codes fills the four registers) and 8 rows as the second, so 8 rows
+// of a key/value head (the query heads that share it, times the rows of the
+// call) fill an instruction.  Queries are scaled by a power of two to the top
+// of fp16's range.  p and p a are rounded to fp16 (half a step, 2^-11, each);
+// the maximum in use follows a row's own only when that has risen by more than
+// 2^4, and p is held times 1/2, so that p <= 8 and the largest a (8000) does
+// not overflow.  Scores, sums and outputs are fp32.
+//
+// A scale or offset of V that is no number must not reach rows that do not see
+// its position (0 * NaN): where some row does not see all positions such
+// values become zeros, and the rows that see them are told to write NaN.
 //
 // The codes' way: cp.async into a ring of three stages a warp (nobody else
 // reads them, so no barrier but the warp's own), 16-byte pieces placed so that
@@ -366,6 +376,15 @@ __device__ __forceinline__ void mma16816(float (&d)[4], uint32_t a0, uint32_t a1
       : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
       : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
 }
+// The same into a fresh D.
+__device__ __forceinline__ void mma16816_new(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2,
+                                             uint32_t a3, uint32_t b0, uint32_t b1) {
+  asm volatile(
+      "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, "
+      "{%8, %9}, {%10, %10, %10, %10};"
+      : "=f"(d[0]), "=f"(d[1]), "=f"(d[2]), "=f"(d[3])
+      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1), "f"(0.f));
+}
 // Transpose of an 8 x 8 matrix of 16-bit values, two a lane.
 __device__ __forceinline__ uint32_t transpose8x8(uint32_t v) {
   uint32_t d;
@@ -382,14 +401,44 @@ __device__ __forceinline__ float ex2(float x) {
   asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
   return y;
 }
-__device__ __forceinline__ float2 half2_at(uint32_t bits) {
-  return __half22float2(*reinterpret_cast<const __half2*>(&bits));
+__device__ __forceinline__ float half_low(uint32_t bits) { return h2f((uint16_t)bits); }
+__device__ __forceinline__ uint32_t mul_half2(uint32_t x, uint32_t y) {
+  const __half2 r = __hmul2(*reinterpret_cast<const __half2*>(&x), *reinterpret_cast<const __half2*>(&y));
+  return *reinterpret_cast<const uint32_t*>(&r);
+}
+// Halves that are no finite numbers, as zeros.
+__device__ __forceinline__ uint32_t finite_half2(uint32_t x) {
+  if ((x & 0x7C00u) == 0x7C00u) x &= 0xFFFF0000u;
+  if ((x & 0x7C000000u) == 0x7C000000u) x &= 0x0000FFFFu;
+  return x;
+}
+__device__ __forceinline__ bool odd_half2(uint32_t x) {
+  return (x & 0x7C00u) == 0x7C00u || (x & 0x7C000000u) == 0x7C000000u;
+}
+
+template <int N>
+__device__ __forceinline__ void lds_words(uint32_t addr, uint32_t (&w)[N]) {
+  if constexpr (N == 1) {
+    w[0] = lds_u32v(addr);
+  } else if constexpr (N == 2) {
+    const uint2 v = lds_v2u(addr);
+    w[0] = v.x;
+    w[1] = v.y;
+  } else {
+    const uint4 v = lds_v4(addr);
+    w[0] = v.x;
+    w[1] = v.y;
+    w[2] = v.z;
+    w[3] = v.w;
+  }
 }
 
 constexpr int kFewWarps = 4;    // of a CTA
 constexpr int kFewStages = 3;   // of a warp's ring
 constexpr int kFewTokens = 32;  // of a stage
-constexpr float kWeightBits = 2.f;  // p is held times 2^2
+constexpr float kWeightBits = -1.f;   // p is held times 2^-1
+constexpr float kWeightScale = 0.5f;
+constexpr float kLazyBits = 4.f;      // how far a row's maximum may rise over the one in use
 
 template <int D>
 struct FewShape {
@@ -410,7 +459,7 @@ struct FewShape {
 };
 
 template <typename T, int D, int NT>
-__global__ void __launch_bounds__(kFewWarps * 32) kv4_few_kernel(const AttentionParams p) {
+__global__ void __launch_bounds__(kFewWarps * 32, NT == 1 && D <= 128 ? 4 : 2) kv4_few_kernel(const AttentionParams p) {
   using S = FewShape<D>;
   constexpr int G = S::kGroups;
   extern __shared__ __align__(128) unsigned char smem[];
@@ -429,7 +478,8 @@ __global__ void __launch_bounds__(kFewWarps * 32) kv4_few_kernel(const Attention
 
   // ---- queries: lane (r, c) holds row r's values that its codes will meet
   uint32_t qf[NT][G][2][4];
-  float qs[NT][G][2], fs[NT][2];
+  uint32_t qz[NT];  // sums over the groups, as two fp16 parts, over 2^7
+  float fs[NT][2];
   int hi[NT][2], lo[NT][2];
   int hi_all = sp.end, lo_all = sp.begin;
 #pragma unroll
@@ -475,15 +525,36 @@ __global__ void __launch_bounds__(kFewWarps * 32) kv4_few_kernel(const Attention
           x[e] *= mul;
           sum[g] += x[e];
         }
-        // code order in a word: values (0, 4), (1, 5) / 16, (2, 6), (3, 7) / 16
-        qf[nt][g][w][0] = pack_f16(x[0], x[4]);
-        qf[nt][g][w][1] = pack_f16(x[1] * 0.0625f, x[5] * 0.0625f);
-        qf[nt][g][w][2] = pack_f16(x[2], x[6]);
-        qf[nt][g][w][3] = pack_f16(x[3] * 0.0625f, x[7] * 0.0625f);
+        // a word's bytes in the order 0, 2 and 1, 3: for each pair what the low
+        // codes and what the bytes are multiplied with
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+          const float h0 = x[2 * i + 1] * 0.0625f, h1 = x[2 * i + 5] * 0.0625f;
+          qf[nt][g][w][2 * i] = pack_f16(x[2 * i] - h0, x[2 * i + 4] - h1);
+          qf[nt][g][w][2 * i + 1] = pack_f16(h0, h1);
+        }
       }
       sum[g] += __shfl_xor_sync(0xFFFFFFFFu, sum[g], 1);
       sum[g] += __shfl_xor_sync(0xFFFFFFFFu, sum[g], 2);
-      sum[g] *= 0x1p-24f;
+      sum[g] *= 0x1p-7f;
+    }
+    // K index 2c, 2c + 1 of the offsets' instruction: the groups' first parts
+    // in turn, then their second ones
+    {
+      float first[G], second[G];
+#pragma unroll
+      for (int g = 0; g < G; ++g) {
+        first[g] = __half2float(__float2half_rn(sum[g]));
+        second[g] = sum[g] - first[g];
+      }
+      if constexpr (G == 1) qz[nt] = c == 0 ? pack_f16(first[0], second[0]) : 0u;
+      if constexpr (G == 2)
+        qz[nt] = c == 0 ? pack_f16(first[0], first[1]) : c == 1 ? pack_f16(second[0], second[1]) : 0u;
+      if constexpr (G == 4)
+        qz[nt] = c == 0   ? pack_f16(first[0], first[1])
+                 : c == 1 ? pack_f16(first[2], first[3])
+                 : c == 2 ? pack_f16(second[0], second[1])
+                          : pack_f16(second[2], second[3]);
     }
     const int pos = sp.pos0 + i;
     const int top_pos = live ? (p.causal ? min(sp.len, pos + 1) : sp.len) : 1 << 30;
@@ -492,8 +563,6 @@ __global__ void __launch_bounds__(kFewWarps * 32) kv4_few_kernel(const Attention
 #pragma unroll
     for (int e = 0; e < 2; ++e) {
       const int from = (2 * c + e) * 4;
-#pragma unroll
-      for (int g = 0; g < G; ++g) qs[nt][g][e] = __shfl_sync(0xFFFFFFFFu, sum[g], from);
       fs[nt][e] = __shfl_sync(0xFFFFFFFFu, back, from);
       hi[nt][e] = __shfl_sync(0xFFFFFFFFu, top_pos, from);
       lo[nt][e] = __shfl_sync(0xFFFFFFFFu, low_pos, from);
@@ -517,11 +586,28 @@ __global__ void __launch_bounds__(kFewWarps * 32) kv4_few_kernel(const Attention
       else record_error(&g_kv4_error, BCQ_ERR_PAGE);
     }
   };
+  // this lane's pieces of 16 positions, from and to (V's rows in the order 0, 2,
+  // 4, 6, 1, 3, 5, 7, and so the next 8); of the params, K's or V's
+  uint32_t k_to[S::kPieces / 2], v_to[S::kPieces / 2];
+#pragma unroll
+  for (int i = 0; i < S::kPieces / 2; ++i) {
+    const int id = i * 32 + lane, row = id / S::kPieces, piece = id % S::kPieces;
+    k_to[i] = S::place(row, piece);
+    v_to[i] = S::kCodes + S::place((row & 8) | ((row & 1) << 2) | ((row >> 1) & 3), piece);
+  }
+  const bool is_vp = lane >= 4 * G;
+  const uint32_t p_to = 2 * S::kCodes + (is_vp ? S::kParam : 0u) + (uint32_t)(lane & (4 * G - 1)) * 16u;
+  const uint8_t* k_from = p.k + lane * 16;
+  const uint8_t* v_from = p.v + lane * 16;
+  const uint8_t* p_from =
+      reinterpret_cast<const uint8_t*>(is_vp ? p.v_param : p.k_param) + (lane & (4 * G - 1)) * 16;
+  int fill = 0;      // the ring's next stage
   uint32_t bad = 0;  // two bits a stage of the ring: halves that have no page
   auto fetch = [&](int s) {
     if (s < mine) {
       if ((s & 15) == 0) look_up(s);
-      const int slot = s % kFewStages;
+      const int slot = fill;
+      fill = fill + 1 == kFewStages ? 0 : fill + 1;
       const uint32_t to = ring + (uint32_t)slot * S::kStage;
       bad &= ~(3u << (2 * slot));
 #pragma unroll
@@ -531,90 +617,102 @@ __global__ void __launch_bounds__(kFewWarps * 32) kv4_few_kernel(const Attention
           bad |= 1u << (2 * slot + half);
           continue;
         }
-        const uint8_t* k = p.k + (int64_t)vec * S::kRow;
-        const uint8_t* v = p.v + (int64_t)vec * S::kRow;
+        const uint8_t* k = k_from + (uint64_t)vec * S::kRow;
+        const uint8_t* v = v_from + (uint64_t)vec * S::kRow;
         const uint32_t at = to + (uint32_t)half * S::kHalf;
 #pragma unroll
         for (int i = 0; i < S::kPieces / 2; ++i) {
-          const int id = i * 32 + lane, row = id / S::kPieces, piece = id % S::kPieces;
-          // V's rows in the order 0, 2, 4, 6, 1, 3, 5, 7 (and so the next 8)
-          const int vrow = (row & 8) | ((row & 1) << 2) | ((row >> 1) & 3);
-          cp_async16(at + S::place(row, piece), k + id * 16);
-          cp_async16(at + S::kCodes + S::place(vrow, piece), v + id * 16);
+          cp_async16(at + k_to[i], k + i * 512);
+          cp_async16(at + v_to[i], v + i * 512);
         }
         if (lane < 8 * G) {
-          const int kv = lane >= 4 * G, piece = lane & (4 * G - 1);
-          const __half2* src = (kv ? p.v_param : p.k_param) + (int64_t)vec * G;
-          cp_async16(at + 2 * S::kCodes + (uint32_t)kv * S::kParam + piece * 16,
-                     reinterpret_cast<const uint8_t*>(src) + piece * 16);
+          cp_async16(at + p_to, p_from + (uint64_t)vec * (G * 4));
         }
       }
     }
     cp_async_commit();
   };
 
-  float o[NT][G][4][4] = {}, zo[NT][G][2] = {}, m[NT][2], l[NT][2] = {};
+  // where this lane's pieces lie in 16 positions: K's words 2c and 2c + 1 of
+  // position r, V's word r of position 2c, K's params of position r and V's of
+  // position 2c.  The others' places differ by whole rows (S::place repeats
+  // every four).
+  uint32_t k_at[G], v_at[G];
+#pragma unroll
+  for (int g = 0; g < G; ++g) {
+    k_at[g] = S::place(r, 2 * g + (c >> 1)) + (uint32_t)(c & 1) * 8u;
+    v_at[g] = S::kCodes + S::place(c, 2 * g + (r >> 2)) + (uint32_t)(r & 3) * 4u;
+  }
+  const uint32_t kp_at = 2 * S::kCodes + (uint32_t)(r * G * 4);
+  const uint32_t vp_at = 2 * S::kCodes + S::kParam + (uint32_t)(2 * c * G * 4);
+
+  // nb: what is added to a score for p's exponent, kWeightBits - m
+  float o[NT][G][4][4] = {}, zo[NT][4] = {}, m[NT][2], nb[NT][2] = {}, l[NT][2] = {};
+  uint32_t poison = 0;  // bit (nt * 2 + e) * G + g: that row's group is NaN
 #pragma unroll
   for (int nt = 0; nt < NT; ++nt) m[nt][0] = m[nt][1] = -INFINITY;
-  for (int s = 0; s < kFewStages - 1; ++s) fetch(s);
-  for (int s = 0; s < mine; ++s) {
-    cp_async_wait<kFewStages - 2>();
-    __syncwarp();
-    fetch(s + kFewStages - 1);
-    const int slot = s % kFewStages;
-    const uint32_t at0 = ring + (uint32_t)slot * S::kStage;
-    const int j0 = begin + (s * kFewWarps + warp) * kFewTokens;
 
+  // One stage: 32 positions from j0.  WHOLE: every row sees all of them.
+  auto stage = [&](auto whole_type, uint32_t at0, int j0, uint32_t gone) {
+    constexpr bool WHOLE = decltype(whole_type)::value;
     // scores u[..]: positions r and r + 8 of each half, rows 2c and 2c + 1
     float u[2][NT][4];
 #pragma unroll
     for (int half = 0; half < 2; ++half) {
       const uint32_t at = at0 + (uint32_t)half * S::kHalf;
-      float acc[NT][G][4] = {};
+      float acc[NT][G][4];
 #pragma unroll
       for (int g = 0; g < G; ++g) {
         // words 2c and 2c + 1 of the group, of positions r and r + 8
-        const uint32_t in = (uint32_t)(c & 1) * 8u;
-        const uint2 wa = lds_v2u(at + S::place(r, 2 * g + (c >> 1)) + in);
-        const uint2 wb = lds_v2u(at + S::place(r + 8, 2 * g + (c >> 1)) + in);
+        const uint2 wa = lds_v2u(at + k_at[g]);
+        const uint2 wb = lds_v2u(at + k_at[g] + 8 * S::kRow);
 #pragma unroll
         for (int w = 0; w < 2; ++w) {
           const uint32_t x = w ? wa.y : wa.x, y = w ? wb.y : wb.x;
+          const uint32_t x0 = x & 0x00FF00FFu, y0 = y & 0x00FF00FFu;            // bytes 0 and 2
+          const uint32_t x1 = prmt(x, 0u, 0x4341), y1 = prmt(y, 0u, 0x4341);    // bytes 1 and 3
 #pragma unroll
-          for (int nt = 0; nt < NT; ++nt)
-            mma16816(acc[nt][g], x & 0x000F000Fu, y & 0x000F000Fu, x & 0x00F000F0u, y & 0x00F000F0u,
-                     qf[nt][g][w][0], qf[nt][g][w][1]);
-          const uint32_t x2 = x >> 8, y2 = y >> 8;
-#pragma unroll
-          for (int nt = 0; nt < NT; ++nt)
-            mma16816(acc[nt][g], x2 & 0x000F000Fu, y2 & 0x000F000Fu, x2 & 0x00F000F0u,
-                     y2 & 0x00F000F0u, qf[nt][g][w][2], qf[nt][g][w][3]);
+          for (int nt = 0; nt < NT; ++nt) {
+            if (w == 0)
+              mma16816_new(acc[nt][g], x & 0x000F000Fu, y & 0x000F000Fu, x0, y0, qf[nt][g][w][0],
+                           qf[nt][g][w][1]);
+            else
+              mma16816(acc[nt][g], x & 0x000F000Fu, y & 0x000F000Fu, x0, y0, qf[nt][g][w][0],
+                       qf[nt][g][w][1]);
+            mma16816(acc[nt][g], x1 & 0x000F000Fu, y1 & 0x000F000Fu, x1, y1, qf[nt][g][w][2],
+                     qf[nt][g][w][3]);
+          }
         }
       }
-      const uint32_t pa = at + 2 * S::kCodes + (uint32_t)(r * G * 4);
+      // (a, z) of the groups, of positions r and r + 8
+      uint32_t az[2][G];
 #pragma unroll
-      for (int nt = 0; nt < NT; ++nt)
+      for (int e = 0; e < 2; ++e) lds_words<G>(at + kp_at + (uint32_t)(8 * e * G * 4), az[e]);
+      // the offsets, two groups a lane
+      uint32_t z2[2];
 #pragma unroll
-        for (int e = 0; e < 4; ++e) u[half][nt][e] = 0.f;
+      for (int e = 0; e < 2; ++e) {
+        if constexpr (G == 1) z2[e] = prmt(az[e][0], az[e][0], 0x3232);
+        if constexpr (G == 2) z2[e] = prmt(az[e][0], az[e][1], 0x7632);
+        if constexpr (G == 4)
+          z2[e] = (c & 1) ? prmt(az[e][2], az[e][3], 0x7632) : prmt(az[e][0], az[e][1], 0x7632);
+      }
 #pragma unroll
-      for (int g = 0; g < G; ++g)
+      for (int nt = 0; nt < NT; ++nt) {
+        float t[4];
+        mma16816_new(t, z2[0], z2[1], 0u, 0u, qz[nt], 0u);
 #pragma unroll
-        for (int e8 = 0; e8 < 2; ++e8) {
-          const float2 az = half2_at(lds_u32v(pa + (uint32_t)(e8 * 8 * G * 4 + g * 4)));
+        for (int e = 0; e < 4; ++e) {
+          float x = t[e] * 0x1p-17f;
 #pragma unroll
-          for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-            for (int e = 0; e < 2; ++e)
-              u[half][nt][2 * e8 + e] = fmaf(az.x, acc[nt][g][2 * e8 + e],
-                                             fmaf(az.y, qs[nt][g][e], u[half][nt][2 * e8 + e]));
+          for (int g = 0; g < G; ++g) x = fmaf(half_low(az[e >> 1][g]), acc[nt][g][e], x);
+          u[half][nt][e] = x;
         }
+      }
     }
 
-    // masks, where the 32 positions are not seen by all rows
-    const uint32_t gone = (bad >> (2 * slot)) & 3u;
-    const bool whole = j0 >= lo_all && j0 + kFewTokens <= min(hi_all, end) && gone == 0;
-    uint32_t seen = 0xFFFFFFFFu;  // bit half * 8 NT + nt * 4 + e
-    if (!whole) {
+    uint32_t seen = 0xFFFFFFFFu;  // bit half * 4 NT + nt * 4 + e
+    if (!WHOLE) {
       seen = 0;
 #pragma unroll
       for (int half = 0; half < 2; ++half)
@@ -629,37 +727,38 @@ __global__ void __launch_bounds__(kFewWarps * 32) kv4_few_kernel(const Attention
           }
     }
 
-    // running maximum (a factor fs >= 0 makes it the scores')
-    float fix[NT][2];
+    // the maximum in use (a factor fs >= 0 makes u the score)
+    float top[NT][2];
     bool moved = false;
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
       for (int e = 0; e < 2; ++e) {
-        float t = fmaxf(fmaxf(u[0][nt][e], u[0][nt][e + 2]), fmaxf(u[1][nt][e], u[1][nt][e + 2]));
-        t = fmaxf(t, __shfl_xor_sync(0xFFFFFFFFu, t, 4));
-        t = fmaxf(t, __shfl_xor_sync(0xFFFFFFFFu, t, 8));
-        t = fmaxf(t, __shfl_xor_sync(0xFFFFFFFFu, t, 16));
-        const float now = fmaxf(m[nt][e], t * fs[nt][e]);
-        fix[nt][e] = now == -INFINITY ? 1.f : ex2(m[nt][e] - now);
-        moved |= now != m[nt][e];
-        m[nt][e] = now;
+        top[nt][e] = fmaxf(fmaxf(u[0][nt][e], u[0][nt][e + 2]), fmaxf(u[1][nt][e], u[1][nt][e + 2]));
+        moved |= top[nt][e] * fs[nt][e] > m[nt][e] + kLazyBits;
       }
     if (__any_sync(0xFFFFFFFFu, moved)) {
 #pragma unroll
       for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
         for (int e = 0; e < 2; ++e) {
-          l[nt][e] *= fix[nt][e];
+          float t = top[nt][e];
+          t = fmaxf(t, __shfl_xor_sync(0xFFFFFFFFu, t, 4));
+          t = fmaxf(t, __shfl_xor_sync(0xFFFFFFFFu, t, 8));
+          t = fmaxf(t, __shfl_xor_sync(0xFFFFFFFFu, t, 16));
+          const float now = fmaxf(m[nt][e], t * fs[nt][e]);
+          const float fix = now == -INFINITY ? 1.f : ex2(m[nt][e] - now);
+          m[nt][e] = now;
+          nb[nt][e] = now == -INFINITY ? 0.f : kWeightBits - now;
+          l[nt][e] *= fix;
+          zo[nt][e] *= fix;
 #pragma unroll
-          for (int g = 0; g < G; ++g) {
-            zo[nt][g][e] *= fix[nt][e];
+          for (int g = 0; g < G; ++g)
 #pragma unroll
             for (int j = 0; j < 4; ++j) {
-              o[nt][g][j][e] *= fix[nt][e];
-              o[nt][g][j][e + 2] *= fix[nt][e];
+              o[nt][g][j][e] *= fix;
+              o[nt][g][j][e + 2] *= fix;
             }
-          }
         }
     }
 
@@ -667,55 +766,99 @@ __global__ void __launch_bounds__(kFewWarps * 32) kv4_few_kernel(const Attention
 #pragma unroll
     for (int half = 0; half < 2; ++half) {
       const uint32_t at = at0 + (uint32_t)half * S::kHalf;
+      const uint32_t pa = at + 2 * S::kCodes + S::kParam;
+      uint32_t b0[NT], b1[NT];  // p of positions 2c, 2c + 1, and 2c + 8, 2c + 9, of row r
 #pragma unroll
-      for (int nt = 0; nt < NT; ++nt)
+      for (int nt = 0; nt < NT; ++nt) {
+        float w[4];
 #pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          const float base = m[nt][e & 1] == -INFINITY ? 0.f : m[nt][e & 1];
-          const float w = ex2(fmaf(u[half][nt][e], fs[nt][e & 1], kWeightBits - base));
-          u[half][nt][e] = w;
-          l[nt][e & 1] += w;
+        for (int e = 0; e < 4; ++e) w[e] = ex2(fmaf(u[half][nt][e], fs[nt][e & 1], nb[nt][e & 1]));
+        l[nt][0] += w[0] + w[2];
+        l[nt][1] += w[1] + w[3];
+        b0[nt] = transpose8x8(pack_f16(w[0], w[1]));
+        b1[nt] = transpose8x8(pack_f16(w[2], w[3]));
+      }
+      // (a, z) of positions 2c, 2c + 1, 2c + 8, 2c + 9
+      uint32_t az[4][G];
+#pragma unroll
+      for (int k = 0; k < 4; ++k) lds_words<G>(at + vp_at + (uint32_t)(((k & 1) + 8 * (k >> 1)) * G * 4), az[k]);
+      if (!WHOLE) {
+        bool odd = false;
+#pragma unroll
+        for (int k = 0; k < 4; ++k)
+#pragma unroll
+          for (int g = 0; g < G; ++g) {
+            odd |= odd_half2(az[k][g]);
+            az[k][g] = finite_half2(az[k][g]);
+          }
+        if (__any_sync(0xFFFFFFFFu, odd)) {
+#pragma unroll
+          for (int e8 = 0; e8 < 2; ++e8) {
+            uint32_t own[G];
+            lds_words<G>(pa + (uint32_t)((r + 8 * e8) * G * 4), own);
+#pragma unroll
+            for (int g = 0; g < G; ++g)
+#pragma unroll
+              for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+                for (int e = 0; e < 2; ++e)
+                  if (odd_half2(own[g]) && ((seen >> (half * 4 * NT + nt * 4 + 2 * e8 + e)) & 1u))
+                    poison |= 1u << ((nt * 2 + e) * G + g);
+          }
         }
-      const uint32_t pa = at + 2 * S::kCodes + S::kParam + (uint32_t)(r * G * 4);
+      }
+      // row g < G of the offsets' instruction: the group's z
+      uint32_t za = 0, zb = 0;
+#pragma unroll
+      for (int g = 0; g < G; ++g)
+        if (r == g) {
+          za = prmt(az[0][g], az[1][g], 0x7632);
+          zb = prmt(az[2][g], az[3][g], 0x7632);
+        }
+#pragma unroll
+      for (int nt = 0; nt < NT; ++nt) mma16816(zo[nt], za, 0u, zb, 0u, b0[nt], b1[nt]);
 #pragma unroll
       for (int g = 0; g < G; ++g) {
-        const float2 az0 = half2_at(lds_u32v(pa + (uint32_t)(g * 4)));
-        const float2 az1 = half2_at(lds_u32v(pa + (uint32_t)(8 * G * 4 + g * 4)));
-        uint32_t b0[NT], b1[NT];
+        const uint32_t a01 = prmt(az[0][g], az[1][g], 0x5410), a23 = prmt(az[2][g], az[3][g], 0x5410);
+        // word r of the group, of positions 2c, 2c + 1, 2c + 8, 2c + 9
+        const uint32_t va = at + v_at[g];
+        const uint32_t v0 = lds_u32v(va), v1 = lds_u32v(va + 4 * S::kRow);
+        const uint32_t v2 = lds_u32v(va + 8 * S::kRow), v3 = lds_u32v(va + 12 * S::kRow);
+        uint32_t p0[NT], p1[NT];
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt) {
-          float w[4], z[4];
-#pragma unroll
-          for (int e = 0; e < 4; ++e) {
-            w[e] = u[half][nt][e] * (e < 2 ? az0.x : az1.x);
-            z[e] = u[half][nt][e] * (e < 2 ? az0.y : az1.y);
-            // what a mask hides may be no number
-            if (!whole && !((seen >> (half * 4 * NT + nt * 4 + e)) & 1u)) w[e] = z[e] = 0.f;
-          }
-          zo[nt][g][0] += z[0] + z[2];
-          zo[nt][g][1] += z[1] + z[3];
-          b0[nt] = transpose8x8(pack_f16(w[0], w[1]));
-          b1[nt] = transpose8x8(pack_f16(w[2], w[3]));
+          p0[nt] = mul_half2(b0[nt], a01);
+          p1[nt] = mul_half2(b1[nt], a23);
         }
-        // word r of the group, of positions 2c, 2c + 1, 2c + 8, 2c + 9
-        const uint32_t in = (uint32_t)(r & 3) * 4u;
-        const int piece = 2 * g + (r >> 2);
-        const uint32_t va = at + S::kCodes;
-        const uint32_t v0 = lds_u32v(va + S::place(c, piece) + in);
-        const uint32_t v1 = lds_u32v(va + S::place(c + 4, piece) + in);
-        const uint32_t v2 = lds_u32v(va + S::place(c + 8, piece) + in);
-        const uint32_t v3 = lds_u32v(va + S::place(c + 12, piece) + in);
 #pragma unroll
-        for (int j = 0; j < 4; ++j) {  // byte j: values 8r + 2j and 8r + 2j + 1
-          const uint32_t x = prmt(v0, v1, (uint32_t)(j | (4 + j) << 8));
-          const uint32_t y = prmt(v2, v3, (uint32_t)(j | (4 + j) << 8));
+        for (int j = 0; j < 4; j += 2) {  // byte j: values 8r + 2j and 8r + 2j + 1
+          const uint32_t x = prmt(v0, v1, j == 0 ? 0x5410 : 0x7632);  // bytes j, j + 1 of each
+          const uint32_t y = prmt(v2, v3, j == 0 ? 0x5410 : 0x7632);
+          const uint32_t x0 = x & 0x00FF00FFu, y0 = y & 0x00FF00FFu;
+          const uint32_t x1 = prmt(x, 0u, 0x4341), y1 = prmt(y, 0u, 0x4341);
 #pragma unroll
-          for (int nt = 0; nt < NT; ++nt)
-            mma16816(o[nt][g][j], x & 0x000F000Fu, x & 0x00F000F0u, y & 0x000F000Fu, y & 0x00F000F0u,
-                     b0[nt], b1[nt]);
+          for (int nt = 0; nt < NT; ++nt) {
+            mma16816(o[nt][g][j], x & 0x000F000Fu, x0, y & 0x000F000Fu, y0, p0[nt], p1[nt]);
+            mma16816(o[nt][g][j + 1], x1 & 0x000F000Fu, x1, y1 & 0x000F000Fu, y1, p0[nt], p1[nt]);
+          }
         }
       }
     }
+  };
+
+  for (int s = 0; s < kFewStages - 1; ++s) fetch(s);
+  for (int s = 0, slot = 0; s < mine; ++s) {
+    cp_async_wait<kFewStages - 2>();
+    __syncwarp();
+    fetch(s + kFewStages - 1);
+    const uint32_t at0 = ring + (uint32_t)slot * S::kStage;
+    const int j0 = begin + (s * kFewWarps + warp) * kFewTokens;
+    const uint32_t gone = (bad >> (2 * slot)) & 3u;
+    if (j0 >= lo_all && j0 + kFewTokens <= min(hi_all, end) && gone == 0)
+      stage(std::true_type(), at0, j0, 0u);
+    else
+      stage(std::false_type(), at0, j0, gone);
+    if (++slot == kFewStages) slot = 0;
   }
   launch_dependents();  // the joining kernel may be set up
   cp_async_wait<0>();
@@ -732,8 +875,13 @@ __global__ void __launch_bounds__(kFewWarps * 32) kv4_few_kernel(const Attention
 #pragma unroll
       for (int step = 4; step < 32; step *= 2) {
         l[nt][e] += __shfl_xor_sync(0xFFFFFFFFu, l[nt][e], step);
+        poison |= __shfl_xor_sync(0xFFFFFFFFu, poison, step);
+      }
+      float z[G];  // the offsets' sum of group g lies with the lanes of r = g
 #pragma unroll
-        for (int g = 0; g < G; ++g) zo[nt][g][e] += __shfl_xor_sync(0xFFFFFFFFu, zo[nt][g][e], step);
+      for (int g = 0; g < G; ++g) {
+        z[g] = __shfl_sync(0xFFFFFFFFu, zo[nt][e], g * 4 + c);
+        if ((poison >> ((nt * 2 + e) * G + g)) & 1u) z[g] = __uint_as_float(0x7FC00000u);
       }
       const int row = warp * kRows + nt * 8 + 2 * c + e;
       if (r == 0) {
@@ -745,8 +893,8 @@ __global__ void __launch_bounds__(kFewWarps * 32) kv4_few_kernel(const Attention
 #pragma unroll
         for (int j = 0; j < 4; ++j)
           *reinterpret_cast<float2*>(so + row * D + g * kKvGroup + 8 * r + 2 * j) =
-              make_float2(fmaf(o[nt][g][j][e], 0x1p24f, zo[nt][g][e]),
-                          fmaf(o[nt][g][j][e + 2], 0x1p20f, zo[nt][g][e]));
+              make_float2(fmaf(o[nt][g][j][e], 0x1p24f, z[g]),
+                          fmaf(o[nt][g][j][e + 2] - o[nt][g][j][e], 0x1p20f, z[g]));
     }
   __syncthreads();
   for (int id = threadIdx.x; id < row_n * (D / 4); id += kFewWarps * 32) {
@@ -916,15 +1064,19 @@ struct AttentionPlan {
   int nt, rows, row_blocks, splits, chunk;
 };
 
-// Parts: `room` CTAs run at once; those beyond start as others end, the last of
-// them alone on average for half of one's time.  A CTA costs about as much as
-// `start` positions before and after its positions.
-void plan_parts(AttentionPlan* f, double units, int max_kv, double room, double start) {
+// Parts: `room` CTAs run at once, each worth its positions and `start` more.
+// Of sequences of different lengths three quarters of max_kv are thought to
+// be there; the time is the whole work's share and half a part, or a part.
+// Splitting at all costs `join` positions.
+void plan_parts(AttentionPlan* f, double units, int B, int max_kv, double room, double start,
+                double join) {
   double best = 0;
+  const double mean = B > 1 ? 0.75 * max_kv : max_kv;
   for (int s = 1; s <= 512 && (s == 1 || (int64_t)(s - 1) * 128 < max_kv); s += 1 + s / 8) {
     const int chunk = (int)std::min<int64_t>((((int64_t)max_kv + s - 1) / s + 127) / 128 * 128, 1 << 30);
-    const double waves = units * s / room;
-    const double cost = (waves <= 1 ? 1.0 : waves + 0.5) * (chunk + start) + s;
+    const double one = chunk + start, share = units * (mean + mean / max_kv * s * start) / room;
+    const double cost =
+        (units * s <= room && B == 1 ? one : std::max(one, share + one / 2)) + s + (s > 1 ? join : 0.0);
     if (best == 0 || cost < best) {
       best = cost;
       f->splits = s;
@@ -933,8 +1085,8 @@ void plan_parts(AttentionPlan* f, double units, int max_kv, double room, double 
   }
 }
 
-// The few-row kernel passes over the positions once for every 16 rows, three
-// CTAs an SM; the many-row kernel once for every 256 (128 where D = 256).
+// The few-row kernel passes over the positions once for every 16 rows, four CTAs
+// an SM (two where rows or values are many); the many-row kernel once for every 256 (128 where D = 256).
 AttentionPlan plan_attention(const bcq_kv4* c, int q_heads, int B, int max_q, int max_kv) {
   AttentionPlan f;
   const int64_t rows = (int64_t)max_q * (q_heads / c->heads);
@@ -943,8 +1095,8 @@ AttentionPlan plan_attention(const bcq_kv4* c, int q_heads, int B, int max_q, in
   f.rows = !many ? 8 * f.nt : c->head_dim == 256 ? 128 : 256;
   f.row_blocks = (int)std::min<int64_t>((rows + f.rows - 1) / f.rows, INT32_MAX);
   const double units = (double)f.row_blocks * c->heads * B;
-  if (many) plan_parts(&f, units, max_kv, 148, 512);
-  else plan_parts(&f, units, max_kv, 444, 160);
+  if (many) plan_parts(&f, units, B, max_kv, 148, 1024, 2048);
+  else plan_parts(&f, units, B, max_kv, f.nt == 1 && c->head_dim <= 128 ? 592 : 296, 160, 128);
   return f;
 }
 

@@ -448,7 +448,7 @@ __global__ void __launch_bounds__(ManyShape<D>::kThreads, 1) kv4_many_kernel(con
     } else {
       // ------------------------------------------------------------ the outputs
       const bool none = m == -INFINITY && l == 0.f, split = sp.parts > 1;
-      const float inv = none ? 0.f : split ? 4.f : 1.f / l;  // parts are held times 2^kWeightBits
+      const float inv = none ? 0.f : split ? kWeightScale : 1.f / l;
       const int64_t at = ((int64_t)part * p.T + token) * p.q_heads + h;
       for (int c = 0; c < D; c += 32) {
         uint32_t o[32];
@@ -485,7 +485,7 @@ __global__ void __launch_bounds__(ManyShape<D>::kThreads, 1) kv4_many_kernel(con
       if (live && split) {
         float* ml = p.part + (int64_t)p.splits * p.T * p.q_heads * D + at * 2;
         ml[0] = m;
-        ml[1] = l * 4.f;
+        ml[1] = l * kWeightScale;
       } else if (live && p.lse) {
         p.lse[token * p.q_heads + h] = none ? -INFINITY : (m + log2f(l)) * 0.69314718055994531f;
       }
