@@ -70,17 +70,17 @@ __device__ __forceinline__ int2 rows_of(const Places& p, int b) {
   return p.cu ? make_int2(p.cu[b], p.cu[b + 1] - p.cu[b]) : make_int2(b, 1);
 }
 
-// The slot (page * page_size + offset) of position j of sequence b, or -1.
-__device__ __forceinline__ int64_t slot_of(const Places& p, int b, int j) {
-  if (j < 0 || j / p.page_size >= p.table_width) return -1;
-  const int page = p.table[(int64_t)b * p.table_width + j / p.page_size];
+// The vector of position j of sequence b, head h, as an index into [pages]
+// [heads][page_size]; -1 where the cache has none.  (A cache has fewer than
+// 2^32 vectors: one takes 72 bytes or more.)
+__device__ __forceinline__ int64_t vector_at(const Places& p, int b, int j, int h) {
+  if (j < 0) return -1;
+  const int entry = j / p.page_size;
+  if (entry >= p.table_width) return -1;
+  const int page = p.table[(int64_t)b * p.table_width + entry];
   if (page < 0 || page >= p.pages) return -1;
-  return (int64_t)page * p.page_size + j % p.page_size;
-}
-
-// The vector (token slot, head) as an index into [pages][heads][page_size].
-__device__ __forceinline__ int64_t vector_of(const Places& p, int64_t slot, int h) {
-  return (slot / p.page_size * p.heads + h) * p.page_size + slot % p.page_size;
+  return (int64_t)((uint64_t)((uint32_t)page * (uint32_t)p.heads + (uint32_t)h) * (uint32_t)p.page_size) +
+         (j - entry * p.page_size);
 }
 
 // --------------------------------------------------- rows in, rows out
@@ -114,8 +114,7 @@ __device__ __forceinline__ void locate_rows(const Places& p, int t0, int T, int6
     const int b = p.cu ? count[tid] : t;
     if (t < T && b < p.B && (!p.cu || t >= p.cu[0])) {
       const int2 rows = rows_of(p, b);
-      const int64_t slot = slot_of(p, b, p.kv_len[b] - rows.y + (t - rows.x));
-      at = slot < 0 ? -1 : vector_of(p, slot, 0);
+      at = vector_at(p, b, p.kv_len[b] - rows.y + (t - rows.x), 0);
     }
     if (at == -1) record_error(&g_kv4_error, BCQ_ERR_PAGE);
     place[tid] = at;
@@ -476,6 +475,70 @@ __global__ void __launch_bounds__(kFewWarps * 32, NT == 1 && D <= 128 ? 4 : 2) k
   const int row0 = block * p.rows;                       // of the key/value head's rows
   const int row_n = min(p.rows, sp.rows * p.group - row0);
 
+  // ---- the positions
+  const int begin = sp.begin + part * sp.chunk, end = min(sp.end, begin + sp.chunk);
+  const int stages = (end - begin + kFewTokens - 1) / kFewTokens;
+  const int mine = stages > warp ? (stages - warp + kFewWarps - 1) / kFewWarps : 0;
+  const uint32_t ring = smem_u32(smem) + (uint32_t)warp * S::kRing;
+  uint32_t vecs = 0xFFFFFFFFu;  // lane l: first vector of half l & 1 of stage (l >> 1) of the next 16
+  auto look_up = [&](int s) {   // page table entries of stages s .. s + 15
+    const int j = begin + ((s + (lane >> 1)) * kFewWarps + warp) * kFewTokens + (lane & 1) * 16;
+    vecs = 0xFFFFFFFFu;
+    if (j < end) {
+      const int64_t vec = vector_at(p.at, b, j, kvh);
+      if (vec >= 0) vecs = (uint32_t)vec;
+      else record_error(&g_kv4_error, BCQ_ERR_PAGE);
+    }
+  };
+  // this lane's pieces of 16 positions, from and to (V's rows in the order 0, 2,
+  // 4, 6, 1, 3, 5, 7, and so the next 8); of the params, K's or V's
+  uint32_t k_to[S::kPieces / 2], v_to[S::kPieces / 2];
+#pragma unroll
+  for (int i = 0; i < S::kPieces / 2; ++i) {
+    const int id = i * 32 + lane, row = id / S::kPieces, piece = id % S::kPieces;
+    k_to[i] = S::place(row, piece);
+    v_to[i] = S::kCodes + S::place((row & 8) | ((row & 1) << 2) | ((row >> 1) & 3), piece);
+  }
+  const bool is_vp = lane >= 4 * G;
+  const uint32_t p_to = 2 * S::kCodes + (is_vp ? S::kParam : 0u) + (uint32_t)(lane & (4 * G - 1)) * 16u;
+  const uint8_t* k_from = p.k + lane * 16;
+  const uint8_t* v_from = p.v + lane * 16;
+  const uint8_t* p_from =
+      reinterpret_cast<const uint8_t*>(is_vp ? p.v_param : p.k_param) + (lane & (4 * G - 1)) * 16;
+  int fill = 0;      // the ring's next stage
+  uint32_t bad = 0;  // two bits a stage of the ring: halves that have no page
+  auto fetch = [&](int s) {
+    if (s < mine) {
+      if ((s & 15) == 0) look_up(s);
+      const int slot = fill;
+      fill = fill + 1 == kFewStages ? 0 : fill + 1;
+      const uint32_t to = ring + (uint32_t)slot * S::kStage;
+      bad &= ~(3u << (2 * slot));
+#pragma unroll
+      for (int half = 0; half < 2; ++half) {
+        const uint32_t vec = __shfl_sync(0xFFFFFFFFu, vecs, 2 * (s & 15) + half);
+        if (vec == 0xFFFFFFFFu) {
+          bad |= 1u << (2 * slot + half);
+          continue;
+        }
+        const uint8_t* k = k_from + (uint64_t)vec * S::kRow;
+        const uint8_t* v = v_from + (uint64_t)vec * S::kRow;
+        const uint32_t at = to + (uint32_t)half * S::kHalf;
+#pragma unroll
+        for (int i = 0; i < S::kPieces / 2; ++i) {
+          cp_async16(at + k_to[i], k + i * 512);
+          cp_async16(at + v_to[i], v + i * 512);
+        }
+        if (lane < 8 * G) {
+          cp_async16(at + p_to, p_from + (uint64_t)vec * (G * 4));
+        }
+      }
+    }
+    cp_async_commit();
+  };
+  // the first stages are on their way while the queries are made ready
+  for (int s = 0; s < kFewStages - 1; ++s) fetch(s);
+
   // ---- queries: lane (r, c) holds row r's values that its codes will meet
   uint32_t qf[NT][G][2][4];
   uint32_t qz[NT];  // sums over the groups, as two fp16 parts, over 2^7
@@ -570,68 +633,6 @@ __global__ void __launch_bounds__(kFewWarps * 32, NT == 1 && D <= 128 ? 4 : 2) k
     hi_all = min(hi_all, (int)__reduce_min_sync(0xFFFFFFFFu, top_pos));
     lo_all = max(lo_all, (int)__reduce_max_sync(0xFFFFFFFFu, low_pos));
   }
-
-  // ---- the positions
-  const int begin = sp.begin + part * sp.chunk, end = min(sp.end, begin + sp.chunk);
-  const int stages = (end - begin + kFewTokens - 1) / kFewTokens;
-  const int mine = stages > warp ? (stages - warp + kFewWarps - 1) / kFewWarps : 0;
-  const uint32_t ring = smem_u32(smem) + (uint32_t)warp * S::kRing;
-  uint32_t vecs = 0xFFFFFFFFu;  // lane l: first vector of half l & 1 of stage (l >> 1) of the next 16
-  auto look_up = [&](int s) {   // page table entries of stages s .. s + 15
-    const int j = begin + ((s + (lane >> 1)) * kFewWarps + warp) * kFewTokens + (lane & 1) * 16;
-    vecs = 0xFFFFFFFFu;
-    if (j < end) {
-      const int64_t slot = slot_of(p.at, b, j);
-      if (slot >= 0) vecs = (uint32_t)vector_of(p.at, slot, kvh);
-      else record_error(&g_kv4_error, BCQ_ERR_PAGE);
-    }
-  };
-  // this lane's pieces of 16 positions, from and to (V's rows in the order 0, 2,
-  // 4, 6, 1, 3, 5, 7, and so the next 8); of the params, K's or V's
-  uint32_t k_to[S::kPieces / 2], v_to[S::kPieces / 2];
-#pragma unroll
-  for (int i = 0; i < S::kPieces / 2; ++i) {
-    const int id = i * 32 + lane, row = id / S::kPieces, piece = id % S::kPieces;
-    k_to[i] = S::place(row, piece);
-    v_to[i] = S::kCodes + S::place((row & 8) | ((row & 1) << 2) | ((row >> 1) & 3), piece);
-  }
-  const bool is_vp = lane >= 4 * G;
-  const uint32_t p_to = 2 * S::kCodes + (is_vp ? S::kParam : 0u) + (uint32_t)(lane & (4 * G - 1)) * 16u;
-  const uint8_t* k_from = p.k + lane * 16;
-  const uint8_t* v_from = p.v + lane * 16;
-  const uint8_t* p_from =
-      reinterpret_cast<const uint8_t*>(is_vp ? p.v_param : p.k_param) + (lane & (4 * G - 1)) * 16;
-  int fill = 0;      // the ring's next stage
-  uint32_t bad = 0;  // two bits a stage of the ring: halves that have no page
-  auto fetch = [&](int s) {
-    if (s < mine) {
-      if ((s & 15) == 0) look_up(s);
-      const int slot = fill;
-      fill = fill + 1 == kFewStages ? 0 : fill + 1;
-      const uint32_t to = ring + (uint32_t)slot * S::kStage;
-      bad &= ~(3u << (2 * slot));
-#pragma unroll
-      for (int half = 0; half < 2; ++half) {
-        const uint32_t vec = __shfl_sync(0xFFFFFFFFu, vecs, 2 * (s & 15) + half);
-        if (vec == 0xFFFFFFFFu) {
-          bad |= 1u << (2 * slot + half);
-          continue;
-        }
-        const uint8_t* k = k_from + (uint64_t)vec * S::kRow;
-        const uint8_t* v = v_from + (uint64_t)vec * S::kRow;
-        const uint32_t at = to + (uint32_t)half * S::kHalf;
-#pragma unroll
-        for (int i = 0; i < S::kPieces / 2; ++i) {
-          cp_async16(at + k_to[i], k + i * 512);
-          cp_async16(at + v_to[i], v + i * 512);
-        }
-        if (lane < 8 * G) {
-          cp_async16(at + p_to, p_from + (uint64_t)vec * (G * 4));
-        }
-      }
-    }
-    cp_async_commit();
-  };
 
   // where this lane's pieces lie in 16 positions: K's words 2c and 2c + 1 of
   // position r, V's word r of position 2c, K's params of position r and V's of
@@ -846,7 +847,6 @@ __global__ void __launch_bounds__(kFewWarps * 32, NT == 1 && D <= 128 ? 4 : 2) k
     }
   };
 
-  for (int s = 0; s < kFewStages - 1; ++s) fetch(s);
   for (int s = 0, slot = 0; s < mine; ++s) {
     cp_async_wait<kFewStages - 2>();
     __syncwarp();
@@ -940,16 +940,21 @@ __global__ void __launch_bounds__(kFewWarps * 32, NT == 1 && D <= 128 ? 4 : 2) k
   }
 }
 
-// Joins the parts of the rows that were split, each in the same order whenever
-// it runs: a CTA a row and head, D / 4 threads a part, 512 / D parts at a time.
+// Joins the parts of the rows that were split, in the same order whenever it
+// runs: a CTA a row and head.  Every part's (max, sum) at once first, which
+// give its weight; then D / 4 threads a part, 512 / D parts at a time, whose
+// loads wait for nothing.
+constexpr int kMostParts = 512;
+
 template <typename T, int D>
 __global__ void __launch_bounds__(128) kv4_join_kernel(const AttentionParams p) {
   constexpr int kLanes = D / 4, kSets = 128 / kLanes;
+  __shared__ float weight[kMostParts];
   __shared__ float4 so[kSets][kLanes];
-  __shared__ float sm[kSets][2];
+  __shared__ float red[2][4];
   const int64_t id = blockIdx.x;
   const int t = (int)(id / p.q_heads), h = (int)(id % p.q_heads);
-  const int set = threadIdx.x / kLanes, lane = threadIdx.x % kLanes;
+  const int tid = threadIdx.x, set = tid / kLanes, lane = tid % kLanes;
   const int b = sequence_of(p.at, t);
   if (b < 0) return;
   const int row = (t - rows_of(p.at, b).x) * p.group + h % p.group;
@@ -959,41 +964,69 @@ __global__ void __launch_bounds__(128) kv4_join_kernel(const AttentionParams p) 
   const int64_t step = (int64_t)p.T * p.q_heads;
   const float* ml = p.part + (int64_t)p.splits * step * D + id * 2;
   const float* src = p.part + id * D + lane * 4;
-  float top = -INFINITY, sum = 0.f;
+  // the first parts' values are asked for before the weights are known
+  constexpr int kAhead = 4;
+  float4 y[kAhead];
+#pragma unroll
+  for (int k = 0; k < kAhead; ++k)
+    if (set + k * kSets < sp.parts) y[k] = *reinterpret_cast<const float4*>(src + (set + k * kSets) * step * D);
+  float2 own[kMostParts / 128];
+  float top = -INFINITY;
+#pragma unroll
+  for (int k = 0; k < kMostParts / 128; ++k) {
+    own[k] = make_float2(-INFINITY, 0.f);
+    if (tid + 128 * k < sp.parts) own[k] = *reinterpret_cast<const float2*>(ml + (tid + 128 * k) * step * 2);
+    top = fmaxf(top, own[k].x);
+  }
+#pragma unroll
+  for (int o = 16; o; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xFFFFFFFFu, top, o));
+  if ((tid & 31) == 0) red[0][tid >> 5] = top;
+  __syncthreads();
+  top = fmaxf(fmaxf(red[0][0], red[0][1]), fmaxf(red[0][2], red[0][3]));
+  float sum = 0.f;
+#pragma unroll
+  for (int k = 0; k < kMostParts / 128; ++k) {
+    const bool nothing = own[k].x == -INFINITY && own[k].y == 0.f;
+    const float w = nothing ? 0.f : ex2(own[k].x - top);
+    if (tid + 128 * k < sp.parts) weight[tid + 128 * k] = w;
+    if (!nothing) sum = fmaf(own[k].y, w, sum);
+  }
+#pragma unroll
+  for (int o = 16; o; o >>= 1) sum += __shfl_xor_sync(0xFFFFFFFFu, sum, o);
+  if ((tid & 31) == 0) red[1][tid >> 5] = sum;
+  __syncthreads();
+  sum = (red[1][0] + red[1][1]) + (red[1][2] + red[1][3]);
   float4 x = make_float4(0.f, 0.f, 0.f, 0.f);
-  auto add = [](float& top, float& sum, float4& x, float m, float l, const float4& y) {
-    if (m == -INFINITY && l == 0.f) return;  // nothing seen
-    const float now = fmaxf(top, m);
-    const float f = sum == 0.f && top == -INFINITY ? 0.f : ex2(top - now), g = ex2(m - now);
-    sum = sum * f + l * g;
-    x.x = x.x * f + y.x * g;
-    x.y = x.y * f + y.y * g;
-    x.z = x.z * f + y.z * g;
-    x.w = x.w * f + y.w * g;
-    top = now;
+  auto add = [&](const float4& v, int i) {
+    const float w = weight[i];
+    x.x = fmaf(v.x, w, x.x);
+    x.y = fmaf(v.y, w, x.y);
+    x.z = fmaf(v.z, w, x.z);
+    x.w = fmaf(v.w, w, x.w);
   };
-#pragma unroll 4
-  for (int i = set; i < sp.parts; i += kSets) {
-    const float2 s = *reinterpret_cast<const float2*>(ml + i * step * 2);
-    const float4 y = *reinterpret_cast<const float4*>(src + i * step * D);
-    add(top, sum, x, s.x, s.y, y);
-  }
+#pragma unroll
+  for (int k = 0; k < kAhead; ++k)
+    if (set + k * kSets < sp.parts) add(y[k], set + k * kSets);
+#pragma unroll 8
+  for (int i = set + kAhead * kSets; i < sp.parts; i += kSets)
+    add(*reinterpret_cast<const float4*>(src + i * step * D), i);
   so[set][lane] = x;
-  if (lane == 0) {
-    sm[set][0] = top;
-    sm[set][1] = sum;
-  }
   __syncthreads();
   if (set != 0) return;
 #pragma unroll
-  for (int i = 1; i < kSets; ++i) add(top, sum, x, sm[i][0], sm[i][1], so[i][lane]);
+  for (int i = 1; i < kSets; ++i) {
+    x.x += so[i][lane].x;
+    x.y += so[i][lane].y;
+    x.z += so[i][lane].z;
+    x.w += so[i][lane].w;
+  }
   const bool none = top == -INFINITY && sum == 0.f;
   const float inv = none ? 0.f : 1.f / sum;
-  const T y[4] = {from_float<T>(x.x * inv), from_float<T>(x.y * inv), from_float<T>(x.z * inv),
-                  from_float<T>(x.w * inv)};
+  const T out[4] = {from_float<T>(x.x * inv), from_float<T>(x.y * inv), from_float<T>(x.z * inv),
+                    from_float<T>(x.w * inv)};
   *reinterpret_cast<uint2*>(p.out + (int64_t)t * p.ld_o + (int64_t)h * p.hd_o + lane * 4) =
-      *reinterpret_cast<const uint2*>(y);
-  if (p.lse && lane == 0)
+      *reinterpret_cast<const uint2*>(out);
+  if (p.lse && tid == 0)
     p.lse[id] = none ? -INFINITY : (top + log2f(sum) - kWeightBits) * 0.69314718055994531f;
 }
 
@@ -1072,7 +1105,7 @@ void plan_parts(AttentionPlan* f, double units, int B, int max_kv, double room, 
                 double join) {
   double best = 0;
   const double mean = B > 1 ? 0.75 * max_kv : max_kv;
-  for (int s = 1; s <= 512 && (s == 1 || (int64_t)(s - 1) * 128 < max_kv); s += 1 + s / 8) {
+  for (int s = 1; s <= kMostParts && (s == 1 || (int64_t)(s - 1) * 128 < max_kv); s += 1 + s / 8) {
     const int chunk = (int)std::min<int64_t>((((int64_t)max_kv + s - 1) / s + 127) / 128 * 128, 1 << 30);
     const double one = chunk + start, share = units * (mean + mean / max_kv * s * start) / room;
     const double cost =

@@ -220,8 +220,8 @@ __global__ void __launch_bounds__(ManyShape<D>::kThreads, 1) kv4_many_kernel(con
         const int at = begin + j * S::kTokens + (i * 4 + w) * S::kPerWarp + sub;
         vec[i] = 0xFFFFFFFFu;
         if (j < steps && at < end) {
-          const int64_t s = slot_of(p.at, b, at);
-          if (s >= 0) vec[i] = (uint32_t)vector_of(p.at, s, kvh);
+          const int64_t found = vector_at(p.at, b, at, kvh);
+          if (found >= 0) vec[i] = (uint32_t)found;
           else record_error(&g_kv4_error, BCQ_ERR_PAGE);
         }
       }
