@@ -432,6 +432,22 @@ __device__ __forceinline__ void lds_words(uint32_t addr, uint32_t (&w)[N]) {
   }
 }
 
+// 2^n for -126 <= n <= 127.
+__device__ __forceinline__ float power_of_two(int n) { return __uint_as_float((uint32_t)(n + 127) << 23); }
+// The power that brings a row whose largest magnitude is `top` to the top of
+// fp16's range: 2^14 <= top 2^n < 2^15 (n at most 126; 0 for no finite top).
+__device__ __forceinline__ int row_power(float top) {
+  if (!(top > 0.f && top < INFINITY)) return 0;
+  return min(126, 141 - (int)(__float_as_uint(top) >> 23));
+}
+// What makes such a row's products scores in powers of two: |scale| log2(e)
+// 2^n.  Never zero, so that a hidden score stays at -infinity.
+__device__ __forceinline__ float score_factor(float scale, int n) {
+  if (scale == 0.f) return 1.f;  // the row itself is taken times zero
+  const int h = n / 2;
+  return fmaxf(fabsf(scale) * 1.4426950408889634f * power_of_two(h) * power_of_two(n - h), 1e-37f);
+}
+
 constexpr int kFewWarps = 4;    // of a CTA
 constexpr int kFewStages = 3;   // of a warp's ring
 constexpr int kFewTokens = 32;  // of a stage
@@ -474,6 +490,22 @@ __global__ void __launch_bounds__(kFewWarps * 32, NT == 1 && D <= 128 ? 4 : 2) k
   if (part >= sp.parts) return;
   const int row0 = block * p.rows;                       // of the key/value head's rows
   const int row_n = min(p.rows, sp.rows * p.group - row0);
+
+  // the queries are asked for before the cache is
+  uint4 raw_q[NT][G][2];
+#pragma unroll
+  for (int nt = 0; nt < NT; ++nt) {
+    const int row = row0 + nt * 8 + r, i = row / p.group;
+    const uint16_t* src = p.q + (int64_t)(sp.first_row + i) * p.ld_q +
+                          (int64_t)(kvh * p.group + row - i * p.group) * p.hd_q;
+#pragma unroll
+    for (int g = 0; g < G; ++g)
+#pragma unroll
+      for (int w = 0; w < 2; ++w) {
+        raw_q[nt][g][w] = make_uint4(0, 0, 0, 0);
+        if (nt * 8 + r < row_n) raw_q[nt][g][w] = ldg_nc_v4(src + g * kKvGroup + (2 * c + w) * 8);
+      }
+  }
 
   // ---- the positions
   const int begin = sp.begin + part * sp.chunk, end = min(sp.end, begin + sp.chunk);
@@ -549,16 +581,14 @@ __global__ void __launch_bounds__(kFewWarps * 32, NT == 1 && D <= 128 ? 4 : 2) k
   for (int nt = 0; nt < NT; ++nt) {
     const int row = nt * 8 + r;
     const bool live = row < row_n;
-    const int i = live ? (row0 + row) / p.group : 0, h = live ? (row0 + row) % p.group : 0;
-    const uint16_t* src = p.q + (int64_t)(sp.first_row + i) * p.ld_q + (int64_t)(kvh * p.group + h) * p.hd_q;
+    const int i = live ? (row0 + row) / p.group : 0;
     float f[G][2][8];
     float top = 0.f;
 #pragma unroll
     for (int g = 0; g < G; ++g)
 #pragma unroll
       for (int w = 0; w < 2; ++w) {
-        uint4 raw = make_uint4(0, 0, 0, 0);
-        if (live) raw = *reinterpret_cast<const uint4*>(src + g * kKvGroup + (2 * c + w) * 8);
+        const uint4 raw = raw_q[nt][g][w];
         const uint32_t words[4] = {raw.x, raw.y, raw.z, raw.w};
 #pragma unroll
         for (int e = 0; e < 8; ++e) {
@@ -568,14 +598,9 @@ __global__ void __launch_bounds__(kFewWarps * 32, NT == 1 && D <= 128 ? 4 : 2) k
       }
     top = fmaxf(top, __shfl_xor_sync(0xFFFFFFFFu, top, 1));
     top = fmaxf(top, __shfl_xor_sync(0xFFFFFFFFu, top, 2));
-    // 2^14 <= top 2^up < 2^15
-    int up = 0;
-    if (top > 0.f && top < INFINITY) up = min(126, 14 - (int)floorf(log2f(top)));
-    const float sign = p.scale < 0.f ? -1.f : p.scale == 0.f ? 0.f : 1.f;
-    const float mul = ldexpf(sign, up);
-    // never zero, so that a hidden score stays at -infinity
-    const float back =
-        sign == 0.f ? 1.f : fmaxf(ldexpf(fabsf(p.scale) * 1.4426950408889634f, 24 - up), 1e-37f);
+    const int up = row_power(top);
+    const float mul = p.scale < 0.f ? -power_of_two(up) : p.scale == 0.f ? 0.f : power_of_two(up);
+    const float back = score_factor(p.scale, 24 - up);
     float sum[G];
 #pragma unroll
     for (int g = 0; g < G; ++g) {
@@ -1097,22 +1122,34 @@ struct AttentionPlan {
   int nt, rows, row_blocks, splits, chunk;
 };
 
-// Parts: `room` CTAs run at once, each worth its positions and `start` more.
-// Of sequences of different lengths three quarters of max_kv are thought to
-// be there; the time is the whole work's share and half a part, or a part.
-// Splitting at all costs `join` positions.
-void plan_parts(AttentionPlan* f, double units, int B, int max_kv, double room, double start,
+// How many parts the positions are cut into.  `each` CTAs fit an SM; a CTA
+// costs its positions and `start` more, splitting at all `join` positions.
+// While all run at once the fullest SM decides, and fewer than `each` on it
+// run faster, though not in proportion (measured: 0.4, 0.55, 0.8 and 1 of the
+// time with 1 to 4 of 4).  Beyond that CTAs start as others end: the whole
+// work's share and half a part, or a part.  Of sequences of different lengths
+// three quarters of max_kv are thought to be there.
+void plan_parts(AttentionPlan* f, int64_t units, int B, int max_kv, int each, double start,
                 double join) {
+  static const double kPace[5] = {0, 0.4, 0.55, 0.8, 1.0};
   double best = 0;
-  const double mean = B > 1 ? 0.75 * max_kv : max_kv;
-  for (int s = 1; s <= kMostParts && (s == 1 || (int64_t)(s - 1) * 128 < max_kv); s += 1 + s / 8) {
+  const double mean = B > 1 ? 0.75 * max_kv : max_kv, room = 148.0 * each;
+  for (int s = 1; s <= kMostParts && (s == 1 || (int64_t)(s - 1) * 128 < max_kv); s += s < 80 ? 1 : s / 16) {
     const int chunk = (int)std::min<int64_t>((((int64_t)max_kv + s - 1) / s + 127) / 128 * 128, 1 << 30);
-    const double one = chunk + start, share = units * (mean + mean / max_kv * s * start) / room;
-    const double cost =
-        (units * s <= room && B == 1 ? one : std::max(one, share + one / 2)) + s + (s > 1 ? join : 0.0);
+    const int parts = (max_kv + chunk - 1) / chunk;
+    const int64_t ctas = units * parts;
+    double cost;
+    if (ctas <= (int64_t)room) {
+      const int fullest = (int)((ctas + 147) / 148);
+      cost = chunk * (each == 1 ? 1.0 : kPace[std::min(4, fullest * 4 / each)]) + start;
+    } else {
+      cost = std::max(chunk + start, (double)units * (mean + mean / max_kv * parts * start) / room +
+                                         (chunk + start) / 2);
+    }
+    cost += parts > 1 ? join + parts : 0;
     if (best == 0 || cost < best) {
       best = cost;
-      f->splits = s;
+      f->splits = parts;
       f->chunk = chunk;
     }
   }
@@ -1127,9 +1164,9 @@ AttentionPlan plan_attention(const bcq_kv4* c, int q_heads, int B, int max_q, in
   f.nt = many ? 0 : rows <= 8 || c->head_dim == 256 ? 1 : 2;
   f.rows = !many ? 8 * f.nt : c->head_dim == 256 ? 128 : 256;
   f.row_blocks = (int)std::min<int64_t>((rows + f.rows - 1) / f.rows, INT32_MAX);
-  const double units = (double)f.row_blocks * c->heads * B;
-  if (many) plan_parts(&f, units, B, max_kv, 148, 1024, 2048);
-  else plan_parts(&f, units, B, max_kv, f.nt == 1 && c->head_dim <= 128 ? 592 : 296, 160, 128);
+  const int64_t units = (int64_t)f.row_blocks * c->heads * B;
+  if (many) plan_parts(&f, units, B, max_kv, 1, 1024, 2048);
+  else plan_parts(&f, units, B, max_kv, f.nt == 1 && c->head_dim <= 128 ? 4 : 2, 160, 128);
   return f;
 }
 

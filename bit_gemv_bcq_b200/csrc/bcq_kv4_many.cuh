@@ -315,11 +315,9 @@ __global__ void __launch_bounds__(ManyShape<D>::kThreads, 1) kv4_many_kernel(con
         for (int e = 0; e < 8; ++e)
           top = fmaxf(top, fabsf(bits_to_float<T>((x[e >> 1] >> (16 * (e & 1))) & 0xFFFFu)));
       }
-      int up = 0;  // 2^14 <= top 2^up < 2^15
-      if (top > 0.f && top < INFINITY) up = min(126, 14 - (int)floorf(log2f(top)));
-      const float sign = p.scale < 0.f ? -1.f : p.scale == 0.f ? 0.f : 1.f;
-      const float mul = ldexpf(sign, up);
-      fs = sign == 0.f ? 1.f : fmaxf(ldexpf(fabsf(p.scale) * 1.4426950408889634f, -up), 1e-37f);
+      const int up = row_power(top);
+      const float mul = p.scale < 0.f ? -power_of_two(up) : p.scale == 0.f ? 0.f : power_of_two(up);
+      fs = score_factor(p.scale, -up);
       const uint32_t to = sbase + (uint32_t)t * S::kQTile + (uint32_t)r * 128u;
 #pragma unroll 4
       for (int c = 0; c < D / 8; ++c) {
