@@ -4,14 +4,17 @@
 //
 //   S = Q K^T,  P = exp2(S fs - m),  O += P V  for 128 rows of a key/value head
 // (query heads that share it times rows of the call) a tile, two tiles a CTA
-// (one where D = 256 leaves tensor memory for no more), and 128 (64) positions
-// at a time.  Four warps turn the codes into fp16 operands in shared memory,
-// once for both tiles: c from its bits (1024 + c or 1024 + 16 c, exactly), then
-// a c + z with one rounding to fp16 (half a step, 2^-11).  One warp issues the
-// products; a tile's softmax (four warps, a thread a row) runs while the tensor
-// core works for the other tile.  P replaces S in tensor memory, in fp16 (the
-// second rounding of 2^-11); O stays there, and is scaled only when a row's
-// maximum has risen by more than 2^8 over the one in use, so p stays below 256.
+// (one where D = 256 leaves tensor memory for no more), and 64 positions a
+// step.  Four warps turn the codes into fp16 operands in shared memory, once
+// for both tiles: c from its bits (1024 + c or 1024 + 16 c, exactly), then a c +
+// z with one rounding to fp16 (half a step, 2^-11).  One warp issues the
+// products; four warps a tile do its softmax, a thread a row.  S has two
+// buffers a tile, so that a step's scores are there when the softmax of the
+// one before ends (steps of 128 positions leave tensor memory for one: the
+// softmax then waits for two products a step, 5200 cycles for 128 positions).
+// P replaces S in tensor memory, in fp16 (the second rounding of 2^-11); O
+// stays there, and is scaled only when a row's maximum has risen by more than
+// 2^8 over the one in use, so p stays below 256.
 // Queries are scaled by a power of two a row to the top of fp16's range.
 // Within eight values of a vector both operands have the order 0 4 1 5 2 6 3 7,
 // in which masks yield them; outputs are put right as they are written.
@@ -29,26 +32,59 @@ namespace {
 template <int D>
 struct ManyShape {
   static constexpr int kTiles = D == 256 ? 1 : 2;
-  static constexpr int kTokens = D == 256 ? 64 : 128;        // of a step
+  static constexpr int kTokens = 64;                         // of a step
+  static constexpr int kBufs = D == 256 ? 2 : 3;             // of K's and V's operands, each
   static constexpr int kBlocks = D / 64;                     // 128-byte column blocks of a vector
   static constexpr uint32_t kQBlock = 128 * 128;             // bytes of 64 columns of 128 rows
   static constexpr uint32_t kQTile = kBlocks * kQBlock;
   static constexpr uint32_t kKvBlock = kTokens * 128;
   static constexpr uint32_t kKvTile = kBlocks * kKvBlock;
-  static constexpr uint32_t kOffK = kTiles * kQTile;         // two buffers
-  static constexpr uint32_t kOffV = kOffK + 2 * kKvTile;     // two buffers
-  static constexpr uint32_t kOffBar = kOffV + 2 * kKvTile;
-  // per step (ring of four): words of the positions without a page, and of V's
-  // groups that are no numbers
+  static constexpr uint32_t kOffK = kTiles * kQTile;
+  static constexpr uint32_t kOffV = kOffK + kBufs * kKvTile;
+  static constexpr uint32_t kOffBar = kOffV + kBufs * kKvTile;
+  // a step's mask words: the positions without a page, and V's groups that are
+  // no numbers.  A ring of eight: K's operands of step j + 8 come after the
+  // scores of step j + 8 - kBufs, and so after the softmax of step j + 3.
   static constexpr int kPieces = D / 32;                     // 16-byte pieces of a vector's codes
   static constexpr int kPasses = kTokens * kPieces / 128;    // pieces a thread and step
   static constexpr int kPerWarp = 32 / kPieces;              // positions a warp and pass
   static constexpr int kWords = kPasses * 4;
   static constexpr uint32_t kOffMask = kOffBar + 256;
-  static constexpr uint32_t kSmem = 1024 + kOffMask + 2 * 4 * kWords * 4;
-  static constexpr int kOCol = kTiles * kTokens;             // tensor memory: S tiles, then O tiles
+  static constexpr uint32_t kSmem = 1024 + kOffMask + 2 * 8 * kWords * 4;
+  static constexpr int kOCol = 2 * kTiles * kTokens;         // tensor memory: S buffers, then O tiles
   static constexpr int kThreads = 32 * (4 * kTiles + 4 + 1); // softmax, codes, MMA
 };
+
+// A ring's slot and the round it is in.
+struct RingAt {
+  int slot = 0, round = 0;
+  __device__ __forceinline__ void step(int slots) {
+    if (++slot == slots) {
+      slot = 0;
+      ++round;
+    }
+  }
+};
+
+// Two fp32 values at once.
+__device__ __forceinline__ uint64_t pack_f32x2(float a, float b) {
+  uint64_t d;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(d) : "f"(a), "f"(b));
+  return d;
+}
+__device__ __forceinline__ void unpack_f32x2(uint64_t v, float& a, float& b) {
+  asm("mov.b64 {%0, %1}, %2;" : "=f"(a), "=f"(b) : "l"(v));
+}
+__device__ __forceinline__ uint64_t fma_f32x2(uint64_t a, uint64_t b, uint64_t c) {
+  uint64_t d;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(d) : "l"(a), "l"(b), "l"(c));
+  return d;
+}
+__device__ __forceinline__ uint64_t add_f32x2(uint64_t a, uint64_t b) {
+  uint64_t d;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
+  return d;
+}
 
 // Shared-memory descriptor, 128-byte swizzle: `lead` bytes between 64-element
 // blocks of a contiguous M or N (1 where K is contiguous), `stride` bytes
@@ -119,24 +155,27 @@ __global__ void __launch_bounds__(ManyShape<D>::kThreads, 1) kv4_many_kernel(con
   const int steps = end > begin ? (end - begin + S::kTokens - 1) / S::kTokens : 0;
   const int tiles = row_n > 128 ? 2 : 1;  // of this CTA
 
+  // S, P and their tiles' barriers: [tile][buffer]
   const uint32_t bar = sbase + S::kOffBar;
-  const uint32_t q_full = bar, k_full = bar + 8, k_empty = bar + 24, v_full = bar + 40,
-                 v_empty = bar + 56, s_full = bar + 72, p_full = bar + 88, o_done = bar + 104,
-                 drain = bar + 120, slot = bar + 128;
+  const uint32_t q_full = bar, k_full = bar + 8, k_empty = bar + 32, v_full = bar + 56,
+                 v_empty = bar + 80, s_full = bar + 104, p_full = bar + 136, o_done = bar + 168,
+                 drain = bar + 184, slot = bar + 192;
   constexpr int kCodeWarp0 = 4 * S::kTiles, kMmaWarp = kCodeWarp0 + 4;
   if (warp == kMmaWarp) {
     if (lane == 0) {
       mbar_init(q_full, (uint32_t)(4 * tiles));
       mbar_init(drain, 1);
-      for (int i = 0; i < 2; ++i) {
+      for (int i = 0; i < S::kBufs; ++i) {
         mbar_init(k_full + 8 * i, 4);
         mbar_init(k_empty + 8 * i, 1);
         mbar_init(v_full + 8 * i, 4);
         mbar_init(v_empty + 8 * i, 1);
+      }
+      for (int i = 0; i < 4; ++i) {
         mbar_init(s_full + 8 * i, 1);
         mbar_init(p_full + 8 * i, 4);
-        mbar_init(o_done + 8 * i, 1);
       }
+      for (int i = 0; i < 2; ++i) mbar_init(o_done + 8 * i, 1);
       fence_mbar_init();
     }
     __syncwarp();
@@ -163,44 +202,44 @@ __global__ void __launch_bounds__(ManyShape<D>::kThreads, 1) kv4_many_kernel(con
     const uint64_t qd = umma_desc_sw128(sbase), kd = umma_desc_sw128(sbase + S::kOffK);
     const uint64_t vd = umma_desc_blocks(sbase + S::kOffV, S::kKvBlock, 1024);
     bool ok = steps == 0 || wait(q_full, 0);
-    auto scores = [&](int t, int j) {
+    RingAt ka, va;
+    auto scores = [&](int j) {  // of step j, both tiles
+      if (!(ok = wait(k_full + 8u * ka.slot, ka.round))) return;
+      umma_fence_after();
       if (one) {
+        for (int t = 0; t < tiles; ++t) {
 #pragma unroll
-        for (int i = 0; i < D / 16; ++i)
-          umma_f16_ss(tmem + (uint32_t)(t * S::kTokens),
-                      qd + (uint32_t)((t * S::kQTile + (i >> 2) * S::kQBlock + (i & 3) * 32) >> 4),
-                      kd + (uint32_t)(((j & 1) * S::kKvTile + (i >> 2) * S::kKvBlock + (i & 3) * 32) >> 4),
-                      kIdS, i != 0);
-        umma_commit(s_full + 8u * t);
-        if (t == tiles - 1) umma_commit(k_empty + 8u * (j & 1));
+          for (int i = 0; i < D / 16; ++i)
+            umma_f16_ss(tmem + (uint32_t)((2 * t + (j & 1)) * S::kTokens),
+                        qd + (uint32_t)((t * S::kQTile + (i >> 2) * S::kQBlock + (i & 3) * 32) >> 4),
+                        kd + (uint32_t)((ka.slot * S::kKvTile + (i >> 2) * S::kKvBlock + (i & 3) * 32) >> 4),
+                        kIdS, i != 0);
+          umma_commit(s_full + 8u * (2 * t + (j & 1)));
+        }
+        umma_commit(k_empty + 8u * ka.slot);
       }
+      ka.step(S::kBufs);
     };
+    if (steps > 0 && ok) scores(0);
     for (int j = 0; j < steps && ok; ++j) {
-      if (j == 0) {
-        if (!(ok = wait(k_full, 0))) break;
-        umma_fence_after();
-        for (int t = 0; t < tiles; ++t) scores(t, 0);
-      }
-      for (int t = 0; t < tiles && ok; ++t) {
-        if (t == 0 && !(ok = wait(v_full + 8u * (j & 1), j >> 1))) break;
-        if (!(ok = wait(p_full + 8u * t, j))) break;
+      // the next scores go over the last step's weights, behind the product
+      // that reads them
+      if (j + 1 < steps) scores(j + 1);
+      if (!ok || !(ok = wait(v_full + 8u * va.slot, va.round))) break;
+      for (int t = 0; t < tiles; ++t) {
+        const int s = 2 * t + (j & 1);
+        if (!(ok = wait(p_full + 8u * s, j >> 1))) break;
         umma_fence_after();
         if (one) {
 #pragma unroll
           for (int i = 0; i < S::kTokens / 16; ++i)
-            umma_f16_ts(tmem + (uint32_t)(S::kOCol + t * D), tmem + (uint32_t)(t * S::kTokens + i * 8),
-                        vd + (uint32_t)(((j & 1) * S::kKvTile + i * 2048) >> 4), kIdO, (j | i) != 0);
+            umma_f16_ts(tmem + (uint32_t)(S::kOCol + t * D), tmem + (uint32_t)(s * S::kTokens + i * 8),
+                        vd + (uint32_t)((va.slot * S::kKvTile + i * 2048) >> 4), kIdO, (j | i) != 0);
           umma_commit(o_done + 8u * t);
-          if (t == tiles - 1) umma_commit(v_empty + 8u * (j & 1));
-        }
-        if (j + 1 < steps) {
-          if (t == 0) {
-            if (!(ok = wait(k_full + 8u * ((j + 1) & 1), (j + 1) >> 1))) break;
-            umma_fence_after();
-          }
-          scores(t, j + 1);  // over P, after the product that reads it
         }
       }
+      if (ok && one) umma_commit(v_empty + 8u * va.slot);
+      va.step(S::kBufs);
     }
     if (!ok) {
       give_up();
@@ -270,23 +309,24 @@ __global__ void __launch_bounds__(ManyShape<D>::kThreads, 1) kv4_many_kernel(con
       fence_proxy_async_smem();
     };
     bool ok = true;
+    RingAt at;
     look_up(0);
     load(p.k, p.k_param);
-    for (int j = 0; j < steps; ++j) {
+    for (int j = 0; j < steps; ++j, at.step(S::kBufs)) {
       uint32_t now[S::kPasses];
 #pragma unroll
       for (int i = 0; i < S::kPasses; ++i) now[i] = vec[i];
-      if (j >= 2 && !(ok = wait(k_empty + 8u * (j & 1), (j >> 1) - 1))) break;
-      store(sbase + S::kOffK + (uint32_t)(j & 1) * S::kKvTile, false, masks + (j & 3) * S::kWords, now, j);
+      if (at.round > 0 && !(ok = wait(k_empty + 8u * at.slot, at.round - 1))) break;
+      store(sbase + S::kOffK + (uint32_t)at.slot * S::kKvTile, false, masks + (j & 7) * S::kWords, now, j);
       load(p.v, p.v_param);
       __syncwarp();
-      if (lane == 0) mbar_arrive_cta(k_full + 8u * (j & 1));
+      if (lane == 0) mbar_arrive_cta(k_full + 8u * at.slot);
       look_up(j + 1);
-      if (j >= 2 && !(ok = wait(v_empty + 8u * (j & 1), (j >> 1) - 1))) break;
-      store(sbase + S::kOffV + (uint32_t)(j & 1) * S::kKvTile, true, masks + (4 + (j & 3)) * S::kWords, now, j);
+      if (at.round > 0 && !(ok = wait(v_empty + 8u * at.slot, at.round - 1))) break;
+      store(sbase + S::kOffV + (uint32_t)at.slot * S::kKvTile, true, masks + (8 + (j & 7)) * S::kWords, now, j);
       load(p.k, p.k_param);
       __syncwarp();
-      if (lane == 0) mbar_arrive_cta(v_full + 8u * (j & 1));
+      if (lane == 0) mbar_arrive_cta(v_full + 8u * at.slot);
     }
     if (!ok) give_up();
   } else if (warp < 4 * tiles) {
@@ -337,7 +377,7 @@ __global__ void __launch_bounds__(ManyShape<D>::kThreads, 1) kv4_many_kernel(con
       if (lane == 0) mbar_arrive_cta(q_full);
     }
     const uint32_t lanes = (uint32_t)((warp & 3) * 32) << 16;
-    const uint32_t ts = tmem + lanes + (uint32_t)(t * S::kTokens), to = tmem + lanes + (uint32_t)(S::kOCol + t * D);
+    const uint32_t ts0 = tmem + lanes + (uint32_t)(2 * t * S::kTokens), to = tmem + lanes + (uint32_t)(S::kOCol + t * D);
     // whether position `token` of a step's mask words is marked, for piece q
     auto marked = [&](const uint32_t* word, int token, int q) {
       const int at = token / S::kPerWarp;
@@ -353,9 +393,9 @@ __global__ void __launch_bounds__(ManyShape<D>::kThreads, 1) kv4_many_kernel(con
       return all != 0;
     };
     auto look_for_nan = [&](int j) {  // V's groups of step j, once its product is done
-      const uint32_t* word = masks + (4 + (j & 3)) * S::kWords;
+      const uint32_t* word = masks + (8 + (j & 7)) * S::kWords;
       if (!any_word(word)) return;
-      const uint32_t* gone = masks + (j & 3) * S::kWords;
+      const uint32_t* gone = masks + (j & 7) * S::kWords;
       for (int k = 0; k < S::kTokens; ++k) {
         const int at = begin + j * S::kTokens + k;
         if (at < lo || at >= min(hi, end) || marked(gone, k, 0)) continue;
@@ -365,36 +405,31 @@ __global__ void __launch_bounds__(ManyShape<D>::kThreads, 1) kv4_many_kernel(con
     };
     bool ok = true;
     for (int j = 0; j < steps; ++j) {
-      if (!(ok = wait(s_full + 8u * t, j))) break;
+      const uint32_t ts = ts0 + (uint32_t)((j & 1) * S::kTokens);
+      if (!(ok = wait(s_full + 8u * (2 * t + (j & 1)), j >> 1))) break;
       umma_fence_after();
+      uint32_t s[2][32];
+      tmem_ld32(ts, s[0]);
+      tmem_ld32(ts + 32, s[1]);
+      tmem_wait_ld();
       if (j > 0) look_for_nan(j - 1);
       const int j0 = begin + j * S::kTokens;
-      const uint32_t* gone = masks + (j & 3) * S::kWords;
+      const uint32_t* gone = masks + (j & 7) * S::kWords;
       const bool holes = any_word(gone);
-      const bool whole = j0 >= lo_all && j0 + S::kTokens <= hi_all && !holes;
-      auto hide = [&](uint32_t (&s)[32], int c) {
+      if (holes || j0 < lo_all || j0 + S::kTokens > hi_all) {
 #pragma unroll
-        for (int k = 0; k < 32; ++k) {
-          const int at = j0 + c + k;
-          if (at < lo || at >= min(hi, end) || (holes && marked(gone, c + k, 0))) s[k] = 0xFF800000u;
+        for (int k = 0; k < 64; ++k) {
+          const int at = j0 + k;
+          if (at < lo || at >= min(hi, end) || (holes && marked(gone, k, 0))) s[k >> 5][k & 31] = 0xFF800000u;
         }
-      };
-      float top = -INFINITY;
-#pragma unroll 1
-      for (int c = 0; c < S::kTokens; c += 32) {
-        uint32_t s[32];
-        tmem_ld32(ts + (uint32_t)c, s);
-        tmem_wait_ld();
-        if (!whole) hide(s, c);
-        float x[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
-#pragma unroll
-        for (int k = 0; k < 32; ++k) x[k & 3] = fmaxf(x[k & 3], __uint_as_float(s[k]));
-        top = fmaxf(top, fmaxf(fmaxf(x[0], x[1]), fmaxf(x[2], x[3])));
       }
-      const float now = top * fs;
-      const bool moved = now > m + 8.f || (m == -INFINITY && now > -INFINITY);
+      float x4[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+#pragma unroll
+      for (int k = 0; k < 64; ++k) x4[k & 3] = fmaxf(x4[k & 3], __uint_as_float(s[k >> 5][k & 31]));
+      const float now = fmaxf(fmaxf(x4[0], x4[1]), fmaxf(x4[2], x4[3])) * fs;
+      const bool moved = now > m + 8.f;  // the first finite maximum moves from -infinity
       if (__any_sync(0xFFFFFFFFu, moved)) {
-        const float f = moved ? (m == -INFINITY ? 0.f : ex2(m - now)) : 1.f;
+        const float f = moved ? ex2(m - now) : 1.f;
         if (j > 0) {
           if (!(ok = wait(o_done + 8u * t, j - 1))) break;
           umma_fence_after();
@@ -414,30 +449,36 @@ __global__ void __launch_bounds__(ManyShape<D>::kThreads, 1) kv4_many_kernel(con
         }
       }
       const float base = m == -INFINITY ? 0.f : m;
-      float sum[4] = {0.f, 0.f, 0.f, 0.f};
-#pragma unroll 1
-      for (int c = 0; c < S::kTokens; c += 32) {
-        uint32_t s[32], w[16];
-        tmem_ld32(ts + (uint32_t)c, s);
-        tmem_wait_ld();
-        if (!whole) hide(s, c);
+      const uint64_t fs2 = pack_f32x2(fs, fs), base2 = pack_f32x2(-base, -base);
+      uint64_t sum2[2] = {0, 0};
+#pragma unroll
+      for (int c = 0; c < 2; ++c) {
+        uint32_t w[16];
 #pragma unroll
         for (int k = 0; k < 16; ++k) {
-          const float x = ex2(fmaf(__uint_as_float(s[2 * k]), fs, -base));
-          const float y = ex2(fmaf(__uint_as_float(s[2 * k + 1]), fs, -base));
-          sum[k & 3] += x + y;
+          float x, y;
+          unpack_f32x2(fma_f32x2(pack_f32x2(__uint_as_float(s[c][2 * k]), __uint_as_float(s[c][2 * k + 1])),
+                                 fs2, base2),
+                       x, y);
+          x = ex2(x);
+          y = ex2(y);
+          sum2[k & 1] = add_f32x2(sum2[k & 1], pack_f32x2(x, y));
           w[k] = pack_f16(x, y);
         }
-        tmem_st16(ts + (uint32_t)(c / 2), w);  // over scores that this thread has read
+        tmem_st16(ts + (uint32_t)(16 * c), w);  // over scores that this thread has read
       }
-      l += (sum[0] + sum[1]) + (sum[2] + sum[3]);
+      float sa, sb;
+      unpack_f32x2(add_f32x2(sum2[0], sum2[1]), sa, sb);
+      l += sa + sb;
       tmem_wait_st();
       umma_fence_before();
       __syncwarp();
-      if (lane == 0) mbar_arrive_cta(p_full + 8u * t);
+      if (lane == 0) mbar_arrive_cta(p_full + 8u * (2 * t + (j & 1)));
     }
     if (steps > 0 && ok) {
-      ok = wait(o_done + 8u * t, steps - 1);
+      // the last scores come behind the product of two steps before, and a wait by
+      // parity has to be for the next round but none: one round at a time
+      ok = (steps < 2 || wait(o_done + 8u * t, steps - 2)) && wait(o_done + 8u * t, steps - 1);
       umma_fence_after();
       if (ok) look_for_nan(steps - 1);
     }
