@@ -5,8 +5,8 @@
 //   S = Q K^T,  P = exp2(S fs - m),  O += P V  for 128 rows of a key/value head
 // (query heads that share it times rows of the call) a tile, two tiles a CTA
 // (one where D = 256 leaves tensor memory for no more), and 64 positions a
-// step.  Four warps turn the codes into fp16 operands in shared memory, once
-// for both tiles: c from its bits (1024 + c or 1024 + 16 c, exactly), then a c +
+// step.  Four warps for K and four for V turn the codes into fp16 operands in
+// shared memory, once for both tiles: c from its bits (1024 + c or 1024 + 16 c, exactly), then a c +
 // z with one rounding to fp16 (half a step, 2^-11).  One warp issues the
 // products; four warps a tile do its softmax, a thread a row.  S has two
 // buffers a tile, so that a step's scores are there when the softmax of the
@@ -52,7 +52,10 @@ struct ManyShape {
   static constexpr uint32_t kOffMask = kOffBar + 256;
   static constexpr uint32_t kSmem = 1024 + kOffMask + 2 * 8 * kWords * 4;
   static constexpr int kOCol = 2 * kTiles * kTokens;         // tensor memory: S buffers, then O tiles
-  static constexpr int kThreads = 32 * (4 * kTiles + 4 + 1); // softmax, codes, MMA
+  // softmax, K's and V's codes, MMA.  Two tiles' 20 warps start with 96
+  // registers a thread, 61440 in all, and share them anew by groups of four
+  // warps: 2 * 128 * 128 (softmax) + 2 * 128 * 80 (codes) + 128 * 56 = 60416.
+  static constexpr int kThreads = kTiles == 2 ? 640 : 416;
 };
 
 // A ring's slot and the round it is in.
@@ -160,7 +163,7 @@ __global__ void __launch_bounds__(ManyShape<D>::kThreads, 1) kv4_many_kernel(con
   const uint32_t q_full = bar, k_full = bar + 8, k_empty = bar + 32, v_full = bar + 56,
                  v_empty = bar + 80, s_full = bar + 104, p_full = bar + 136, o_done = bar + 168,
                  drain = bar + 184, slot = bar + 192;
-  constexpr int kCodeWarp0 = 4 * S::kTiles, kMmaWarp = kCodeWarp0 + 4;
+  constexpr int kCodeWarp0 = 4 * S::kTiles, kMmaWarp = kCodeWarp0 + 8;
   if (warp == kMmaWarp) {
     if (lane == 0) {
       mbar_init(q_full, (uint32_t)(4 * tiles));
@@ -193,7 +196,9 @@ __global__ void __launch_bounds__(ManyShape<D>::kThreads, 1) kv4_many_kernel(con
     if (lane == 0) record_error(&g_kv4_error, BCQ_ERR_TIMEOUT);
   };
 
-  if (warp == kMmaWarp) {
+  if (warp >= kMmaWarp) {
+    if (S::kTiles == 2) asm volatile("setmaxnreg.dec.sync.aligned.u32 56;");
+    if (warp == kMmaWarp) {
     // ------------------------------------------------------------ the products
     const bool one = elect_one();
     // fp16 A and B, fp32 D, M = 128; V has its values (N) contiguous
@@ -246,91 +251,103 @@ __global__ void __launch_bounds__(ManyShape<D>::kThreads, 1) kv4_many_kernel(con
       if (one) umma_commit(drain);
       mbar_wait_bounded(drain, 0, kWaitNs);
     }
+    }
   } else if (warp >= kCodeWarp0) {
     // --------------------------------------------------------------- the codes
-    const int w = warp - kCodeWarp0;
+    if (S::kTiles == 2) asm volatile("setmaxnreg.dec.sync.aligned.u32 80;");
+    const bool is_v = warp >= kCodeWarp0 + 4;
+    const int w = (warp - kCodeWarp0) & 3;
     const int piece = lane % S::kPieces, sub = lane / S::kPieces;
     // the order in which a thread writes its four words, and with it the banks
     const int turn = D == 256 ? piece >> 1 : D == 128 ? (piece >> 1) << 1 : 0;
+    const uint8_t* code = (is_v ? p.v : p.k) + piece * 16;
+    const __half2* param = (is_v ? p.v_param : p.k_param) + (piece >> 1);
+    const uint32_t tiles_at = sbase + (is_v ? S::kOffV : S::kOffK), full = is_v ? v_full : k_full,
+                   empty = is_v ? v_empty : k_empty;
+    uint32_t* mask = masks + (is_v ? 8 * S::kWords : 0);
+    struct Piece {
+      uint4 codes;
+      uint32_t az;
+      bool gone;  // a position that has no page
+    };
     uint32_t vec[S::kPasses];
     auto look_up = [&](int j) {  // this thread's positions of step j
 #pragma unroll
       for (int i = 0; i < S::kPasses; ++i) {
         const int at = begin + j * S::kTokens + (i * 4 + w) * S::kPerWarp + sub;
-        vec[i] = 0xFFFFFFFFu;
+        vec[i] = 0xFFFFFFFEu;  // beyond the end
         if (j < steps && at < end) {
           const int64_t found = vector_at(p.at, b, at, kvh);
-          if (found >= 0) vec[i] = (uint32_t)found;
-          else record_error(&g_kv4_error, BCQ_ERR_PAGE);
+          vec[i] = (uint32_t)found;
+          if (found < 0) record_error(&g_kv4_error, BCQ_ERR_PAGE);
         }
       }
     };
-    uint4 codes[S::kPasses];
-    uint32_t az[S::kPasses];
-    auto load = [&](const uint8_t* code, const __half2* param) {
+    auto load = [&](Piece (&x)[S::kPasses]) {
 #pragma unroll
       for (int i = 0; i < S::kPasses; ++i) {
-        codes[i] = make_uint4(0, 0, 0, 0);
-        az[i] = 0;
-        if (vec[i] != 0xFFFFFFFFu) {
-          codes[i] = *reinterpret_cast<const uint4*>(code + (int64_t)vec[i] * (D / 2) + piece * 16);
-          az[i] = *reinterpret_cast<const uint32_t*>(param + (int64_t)vec[i] * G + (piece >> 1));
+        x[i].codes = make_uint4(0, 0, 0, 0);
+        x[i].az = 0;
+        x[i].gone = vec[i] == 0xFFFFFFFFu;
+        if (vec[i] < 0xFFFFFFFEu) {
+          x[i].codes = *reinterpret_cast<const uint4*>(code + (uint64_t)vec[i] * (D / 2));
+          x[i].az = *reinterpret_cast<const uint32_t*>(param + (uint64_t)vec[i] * G);
         }
       }
     };
-    // codes and params into a tile; for V what is no number becomes zero.  The
-    // mask word of a pass: lanes without a position's page (K), or with such a
-    // group (V)
-    auto store = [&](uint32_t tile, bool is_v, uint32_t* mask, const uint32_t (&at)[S::kPasses], int j) {
+    // into a tile; for V what is no number becomes zero.  The mask word of a
+    // pass: lanes of a position without a page (K), or of such a group (V)
+    auto store = [&](uint32_t tile, uint32_t* word_at, const Piece (&x)[S::kPasses]) {
 #pragma unroll
       for (int i = 0; i < S::kPasses; ++i) {
         const int token = (i * 4 + w) * S::kPerWarp + sub;
-        __half2 f = *reinterpret_cast<const __half2*>(&az[i]);
-        const bool odd = (az[i] & 0x7C00u) == 0x7C00u || (az[i] & 0x7C000000u) == 0x7C000000u;
-        const bool gone = at[i] == 0xFFFFFFFFu && begin + j * S::kTokens + token < end;
-        if (is_v && odd) f = __floats2half2_rn(0.f, 0.f);
-        const uint32_t word = __ballot_sync(0xFFFFFFFFu, is_v ? odd : gone);
-        if (lane == 0) mask[i * 4 + w] = word;
-        uint4 c = codes[i];
+        uint32_t az = x[i].az;
+        const bool odd = odd_half2(az);
+        const uint32_t word = __ballot_sync(0xFFFFFFFFu, is_v ? odd : x[i].gone);
+        if (lane == 0) word_at[i * 4 + w] = word;
+        if (is_v && odd) az = 0;
+        uint4 c = x[i].codes;
         if (turn & 2) c = make_uint4(c.z, c.w, c.x, c.y);
         if (turn & 1) c = make_uint4(c.y, c.x, c.w, c.z);
+        const __half2 f = *reinterpret_cast<const __half2*>(&az);
         const __half2 a = __low2half2(f), z = __high2half2(f);
         const uint32_t row = tile + (uint32_t)((piece >> 1) * S::kKvBlock) + (uint32_t)token * 128u;
         const uint32_t cs[4] = {c.x, c.y, c.z, c.w};
+        uint4 v[4];
+#pragma unroll
+        for (int e = 0; e < 4; ++e) v[e] = word_values(cs[e], a, z);
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
           const uint32_t chunk = (uint32_t)((piece & 1) * 4 + (e ^ turn)) ^ (uint32_t)(token & 7);
-          const uint4 v = word_values(cs[e], a, z);
-          asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(row + (chunk << 4)), "r"(v.x),
-                       "r"(v.y), "r"(v.z), "r"(v.w)
+          asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(row + (chunk << 4)), "r"(v[e].x),
+                       "r"(v[e].y), "r"(v[e].z), "r"(v[e].w)
                        : "memory");
         }
       }
       fence_proxy_async_smem();
     };
+    // a step's codes are asked for a step ahead, their places two
     bool ok = true;
     RingAt at;
+    Piece now[S::kPasses], next[S::kPasses];
     look_up(0);
-    load(p.k, p.k_param);
+    load(now);
+    look_up(1);
     for (int j = 0; j < steps; ++j, at.step(S::kBufs)) {
-      uint32_t now[S::kPasses];
+      load(next);
+      look_up(j + 2);
+      if (at.round > 0 && !(ok = wait(empty + 8u * at.slot, at.round - 1))) break;
+      store(tiles_at + (uint32_t)at.slot * S::kKvTile, mask + (j & 7) * S::kWords, now);
+      __syncwarp();
+      if (lane == 0) mbar_arrive_cta(full + 8u * at.slot);
 #pragma unroll
-      for (int i = 0; i < S::kPasses; ++i) now[i] = vec[i];
-      if (at.round > 0 && !(ok = wait(k_empty + 8u * at.slot, at.round - 1))) break;
-      store(sbase + S::kOffK + (uint32_t)at.slot * S::kKvTile, false, masks + (j & 7) * S::kWords, now, j);
-      load(p.v, p.v_param);
-      __syncwarp();
-      if (lane == 0) mbar_arrive_cta(k_full + 8u * at.slot);
-      look_up(j + 1);
-      if (at.round > 0 && !(ok = wait(v_empty + 8u * at.slot, at.round - 1))) break;
-      store(sbase + S::kOffV + (uint32_t)at.slot * S::kKvTile, true, masks + (8 + (j & 7)) * S::kWords, now, j);
-      load(p.k, p.k_param);
-      __syncwarp();
-      if (lane == 0) mbar_arrive_cta(v_full + 8u * at.slot);
+      for (int i = 0; i < S::kPasses; ++i) now[i] = next[i];
     }
     if (!ok) give_up();
-  } else if (warp < 4 * tiles) {
+  } else {
     // -------------------------------------------------------------- the softmax
+    if (S::kTiles == 2) asm volatile("setmaxnreg.inc.sync.aligned.u32 128;");
+    if (warp < 4 * tiles) {
     const int t = warp >> 2, r = (warp & 3) * 32 + lane;  // tile, row of it
     const int row = t * 128 + r;
     const bool live = row < row_n;
@@ -529,6 +546,7 @@ __global__ void __launch_bounds__(ManyShape<D>::kThreads, 1) kv4_many_kernel(con
         p.lse[token * p.q_heads + h] = none ? -INFINITY : (m + log2f(l)) * 0.69314718055994531f;
       }
     }
+  }
   }
   launch_dependents();
   __syncwarp();
