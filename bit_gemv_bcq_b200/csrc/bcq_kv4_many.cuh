@@ -69,6 +69,11 @@ struct RingAt {
   }
 };
 
+__device__ __forceinline__ float max3(float a, float b, float c) {
+  float d;
+  asm("max.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(b), "f"(c));
+  return d;
+}
 // Two fp32 values at once.
 __device__ __forceinline__ uint64_t pack_f32x2(float a, float b) {
   uint64_t d;
@@ -143,10 +148,11 @@ __global__ void __launch_bounds__(ManyShape<D>::kThreads, 1) kv4_many_kernel(con
   uint32_t* masks = reinterpret_cast<uint32_t*>(smem_raw + (sbase - smem_u32(smem_raw)) + S::kOffMask);
   const int warp = __shfl_sync(0xFFFFFFFFu, (int)threadIdx.x >> 5, 0), lane = threadIdx.x & 31;
 
-  // the last blocks of rows see the most: they go first
-  const int block = p.row_blocks - 1 - (int)(blockIdx.x % p.row_blocks);
-  const int kvh = blockIdx.x / p.row_blocks % p.at.heads;
-  const int b = blockIdx.x / p.row_blocks / p.at.heads, part = blockIdx.y;
+  // the last blocks of rows see the most: theirs go first, of every sequence
+  // and head
+  const int pairs = p.at.heads * p.at.B, pair = blockIdx.x % pairs;
+  const int block = p.row_blocks - 1 - (int)(blockIdx.x / pairs);
+  const int kvh = pair % p.at.heads, b = pair / p.at.heads, part = blockIdx.y;
   const Span sp = span_of(p, b, block);
   if (part == 0 && block == 0 && kvh == 0 && threadIdx.x == 0) {
     if (rows_of(p.at, b).y > p.max_q) record_error(&g_kv4_error, BCQ_ERR_SHAPE);
@@ -189,8 +195,12 @@ __global__ void __launch_bounds__(ManyShape<D>::kThreads, 1) kv4_many_kernel(con
   umma_fence_after();
   const uint32_t tmem = lds_u32v(slot);
   constexpr unsigned long long kWaitNs = 2000000000ull;
+  // A waiting thread that sleeps takes some 400 cycles to wake: look a while first.
   auto wait = [&](uint32_t at, int round) {
-    return __all_sync(0xFFFFFFFFu, mbar_wait_bounded(at, (uint32_t)round & 1u, kWaitNs)) != 0;
+    bool there = false;
+#pragma unroll 1
+    for (int i = 0; i < 64 && !there; ++i) there = mbar_test(at, (uint32_t)round & 1u);
+    return __all_sync(0xFFFFFFFFu, there || mbar_wait_bounded(at, (uint32_t)round & 1u, kWaitNs)) != 0;
   };
   auto give_up = [&]() {
     if (lane == 0) record_error(&g_kv4_error, BCQ_ERR_TIMEOUT);
@@ -257,9 +267,8 @@ __global__ void __launch_bounds__(ManyShape<D>::kThreads, 1) kv4_many_kernel(con
     if (S::kTiles == 2) asm volatile("setmaxnreg.dec.sync.aligned.u32 80;");
     const bool is_v = warp >= kCodeWarp0 + 4;
     const int w = (warp - kCodeWarp0) & 3;
-    const int piece = lane % S::kPieces, sub = lane / S::kPieces;
-    // the order in which a thread writes its four words, and with it the banks
-    const int turn = D == 256 ? piece >> 1 : D == 128 ? (piece >> 1) << 1 : 0;
+    // eight lanes in turn store eight positions' same piece: all banks
+    const int piece = lane / S::kPerWarp, sub = lane % S::kPerWarp;
     const uint8_t* code = (is_v ? p.v : p.k) + piece * 16;
     const __half2* param = (is_v ? p.v_param : p.k_param) + (piece >> 1);
     const uint32_t tiles_at = sbase + (is_v ? S::kOffV : S::kOffK), full = is_v ? v_full : k_full,
@@ -270,78 +279,83 @@ __global__ void __launch_bounds__(ManyShape<D>::kThreads, 1) kv4_many_kernel(con
       uint32_t az;
       bool gone;  // a position that has no page
     };
-    uint32_t vec[S::kPasses];
-    auto look_up = [&](int j) {  // this thread's positions of step j
-#pragma unroll
-      for (int i = 0; i < S::kPasses; ++i) {
-        const int at = begin + j * S::kTokens + (i * 4 + w) * S::kPerWarp + sub;
-        vec[i] = 0xFFFFFFFEu;  // beyond the end
-        if (j < steps && at < end) {
-          const int64_t found = vector_at(p.at, b, at, kvh);
-          vec[i] = (uint32_t)found;
-          if (found < 0) record_error(&g_kv4_error, BCQ_ERR_PAGE);
-        }
+    // The positions of a warp and pass lie in one page.  Lane l looks up pass l
+    // % kPasses of step l / kPasses of the next 32 / kPasses: the vector of
+    // their first position.
+    constexpr int kAhead = 32 / S::kPasses;
+    constexpr uint32_t kNone = 0xFFFFFFFEu, kGone = 0xFFFFFFFFu;  // beyond the end, without a page
+    uint32_t vecs = kNone;
+    auto look_up = [&](int j) {
+      const int at = begin + (j + lane / S::kPasses) * S::kTokens +
+                     (lane % S::kPasses * 4 + w) * S::kPerWarp;
+      vecs = kNone;
+      if (at < end) {
+        const int64_t found = vector_at(p.at, b, at, kvh);
+        vecs = (uint32_t)found;
+        if (found < 0) record_error(&g_kv4_error, BCQ_ERR_PAGE);
       }
     };
-    auto load = [&](Piece (&x)[S::kPasses]) {
+    auto load = [&](Piece (&x)[S::kPasses], int j) {
+      if (j % kAhead == 0) look_up(j);
 #pragma unroll
       for (int i = 0; i < S::kPasses; ++i) {
+        uint32_t vec = __shfl_sync(0xFFFFFFFFu, vecs, j % kAhead * S::kPasses + i);
+        const int at = begin + j * S::kTokens + (i * 4 + w) * S::kPerWarp + sub;
         x[i].codes = make_uint4(0, 0, 0, 0);
         x[i].az = 0;
-        x[i].gone = vec[i] == 0xFFFFFFFFu;
-        if (vec[i] < 0xFFFFFFFEu) {
-          x[i].codes = *reinterpret_cast<const uint4*>(code + (uint64_t)vec[i] * (D / 2));
-          x[i].az = *reinterpret_cast<const uint32_t*>(param + (uint64_t)vec[i] * G);
+        x[i].gone = vec == kGone;
+        if (vec < kNone && at < end) {
+          vec += (uint32_t)sub;
+          x[i].codes = *reinterpret_cast<const uint4*>(code + (uint64_t)vec * (D / 2));
+          x[i].az = *reinterpret_cast<const uint32_t*>(param + (uint64_t)vec * G);
         }
       }
     };
+    uint32_t to[4];  // where this lane's four words go in a row of eight positions
+#pragma unroll
+    for (int e = 0; e < 4; ++e)
+      to[e] = (uint32_t)((piece >> 1) * S::kKvBlock + (w * S::kPerWarp + sub) * 128) +
+              ((uint32_t)(((piece & 1) * 4 + e) ^ ((w * S::kPerWarp + sub) & 7)) << 4);
     // into a tile; for V what is no number becomes zero.  The mask word of a
     // pass: lanes of a position without a page (K), or of such a group (V)
     auto store = [&](uint32_t tile, uint32_t* word_at, const Piece (&x)[S::kPasses]) {
 #pragma unroll
       for (int i = 0; i < S::kPasses; ++i) {
-        const int token = (i * 4 + w) * S::kPerWarp + sub;
         uint32_t az = x[i].az;
         const bool odd = odd_half2(az);
         const uint32_t word = __ballot_sync(0xFFFFFFFFu, is_v ? odd : x[i].gone);
         if (lane == 0) word_at[i * 4 + w] = word;
         if (is_v && odd) az = 0;
-        uint4 c = x[i].codes;
-        if (turn & 2) c = make_uint4(c.z, c.w, c.x, c.y);
-        if (turn & 1) c = make_uint4(c.y, c.x, c.w, c.z);
+        const uint4 c = x[i].codes;
         const __half2 f = *reinterpret_cast<const __half2*>(&az);
         const __half2 a = __low2half2(f), z = __high2half2(f);
-        const uint32_t row = tile + (uint32_t)((piece >> 1) * S::kKvBlock) + (uint32_t)token * 128u;
-        const uint32_t cs[4] = {c.x, c.y, c.z, c.w};
-        uint4 v[4];
+        const uint4 v[4] = {word_values(c.x, a, z), word_values(c.y, a, z), word_values(c.z, a, z),
+                            word_values(c.w, a, z)};
 #pragma unroll
-        for (int e = 0; e < 4; ++e) v[e] = word_values(cs[e], a, z);
-#pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          const uint32_t chunk = (uint32_t)((piece & 1) * 4 + (e ^ turn)) ^ (uint32_t)(token & 7);
-          asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(row + (chunk << 4)), "r"(v[e].x),
-                       "r"(v[e].y), "r"(v[e].z), "r"(v[e].w)
+        for (int e = 0; e < 4; ++e)
+          asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(
+                           tile + to[e] + (uint32_t)(i * 4 * S::kPerWarp * 128)),
+                       "r"(v[e].x), "r"(v[e].y), "r"(v[e].z), "r"(v[e].w)
                        : "memory");
-        }
       }
       fence_proxy_async_smem();
     };
-    // a step's codes are asked for a step ahead, their places two
+    // a step's codes are asked for a step ahead
     bool ok = true;
     RingAt at;
-    Piece now[S::kPasses], next[S::kPasses];
-    look_up(0);
-    load(now);
-    look_up(1);
-    for (int j = 0; j < steps; ++j, at.step(S::kBufs)) {
-      load(next);
-      look_up(j + 2);
-      if (at.round > 0 && !(ok = wait(empty + 8u * at.slot, at.round - 1))) break;
+    Piece x[2][S::kPasses];
+    auto one_step = [&](int j, Piece (&now)[S::kPasses], Piece (&next)[S::kPasses]) {
+      load(next, j + 1);
+      if (at.round > 0 && !(ok = wait(empty + 8u * at.slot, at.round - 1))) return;
       store(tiles_at + (uint32_t)at.slot * S::kKvTile, mask + (j & 7) * S::kWords, now);
       __syncwarp();
       if (lane == 0) mbar_arrive_cta(full + 8u * at.slot);
-#pragma unroll
-      for (int i = 0; i < S::kPasses; ++i) now[i] = next[i];
+      at.step(S::kBufs);
+    };
+    load(x[0], 0);
+    for (int j = 0; j < steps && ok; j += 2) {
+      one_step(j, x[0], x[1]);
+      if (ok && j + 1 < steps) one_step(j + 1, x[1], x[0]);
     }
     if (!ok) give_up();
   } else {
@@ -398,7 +412,7 @@ __global__ void __launch_bounds__(ManyShape<D>::kThreads, 1) kv4_many_kernel(con
     // whether position `token` of a step's mask words is marked, for piece q
     auto marked = [&](const uint32_t* word, int token, int q) {
       const int at = token / S::kPerWarp;
-      return (word[at] >> (token % S::kPerWarp * S::kPieces + q)) & 1u;
+      return (word[at] >> (q * S::kPerWarp + token % S::kPerWarp)) & 1u;
     };
     auto any_word = [&](const uint32_t* word) {
       uint32_t all = 0;
@@ -442,7 +456,9 @@ __global__ void __launch_bounds__(ManyShape<D>::kThreads, 1) kv4_many_kernel(con
       }
       float x4[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
 #pragma unroll
-      for (int k = 0; k < 64; ++k) x4[k & 3] = fmaxf(x4[k & 3], __uint_as_float(s[k >> 5][k & 31]));
+      for (int k = 0; k < 64; k += 2)
+        x4[(k >> 1) & 3] = max3(x4[(k >> 1) & 3], __uint_as_float(s[k >> 5][k & 31]),
+                                __uint_as_float(s[k >> 5][(k & 31) + 1]));
       const float now = fmaxf(fmaxf(x4[0], x4[1]), fmaxf(x4[2], x4[3])) * fs;
       const bool moved = now > m + 8.f;  // the first finite maximum moves from -infinity
       if (__any_sync(0xFFFFFFFFu, moved)) {
