@@ -593,9 +593,27 @@ _DTYPES = {torch.float16: 0, torch.bfloat16: 1, torch.float32: 2}   # BCQ_F16, B
 _HALVES = (torch.float16, torch.bfloat16)
 I8_MAX_K = 65536
 
-# The calls below take a few microseconds on the GPU at their smallest, so the
-# checks read each property of a tensor once and streams and devices are
-# compared by number.
+# The calls below take a few microseconds on the GPU at their smallest.  The
+# usual ones -- on the current stream of the current device, nothing to refuse
+# -- go through _fast (csrc/bcq_fast.cpp), which returns NotImplemented for any
+# other; then the code here checks, names what is wrong, and calls.  It reads
+# each property of a tensor once and compares streams and devices by number.
+
+_FAST_ENTRY_POINTS = ("bcq_quantize_i8", "bcq_gemm_i8", "bcq_linear_i8_workspace_bytes",
+                      "bcq_linear_i8", "bcq_kv4_append", "bcq_kv4_read",
+                      "bcq_kv4_attention_workspace_bytes", "bcq_kv4_attention")
+_fast_module = None
+
+
+def _fast():
+    """The module of the fast calls, bound to the library."""
+    global _fast_module
+    if _fast_module is None:
+        L = lib()
+        from . import _fast as module
+        module.bind(*(ctypes.cast(getattr(L, n), ctypes.c_void_p).value for n in _FAST_ENTRY_POINTS))
+        _fast_module = module
+    return _fast_module
 
 
 def _raw_stream(stream, index: int) -> int:
@@ -685,6 +703,10 @@ def quantize_i8(x: torch.Tensor, stream=None):
     (bcq_quantize_i8): (codes int8 [M][K] whose rows start on multiples of 16
     bytes, scale fp32 [M]); codes * scale is x to half a step.  Activations: a
     row per token; weights, once: a row per output channel."""
+    if stream is None:
+        y = (_fast_module or _fast()).quantize_i8(x)
+        if y is not NotImplemented:
+            return y
     ldx = _need_matrix(x, "x", _HALVES)
     M, K = x.shape
     index = x.get_device()
@@ -704,6 +726,10 @@ def gemm_i8(x: torch.Tensor, x_scale: torch.Tensor, w: torch.Tensor, w_scale: to
     scales [M] and [N]; y is fp16, bf16 or fp32."""
     if dtype not in _DTYPES:
         raise ValueError("dtype must be float16, bfloat16 or float32")
+    if stream is None:
+        y = (_fast_module or _fast()).gemm_i8(x, x_scale, w, w_scale, _DTYPES[dtype], out)
+        if y is not NotImplemented:
+            return y
     ldx = _need_codes(x, "x")
     index = x.get_device()
     ldw = _need_codes(w, "w", index)
@@ -725,6 +751,10 @@ def linear_i8(x: torch.Tensor, w: torch.Tensor, w_scale: torch.Tensor,
     """y = x W^T for fp16 or bf16 x [M][K] and an 8-bit weight (codes w [N][K],
     w_scale [N]): quantize_i8 of x's rows and gemm_i8 in one call
     (bcq_linear_i8); y [M][N] has x's type."""
+    if stream is None:
+        y = (_fast_module or _fast()).linear_i8(x, w, w_scale, out)
+        if y is not NotImplemented:
+            return y
     ldx = _need_matrix(x, "x", _HALVES)
     index = x.get_device()
     ldw = _need_codes(w, "w", index)
@@ -858,6 +888,9 @@ def kv4_append(cache: Kv4Cache, k: torch.Tensor, v: torch.Tensor, table: torch.T
     distance) into the cache (bcq_kv4_append).  kv_len [B] counts the new
     tokens in: row i of a sequence's n rows cu[b]..cu[b + 1] - 1 goes to
     position kv_len - n + i.  Without cu each sequence has one row."""
+    if stream is None and (_fast_module or _fast()).kv4_append(
+            cache.k, cache.k_param, cache.v, cache.v_param, table, kv_len, cu, k, v) is None:
+        return
     index = cache.k.get_device()
     c, heads, _, D = cache._c()
     T, _, ldk, hdk = _need_heads(k, "k", heads, D, index)
@@ -884,6 +917,11 @@ def kv4_read(cache: Kv4Cache, table: torch.Tensor, kv_len: torch.Tensor,
     if T is None:
         raise ValueError("with cu, give tokens (or k and v)")
     T = int(T)
+    if stream is None and k is None:
+        y = (_fast_module or _fast()).kv4_read(cache.k, cache.k_param, cache.v, cache.v_param, table,
+                                               kv_len, cu, T, _DTYPES[dtype])
+        if y is not NotImplemented:
+            return y
     index = cache.k.get_device()
     c, heads, _, D = cache._c()
     B, W, p_table, p_len, p_cu = _need_places(table, kv_len, cu, T, index)
@@ -916,6 +954,12 @@ def kv4_attention(q: torch.Tensor, cache: Kv4Cache, table: torch.Tensor, kv_len:
     near one fast); window > 0 lets a row see that many positions, its own the
     last; scale is 1 / sqrt(D) when not given.  A row that sees nothing gives
     zeros and -inf; rows that cu gives to no sequence are left as they were."""
+    if stream is None and out is None:
+        y = (_fast_module or _fast()).kv4_attention(
+            cache.k, cache.k_param, cache.v, cache.v_param, table, kv_len, cu, q, max_q, max_kv,
+            causal, window, scale, return_lse)
+        if y is not NotImplemented:
+            return y
     index = cache.k.get_device()
     c, heads, page_size, D = cache._c()
     T, H, ldq, hdq = _need_heads(q, "q", None, D, index)

@@ -5,7 +5,9 @@ Each translation unit of csrc/ is compiled to an object under _build/ (in
 parallel; an object is rebuilt only when its source or a header it includes
 changed), then the objects are linked.  The CUDA runtime is linked
 statically and its symbols are kept private to the library, so the
-process's other CUDA users (torch) are not affected.
+process's other CUDA users (torch) are not affected.  The binding's fast
+calls (csrc/bcq_fast.cpp, a CPython module over torch's headers) become
+_fast.so next to it, with g++.
 """
 from __future__ import annotations
 
@@ -22,6 +24,8 @@ CSRC = os.path.join(HERE, "csrc")
 INCLUDE = os.path.join(ROOT, "include")
 OBJ = os.path.join(ROOT, "_build", "libbcq")
 LIB = os.path.join(HERE, "libbcq.so")
+FAST_SRC = os.path.join(CSRC, "bcq_fast.cpp")
+FAST = os.path.join(HERE, "_fast.so")
 
 ARCH = ["-gencode", "arch=compute_100a,code=sm_100a"]
 CFLAGS = ["-O3", "-std=c++17", "-lineinfo", "--expt-relaxed-constexpr",
@@ -72,7 +76,29 @@ def _compile(nvcc: str, src: str, verbose: bool) -> str:
     return obj
 
 
+def build_fast(force: bool = False) -> str:
+    """_fast.so against the torch of this interpreter (its headers and
+    libraries' names; nothing of it is loaded)."""
+    import importlib.util
+    import sysconfig
+    torch_dir = os.path.dirname(importlib.util.find_spec("torch").origin)
+    version = os.path.join(torch_dir, "version.py")
+    if force or _stale(FAST, [FAST_SRC, os.path.join(INCLUDE, "bcq.h"), version]):
+        cuda = os.environ.get("CUDA_HOME", "/usr/local/cuda")
+        inc = [os.path.join(torch_dir, "include"),
+               os.path.join(torch_dir, "include", "torch", "csrc", "api", "include"),
+               os.path.join(cuda, "include"), sysconfig.get_paths()["include"], INCLUDE]
+        tmp = FAST + f".tmp{os.getpid()}"
+        subprocess.run([os.environ.get("CXX", "g++"), "-O2", "-std=c++17", "-fPIC", "-shared", "-w",
+                        *[f"-I{d}" for d in inc], FAST_SRC, "-o", tmp,
+                        "-L" + os.path.join(torch_dir, "lib"), "-lc10", "-lc10_cuda", "-ltorch_cpu",
+                        "-ltorch_python"], check=True)
+        os.replace(tmp, FAST)
+    return FAST
+
+
 def build(force: bool = False, verbose: bool = False) -> str:
+    build_fast(force)
     nvcc = os.environ.get("NVCC", "nvcc")
     os.makedirs(OBJ, exist_ok=True)
     srcs = sources()

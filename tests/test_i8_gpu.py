@@ -231,6 +231,24 @@ def test_no_rows():
     assert api.gemm_i8(q, s, w, sw).shape == (0, 32)
 
 
+@pytest.mark.parametrize("M,K", [(1, 64), (5, 100), (40, 1000)])
+def test_fast_calls_are_the_same_calls(M, K):
+    """With the current stream named the binding takes its long way: the same bits."""
+    st = torch.cuda.current_stream()
+    x = _activations(M, K, BF16, 1)
+    q, s = api.quantize_i8(x)
+    q2, s2 = api.quantize_i8(x, stream=st)
+    assert torch.equal(q, q2) and torch.equal(s, s2) and q.stride(0) == q2.stride(0)
+    w, sw = _codes(70, K, 2)
+    for dtype in (F16, BF16, F32):
+        y = api.gemm_i8(q, s, w, sw, dtype=dtype)
+        assert torch.equal(y, api.gemm_i8(q, s, w, sw, dtype=dtype, stream=st)) and y.dtype == dtype
+        out = torch.empty_like(y)
+        assert api.gemm_i8(q, s, w, sw, dtype=dtype, out=out) is out and torch.equal(out, y)
+    y = api.linear_i8(x, w, sw)
+    assert torch.equal(y, api.linear_i8(x, w, sw, stream=st)) and y.dtype == BF16
+
+
 def test_side_stream_and_two_graphs_at_once():
     N, K = 600, 1024
     w, sw = api.quantize_i8(_activations(N, K, F16, 3, 0.02))

@@ -538,6 +538,31 @@ def test_captured_and_replayed_with_other_lengths():
             _check_attention(c, q, out, None, what=str(lens))
 
 
+def test_fast_calls_are_the_same_calls():
+    """With the current stream named the binding takes its long way: the same bits."""
+    st = torch.cuda.current_stream()
+    c, k, v = _append_case([40, 70], [5, 70], 2, 128, 16, BF16)
+    api.kv4_append(c.cache, k, v, c.t_table, c.t_len, c.t_cu)
+    d = Case([40, 70], [5, 70], 2, 128, 16)
+    api.kv4_append(d.cache, k, v, d.t_table, d.t_len, d.t_cu, stream=st)
+    for n in ("k", "k_param", "v", "v_param"):
+        a, b = getattr(c.cache, n), getattr(d.cache, n)
+        assert torch.equal(a.view(torch.uint8), b.view(torch.uint8))
+    for dtype in (F16, BF16, F32):
+        x = api.kv4_read(c.cache, c.t_table, c.t_len, c.t_cu, tokens=75, dtype=dtype)
+        y = api.kv4_read(c.cache, c.t_table, c.t_len, c.t_cu, tokens=75, dtype=dtype, stream=st)
+        assert x[0].dtype == dtype and all(torch.equal(a, b) for a, b in zip(x, y))
+    row = torch.randn(75, 1024 + 8, device="cuda").half()
+    q = row[:, :1024].view(75, 8, 128)
+    for kw in (dict(), dict(max_q=70, max_kv=70), dict(window=5, scale=0.3, return_lse=True), dict(causal=False),
+               dict(scale=1, return_lse=True, max_q=70)):
+        x = api.kv4_attention(q, c.cache, c.t_table, c.t_len, c.t_cu, **kw)
+        y = api.kv4_attention(q, c.cache, c.t_table, c.t_len, c.t_cu, stream=st, **kw)
+        x, y = (z if isinstance(z, tuple) else (z,) for z in (x, y))
+        assert len(x) == len(y) == 1 + bool(kw.get("return_lse"))
+        assert all(torch.equal(a, b) for a, b in zip(x, y))
+
+
 def test_side_stream():
     c = Case([500, 30], [1, 1], 2, 128, 16)
     q = _queries(2, 8, 128, F16)

@@ -183,6 +183,28 @@ def test_kv4_attention_refusals(L):
     assert _kv4(L, "attention", lse=P16 + 2) == api.BCQ_ERR_ALIGN
 
 
+# -------------------------------------------------------------- fast calls
+
+def test_fast_module_leaves_other_calls_alone(L):
+    """Bound to the library, and NotImplemented for whatever is no usual call:
+    tensors that are not on a GPU, other objects, other numbers of arguments."""
+    f = api._fast()
+    h, i = torch.zeros(4, 64, dtype=torch.float16), torch.zeros(4, 64, dtype=torch.int8)
+    for call in (f.quantize_i8, f.gemm_i8, f.linear_i8, f.kv4_append, f.kv4_read, f.kv4_attention):
+        for n in range(16):
+            assert call(*[h] * n) is NotImplemented
+            assert call(*[None] * n) is NotImplemented
+            assert call(*[i, "x", 1, None, 2.5][:n]) is NotImplemented
+    with pytest.raises(TypeError):
+        f.bind(1, 2)
+    with pytest.raises(ValueError):
+        f.bind(*[0] * 8)
+    for n, call in (("quantize_i8", lambda: api.quantize_i8(h)),
+                    ("linear_i8", lambda: api.linear_i8(h, i, h[0].float()))):
+        with pytest.raises(ValueError):
+            call()
+
+
 # -------------------------------------------------- refusals of the binding
 
 @pytest.fixture
@@ -198,6 +220,8 @@ def host(monkeypatch):
                     return 0
                 raise AssertionError(name + " was reached")
             return call
+    libbuild.build()
+    api._fast()
     monkeypatch.setattr(api, "lib", lambda: NoLibrary())
     return lambda *size, dtype=torch.float16: torch.zeros(*size, dtype=dtype).as_subclass(Cuda)
 
