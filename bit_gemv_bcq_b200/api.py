@@ -119,7 +119,7 @@ def lib():
         L.bcq_kv4_read.restype = I
         L.bcq_kv4_read.argtypes = [P, P, P, I, I, P, I, P, P, I, P]
         L.bcq_kv4_attention_workspace_bytes.restype = S
-        L.bcq_kv4_attention_workspace_bytes.argtypes = [P, I, I, I, I, I]
+        L.bcq_kv4_attention_workspace_bytes.argtypes = [P, I, I, I, I, I, I]
         L.bcq_kv4_attention.restype = I
         L.bcq_kv4_attention.argtypes = [P, P, Q, Q, I, I, I, P, I, P, P, I, I, I, I, I,
                                         ctypes.c_float, P, Q, Q, P, P, S, P]
@@ -981,7 +981,7 @@ def kv4_attention(q: torch.Tensor, cache: Kv4Cache, table: torch.Tensor, kv_len:
         max_q = 1 if cu is None else max(T, 1)
     if max_kv is None:
         max_kv = W * page_size
-    need = lib().bcq_kv4_attention_workspace_bytes(c, T, H, B, max_q, max_kv)
+    need = lib().bcq_kv4_attention_workspace_bytes(c, T, H, B, max_q, max_kv, window)
     ws = _new(q, (need,), torch.uint8, stream) if need else None
     _run("bcq_kv4_attention", index, c, q.data_ptr(), ldq, hdq, _DTYPES[q.dtype], T, H, p_table, W,
          p_len, p_cu, B, max_q, max_kv, 1 if causal else 0, window,

@@ -288,7 +288,7 @@ PyObject* kv4_attention(PyObject*, PyObject* const* a, Py_ssize_t n) {
       window > INT32_MAX)
     return no();
   const int64_t D = s.c.head_dim;
-  const size_t need = p_attention_bytes(&s.c, (int)T, (int)H, s.B, (int)max_q, (int)max_kv);
+  const size_t need = p_attention_bytes(&s.c, (int)T, (int)H, s.B, (int)max_q, (int)max_kv, (int)window);
   at::Tensor out = empty(*q, {T, H, D}, q->scalar_type()), lse, ws;
   if (lse_too) lse = empty(*q, {T, H}, at::kFloat);
   if (need) ws = empty(*q, {(int64_t)need}, at::kByte);

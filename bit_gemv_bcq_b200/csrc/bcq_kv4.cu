@@ -273,14 +273,12 @@ __global__ void __launch_bounds__(kRowThreads) kv4_read_kernel(const ReadParams 
 // Attention of few rows a key/value head: decode steps, drafts, short chunks.
 //
 // A warp takes 32 positions at a time, the codes as they lie in the cache.  A
-// byte of two codes, low + 16 high, masked out of a word is the fp16 subnormal
-// (low + 16 high) 2^-24, and its low nibble low 2^-24; the tensor core
-// multiplies both exactly, so codes become operands by one AND or byte permute
-// each, without a conversion, a scale or an offset.  With the two as operands
-//   q_l low + q_h high = (q_l - q_h / 16) low + (q_h / 16) (low + 16 high),
-// the first factor rounded to fp16, and of V's sums over positions the one of
-// the high codes is the difference of the bytes' and the low ones' over 16.
-// Scales and offsets are applied to the results,
+// nibble masked out of a word is the fp16 subnormal c 2^-24 (the high one of a
+// byte c 2^-20), which the tensor core multiplies exactly, so a code becomes
+// an operand by one AND, without a conversion, a scale or an offset: those are
+// applied to the results (for V, whole bytes low + 16 high stand in for the
+// high codes, one operation less; their sums' difference from the low codes'
+// over 16 is the high codes' sum),
 //   q . K_t = sum_g  a_tg (sum_{d in g} q_d c_td) + z_tg (sum_{d in g} q_d)
 //   out_d   = sum_t (p_t a_tg) c_td + sum_t p_t z_tg,
 // a few operations a position instead of one a value; the two sums with the
@@ -613,14 +611,11 @@ __global__ void __launch_bounds__(kFewWarps * 32, NT == 1 && D <= 128 ? 4 : 2) k
           x[e] *= mul;
           sum[g] += x[e];
         }
-        // a word's bytes in the order 0, 2 and 1, 3: for each pair what the low
-        // codes and what the bytes are multiplied with
-#pragma unroll
-        for (int i = 0; i < 2; ++i) {
-          const float h0 = x[2 * i + 1] * 0.0625f, h1 = x[2 * i + 5] * 0.0625f;
-          qf[nt][g][w][2 * i] = pack_f16(x[2 * i] - h0, x[2 * i + 4] - h1);
-          qf[nt][g][w][2 * i + 1] = pack_f16(h0, h1);
-        }
+        // code order in a word: values (0, 4), (1, 5) / 16, (2, 6), (3, 7) / 16
+        qf[nt][g][w][0] = pack_f16(x[0], x[4]);
+        qf[nt][g][w][1] = pack_f16(x[1] * 0.0625f, x[5] * 0.0625f);
+        qf[nt][g][w][2] = pack_f16(x[2], x[6]);
+        qf[nt][g][w][3] = pack_f16(x[3] * 0.0625f, x[7] * 0.0625f);
       }
       sum[g] += __shfl_xor_sync(0xFFFFFFFFu, sum[g], 1);
       sum[g] += __shfl_xor_sync(0xFFFFFFFFu, sum[g], 2);
@@ -695,18 +690,17 @@ __global__ void __launch_bounds__(kFewWarps * 32, NT == 1 && D <= 128 ? 4 : 2) k
 #pragma unroll
         for (int w = 0; w < 2; ++w) {
           const uint32_t x = w ? wa.y : wa.x, y = w ? wb.y : wb.x;
-          const uint32_t x0 = x & 0x00FF00FFu, y0 = y & 0x00FF00FFu;            // bytes 0 and 2
-          const uint32_t x1 = prmt(x, 0u, 0x4341), y1 = prmt(y, 0u, 0x4341);    // bytes 1 and 3
+          const uint32_t x2 = x >> 8, y2 = y >> 8;
 #pragma unroll
           for (int nt = 0; nt < NT; ++nt) {
             if (w == 0)
-              mma16816_new(acc[nt][g], x & 0x000F000Fu, y & 0x000F000Fu, x0, y0, qf[nt][g][w][0],
-                           qf[nt][g][w][1]);
+              mma16816_new(acc[nt][g], x & 0x000F000Fu, y & 0x000F000Fu, x & 0x00F000F0u,
+                           y & 0x00F000F0u, qf[nt][g][w][0], qf[nt][g][w][1]);
             else
-              mma16816(acc[nt][g], x & 0x000F000Fu, y & 0x000F000Fu, x0, y0, qf[nt][g][w][0],
-                       qf[nt][g][w][1]);
-            mma16816(acc[nt][g], x1 & 0x000F000Fu, y1 & 0x000F000Fu, x1, y1, qf[nt][g][w][2],
-                     qf[nt][g][w][3]);
+              mma16816(acc[nt][g], x & 0x000F000Fu, y & 0x000F000Fu, x & 0x00F000F0u,
+                       y & 0x00F000F0u, qf[nt][g][w][0], qf[nt][g][w][1]);
+            mma16816(acc[nt][g], x2 & 0x000F000Fu, y2 & 0x000F000Fu, x2 & 0x00F000F0u,
+                     y2 & 0x00F000F0u, qf[nt][g][w][2], qf[nt][g][w][3]);
           }
         }
       }
@@ -1155,18 +1149,25 @@ void plan_parts(AttentionPlan* f, int64_t units, int B, int max_kv, int each, do
   }
 }
 
-// The few-row kernel passes over the positions once for every 16 rows, four CTAs
-// an SM (two where rows or values are many); the many-row kernel once for every 256 (128 where D = 256).
-AttentionPlan plan_attention(const bcq_kv4* c, int q_heads, int B, int max_q, int max_kv) {
+// The few-row kernel passes over the positions once for every 16 rows, four
+// CTAs an SM (two where rows or values are many), with exact products of
+// queries and codes; the many-row kernel once for every 256 (128 where D =
+// 256), with keys rounded to fp16.  Over few positions those roundings do not
+// average out of lse (1e-5 of it below 500), and little is saved: such calls
+// stay with the first.
+AttentionPlan plan_attention(const bcq_kv4* c, int q_heads, int B, int max_q, int max_kv, int window) {
   AttentionPlan f;
   const int64_t rows = (int64_t)max_q * (q_heads / c->heads);
-  const bool many = rows > 48;
+  const bool many = rows > 48 && max_kv >= 512 && (window == 0 || window >= 512);
   f.nt = many ? 0 : rows <= 8 || c->head_dim == 256 ? 1 : 2;
   f.rows = !many ? 8 * f.nt : c->head_dim == 256 ? 128 : 256;
   f.row_blocks = (int)std::min<int64_t>((rows + f.rows - 1) / f.rows, INT32_MAX);
   const int64_t units = (int64_t)f.row_blocks * c->heads * B;
-  if (many) plan_parts(&f, units, B, max_kv, 1, 1024, 2048);
-  else plan_parts(&f, units, B, max_kv, f.nt == 1 && c->head_dim <= 128 ? 4 : 2, 160, 128);
+  // what a block of rows sees at most
+  const int seen = window == 0 ? max_kv
+                               : (int)std::min<int64_t>(max_kv, (int64_t)window + f.rows * c->heads / q_heads + 32);
+  if (many) plan_parts(&f, units, B, seen, 1, 1024, 2048);
+  else plan_parts(&f, units, B, seen, f.nt == 1 && c->head_dim <= 128 ? 4 : 2, 160, 128);
   return f;
 }
 
@@ -1295,11 +1296,11 @@ bcq_status bcq_kv4_read(const bcq_kv4* cache, void* k, void* v, int dtype, int T
 }
 
 size_t bcq_kv4_attention_workspace_bytes(const bcq_kv4* cache, int T, int q_heads, int B,
-                                         int max_q, int max_kv) {
+                                         int max_q, int max_kv, int window) {
   if (!cache || !cache_sizes_ok(cache) || !head_dim_ok(cache->head_dim) || T < 0 || B < 1 ||
-      max_q < 1 || max_kv < 1 || q_heads < 1 || q_heads % cache->heads)
+      max_q < 1 || max_kv < 1 || window < 0 || q_heads < 1 || q_heads % cache->heads)
     return 0;
-  const AttentionPlan f = plan_attention(cache, q_heads, B, max_q, max_kv);
+  const AttentionPlan f = plan_attention(cache, q_heads, B, max_q, max_kv, window);
   if (f.splits == 1) return 0;
   return (size_t)f.splits * (size_t)T * (size_t)q_heads * (size_t)(cache->head_dim + 2) * 4;
 }
@@ -1319,7 +1320,7 @@ bcq_status bcq_kv4_attention(const bcq_kv4* cache, const void* q, int64_t ld_q, 
   if ((s = check_rows(q, ld_q, hd_q, dtype)) != BCQ_OK) return s;
   if ((s = check_rows(out, ld_o, hd_o, dtype)) != BCQ_OK) return s;
   if (lse && !aligned(lse, 4)) return BCQ_ERR_ALIGN;
-  const size_t need = bcq_kv4_attention_workspace_bytes(cache, T, q_heads, B, max_q, max_kv);
+  const size_t need = bcq_kv4_attention_workspace_bytes(cache, T, q_heads, B, max_q, max_kv, window);
   if (need > 0) {
     if (!workspace || workspace_bytes < need) return BCQ_ERR_NULL;
     if (!aligned(workspace, 16)) return BCQ_ERR_ALIGN;
@@ -1342,7 +1343,7 @@ bcq_status bcq_kv4_attention(const bcq_kv4* cache, const void* q, int64_t ld_q, 
                        causal,
                        window,
                        scale};
-  const AttentionPlan f = plan_attention(cache, q_heads, B, max_q, max_kv);
+  const AttentionPlan f = plan_attention(cache, q_heads, B, max_q, max_kv, window);
   p.group = q_heads / cache->heads;
   p.rows = f.rows;
   p.row_blocks = f.row_blocks;

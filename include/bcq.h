@@ -526,7 +526,7 @@ bcq_status bcq_kv4_read(const bcq_kv4* cache, void* k, void* v, int dtype, int T
  * ones).  It depends on the host's bounds only, never on the lengths.
  */
 size_t bcq_kv4_attention_workspace_bytes(const bcq_kv4* cache, int T, int q_heads, int B,
-                                         int max_q, int max_kv);
+                                         int max_q, int max_kv, int window);
 
 /*
  * Attention of this call's rows over the cache (which holds their own K and V
