@@ -1158,7 +1158,7 @@ void plan_parts(AttentionPlan* f, int64_t units, int B, int max_kv, int each, do
 AttentionPlan plan_attention(const bcq_kv4* c, int q_heads, int B, int max_q, int max_kv, int window) {
   AttentionPlan f;
   const int64_t rows = (int64_t)max_q * (q_heads / c->heads);
-  const bool many = rows > 48 && max_kv >= 512 && (window == 0 || window >= 512);
+  const bool many = rows > 96 && max_kv >= 512 && (window == 0 || window >= 512);
   f.nt = many ? 0 : rows <= 8 || c->head_dim == 256 ? 1 : 2;
   f.rows = !many ? 8 * f.nt : c->head_dim == 256 ? 128 : 256;
   f.row_blocks = (int)std::min<int64_t>((rows + f.rows - 1) / f.rows, INT32_MAX);

@@ -50,7 +50,8 @@ struct ManyShape {
   static constexpr int kPerWarp = 32 / kPieces;              // positions a warp and pass
   static constexpr int kWords = kPasses * 4;
   static constexpr uint32_t kOffMask = kOffBar + 256;
-  static constexpr uint32_t kSmem = 1024 + kOffMask + 2 * 8 * kWords * 4;
+  static constexpr uint32_t kOffOdd = kOffMask + 2 * 8 * kWords * 4;  // whether any mask word is not zero
+  static constexpr uint32_t kSmem = 1024 + kOffOdd + 16;
   static constexpr int kOCol = 2 * kTiles * kTokens;         // tensor memory: S buffers, then O tiles
   // softmax, K's and V's codes, MMA.  Two tiles' 20 warps start with 96
   // registers a thread, 61440 in all, and share them anew by groups of four
@@ -185,6 +186,7 @@ __global__ void __launch_bounds__(ManyShape<D>::kThreads, 1) kv4_many_kernel(con
         mbar_init(p_full + 8 * i, 4);
       }
       for (int i = 0; i < 2; ++i) mbar_init(o_done + 8 * i, 1);
+      sts_f32(sbase + S::kOffOdd, 0.f);
       fence_mbar_init();
     }
     __syncwarp();
@@ -324,7 +326,10 @@ __global__ void __launch_bounds__(ManyShape<D>::kThreads, 1) kv4_many_kernel(con
         uint32_t az = x[i].az;
         const bool odd = odd_half2(az);
         const uint32_t word = __ballot_sync(0xFFFFFFFFu, is_v ? odd : x[i].gone);
-        if (lane == 0) word_at[i * 4 + w] = word;
+        if (lane == 0) {
+          word_at[i * 4 + w] = word;
+          if (word) sts_f32(sbase + S::kOffOdd, 1.f);
+        }
         if (is_v && odd) az = 0;
         const uint4 c = x[i].codes;
         const __half2 f = *reinterpret_cast<const __half2*>(&az);
@@ -375,33 +380,47 @@ __global__ void __launch_bounds__(ManyShape<D>::kThreads, 1) kv4_many_kernel(con
     float fs = 0.f, m = -INFINITY, l = 0.f;
     uint32_t poison = 0;  // groups of the output that a seen position makes NaN
     if (steps > 0) {
+      // all of a row at once (half, where it is 512 bytes), and again from L1
       const uint16_t* src = p.q + token * p.ld_q + (int64_t)h * p.hd_q;
-      float top = 0.f;
-#pragma unroll 4
-      for (int c = 0; c < D / 8; ++c) {
-        uint4 raw = make_uint4(0, 0, 0, 0);
-        if (live) raw = *reinterpret_cast<const uint4*>(src + c * 8);
-        const uint32_t x[4] = {raw.x, raw.y, raw.z, raw.w};
+      constexpr int kBatch = D / 8 < 16 ? D / 8 : 16;
+      uint4 raw[kBatch];
+      auto fetch = [&](int c0) {
 #pragma unroll
-        for (int e = 0; e < 8; ++e)
-          top = fmaxf(top, fabsf(bits_to_float<T>((x[e >> 1] >> (16 * (e & 1))) & 0xFFFFu)));
+        for (int c = 0; c < kBatch; ++c) {
+          raw[c] = make_uint4(0, 0, 0, 0);
+          if (live) raw[c] = *reinterpret_cast<const uint4*>(src + (c0 + c) * 8);
+        }
+      };
+      uint32_t top2 = 0;  // |x| by its bits, two at a time
+#pragma unroll
+      for (int c0 = 0; c0 < D / 8; c0 += kBatch) {
+        fetch(c0);
+#pragma unroll
+        for (int c = 0; c < kBatch; ++c)
+          top2 = __vmaxu2(__vmaxu2(__vmaxu2(top2, raw[c].x & 0x7FFF7FFFu), raw[c].y & 0x7FFF7FFFu),
+                          __vmaxu2(raw[c].z & 0x7FFF7FFFu, raw[c].w & 0x7FFF7FFFu));
       }
+      const float top = bits_to_float<T>(max(top2 & 0xFFFFu, top2 >> 16));  // not finite: power 0
       const int up = row_power(top);
       const float mul = p.scale < 0.f ? -power_of_two(up) : p.scale == 0.f ? 0.f : power_of_two(up);
       fs = score_factor(p.scale, -up);
       const uint32_t to = sbase + (uint32_t)t * S::kQTile + (uint32_t)r * 128u;
-#pragma unroll 4
-      for (int c = 0; c < D / 8; ++c) {
-        uint4 raw = make_uint4(0, 0, 0, 0);
-        if (live) raw = *reinterpret_cast<const uint4*>(src + c * 8);
-        const uint32_t x[4] = {raw.x, raw.y, raw.z, raw.w};
-        float f[8];
 #pragma unroll
-        for (int e = 0; e < 8; ++e) f[e] = bits_to_float<T>((x[e >> 1] >> (16 * (e & 1))) & 0xFFFFu) * mul;
-        const uint32_t at = to + (uint32_t)(c >> 3) * S::kQBlock + (uint32_t)(((c & 7) ^ (r & 7)) << 4);
-        asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(at), "r"(pack_f16(f[0], f[4])),
-                     "r"(pack_f16(f[1], f[5])), "r"(pack_f16(f[2], f[6])), "r"(pack_f16(f[3], f[7]))
-                     : "memory");
+      for (int c0 = 0; c0 < D / 8; c0 += kBatch) {
+        if (D / 8 > kBatch) fetch(c0);
+#pragma unroll
+        for (int c = 0; c < kBatch; ++c) {
+          const uint32_t x[4] = {raw[c].x, raw[c].y, raw[c].z, raw[c].w};
+          float f[8];
+#pragma unroll
+          for (int e = 0; e < 8; ++e)
+            f[e] = bits_to_float<T>((x[e >> 1] >> (16 * (e & 1))) & 0xFFFFu) * mul;
+          const int at8 = c0 + c;
+          const uint32_t at = to + (uint32_t)(at8 >> 3) * S::kQBlock + (uint32_t)(((at8 & 7) ^ (r & 7)) << 4);
+          asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(at), "r"(pack_f16(f[0], f[4])),
+                       "r"(pack_f16(f[1], f[5])), "r"(pack_f16(f[2], f[6])), "r"(pack_f16(f[3], f[7]))
+                       : "memory");
+        }
       }
       fence_proxy_async_smem();
       __syncwarp();
@@ -414,18 +433,10 @@ __global__ void __launch_bounds__(ManyShape<D>::kThreads, 1) kv4_many_kernel(con
       const int at = token / S::kPerWarp;
       return (word[at] >> (q * S::kPerWarp + token % S::kPerWarp)) & 1u;
     };
-    auto any_word = [&](const uint32_t* word) {
-      uint32_t all = 0;
-#pragma unroll
-      for (int i = 0; i < S::kWords; i += 4) {
-        const uint4 x = lds_v4(smem_u32(word + i));
-        all |= x.x | x.y | x.z | x.w;
-      }
-      return all != 0;
-    };
-    auto look_for_nan = [&](int j) {  // V's groups of step j, once its product is done
+    // Once something is odd (the words are rarely looked at): V's groups of step
+    // j, after its product.
+    auto look_for_nan = [&](int j) {
       const uint32_t* word = masks + (8 + (j & 7)) * S::kWords;
-      if (!any_word(word)) return;
       const uint32_t* gone = masks + (j & 7) * S::kWords;
       for (int k = 0; k < S::kTokens; ++k) {
         const int at = begin + j * S::kTokens + k;
@@ -434,19 +445,37 @@ __global__ void __launch_bounds__(ManyShape<D>::kThreads, 1) kv4_many_kernel(con
           if (marked(word, k, 2 * g)) poison |= 1u << g;
       }
     };
-    bool ok = true;
+    // The two tiles' warps of a scheduler take turns at the exponentials, which
+    // have a unit to themselves there: one's other work runs beside the other's.
+    // (Left alone they go in step, and the unit stands idle for both.)  Barrier
+    // 1 + 2 q + t is tile t's turn.
+    const bool turns = tiles == 2;
+    auto take_turn = [&]() {
+      if (turns) named_barrier_sync(1 + 2 * (warp & 3) + t, 64);
+    };
+    auto give_turn = [&]() {
+      if (turns) asm volatile("bar.arrive %0, 64;" ::"r"(1 + 2 * (warp & 3) + (t ^ 1)) : "memory");
+    };
+    if (steps > 0 && t == 1) give_turn();
+    int taken = 0;
+    bool ok = true, there = false;  // there: the next scores, seen ahead
     for (int j = 0; j < steps; ++j) {
       const uint32_t ts = ts0 + (uint32_t)((j & 1) * S::kTokens);
-      if (!(ok = wait(s_full + 8u * (2 * t + (j & 1)), j >> 1))) break;
+      if (!__all_sync(0xFFFFFFFFu, there) &&
+          !(ok = wait(s_full + 8u * (2 * t + (j & 1)), j >> 1)))
+        break;
       umma_fence_after();
+      // shared memory answers slowly while the tensor core reads its operands
+      // there: what is not needed at once is asked for ahead of the scores
+      const uint32_t odd = lds_u32v(sbase + S::kOffOdd);
       uint32_t s[2][32];
       tmem_ld32(ts, s[0]);
       tmem_ld32(ts + 32, s[1]);
       tmem_wait_ld();
-      if (j > 0) look_for_nan(j - 1);
+      const bool holes = __any_sync(0xFFFFFFFFu, odd != 0);
+      if (holes && j > 0) look_for_nan(j - 1);
       const int j0 = begin + j * S::kTokens;
       const uint32_t* gone = masks + (j & 7) * S::kWords;
-      const bool holes = any_word(gone);
       if (holes || j0 < lo_all || j0 + S::kTokens > hi_all) {
 #pragma unroll
         for (int k = 0; k < 64; ++k) {
@@ -484,6 +513,8 @@ __global__ void __launch_bounds__(ManyShape<D>::kThreads, 1) kv4_many_kernel(con
       const float base = m == -INFINITY ? 0.f : m;
       const uint64_t fs2 = pack_f32x2(fs, fs), base2 = pack_f32x2(-base, -base);
       uint64_t sum2[2] = {0, 0};
+      take_turn();
+      ++taken;
 #pragma unroll
       for (int c = 0; c < 2; ++c) {
         uint32_t w[16];
@@ -500,6 +531,8 @@ __global__ void __launch_bounds__(ManyShape<D>::kThreads, 1) kv4_many_kernel(con
         }
         tmem_st16(ts + (uint32_t)(16 * c), w);  // over scores that this thread has read
       }
+      give_turn();
+      there = j + 1 < steps && mbar_test(s_full + 8u * (2 * t + ((j + 1) & 1)), (uint32_t)((j + 1) >> 1) & 1u);
       float sa, sb;
       unpack_f32x2(add_f32x2(sum2[0], sum2[1]), sa, sb);
       l += sa + sb;
@@ -508,12 +541,13 @@ __global__ void __launch_bounds__(ManyShape<D>::kThreads, 1) kv4_many_kernel(con
       __syncwarp();
       if (lane == 0) mbar_arrive_cta(p_full + 8u * (2 * t + (j & 1)));
     }
+    for (; taken < steps; ++taken) give_turn();  // after a wait that ran out: the other tile's warp goes on
     if (steps > 0 && ok) {
       // the last scores come behind the product of two steps before, and a wait by
       // parity has to be for the next round but none: one round at a time
       ok = (steps < 2 || wait(o_done + 8u * t, steps - 2)) && wait(o_done + 8u * t, steps - 1);
       umma_fence_after();
-      if (ok) look_for_nan(steps - 1);
+      if (ok && lds_u32v(sbase + S::kOffOdd)) look_for_nan(steps - 1);
     }
     if (!ok) {
       give_up();
