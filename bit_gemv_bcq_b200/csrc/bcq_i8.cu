@@ -138,7 +138,8 @@ __global__ void __launch_bounds__(1024) quantize_i8_kernel(const uint16_t* __res
 
 // ------------------------------------------------------------- the product
 
-// y^T in tiles of R <= 128 rows of w by BT <= 256 rows of x: the weight's rows
+// y^T in tiles of R <= 128 rows of w by BT <= 512 rows of x, in one instruction
+// or two of at most 256: the weight's rows
 // are the tensor core's M (its lanes of tensor memory), the tokens its N, so a
 // single token costs no more than the 16 columns that an instruction has at
 // least, and y's rows are written along the lanes.  Both operands come in
@@ -168,7 +169,8 @@ struct GemmParams {
   int64_t ldy;
   int M, N, K;
   int R, BT, rows;      // tile (PAIR: R rows for each CTA); rows the tensor core takes of w, 64 or 128
-  int BX;               // rows of x that a CTA holds (BT, or half of it)
+  int BS;               // rows of x of an instruction
+  int BX;               // of those, what a CTA holds (BS, or half of it)
   int mt, tiles;        // tiles along M, in all
   int KB, G, KG;        // blocks of K, blocks a stage, stages' worth of K
   int stages;           // ring depth
@@ -211,7 +213,9 @@ struct GemmCursor {
   }
 };
 
-template <typename TO, bool PAIR>
+// PAIR: see above; SUBS: instructions along the tile's rows of x (two in pairs
+// only; loops over them would slow the issue of small tiles' copies).
+template <typename TO, bool PAIR, int SUBS>
 __global__ void __launch_bounds__(kGemmThreads, 1)
     gemm_i8_kernel(const __grid_constant__ CUtensorMap wmap, const __grid_constant__ CUtensorMap xmap,
                    const GemmParams p) {
@@ -269,7 +273,7 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
     const bool one = elect_one(), is_w = warp == 0;
     const CUtensorMap* map = is_w ? &wmap : &xmap;
     const uint32_t block = is_w ? p.a_block : p.b_block, base = sbase + (is_w ? 0u : p.b_off);
-    const uint32_t bytes = (uint32_t)(is_w ? p.R : p.BX) * kKBlock * (PAIR ? 2u : 1u);  // of both CTAs
+    const uint32_t bytes = (uint32_t)(is_w ? p.R : SUBS * p.BX) * kKBlock * (PAIR ? 2u : 1u);  // of both CTAs
     // x's codes come from the kernel before; the first weights need not wait for it
     if (!is_w && p.overlap) grid_dependency_wait();
     GemmCursor c;
@@ -293,13 +297,13 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
         const uint32_t bar = full + 8u * c.slot;
         uint32_t to = base + (uint32_t)(c.slot * p.G) * block;
         if (rank == 0) mbar_arrive_expect_tx(bar, bytes * (uint32_t)n);
-        if (PAIR) {
-          const uint32_t leader = map_rank(bar, 0);
-          for (int j = 0; j < n; ++j, to += block)
-            tma_load_2d_pair(to, map, (kb + j) * (int)kKBlock, row, leader);
-        } else {
-          for (int j = 0; j < n; ++j, to += block)
-            tma_load_2d(to, map, (kb + j) * (int)kKBlock, row, bar);
+        const uint32_t leader = PAIR ? map_rank(bar, 0) : bar;
+        for (int j = 0; j < n; ++j, to += block) {
+          const int k = (kb + j) * (int)kKBlock;
+          if (PAIR) tma_load_2d_pair(to, map, k, row, leader);
+          else tma_load_2d(to, map, k, row, bar);
+          if (SUBS == 2 && !is_w)
+            tma_load_2d_pair(to + (uint32_t)p.BX * kKBlock, map, k, row + p.BS, leader);
         }
       }
       if (c.step(p.KG, S, p.workers)) row = first_row();
@@ -308,8 +312,8 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
     // --------------------------------------------------------------- the sums
     const int issuer = warp < 4 ? warp - 2 : warp - 10;
     const bool one = elect_one();
-    // kind::i8: int32 D, signed A and B, both K-major, N = BT, M = rows
-    const uint32_t idesc = (2u << 4) | (1u << 7) | (1u << 10) | ((uint32_t)(p.BT >> 3) << 17) |
+    // kind::i8: int32 D, signed A and B, both K-major, N = BS, M = rows
+    const uint32_t idesc = (2u << 4) | (1u << 7) | (1u << 10) | ((uint32_t)(p.BS >> 3) << 17) |
                            ((uint32_t)((PAIR ? 256 : p.rows) >> 4) << 24);
     const uint64_t ad0 = umma_desc_sw128(sbase), bd0 = umma_desc_sw128(sbase + p.b_off);
     const uint32_t a_units = p.a_block >> 4, b_units = p.b_block >> 4;  // never carry out of the address
@@ -345,6 +349,14 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
               if (rest > 32) mma(d, ad + 2, bd + 2, idesc, 1u);
               if (rest > 64) mma(d, ad + 4, bd + 4, idesc, 1u);
               if (rest > 96) mma(d, ad + 6, bd + 6, idesc, 1u);
+              if (SUBS == 2) {
+                const uint64_t bs = bd + (uint32_t)p.BX * (kKBlock >> 4);
+                const uint32_t ds = d + (uint32_t)p.BS;
+                mma(ds, ad, bs, idesc, more);
+                if (rest > 32) mma(ds, ad + 2, bs + 2, idesc, 1u);
+                if (rest > 64) mma(ds, ad + 4, bs + 4, idesc, 1u);
+                if (rest > 96) mma(ds, ad + 6, bs + 6, idesc, 1u);
+              }
               more = 1;
             }
             commit(empty + 8u * c.slot);
@@ -379,7 +391,7 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
       const float swn = row ? p.sw[n] : 0.f;
       // the tile's sx, fetched while it is summed; two buffers, and the barrier
       // of the next tile parts their uses
-      const uint32_t sxs = sx_off + (uint32_t)(t & 1) * 1024u;
+      const uint32_t sxs = sx_off + (uint32_t)(t & 1) * 2048u;
       for (int c = (int)threadIdx.x - 128; c < p.BT; c += 256)
         sts_f32(sxs + 4u * c, c < cols ? p.sx[m0 + c] : 0.f);
       named_barrier_sync(1, 256);
@@ -509,7 +521,8 @@ bool encode_codes(CUtensorMap* map, const int8_t* p, int64_t rows, int64_t K, in
 
 int round_up(int v, int to) { return (v + to - 1) / to * to; }
 
-// The tile, and whether CTAs work in pairs, that a model of one SM's time likes
+// The tile and the kernel (*kind: 0 single CTAs, 1 pairs, 2 pairs with two
+// instructions along x's rows) that a model of one SM's time likes
 // best.  A block of K takes the longest of: the tensor core (BT / 2 cycles for
 // each of its four instructions), shared memory's reads by it (128 rows of w
 // and those of x at 128 bytes a cycle), the operands' way from L2 (about 50
@@ -517,51 +530,59 @@ int round_up(int v, int to) { return (v + to - 1) / to * to; }
 // the memory's rate (about 24 bytes a cycle an SM).  Rounds of tiles count
 // whole; a tile's output costs about 15 cycles a column when nothing hides it,
 // a pair's start some 1000 cycles.
-void plan_gemm(int M, int N, int K, int sms, GemmParams* p, size_t* smem, int* grid, bool* pair) {
+void plan_gemm(int M, int N, int K, int sms, GemmParams* p, size_t* smem, int* grid, int* kind) {
   const int KB = (K + (int)kKBlock - 1) / (int)kKBlock;
   double best = 0;
   const int mt0 = (M + 255) / 256;
   for (int two = 0; two < 2; ++two) {
     const int workers = two ? sms / 2 : sms;
-    for (int mt = mt0; mt <= mt0 + 4; ++mt) {
-      const int BT = round_up((M + mt - 1) / mt, two ? 32 : 16);
-      if ((int64_t)BT * (mt - 1) >= M || (two && BT < 64)) continue;
-      const int rows_most = two ? 256 : 128;
-      const int64_t least = ((int64_t)(N + rows_most - 1) / rows_most * mt + workers - 1) / workers;
-      for (int64_t rounds = least; rounds <= least + 2; ++rounds) {
-        const int64_t nt_most = std::max<int64_t>(1, rounds * workers / mt);
-        int64_t rows = std::min<int64_t>(rows_most, std::max<int64_t>(8, (N + nt_most - 1) / nt_most));
-        if (two) rows = (rows + 1) / 2 * 2;
-        const int R = (int)(two ? rows / 2 : rows);
-        const int64_t nt = (N + rows - 1) / rows, tiles = nt * mt, whole = (tiles + workers - 1) / workers;
-        const int BX = two ? BT / 2 : BT;
-        const double core = 4.0 * std::max(BT / 2.0, 32.0 + BX / 4.0);
-        const double l2 = 128.0 * (R + BX) / 50.0, dram = mt == 1 ? 128.0 * R / 24.0 : 0;
-        const double cost = whole * KB * std::max(core, std::max(l2, dram)) + 15.0 * BT + 20.0 * whole + (two ? 1000.0 : 0.0);
-        if (best == 0 || cost < best) {
-          best = cost;
-          p->R = std::min(R, N);
-          p->BT = BT;
-          p->BX = BX;
-          p->mt = mt;
-          p->tiles = (int)tiles;
-          p->workers = (int)std::min<int64_t>(workers, tiles);
-          *pair = two != 0;
+    for (int subs = 1; subs <= 1 + two; ++subs) {
+      for (int mt = (M + 256 * subs - 1) / (256 * subs); mt <= mt0 + 4; ++mt) {
+        const int BS = round_up((M + mt * subs - 1) / (mt * subs), two ? 32 : 16), BT = subs * BS;
+        if ((int64_t)BT * (mt - 1) >= M || (two && BS < 64) || (subs == 2 && BS < 128) || BS > 256) continue;
+        const int rows_most = two ? 256 : 128;
+        const int64_t least = ((int64_t)(N + rows_most - 1) / rows_most * mt + workers - 1) / workers;
+        for (int64_t rounds = least; rounds <= least + 2; ++rounds) {
+          const int64_t nt_most = std::max<int64_t>(1, rounds * workers / mt);
+          int64_t rows = std::min<int64_t>(rows_most, std::max<int64_t>(8, (N + nt_most - 1) / nt_most));
+          if (two) rows = (rows + 1) / 2 * 2;
+          const int R = (int)(two ? rows / 2 : rows);
+          const int64_t nt = (N + rows - 1) / rows, tiles = nt * mt, whole = (tiles + workers - 1) / workers;
+          const int BX = two ? BS / 2 : BS;
+          const double core = 4.0 * subs * std::max(BS / 2.0, 32.0 + BX / 4.0);
+          const double l2 = 128.0 * (R + subs * BX) / 50.0, dram = mt == 1 ? 128.0 * R / 24.0 : 0;
+          // outputs that no other tile's sums hide: the last tile's, or all
+          // where tensor memory has no room for a second set of accumulators
+          const double out = 15.0 * BT * (2 * BT > 512 ? whole : 1);
+          const double cost = whole * (KB * std::max(core, std::max(l2, dram)) + 20.0) + out + (two ? 1000.0 : 0.0);
+          if (best == 0 || cost < best) {
+            best = cost;
+            p->R = std::min(R, N);
+            p->BT = BT;
+            *kind = two + subs - 1;
+            p->BS = BS;
+            p->BX = BX;
+            p->mt = mt;
+            p->tiles = (int)tiles;
+            p->workers = (int)std::min<int64_t>(workers, tiles);
+          }
         }
       }
     }
   }
+  const bool pair = *kind > 0;
+  const int subs = *kind == 2 ? 2 : 1;
   p->KB = KB;
-  p->bufs = p->tiles > p->workers ? 2 : 1;
-  p->rows = p->R <= 64 && !*pair ? 64 : 128;
+  p->bufs = p->tiles > p->workers && 2 * p->BT <= 512 ? 2 : 1;
+  p->rows = p->R <= 64 && !pair ? 64 : 128;
   p->a_block = (uint32_t)round_up(p->R, 8) * kKBlock;
-  p->b_block = (uint32_t)p->BX * kKBlock;
+  p->b_block = (uint32_t)(subs * p->BX) * kKBlock;
   const uint32_t block = p->a_block + p->b_block;
   // about 24 KB a stage: a wait costs the MMA warp about 100 cycles, as long
   // as the four instructions of a small block of K take
   p->G = std::max(1, std::min({8, KB, (int)(24576 / block)}));
   p->KG = (KB + p->G - 1) / p->G;
-  const size_t room = kMaxSmem - 1024 /* alignment */ - 16 * kMaxGemmStages - 96 - 2048 /* sx */;
+  const size_t room = kMaxSmem - 1024 /* alignment */ - 16 * kMaxGemmStages - 96 - 4096 /* sx */;
   const uint32_t overrun = (uint32_t)p->rows * kKBlock;  // read of the last block of w, beyond R
   int S = (int)std::min<size_t>(kMaxGemmStages, room / (block * (uint32_t)p->G));
   while (S > 1 && (size_t)S * p->G * p->a_block + overrun > room) --S;
@@ -576,8 +597,8 @@ void plan_gemm(int M, int N, int K, int sms, GemmParams* p, size_t* smem, int* g
   uint32_t cols = 32;
   while (cols < (uint32_t)(p->bufs * p->issuers * p->BT)) cols *= 2;
   p->tmem_cols = cols;
-  *smem = 1024 + p->bar_off + 16 * (size_t)S + 96 + 2048;
-  *grid = *pair ? 2 * p->workers : p->workers;
+  *smem = 1024 + p->bar_off + 16 * (size_t)S + 96 + 4096;
+  *grid = pair ? 2 * p->workers : p->workers;
   p->tiles_each = p->tiles / p->workers;
   p->tiles_more = p->tiles % p->workers;
   p->kg_step = ((uint32_t)p->KG << 16) / (uint32_t)p->workers;
@@ -592,11 +613,11 @@ int sm_count() {
   return n;
 }
 
-template <typename TO, bool PAIR>
+template <typename TO, bool PAIR, int SUBS>
 cudaError_t launch_gemm_t(const CUtensorMap& wmap, const CUtensorMap& xmap, const GemmParams& p,
                           size_t smem, int grid, cudaStream_t st) {
   static std::atomic<uint64_t> done{0};
-  const cudaError_t e = allow_smem(gemm_i8_kernel<TO, PAIR>, kMaxSmem, done);
+  const cudaError_t e = allow_smem(gemm_i8_kernel<TO, PAIR, SUBS>, kMaxSmem, done);
   if (e != cudaSuccess) return e;
   cudaLaunchAttribute attr[2] = {};
   int n = 0;
@@ -617,7 +638,7 @@ cudaError_t launch_gemm_t(const CUtensorMap& wmap, const CUtensorMap& xmap, cons
   cfg.stream = st;
   cfg.attrs = attr;
   cfg.numAttrs = (unsigned)n;
-  return cudaLaunchKernelEx(&cfg, gemm_i8_kernel<TO, PAIR>, wmap, xmap, p);
+  return cudaLaunchKernelEx(&cfg, gemm_i8_kernel<TO, PAIR, SUBS>, wmap, xmap, p);
 }
 
 // overlap: the kernel before in the stream is the quantiser, whose codes and
@@ -639,16 +660,17 @@ cudaError_t launch_gemm(const int8_t* x, int64_t ldx, const float* sx, const int
   p.overlap = overlap;
   size_t smem = 0;
   int grid = 0;
-  bool pair = false;
-  plan_gemm(M, N, K, sms, &p, &smem, &grid, &pair);
+  int kind = 0;
+  plan_gemm(M, N, K, sms, &p, &smem, &grid, &kind);
   CUtensorMap wmap, xmap;
   if (!encode_codes(&wmap, w, N, K, ldw, (uint32_t)p.R) ||
       !encode_codes(&xmap, x, M, K, ldx, (uint32_t)p.BX))
     return cudaErrorInvalidValue;
   auto launch = [&](auto* type) {
     using TO = std::remove_pointer_t<decltype(type)>;
-    return pair ? launch_gemm_t<TO, true>(wmap, xmap, p, smem, grid, st)
-                : launch_gemm_t<TO, false>(wmap, xmap, p, smem, grid, st);
+    return kind == 2   ? launch_gemm_t<TO, true, 2>(wmap, xmap, p, smem, grid, st)
+           : kind == 1 ? launch_gemm_t<TO, true, 1>(wmap, xmap, p, smem, grid, st)
+                       : launch_gemm_t<TO, false, 1>(wmap, xmap, p, smem, grid, st);
   };
   if (dtype == BCQ_F32) return launch((float*)nullptr);
   if (dtype == BCQ_F16) return launch((__half*)nullptr);

@@ -89,21 +89,34 @@ constexpr int kRowThreads = 256;
 
 // Where kRows rows from t0 on go, found by the whole block: place[i] = index of
 // the vector of head 0 (the other heads' lie page_size apart), -1 for a
-// position that the cache does not have, -2 for a row of no sequence.
+// position that the cache does not have, -2 for a row of no sequence.  Two
+// loads one after the other: the sequences' first rows and lengths (up to 256
+// of them, the usual case, kept in shared memory), then the table.
 template <int kRows>
-__device__ __forceinline__ void locate_rows(const Places& p, int t0, int T, int64_t* place,
-                                            int* count) {
+struct RowPlaces {
+  int64_t place[kRows];
+  int count[kRows];
+  int cu[kRowThreads + 1], len[kRowThreads];
+};
+template <int kRows>
+__device__ __forceinline__ void locate_rows(const Places& p, int t0, int T, RowPlaces<kRows>& s) {
   const int tid = threadIdx.x;
+  const bool kept = p.B <= kRowThreads;
   if (p.cu) {
-    if (tid < kRows) count[tid] = 0;
+    if (tid < kRows) s.count[tid] = 0;
+    if (kept) {
+      if (tid == 0) s.cu[0] = p.cu[0];
+      if (tid < p.B) s.len[tid] = p.kv_len[tid];
+    }
     __syncthreads();
     // row t's sequence: how many of cu[1..B] are not above t
     for (int b0 = 1; b0 <= p.B; b0 += kRowThreads) {
       const int end = b0 + tid <= p.B ? p.cu[b0 + tid] : INT32_MAX;
+      if (kept && b0 + tid <= p.B) s.cu[b0 + tid] = end;
 #pragma unroll
       for (int i = 0; i < kRows; ++i) {
         const int n = __popc(__ballot_sync(0xFFFFFFFFu, end <= t0 + i));
-        if ((tid & 31) == 0 && n) atomicAdd(&count[i], n);
+        if ((tid & 31) == 0 && n) atomicAdd(&s.count[i], n);
       }
     }
     __syncthreads();
@@ -111,13 +124,23 @@ __device__ __forceinline__ void locate_rows(const Places& p, int t0, int T, int6
   if (tid < kRows) {
     const int t = t0 + tid;
     int64_t at = -2;
-    const int b = p.cu ? count[tid] : t;
-    if (t < T && b < p.B && (!p.cu || t >= p.cu[0])) {
-      const int2 rows = rows_of(p, b);
-      at = vector_at(p, b, p.kv_len[b] - rows.y + (t - rows.x), 0);
+    const int b = p.cu ? s.count[tid] : t;
+    if (t < T && b < p.B && (!p.cu || t >= (kept ? s.cu[0] : p.cu[0]))) {
+      int first = t, n = 1, len;
+      if (p.cu && kept) {
+        first = s.cu[b];
+        n = s.cu[b + 1] - first;
+        len = s.len[b];
+      } else {
+        const int2 rows = rows_of(p, b);
+        first = rows.x;
+        n = rows.y;
+        len = p.kv_len[b];
+      }
+      at = vector_at(p, b, len - n + (t - first), 0);
     }
     if (at == -1) record_error(&g_kv4_error, BCQ_ERR_PAGE);
-    place[tid] = at;
+    s.place[tid] = at;
   }
   __syncthreads();
 }
@@ -142,74 +165,98 @@ struct Pair16<__nv_bfloat16> {
   using V = __nv_bfloat162;
 };
 
-// A block takes kRows rows; eight lanes a group of 64, eight values a lane, one
-// 32-bit word of codes.  Least and greatest come from packed 16-bit compares
-// that keep a NaN.  The codes' quotient is taken in fp32 with a rounded
-// reciprocal and rounded by adding 1.5 2^23 (conversion instructions run at an
-// eighth of the rate); where it lies within 1e-4 of a half (its error is below
-// 16 * 4 * 2^-24 < 4e-6, and the difference's rounding adds less) the half
-// decides in fp64, where x - z and (c + 1/2) a are exact.
+// A block takes kRows rows, whose values it asks for before it knows their
+// places; eight lanes a group of 64, eight values a lane, one 32-bit word of
+// codes.  Least and greatest come from packed 16-bit compares that keep a NaN.
+// (hi - lo) / 15 is a product with fp32(1 / 15) and Markstein's correction by
+// the remainder, which gives the correctly rounded quotient.  A code's quotient
+// is taken in fp32 with an approximate reciprocal, clamped by the saturation of
+// its fifteenth to 0..1, and rounded by adding 1.5 2^23; conversions, which
+// run at an eighth of the rate, are left out, and four codes become 16 bits by
+// fused multiply-adds.  Where a quotient lies within 1e-4 of a half (its error is
+// below 16 * 6 * 2^-24 < 6e-6, and the difference's rounding adds less) the
+// half decides in fp64, where x - z and (c + 1/2) a are exact.
 template <typename T, int D, int kRows>
-__global__ void __launch_bounds__(kRowThreads) kv4_append_kernel(const AppendParams p) {
+__global__ void __launch_bounds__(kRowThreads, 4) kv4_append_kernel(const AppendParams p) {
   using V = typename Pair16<T>::V;
   constexpr int G = D / kKvGroup, kWords = D / 8;
-  __shared__ int64_t place[kRows];
-  __shared__ int count[kRows];
+  constexpr float kMagic = 12582912.f;  // 1.5 * 2^23: adding it rounds to an integer, halves to even
+  __shared__ RowPlaces<kRows> places;
   const int t0 = (int)blockIdx.x * kRows, heads = p.at.heads;
-  locate_rows<kRows>(p.at, t0, p.T, place, count);
-  for (int i = threadIdx.x; i < 2 * heads * kWords; i += kRowThreads) {
-    const int kv = i >= heads * kWords;
-    const int in = kv ? i - heads * kWords : i;
-    const int h = in / kWords, word = in % kWords;
-    const uint16_t* x = p.x[kv] + (int64_t)h * p.hd[kv] + word * 8;
-    uint4 raw[kRows];
+  const int items = 2 * heads * kWords, lane = threadIdx.x & 31;
+  uint4 raw[kRows];
+  auto fetch = [&](int i) {
+    const int kv = i >= heads * kWords, in = kv ? i - heads * kWords : i;
+    // (chosen, not indexed: a param array with a thread's index is loaded by the lane)
+    const int64_t ld = kv ? p.ld[1] : p.ld[0], hd = kv ? p.hd[1] : p.hd[0];
+    const uint16_t* x = (kv ? p.x[1] : p.x[0]) + (int64_t)(in / kWords) * hd + in % kWords * 8 + t0 * ld;
 #pragma unroll
-    for (int j = 0; j < kRows; ++j) {
+    for (int j = 0; j < kRows; ++j, x += ld) {
       raw[j] = make_uint4(0, 0, 0, 0);
-      if (place[j] >= 0) raw[j] = ldg_nc_v4(x + (int64_t)(t0 + j) * p.ld[kv]);
+      if (t0 + j < p.T && i < items) raw[j] = ldg_nc_v4(x);
     }
-    const uint32_t mask = 0xFFu << (threadIdx.x & 24);
+  };
+  fetch(threadIdx.x);
+  locate_rows<kRows>(p.at, t0, p.T, places);
+  for (int i = threadIdx.x; i - lane < items; i += kRowThreads) {  // whole warps
+    const int kv = i >= heads * kWords, in = kv ? i - heads * kWords : i;
+    const int h = in / kWords, word = in % kWords;
+    if (i >= kRowThreads) fetch(i);
+    uint8_t* const code = (kv ? p.code[1] : p.code[0]) + word * 4;
+    __half2* const param = (kv ? p.param[1] : p.param[0]) + word / 8;
+    const int64_t to_head = (int64_t)h * p.at.page_size;
 #pragma unroll
     for (int j = 0; j < kRows; ++j) {
-      if (place[j] < 0) continue;
+      const int64_t place = places.place[j];
+      if (place < 0) continue;  // for all of the block
       const uint32_t w[4] = {raw[j].x, raw[j].y, raw[j].z, raw[j].w};
       const V* v2 = reinterpret_cast<const V*>(w);
-      V lo2 = __hmin2_nan(__hmin2_nan(v2[0], v2[1]), __hmin2_nan(v2[2], v2[3]));
-      V hi2 = __hmax2_nan(__hmax2_nan(v2[0], v2[1]), __hmax2_nan(v2[2], v2[3]));
+      const V lo2 = __hmin2_nan(__hmin2_nan(v2[0], v2[1]), __hmin2_nan(v2[2], v2[3]));
+      const V hi2 = __hmax2_nan(__hmax2_nan(v2[0], v2[1]), __hmax2_nan(v2[2], v2[3]));
+      V ends;  // (lo, -hi): the least of both
+      ends.x = __hmin_nan(lo2.x, lo2.y);
+      ends.y = __hneg(__hmax_nan(hi2.x, hi2.y));
 #pragma unroll
-      for (int o = 1; o < 8; o <<= 1) {
-        lo2 = __hmin2_nan(lo2, __shfl_xor_sync(mask, lo2, o));
-        hi2 = __hmax2_nan(hi2, __shfl_xor_sync(mask, hi2, o));
-      }
-      const T lo16 = __hmin_nan(lo2.x, lo2.y), hi16 = __hmax_nan(hi2.x, hi2.y);
-      const float lo = (float)lo16, hi = (float)hi16;
+      for (int o = 1; o < 8; o <<= 1) ends = __hmin2_nan(ends, __shfl_xor_sync(0xFFFFFFFFu, ends, o));
+      const float lo = (float)ends.x, hi = -(float)ends.y;
       const bool ok = lo >= -kKvRange && hi <= kKvRange;  // false for a NaN
-      const __half a16 = __float2half_rn(__fdiv_rn(__fsub_rn(hi, lo), 15.f));
+      const float d = __fsub_rn(hi, lo), r15 = 1.f / 15.f;
+      const float q15 = __fmul_rn(d, r15);
+      const __half a16 = __float2half_rn(__fmaf_rn(__fmaf_rn(q15, -15.f, d), r15, q15));
       const __half z16 = __float2half_rn(lo);
       const float a = __half2float(a16), z = __half2float(z16);
       uint32_t codes = 0;
       if (ok && a > 0.f) {
-        const float inv = __fdiv_rn(1.f, a);
+        const float inv = __fdividef(1.f, a * 15.f);
+        float f[8], c[8], off = 0.f;
 #pragma unroll
         for (int e = 0; e < 8; ++e) {
-          const float f = bits_to_float<T>((w[e >> 1] >> (16 * (e & 1))) & 0xFFFFu);
-          const float q = fminf(fmaxf((f - z) * inv, 0.f), 15.f);
-          const float up = q + 12582912.f;  // 1.5 * 2^23: the nearest integer, halves to even
-          uint32_t c = __float_as_uint(up);
-          if (fabsf(q - (up - 12582912.f)) > 0.4999f) {
-            const float below = floorf(q);  // the half in question is below + 1/2
-            const double d = (double)f - (double)z, edge = ((double)below + 0.5) * (double)a;
-            c = (uint32_t)below;
-            c += d > edge || (d == edge && (c & 1u));
-          }
-          codes |= (c & 15u) << (4 * e);
+          f[e] = bits_to_float<T>((w[e >> 1] >> (16 * (e & 1))) & 0xFFFFu);
+          const float q = __saturatef((f[e] - z) * inv);  // of 15
+          c[e] = __fsub_rn(__fmaf_rn(q, 15.f, kMagic), kMagic);
+          off = fmaxf(off, fabsf(__fmaf_rn(q, 15.f, -c[e])));
         }
+        if (off > 0.4999f) {
+#pragma unroll
+          for (int e = 0; e < 8; ++e) {
+            const float v = __saturatef((f[e] - z) * inv) * 15.f;
+            if (fabsf(v - c[e]) > 0.4999f) {
+              const float below = floorf(v);  // the half in question is below + 1/2
+              const double x = (double)f[e] - (double)z, edge = ((double)below + 0.5) * (double)a;
+              c[e] = below + (x > edge || (x == edge && ((int)below & 1)) ? 1.f : 0.f);
+            }
+          }
+        }
+        const float lo16 = fmaf(c[3], 4096.f, fmaf(c[2], 256.f, fmaf(c[1], 16.f, c[0])));
+        const float hi16 = fmaf(c[7], 4096.f, fmaf(c[6], 256.f, fmaf(c[5], 16.f, c[4])));
+        codes = prmt(__float_as_uint(lo16 + 8388608.f), __float_as_uint(hi16 + 8388608.f), 0x5410);
       }
-      const int64_t vec = place[j] + (int64_t)h * p.at.page_size;
-      *reinterpret_cast<uint32_t*>(p.code[kv] + vec * (D / 2) + word * 4) = codes;
+      if (i >= items) continue;
+      const int64_t vec = place + to_head;
+      *reinterpret_cast<uint32_t*>(code + vec * (D / 2)) = codes;
       if (word % 8 == 0) {
         const __half nan = __ushort_as_half(0x7E00);
-        p.param[kv][vec * G + word / 8] = ok ? __halves2half2(a16, z16) : __halves2half2(nan, nan);
+        param[vec * G] = ok ? __halves2half2(a16, z16) : __halves2half2(nan, nan);
       }
     }
   }
@@ -227,14 +274,17 @@ struct ReadParams {
 template <typename TO, int D, int kRows>
 __global__ void __launch_bounds__(kRowThreads) kv4_read_kernel(const ReadParams p) {
   constexpr int G = D / kKvGroup, kWords = D / 8;
-  __shared__ int64_t place[kRows];
-  __shared__ int count[kRows];
+  __shared__ RowPlaces<kRows> places;
+  const int64_t* place = places.place;
   const int t0 = (int)blockIdx.x * kRows, heads = p.at.heads;
-  locate_rows<kRows>(p.at, t0, p.T, place, count);
+  locate_rows<kRows>(p.at, t0, p.T, places);
   for (int i = threadIdx.x; i < 2 * heads * kWords; i += kRowThreads) {
     const int kv = i >= heads * kWords;
     const int in = kv ? i - heads * kWords : i;
     const int h = in / kWords, word = in % kWords;
+    const uint8_t* const code = (kv ? p.code[1] : p.code[0]) + 4 * word;
+    const __half2* const param = (kv ? p.param[1] : p.param[0]) + word / 8;
+    const int64_t to_head = (int64_t)h * p.at.page_size;
     uint32_t codes[kRows];
     __half2 az[kRows];
 #pragma unroll
@@ -242,12 +292,12 @@ __global__ void __launch_bounds__(kRowThreads) kv4_read_kernel(const ReadParams 
       codes[j] = 0;
       az[j] = __floats2half2_rn(0.f, 0.f);
       if (place[j] >= 0) {
-        const int64_t vec = place[j] + (int64_t)h * p.at.page_size;
-        codes[j] = *reinterpret_cast<const uint32_t*>(p.code[kv] + vec * (D / 2) + 4 * word);
-        az[j] = p.param[kv][vec * G + word / 8];
+        const int64_t vec = place[j] + to_head;
+        codes[j] = *reinterpret_cast<const uint32_t*>(code + vec * (D / 2));
+        az[j] = param[vec * G];
       }
     }
-    TO* y = static_cast<TO*>(p.y[kv]) + ((int64_t)t0 * heads + h) * D + 8 * word;
+    TO* y = static_cast<TO*>(kv ? p.y[1] : p.y[0]) + ((int64_t)t0 * heads + h) * D + 8 * word;
 #pragma unroll
     for (int j = 0; j < kRows; ++j, y += (int64_t)heads * D) {
       if (place[j] == -2) continue;
@@ -1096,8 +1146,8 @@ Places places_of(const bcq_kv4* c, const int32_t* table, int table_width, const 
   return {table, kv_len, cu, table_width, B, c->pages, c->page_size, c->heads};
 }
 
-// f(D, rows a block) as compile-time numbers: one row while that leaves SMs
-// idle otherwise, else four, whose loads are in flight together.
+// f(D, rows a block) as compile-time numbers: one row while more would leave
+// SMs idle, else four, whose loads are in flight together.
 template <typename F>
 void by_shape(int D, int T, const F& f) {
   auto rows = [&](auto d) {
@@ -1140,7 +1190,7 @@ void plan_parts(AttentionPlan* f, int64_t units, int B, int max_kv, int each, do
       cost = std::max(chunk + start, (double)units * (mean + mean / max_kv * parts * start) / room +
                                          (chunk + start) / 2);
     }
-    cost += parts > 1 ? join + parts : 0;
+    cost += parts > 1 ? join + 2.5 * parts : 0;
     if (best == 0 || cost < best) {
       best = cost;
       f->splits = parts;

@@ -497,7 +497,8 @@ typedef struct bcq_kv4 {
  *   k, v   device, [T][heads][D] of `dtype` (BCQ_F16 or BCQ_BF16): rows
  *          ld_k / ld_v and heads hd_k / hd_v elements apart, a vector's D
  *          values contiguous; bases 16-byte aligned, distances multiples of 8.
- *   T      rows of k and v; rows cu[B].. are not read.  cu[B] <= T.
+ *   T      rows of k and v; what rows outside cu[0]..cu[B]-1 hold has no
+ *          effect.  cu[B] <= T.
  * A position must not be written by two rows of one call (two sequences may
  * share pages that neither appends to).
  * Errors: NULL -> BCQ_ERR_NULL; sizes -> BCQ_ERR_SHAPE; misaligned ->

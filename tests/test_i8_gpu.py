@@ -145,7 +145,8 @@ def test_product_matches_the_oracle(M, N, K, dtype):
 
 @pytest.mark.parametrize("M,N,K", [(1, 14336, 4096), (16, 14336, 4096), (16, 4096, 14336), (48, 4096, 4096),
                                    (64, 14336, 4096), (100, 5000, 8192), (128, 14336, 2048), (144, 4096, 3000),
-                                   (250, 9000, 4096), (333, 6000, 4000), (600, 8192, 4096), (1500, 4096, 1100)])
+                                   (250, 9000, 4096), (333, 6000, 4000), (600, 8192, 4096), (1500, 4096, 1100),
+                                   (333, 14336, 1024), (500, 9000, 2048), (512, 28672, 512), (700, 14336, 640)])
 def test_long_sums_and_many_tiles(M, N, K):
     """Rings that wrap, tiles in several rounds: against fp64 on the GPU, three calls in a row."""
     x, sx = _codes(M, K, 3 * M + K)
