@@ -1025,11 +1025,10 @@ __global__ void __launch_bounds__(128) kv4_join_kernel(const AttentionParams p) 
   const int t = (int)(id / p.q_heads), h = (int)(id % p.q_heads);
   const int tid = threadIdx.x, set = tid / kLanes, lane = tid % kLanes;
   const int b = sequence_of(p.at, t);
-  if (b < 0) return;
-  const int row = (t - rows_of(p.at, b).x) * p.group + h % p.group;
-  const Span sp = span_of(p, b, row / p.rows);
-  grid_dependency_wait();
-  if (sp.parts <= 1 || t - sp.first_row >= sp.rows) return;
+  Span sp = {};
+  if (b >= 0) sp = span_of(p, b, ((t - rows_of(p.at, b).x) * p.group + h % p.group) / p.rows);
+  grid_dependency_wait();  // every CTA: this kernel must not end before the one that it joins
+  if (b < 0 || sp.parts <= 1 || t - sp.first_row >= sp.rows) return;
   const int64_t step = (int64_t)p.T * p.q_heads;
   const float* ml = p.part + (int64_t)p.splits * step * D + id * 2;
   const float* src = p.part + id * D + lane * 4;
@@ -1124,7 +1123,8 @@ bcq_status check_cache(const bcq_kv4* c, int T, const int32_t* table, int table_
   if (!c || !c->k || !c->k_param || !c->v || !c->v_param || !table || !kv_len)
     return BCQ_ERR_NULL;
   if (!cache_sizes_ok(c) || T < 0 || B < 1 || table_width < 1 ||
-      (int64_t)table_width * c->page_size > INT32_MAX || (!cu && T != B))
+      (int64_t)table_width * c->page_size > INT32_MAX || (!cu && T != B) ||
+      (double)c->pages * c->heads * c->page_size >= 4294967294.0 /* vectors are numbered in 32 bits */)
     return BCQ_ERR_SHAPE;
   if (!head_dim_ok(c->head_dim)) return BCQ_ERR_UNSUPPORTED;
   if (!aligned(c->k, 16) || !aligned(c->k_param, 16) || !aligned(c->v, 16) ||

@@ -77,11 +77,12 @@ def visible(n, new, i, causal=True, window=0):
     return see
 
 
-def attention(q, k, kp, v, vp, table, kv_len, cu, scale, causal=True, window=0):
+def attention(q, k, kp, v, vp, table, kv_len, cu, scale, causal=True, window=0, hidden=()):
     """q [T][H][D]; the cache's arrays; returns (out, lse, mag): fp64 [T][H][D],
     [T][H], and a dict of the sums that tolerances are made of -- "v": sum_j p_j
     (a code + |z|)_j of V [T][H][D], "s": the largest |scale| sum_d |q_d| (a
-    code + |z|)_d of K over a row's positions [T][H].  Rows of no sequence are NaN."""
+    code + |z|)_d of K over a row's positions [T][H].  Rows of no sequence are NaN.  hidden: positions that no
+    row sees."""
     q = np.asarray(q, dtype=np.float64)
     T, H, D = q.shape
     heads = k.shape[1]
@@ -95,6 +96,7 @@ def attention(q, k, kp, v, vp, table, kv_len, cu, scale, causal=True, window=0):
         for i in range(new):
             t = cu[b] + i
             see = visible(n, new, i, causal, window)
+            see[[j for j in hidden if j < n]] = False
             for h in range(H):
                 g = h // (H // heads)
                 out[t, h], lse[t, h] = 0.0, -np.inf

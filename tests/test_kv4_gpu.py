@@ -113,8 +113,13 @@ def _check_attention(c, q, out, lse, scale=None, causal=True, window=0, what="")
         assert (d <= t).all(), f"{what}: lse off by {d.max():.3e}"
 
 
-def _run(c, q, **kw):
-    args = dict(max_q=max(c.new), max_kv=max(max(c.lens), 1), return_lse=True)
+# Hints for max_kv: what the case has (few positions: the kernel of few rows),
+# and one under which the kernel of many rows runs wherever there are many.
+HINTS = pytest.mark.parametrize("hint", [None, 4000])
+
+
+def _run(c, q, hint=None, **kw):
+    args = dict(max_q=max(c.new), max_kv=hint or max(max(c.lens), 1), return_lse=True)
     args.update(kw)
     return api.kv4_attention(q, c.cache, c.t_table, c.t_len, c.t_cu, **args)
 
@@ -270,31 +275,37 @@ def test_one_token_each(D, H, heads, dtype):
 @pytest.mark.parametrize("dtype", [F16, BF16])
 @pytest.mark.parametrize("lens,new,H,heads,D,page_size", [
     ([5], [5], 2, 1, 64, 16), ([40, 3, 77], [7, 3, 2], 8, 2, 128, 16), ([130, 64], [33, 64], 4, 4, 64, 32),
-    ([300], [150], 12, 3, 128, 48), ([70, 0, 71], [5, 0, 70], 6, 1, 256, 64), ([256], [256], 2, 2, 128, 128),
+    ([300], [150], 12, 3, 128, 48), ([600, 530], [300, 1], 8, 2, 128, 16), ([520], [400], 7, 1, 256, 48),
+    ([1100], [97], 2, 2, 64, 16), ([129, 5], [129, 5], 32, 2, 128, 16), ([70, 0, 71], [5, 0, 70], 6, 1, 256, 64), ([256], [256], 2, 2, 128, 128),
     ([1000, 513], [3, 129], 4, 1, 128, 64), ([260, 259], [1, 140], 5, 1, 64, 16)])
-def test_several_rows(lens, new, H, heads, D, page_size, dtype):
+@HINTS
+def test_several_rows(lens, new, H, heads, D, page_size, dtype, hint):
     c = Case(lens, new, heads, D, page_size, seed=sum(lens))
     q = _queries(c.T, H, D, dtype, seed=1)
-    out, lse = _run(c, q)
+    out, lse = _run(c, q, hint)
     _check_attention(c, q, out, lse)
 
 
 @pytest.mark.parametrize("causal,window", [(True, 1), (True, 5), (True, 16), (True, 64), (True, 1000),
-                                           (False, 0), (False, 9)])
-@pytest.mark.parametrize("lens,new", [([33, 100], [1, 1]), ([50, 20], [20, 20]), ([200], [140])])
-def test_masks(lens, new, causal, window):
-    c = Case(lens, new, 2, 128, 16, seed=window)
-    q = _queries(c.T, 8, 128, F16, seed=2)
-    out, lse = _run(c, q, causal=causal, window=window)
+                                           (False, 0), (False, 9), (True, 512), (False, 600)])
+@pytest.mark.parametrize("lens,new", [([33, 100], [1, 1]), ([50, 20], [20, 20]), ([200], [140]),
+                                      ([700, 90], [150, 90])])
+@HINTS
+@pytest.mark.parametrize("D", [64, 128, 256])
+def test_masks(lens, new, causal, window, hint, D):
+    c = Case(lens, new, 2, D, 16, seed=window)
+    q = _queries(c.T, 8, D, F16, seed=2)
+    out, lse = _run(c, q, hint, causal=causal, window=window)
     _check_attention(c, q, out, lse, causal=causal, window=window)
 
 
-@pytest.mark.parametrize("n,new,H", [(3, 8, 4), (0, 2, 8), (10, 200, 4), (0, 1, 1)])
-def test_rows_that_see_nothing(n, new, H):
+@pytest.mark.parametrize("n,new,H", [(3, 8, 4), (0, 2, 8), (10, 200, 4), (0, 1, 1), (0, 300, 2), (70, 300, 4)])
+@HINTS
+def test_rows_that_see_nothing(n, new, H, hint):
     """More rows than tokens: the first rows lie before position 0."""
     c = Case([n, 40], [new, 1], 1, 128, 16)
     q = _queries(c.T, H, 128, F16)
-    out, lse = _run(c, q)
+    out, lse = _run(c, q, hint)
     _check_attention(c, q, out, lse)
     empty = max(0, new - n)
     assert (out[:empty] == 0).all() and torch.isneginf(lse[:empty]).all()
@@ -302,33 +313,37 @@ def test_rows_that_see_nothing(n, new, H):
 
 @pytest.mark.parametrize("new", [1, 4, 160])
 @pytest.mark.parametrize("scale", [0.0, -0.3, 1.0, 4.0])
-def test_scales_of_the_scores(scale, new):
+@HINTS
+def test_scales_of_the_scores(scale, new, hint):
     c = Case([200, 30], [new, 1], 2, 64, 16)
     q = _queries(c.T, 4, 64, F16)
-    out, lse = _run(c, q, scale=scale)
+    out, lse = _run(c, q, hint, scale=scale)
     _check_attention(c, q, out, lse, scale=scale)
 
 
 @pytest.mark.parametrize("new", [1, 150])
 @pytest.mark.parametrize("dtype,mag", [(F16, 1e-4), (F16, 300.0), (F16, 3e4), (BF16, 1e-12), (BF16, 1e6), (BF16, 1e30)])
-def test_queries_of_any_magnitude(dtype, mag, new):
+@HINTS
+def test_queries_of_any_magnitude(dtype, mag, new, hint):
     """The factor keeps the scores where they are; fp16's and fp32's ranges must not matter in between."""
     c = Case([180, 9], [new, 1], 2, 128, 16)
     q = _queries(c.T, 4, 128, dtype).float().clamp(-2, 2).mul(mag).to(dtype)
     scale = 128 ** -0.5 / mag
-    out, lse = _run(c, q, scale=scale)
+    out, lse = _run(c, q, hint, scale=scale)
     _check_attention(c, q, out, lse, scale=scale)
 
 
 @pytest.mark.parametrize("new", [1, 6, 140])
-def test_nan_stays_where_it_belongs(new):
-    c = Case([160, 50], [new, 1], 2, 128, 16)
-    q = _queries(c.T, 8, 128, F16)
-    ref, _ = _run(c, q)
+@pytest.mark.parametrize("D", [64, 128, 256])
+@HINTS
+def test_nan_stays_where_it_belongs(new, D, hint):
+    c = Case([160, 50], [new, 1], 2, D, 16)
+    q = _queries(c.T, 8, D, F16)
+    ref, _ = _run(c, q, hint)
     q2 = q.clone()
     q2[0, 3, 5] = float("nan")
     q2[-1, 6, 0] = float("inf")
-    out, _ = _run(c, q2)
+    out, _ = _run(c, q2, hint)
     assert torch.isnan(out[0, 3]).all() and torch.isnan(out[-1, 6]).all()
     keep = torch.ones(c.T, 8, dtype=torch.bool)
     keep[0, 3] = keep[-1, 6] = False
@@ -336,22 +351,33 @@ def test_nan_stays_where_it_belongs(new):
     # a NaN group in the second sequence's key of head 1: that head's rows, nothing else
     p = int(c.table[1, 0])
     c.cache.k_param[p, 1, 3, 0] = float("nan")
-    out, _ = _run(c, q)
+    out, _ = _run(c, q, hint)
     assert torch.isnan(out[-1, 4:]).all()
     assert torch.equal(out[-1, :4], ref[-1, :4]) and torch.equal(out[:-1], ref[:-1])
+    # NaN groups in the first sequence's values, at a position that only the rows
+    # from it on see: that group's outputs of those rows
+    j, g = 160 - new + new // 2, D // 64 - 1
+    p, o = int(c.table[0, j // 16]), j % 16
+    c.cache.v_param[p, 0, o, g, 0] = float("nan")
+    out, lse = _run(c, q, hint)
+    seen = out[new // 2:new, :4]
+    assert torch.isnan(seen[..., 64 * g:]).all() and torch.equal(seen[..., :64 * g], ref[new // 2:new, :4, :64 * g])
+    assert torch.equal(out[:new // 2, :4], ref[:new // 2, :4]) and torch.isfinite(lse[:new, :4]).all()
+    assert torch.equal(out[:new, 4:], ref[:new, 4:])
 
 
 @pytest.mark.parametrize("new", [1, 5, 200])
-def test_strided_queries_and_outputs(new):
+@HINTS
+def test_strided_queries_and_outputs(new, hint):
     c = Case([300, 20], [new, 2], 2, 128, 32)
     q = _queries(c.T, 8, 128, BF16)
-    ref, _ = _run(c, q)
+    ref, _ = _run(c, q, hint)
     fused = torch.full((c.T, 8 * 128 + 4 * 128 + 8), float("nan"), dtype=BF16, device="cuda")
     qs = fused[:, :1024].view(c.T, 8, 128)
     qs.copy_(q)
     buf = torch.full((8, c.T + 1, 136), 3.0, dtype=BF16, device="cuda")   # head-major, padded
     out = buf[:, :c.T, :128].transpose(0, 1)
-    got, _ = _run(c, qs, out=out)
+    got, _ = _run(c, qs, hint, out=out)
     assert got is out and torch.equal(out, ref)
     buf[:, :c.T, :128] = 3.0
     assert (buf == 3.0).all()
@@ -398,6 +424,24 @@ def test_bad_pages_lengths_and_row_counts_are_recorded():
     out = torch.full_like(q, 5.0)
     api.kv4_attention(q, c.cache, c.t_table, c.t_len, _i32([0, 2, 2]), max_q=1, out=out)
     assert api.device_error() == api.BCQ_ERR_SHAPE and (out[1] == 5).all()
+
+
+@pytest.mark.parametrize("D", [64, 128, 256])
+def test_a_missing_page_under_many_rows(D):
+    """Its positions are left out, for every row, and it is recorded."""
+    c = Case([200], [150], 1, D, 16)
+    q = _queries(150, 4, D, F16)
+    t = c.t_table.clone()
+    t[0, 3] = -5                           # positions 48..63
+    out, lse = api.kv4_attention(q, c.cache, t, c.t_len, c.t_cu, max_q=150, max_kv=4000, return_lse=True)
+    assert api.device_error() == api.BCQ_ERR_PAGE
+    ro, rl, mag = kv4.attention(_f64(q), *(c.arrays[n] for n in ("k", "k_param", "v", "v_param")), c.table, c.lens,
+                                c.cu, float(np.float32(D ** -0.5)), hidden=range(48, 64))
+    ds, tol = _tolerances(mag["s"], mag["v"], ro, 200, D, F16)
+    assert (np.abs(_f64(out) - ro) <= tol).all() and (np.abs(_f64(lse) - rl) <= ds + 1e-4).all()
+    few, _ = api.kv4_attention(q, c.cache, t, c.t_len, c.t_cu, max_q=150, max_kv=200, return_lse=True)
+    assert api.device_error() == api.BCQ_ERR_PAGE
+    assert (np.abs(_f64(few) - ro) <= tol).all()
 
 
 def test_no_rows():
