@@ -43,12 +43,26 @@ __device__ __forceinline__ __nv_bfloat16 from_float<__nv_bfloat16>(float v) {
   return __float2bfloat16_rn(v);
 }
 
+// Division of 0 <= n < 2^31 by a number that the host knows, as a product (a
+// division takes some 35 instructions): with s = ceil(log2 d) and m = ceil(2^(31
+// + s) / d), n m / 2^(31 + s) exceeds n / d by less than n / 2^31 / d < 1 / d.
+struct Divisor {
+  int d;
+  uint32_t m;
+  int shift;  // s - 1
+  __device__ __forceinline__ int quotient(int n) const {
+    return d == 1 ? n : (int)(__umulhi((uint32_t)n, m) >> shift);
+  }
+};
+
 // What a call knows of the cache's places.
 struct Places {
   const int32_t* table;
   const int32_t* kv_len;
   const int32_t* cu;
   int table_width, B, pages, page_size, heads;
+  int room;             // positions of a table row
+  Divisor by_page;
 };
 
 // The sequence that row t belongs to: the last b with cu[b] <= t, or -1 when
@@ -75,8 +89,8 @@ __device__ __forceinline__ int2 rows_of(const Places& p, int b) {
 // 2^32 vectors: one takes 72 bytes or more.)
 __device__ __forceinline__ int64_t vector_at(const Places& p, int b, int j, int h) {
   if (j < 0) return -1;
-  const int entry = j / p.page_size;
-  if (entry >= p.table_width) return -1;
+  if (j >= p.room) return -1;
+  const int entry = p.by_page.quotient(j);
   const int page = p.table[(int64_t)b * p.table_width + entry];
   if (page < 0 || page >= p.pages) return -1;
   return (int64_t)((uint64_t)((uint32_t)page * (uint32_t)p.heads + (uint32_t)h) * (uint32_t)p.page_size) +
@@ -363,7 +377,8 @@ struct AttentionParams {
   int64_t ld_q, hd_q, ld_o, hd_o;
   int T, q_heads, max_q, causal, window;
   float scale;
-  int group;       // query heads a key/value head
+  Divisor group;   // query heads a key/value head
+  Divisor by_blocks, by_heads, by_rows;  // row_blocks, the cache's heads, rows
   int rows;        // rows (of a key/value head) a CTA
   int row_blocks;  // CTAs along max_q * group rows
   int splits;      // most CTAs along the positions
@@ -386,10 +401,10 @@ __device__ __forceinline__ Span span_of(const AttentionParams& p, int b, int blo
   s.first_row = r.x;
   s.rows = r.x < 0 ? 0 : min(min(r.y, p.max_q), p.T - r.x);
   const int len = p.at.kv_len[b];
-  s.len = (int)min((int64_t)max(len, 0), (int64_t)p.at.table_width * p.at.page_size);
+  s.len = min(max(len, 0), p.at.room);
   s.pos0 = len - r.y;
-  const int i0 = block * p.rows / p.group;                                  // first and last row
-  const int i1 = min(s.rows - 1, ((block + 1) * p.rows - 1) / p.group);     // (of the sequence)
+  const int i0 = p.group.quotient(block * p.rows);                          // first and last row
+  const int i1 = min(s.rows - 1, p.group.quotient((block + 1) * p.rows - 1));  // (of the sequence)
   s.end = p.causal ? min(s.len, s.pos0 + i1 + 1) : s.len;
   s.begin = p.window > 0 ? max(0, s.pos0 + i0 - p.window + 1) & ~31 : 0;
   const int n = s.end - s.begin;
@@ -397,6 +412,11 @@ __device__ __forceinline__ Span span_of(const AttentionParams& p, int b, int blo
     s.parts = i0 < s.rows ? 1 : 0;  // rows that see nothing are still written
     s.chunk = 0;
     s.end = s.begin;
+    return s;
+  }
+  if (n <= p.chunk) {
+    s.chunk = p.chunk;
+    s.parts = 1;
     return s;
   }
   const int even = (n + p.splits - 1) / p.splits;
@@ -528,8 +548,8 @@ __global__ void __launch_bounds__(kFewWarps * 32, NT == 1 && D <= 128 ? 4 : 2) k
   extern __shared__ __align__(128) unsigned char smem[];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int r = lane >> 2, c = lane & 3;
-  const int block = blockIdx.x % p.row_blocks, kvh = blockIdx.x / p.row_blocks % p.at.heads;
-  const int b = blockIdx.x / p.row_blocks / p.at.heads, part = blockIdx.y;
+  const int pair = p.by_blocks.quotient((int)blockIdx.x), block = (int)blockIdx.x - pair * p.row_blocks;
+  const int b = p.by_heads.quotient(pair), kvh = pair - b * p.at.heads, part = blockIdx.y;
   const Span sp = span_of(p, b, block);
   if (part == 0 && block == 0 && kvh == 0 && threadIdx.x == 0) {
     if (rows_of(p.at, b).y > p.max_q) record_error(&g_kv4_error, BCQ_ERR_SHAPE);
@@ -537,15 +557,15 @@ __global__ void __launch_bounds__(kFewWarps * 32, NT == 1 && D <= 128 ? 4 : 2) k
   }
   if (part >= sp.parts) return;
   const int row0 = block * p.rows;                       // of the key/value head's rows
-  const int row_n = min(p.rows, sp.rows * p.group - row0);
+  const int row_n = min(p.rows, sp.rows * p.group.d - row0);
 
   // the queries are asked for before the cache is
   uint4 raw_q[NT][G][2];
 #pragma unroll
   for (int nt = 0; nt < NT; ++nt) {
-    const int row = row0 + nt * 8 + r, i = row / p.group;
+    const int row = row0 + nt * 8 + r, i = p.group.quotient(row);
     const uint16_t* src = p.q + (int64_t)(sp.first_row + i) * p.ld_q +
-                          (int64_t)(kvh * p.group + row - i * p.group) * p.hd_q;
+                          (int64_t)((kvh - i) * p.group.d + row) * p.hd_q;
 #pragma unroll
     for (int g = 0; g < G; ++g)
 #pragma unroll
@@ -629,7 +649,7 @@ __global__ void __launch_bounds__(kFewWarps * 32, NT == 1 && D <= 128 ? 4 : 2) k
   for (int nt = 0; nt < NT; ++nt) {
     const int row = nt * 8 + r;
     const bool live = row < row_n;
-    const int i = live ? (row0 + row) / p.group : 0;
+    const int i = live ? p.group.quotient(row0 + row) : 0;
     float f[G][2][8];
     float top = 0.f;
 #pragma unroll
@@ -985,7 +1005,7 @@ __global__ void __launch_bounds__(kFewWarps * 32, NT == 1 && D <= 128 ? 4 : 2) k
       x.z = fmaf(y.z, f, x.z);
       x.w = fmaf(y.w, f, x.w);
     }
-    const int i = (row0 + row) / p.group, h = kvh * p.group + (row0 + row) % p.group;
+    const int i = p.group.quotient(row0 + row), h = (kvh - i) * p.group.d + row0 + row;
     const int64_t t = sp.first_row + i;
     if (sp.parts > 1) {
       const int64_t at = ((int64_t)part * p.T + t) * p.q_heads + h;
@@ -1022,11 +1042,12 @@ __global__ void __launch_bounds__(128) kv4_join_kernel(const AttentionParams p) 
   __shared__ float4 so[kSets][kLanes];
   __shared__ float red[2][4];
   const int64_t id = blockIdx.x;
-  const int t = (int)(id / p.q_heads), h = (int)(id % p.q_heads);
+  const int t = (int)((uint32_t)id / (uint32_t)p.q_heads), h = (int)((uint32_t)id % (uint32_t)p.q_heads);
   const int tid = threadIdx.x, set = tid / kLanes, lane = tid % kLanes;
   const int b = sequence_of(p.at, t);
   Span sp = {};
-  if (b >= 0) sp = span_of(p, b, ((t - rows_of(p.at, b).x) * p.group + h % p.group) / p.rows);
+  if (b >= 0)
+    sp = span_of(p, b, p.by_rows.quotient((t - rows_of(p.at, b).x) * p.group.d + h - p.group.quotient(h) * p.group.d));
   grid_dependency_wait();  // every CTA: this kernel must not end before the one that it joins
   if (b < 0 || sp.parts <= 1 || t - sp.first_row >= sp.rows) return;
   const int64_t step = (int64_t)p.T * p.q_heads;
@@ -1141,9 +1162,17 @@ bcq_status check_rows(const void* x, int64_t ld, int64_t hd, int dtype) {
   return !aligned(x, 16) || ld % 8 || hd % 8 ? BCQ_ERR_ALIGN : BCQ_OK;
 }
 
+Divisor divisor(int d) {
+  int s = 0;
+  while (((int64_t)1 << s) < d) ++s;
+  return {d, s == 0 ? 0u : (uint32_t)((((uint64_t)1 << (31 + s)) + (uint64_t)d - 1) / (uint64_t)d), s - 1};
+}
+
 Places places_of(const bcq_kv4* c, const int32_t* table, int table_width, const int32_t* kv_len,
                  const int32_t* cu, int B) {
-  return {table, kv_len, cu, table_width, B, c->pages, c->page_size, c->heads};
+  return {table,    kv_len,       cu,       table_width,
+          B,        c->pages,     c->page_size, c->heads,
+          table_width * c->page_size, divisor(c->page_size)};
 }
 
 // f(D, rows a block) as compile-time numbers: one row while more would leave
@@ -1394,13 +1423,17 @@ bcq_status bcq_kv4_attention(const bcq_kv4* cache, const void* q, int64_t ld_q, 
                        window,
                        scale};
   const AttentionPlan f = plan_attention(cache, q_heads, B, max_q, max_kv, window);
-  p.group = q_heads / cache->heads;
+  p.group = divisor(q_heads / cache->heads);
+  p.by_blocks = divisor(f.row_blocks);
+  p.by_heads = divisor(cache->heads);
+  p.by_rows = divisor(f.rows);
   p.rows = f.rows;
   p.row_blocks = f.row_blocks;
   p.splits = f.splits;
   p.chunk = f.chunk;
   p.part = static_cast<float*>(workspace);
-  if ((int64_t)f.row_blocks * cache->heads * B > INT32_MAX || (int64_t)T * q_heads > INT32_MAX)
+  if ((int64_t)f.row_blocks * cache->heads * B > INT32_MAX || (int64_t)T * q_heads > INT32_MAX ||
+      (int64_t)max_q * (q_heads / cache->heads) > INT32_MAX - 512)
     return BCQ_ERR_SHAPE;
   cudaStream_t st = (cudaStream_t)stream;
   const cudaError_t e = dtype == BCQ_F16 ? launch_attention<__half>(p, cache->head_dim, f.nt, st)

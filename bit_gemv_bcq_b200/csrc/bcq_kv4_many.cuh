@@ -151,16 +151,16 @@ __global__ void __launch_bounds__(ManyShape<D>::kThreads, 1) kv4_many_kernel(con
 
   // the last blocks of rows see the most: theirs go first, of every sequence
   // and head
-  const int pairs = p.at.heads * p.at.B, pair = blockIdx.x % pairs;
-  const int block = p.row_blocks - 1 - (int)(blockIdx.x / pairs);
-  const int kvh = pair % p.at.heads, b = pair / p.at.heads, part = blockIdx.y;
+  const int pairs = p.at.heads * p.at.B, pair = (int)(blockIdx.x % (unsigned)pairs);
+  const int block = p.row_blocks - 1 - (int)(blockIdx.x / (unsigned)pairs);
+  const int b = p.by_heads.quotient(pair), kvh = pair - b * p.at.heads, part = blockIdx.y;
   const Span sp = span_of(p, b, block);
   if (part == 0 && block == 0 && kvh == 0 && threadIdx.x == 0) {
     if (rows_of(p.at, b).y > p.max_q) record_error(&g_kv4_error, BCQ_ERR_SHAPE);
     if (p.at.kv_len[b] != sp.len) record_error(&g_kv4_error, BCQ_ERR_PAGE);
   }
   if (part >= sp.parts) return;
-  const int row0 = block * p.rows, row_n = min(p.rows, sp.rows * p.group - row0);
+  const int row0 = block * p.rows, row_n = min(p.rows, sp.rows * p.group.d - row0);
   const int begin = sp.begin + part * sp.chunk, end = min(sp.end, begin + sp.chunk);
   const int steps = end > begin ? (end - begin + S::kTokens - 1) / S::kTokens : 0;
   const int tiles = row_n > 128 ? 2 : 1;  // of this CTA
@@ -370,8 +370,8 @@ __global__ void __launch_bounds__(ManyShape<D>::kThreads, 1) kv4_many_kernel(con
     const int t = warp >> 2, r = (warp & 3) * 32 + lane;  // tile, row of it
     const int row = t * 128 + r;
     const bool live = row < row_n;
-    const int i = live ? (row0 + row) / p.group : 0;
-    const int h = kvh * p.group + (live ? (row0 + row) % p.group : 0);
+    const int i = live ? p.group.quotient(row0 + row) : 0;
+    const int h = live ? (kvh - i) * p.group.d + row0 + row : 0;
     const int64_t token = sp.first_row + i;
     const int pos = sp.pos0 + i;
     const int hi = live ? (p.causal ? min(end, pos + 1) : end) : 1 << 30;
