@@ -628,6 +628,9 @@ def _raw_stream(stream, index: int) -> int:
 def _run(name: str, index: int, *args) -> None:
     """Call the entry point with device `index` current."""
     f = getattr(lib(), name)
+    # (ctypes would take such a number's low 32 bits)
+    if any(t is ctypes.c_int and not -1 << 31 <= a < 1 << 31 for a, t in zip(args, f.argtypes)):
+        raise BcqError(BCQ_ERR_SHAPE, name)
     if index == torch.cuda.current_device():
         status = f(*args)
     else:

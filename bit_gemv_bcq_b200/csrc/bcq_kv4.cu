@@ -1137,6 +1137,9 @@ bool cache_sizes_ok(const bcq_kv4* c) {
   return c->pages >= 1 && c->heads >= 1 && c->page_size >= 16 && c->page_size % 16 == 0;
 }
 
+// Positions of a sequence; twice as many are still counted in an int.
+constexpr int kMostPositions = 1 << 30;
+
 bool head_dim_ok(int D) { return D == 64 || D == 128 || D == 256; }
 
 bcq_status check_cache(const bcq_kv4* c, int T, const int32_t* table, int table_width,
@@ -1144,7 +1147,7 @@ bcq_status check_cache(const bcq_kv4* c, int T, const int32_t* table, int table_
   if (!c || !c->k || !c->k_param || !c->v || !c->v_param || !table || !kv_len)
     return BCQ_ERR_NULL;
   if (!cache_sizes_ok(c) || T < 0 || B < 1 || table_width < 1 ||
-      (int64_t)table_width * c->page_size > INT32_MAX || (!cu && T != B) ||
+      (int64_t)table_width * c->page_size > kMostPositions || (!cu && T != B) ||
       (double)c->pages * c->heads * c->page_size >= 4294967294.0 /* vectors are numbered in 32 bits */)
     return BCQ_ERR_SHAPE;
   if (!head_dim_ok(c->head_dim)) return BCQ_ERR_UNSUPPORTED;
@@ -1398,6 +1401,11 @@ bcq_status bcq_kv4_attention(const bcq_kv4* cache, const void* q, int64_t ld_q, 
   if (T == 0) return BCQ_OK;
   if ((s = check_rows(q, ld_q, hd_q, dtype)) != BCQ_OK) return s;
   if ((s = check_rows(out, ld_o, hd_o, dtype)) != BCQ_OK) return s;
+  // rows of out that share memory would be written by several threads
+  const int64_t D = cache->head_dim;
+  if ((T > 1 && ld_o < D) || (q_heads > 1 && hd_o < D) ||
+      (T > 1 && q_heads > 1 && ld_o < (q_heads - 1) * hd_o + D && hd_o < (T - 1) * ld_o + D))
+    return BCQ_ERR_SHAPE;
   if (lse && !aligned(lse, 4)) return BCQ_ERR_ALIGN;
   const size_t need = bcq_kv4_attention_workspace_bytes(cache, T, q_heads, B, max_q, max_kv, window);
   if (need > 0) {
@@ -1420,7 +1428,7 @@ bcq_status bcq_kv4_attention(const bcq_kv4* cache, const void* q, int64_t ld_q, 
                        q_heads,
                        max_q,
                        causal,
-                       window,
+                       std::min(window, kMostPositions),  // a wider one hides nothing either
                        scale};
   const AttentionPlan f = plan_attention(cache, q_heads, B, max_q, max_kv, window);
   p.group = divisor(q_heads / cache->heads);

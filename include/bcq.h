@@ -458,7 +458,7 @@ bcq_status bcq_linear_i8(const void* x, int dtype, int64_t ldx, const int8_t* w,
  *                     of each group; 16-byte aligned.
  *   table             device, int32 [B][table_width]: position j of sequence b
  *                     is at page table[b][j / page_size], offset j %
- *                     page_size.
+ *                     page_size; table_width * page_size <= 2^30.
  *   kv_len            device, int32 [B]: tokens of each sequence in the cache,
  *                     the ones of this call among them; at most table_width *
  *                     page_size.  May be 0.
@@ -542,7 +542,7 @@ size_t bcq_kv4_attention_workspace_bytes(const bcq_kv4* cache, int T, int q_head
  *           ld_q and heads hd_q elements apart; base 16-byte aligned,
  *           distances multiples of 8.
  *   out     device, the same type, rows ld_o and heads hd_o elements apart;
- *           same alignment.
+ *           same alignment; no two vectors overlap (-> BCQ_ERR_SHAPE).
  *   lse     device, fp32 [T][q_heads], or NULL: log sum_j exp(scale * q . K_j).
  *   q_heads a multiple of heads, at most 128 times as many.
  *   max_q   no sequence has more rows than this in the call (rows behind it

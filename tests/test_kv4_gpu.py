@@ -311,6 +311,19 @@ def test_rows_that_see_nothing(n, new, H, hint):
     assert (out[:empty] == 0).all() and torch.isneginf(lse[:empty]).all()
 
 
+@pytest.mark.parametrize("window", [2 ** 31 - 1, 2 ** 31 - 4, 2 ** 30, 2 ** 20])
+@pytest.mark.parametrize("new", [8, 300])
+@HINTS
+def test_widest_windows_hide_nothing(window, new, hint):
+    """The first rows lie before position 0, from which the window is counted."""
+    c = Case([3, 40], [new, 1], 1, 128, 16)
+    q = _queries(c.T, 4, 128, F16)
+    out, lse = _run(c, q, hint, window=window)
+    _check_attention(c, q, out, lse)
+    with pytest.raises(api.BcqError):
+        _run(c, q, hint, window=2 ** 32 + 1)
+
+
 @pytest.mark.parametrize("new", [1, 4, 160])
 @pytest.mark.parametrize("scale", [0.0, -0.3, 1.0, 4.0])
 @HINTS

@@ -181,6 +181,15 @@ def test_kv4_attention_refusals(L):
     assert _kv4(L, "attention", out=P16 + 4) == api.BCQ_ERR_ALIGN
     assert _kv4(L, "attention", hdo=4) == api.BCQ_ERR_ALIGN
     assert _kv4(L, "attention", lse=P16 + 2) == api.BCQ_ERR_ALIGN
+    for kw in (dict(ldo=504), dict(ldo=128), dict(hdo=64), dict(ldo=0), dict(hdo=0), dict(ldo=64, hdo=512)):
+        assert _kv4(L, "attention", **kw) == api.BCQ_ERR_SHAPE, kw        # vectors of out that overlap
+
+
+@pytest.mark.parametrize("name", ["append", "read", "attention"])
+def test_kv4_positions_are_counted_in_an_int(L, name):
+    """At most 2^30 positions of a sequence; no GPU is needed to refuse more (T = 0 runs nothing)."""
+    assert _kv4(L, name, T=0, W=1 << 25) == api.BCQ_OK
+    assert _kv4(L, name, T=0, W=(1 << 25) + 1) == api.BCQ_ERR_SHAPE
 
 
 # -------------------------------------------------------------- fast calls
@@ -203,6 +212,14 @@ def test_fast_module_leaves_other_calls_alone(L):
                     ("linear_i8", lambda: api.linear_i8(h, i, h[0].float()))):
         with pytest.raises(ValueError):
             call()
+
+
+def test_numbers_beyond_an_int_are_refused(L):
+    """ctypes would take their low 32 bits: a window of 2^32 + 1 would be one of 1."""
+    for big in ((1 << 32) + 1, 1 << 31, -(1 << 31) - 1):
+        with pytest.raises(api.BcqError) as e:
+            api._run("bcq_quantize_i8", 0, P16, 0, big, 16, 16, P16, 16, P16, None)
+        assert e.value.status == api.BCQ_ERR_SHAPE
 
 
 # -------------------------------------------------- refusals of the binding
