@@ -88,6 +88,7 @@ __global__ void __launch_bounds__(1024) quantize_i8_kernel(const uint16_t* __res
                                                            int64_t ldx, int K, int8_t* q,
                                                            int64_t ldq, float* scale) {
   __shared__ uint32_t s_max[32];
+  grid_dependency_wait();
   launch_dependents();  // the product may fetch its weights meanwhile
   const int64_t m = blockIdx.x;
   const uint16_t* row = x + m * ldx;
@@ -179,7 +180,7 @@ struct GemmParams {
   int workers;          // CTAs, or pairs
   int tiles_each, tiles_more;  // tiles of every worker, workers that have one more
   uint32_t kg_step;     // 2^16 KG / workers: where a worker starts along K
-  int overlap;          // the kernel before makes x's codes and may still run
+  int overlap;          // the kernel before is the quantiser, which writes x's codes and nothing of w
   uint32_t a_block, b_block, b_off, bar_off, tmem_cols;
   unsigned long long timeout_ns;
 };
@@ -274,8 +275,9 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
     const CUtensorMap* map = is_w ? &wmap : &xmap;
     const uint32_t block = is_w ? p.a_block : p.b_block, base = sbase + (is_w ? 0u : p.b_off);
     const uint32_t bytes = (uint32_t)(is_w ? p.R : SUBS * p.BX) * kKBlock * (PAIR ? 2u : 1u);  // of both CTAs
-    // x's codes come from the kernel before; the first weights need not wait for it
-    if (!is_w && p.overlap) grid_dependency_wait();
+    // behind the quantiser the first weights need not wait for it
+    if (!is_w || !p.overlap) grid_dependency_wait();
+    if (!is_w) launch_dependents();  // (this CTA holds its tensor memory)
     GemmCursor c;
     c.start(worker, kg_first, p.KG);
     auto first_row = [&]() {
@@ -381,7 +383,7 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
     const int quarter = warp & 3, each = p.rows >> 2, half = (warp - 4) >> 2;
     const int split = ((p.BT >> 4) + 1) / 2 * 16;
     const int r = lane < each ? quarter * each + lane : 1 << 20;
-    if (p.overlap) grid_dependency_wait();  // sx
+    grid_dependency_wait();  // sx, and y's last use
     for (int t = 0; t < mine; ++t) {
       const int tile = worker + t * p.workers;
       const int nt = p.mt == 1 ? tile : tile / p.mt;
@@ -469,14 +471,13 @@ constexpr unsigned long long kWaitNs = 2000000000ull;         // 2 s
 template <typename T>
 cudaError_t launch_quantize_t(const uint16_t* x, int M, int K, int64_t ldx, int8_t* q, int64_t ldq,
                               float* scale, cudaStream_t st) {
-  if (aligned(x, 16) && (ldx % 8 == 0 || M == 1)) {
-    if (K <= 4096) quantize_i8_kernel<T, 2, true><<<M, 256, 0, st>>>(x, ldx, K, q, ldq, scale);
-    else if (K <= 16384) quantize_i8_kernel<T, 4, true><<<M, 512, 0, st>>>(x, ldx, K, q, ldq, scale);
-    else quantize_i8_kernel<T, 8, true><<<M, 1024, 0, st>>>(x, ldx, K, q, ldq, scale);
-  } else {
-    quantize_i8_kernel<T, 1, false><<<M, 256, 0, st>>>(x, ldx, K, q, ldq, scale);
-  }
-  return cudaGetLastError();
+  auto launch = [&](auto kernel, unsigned threads) {
+    return launch_early(kernel, dim3((unsigned)M), threads, 0, st, x, ldx, K, q, ldq, scale);
+  };
+  if (!aligned(x, 16) || (ldx % 8 && M > 1)) return launch(quantize_i8_kernel<T, 1, false>, 256);
+  if (K <= 4096) return launch(quantize_i8_kernel<T, 2, true>, 256);
+  if (K <= 16384) return launch(quantize_i8_kernel<T, 4, true>, 512);
+  return launch(quantize_i8_kernel<T, 8, true>, 1024);
 }
 
 cudaError_t launch_quantize(const void* x, int dtype, int M, int K, int64_t ldx, int8_t* q,
@@ -627,10 +628,8 @@ cudaError_t launch_gemm_t(const CUtensorMap& wmap, const CUtensorMap& xmap, cons
     attr[n].val.clusterDim.y = 1;
     attr[n++].val.clusterDim.z = 1;
   }
-  if (p.overlap) {
-    attr[n].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    attr[n++].val.programmaticStreamSerializationAllowed = 1;
-  }
+  attr[n].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[n++].val.programmaticStreamSerializationAllowed = 1;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3((unsigned)grid);
   cfg.blockDim = dim3(kGemmThreads);

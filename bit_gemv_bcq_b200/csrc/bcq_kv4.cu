@@ -210,6 +210,8 @@ __global__ void __launch_bounds__(kRowThreads, 4) kv4_append_kernel(const Append
       if (t0 + j < p.T && i < items) raw[j] = ldg_nc_v4(x);
     }
   };
+  grid_dependency_wait();
+  launch_dependents();
   fetch(threadIdx.x);
   locate_rows<kRows>(p.at, t0, p.T, places);
   for (int i = threadIdx.x; i - lane < items; i += kRowThreads) {  // whole warps
@@ -291,6 +293,8 @@ __global__ void __launch_bounds__(kRowThreads) kv4_read_kernel(const ReadParams 
   __shared__ RowPlaces<kRows> places;
   const int64_t* place = places.place;
   const int t0 = (int)blockIdx.x * kRows, heads = p.at.heads;
+  grid_dependency_wait();
+  launch_dependents();
   locate_rows<kRows>(p.at, t0, p.T, places);
   for (int i = threadIdx.x; i < 2 * heads * kWords; i += kRowThreads) {
     const int kv = i >= heads * kWords;
@@ -550,6 +554,7 @@ __global__ void __launch_bounds__(kFewWarps * 32, NT == 1 && D <= 128 ? 4 : 2) k
   const int r = lane >> 2, c = lane & 3;
   const int pair = p.by_blocks.quotient((int)blockIdx.x), block = (int)blockIdx.x - pair * p.row_blocks;
   const int b = p.by_heads.quotient(pair), kvh = pair - b * p.at.heads, part = blockIdx.y;
+  grid_dependency_wait();
   const Span sp = span_of(p, b, block);
   if (part == 0 && block == 0 && kvh == 0 && threadIdx.x == 0) {
     if (rows_of(p.at, b).y > p.max_q) record_error(&g_kv4_error, BCQ_ERR_SHAPE);
@@ -1049,6 +1054,7 @@ __global__ void __launch_bounds__(128) kv4_join_kernel(const AttentionParams p) 
   if (b >= 0)
     sp = span_of(p, b, p.by_rows.quotient((t - rows_of(p.at, b).x) * p.group.d + h - p.group.quotient(h) * p.group.d));
   grid_dependency_wait();  // every CTA: this kernel must not end before the one that it joins
+  launch_dependents();
   if (b < 0 || sp.parts <= 1 || t - sp.first_row >= sp.rows) return;
   const int64_t step = (int64_t)p.T * p.q_heads;
   const float* ml = p.part + (int64_t)p.splits * step * D + id * 2;
@@ -1260,8 +1266,7 @@ cudaError_t launch_few_t(const AttentionParams& p, cudaStream_t st) {
   cudaError_t e = allow_smem(kv4_few_kernel<T, D, NT>, smem, done);
   if (e != cudaSuccess) return e;
   const dim3 grid((unsigned)((int64_t)p.row_blocks * p.at.heads * p.at.B), (unsigned)p.splits);
-  kv4_few_kernel<T, D, NT><<<grid, kFewWarps * 32, smem, st>>>(p);
-  return cudaGetLastError();
+  return launch_early(kv4_few_kernel<T, D, NT>, grid, kFewWarps * 32, smem, st, p);
 }
 
 template <typename T, int D>
@@ -1271,22 +1276,12 @@ cudaError_t launch_many_t(const AttentionParams& p, cudaStream_t st) {
   cudaError_t e = allow_smem(kv4_many_kernel<T, D>, smem, done);
   if (e != cudaSuccess) return e;
   const dim3 grid((unsigned)((int64_t)p.row_blocks * p.at.heads * p.at.B), (unsigned)p.splits);
-  kv4_many_kernel<T, D><<<grid, ManyShape<D>::kThreads, smem, st>>>(p);
-  return cudaGetLastError();
+  return launch_early(kv4_many_kernel<T, D>, grid, ManyShape<D>::kThreads, smem, st, p);
 }
 
 template <typename T, int D>
 cudaError_t launch_join_t(const AttentionParams& p, cudaStream_t st) {
-  cudaLaunchAttribute attr = {};
-  attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  attr.val.programmaticStreamSerializationAllowed = 1;
-  cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3((unsigned)((int64_t)p.T * p.q_heads));
-  cfg.blockDim = dim3(128);
-  cfg.stream = st;
-  cfg.attrs = &attr;
-  cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, kv4_join_kernel<T, D>, p);
+  return launch_early(kv4_join_kernel<T, D>, dim3((unsigned)((int64_t)p.T * p.q_heads)), 128, 0, st, p);
 }
 
 template <typename T, int D>
@@ -1306,8 +1301,6 @@ cudaError_t launch_attention(const AttentionParams& p, int D, int nt, cudaStream
   if (D == 256) return launch_attention_t<T, 256>(p, nt, st);
   return D == 128 ? launch_attention_t<T, 128>(p, nt, st) : launch_attention_t<T, 64>(p, nt, st);
 }
-
-bcq_status launched() { return cudaGetLastError() == cudaSuccess ? BCQ_OK : BCQ_ERR_CUDA; }
 
 }  // namespace
 
@@ -1343,13 +1336,14 @@ bcq_status bcq_kv4_append(const bcq_kv4* cache, const void* k, int64_t ld_k, int
                            reinterpret_cast<__half2*>(cache->v_param)},
                           T};
   cudaStream_t st = (cudaStream_t)stream;
+  cudaError_t e = cudaSuccess;
   by_shape(cache->head_dim, T, [&](auto d, auto rows) {
     constexpr int D = decltype(d)::value, kRows = decltype(rows)::value;
     const unsigned blocks = (unsigned)((T + kRows - 1) / kRows);
-    if (dtype == BCQ_F16) kv4_append_kernel<__half, D, kRows><<<blocks, kRowThreads, 0, st>>>(p);
-    else kv4_append_kernel<__nv_bfloat16, D, kRows><<<blocks, kRowThreads, 0, st>>>(p);
+    if (dtype == BCQ_F16) e = launch_early(kv4_append_kernel<__half, D, kRows>, blocks, kRowThreads, 0, st, p);
+    else e = launch_early(kv4_append_kernel<__nv_bfloat16, D, kRows>, blocks, kRowThreads, 0, st, p);
   });
-  return launched();
+  return e == cudaSuccess ? BCQ_OK : BCQ_ERR_CUDA;
 }
 
 bcq_status bcq_kv4_read(const bcq_kv4* cache, void* k, void* v, int dtype, int T,
@@ -1367,14 +1361,15 @@ bcq_status bcq_kv4_read(const bcq_kv4* cache, void* k, void* v, int dtype, int T
                         {k, v},
                         T};
   cudaStream_t st = (cudaStream_t)stream;
+  cudaError_t e = cudaSuccess;
   by_shape(cache->head_dim, T, [&](auto d, auto rows) {
     constexpr int D = decltype(d)::value, kRows = decltype(rows)::value;
     const unsigned blocks = (unsigned)((T + kRows - 1) / kRows);
-    if (dtype == BCQ_F16) kv4_read_kernel<__half, D, kRows><<<blocks, kRowThreads, 0, st>>>(p);
-    else if (dtype == BCQ_BF16) kv4_read_kernel<__nv_bfloat16, D, kRows><<<blocks, kRowThreads, 0, st>>>(p);
-    else kv4_read_kernel<float, D, kRows><<<blocks, kRowThreads, 0, st>>>(p);
+    if (dtype == BCQ_F16) e = launch_early(kv4_read_kernel<__half, D, kRows>, blocks, kRowThreads, 0, st, p);
+    else if (dtype == BCQ_BF16) e = launch_early(kv4_read_kernel<__nv_bfloat16, D, kRows>, blocks, kRowThreads, 0, st, p);
+    else e = launch_early(kv4_read_kernel<float, D, kRows>, blocks, kRowThreads, 0, st, p);
   });
-  return launched();
+  return e == cudaSuccess ? BCQ_OK : BCQ_ERR_CUDA;
 }
 
 size_t bcq_kv4_attention_workspace_bytes(const bcq_kv4* cache, int T, int q_heads, int B,

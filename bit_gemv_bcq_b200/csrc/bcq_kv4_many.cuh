@@ -154,6 +154,7 @@ __global__ void __launch_bounds__(ManyShape<D>::kThreads, 1) kv4_many_kernel(con
   const int pairs = p.at.heads * p.at.B, pair = (int)(blockIdx.x % (unsigned)pairs);
   const int block = p.row_blocks - 1 - (int)(blockIdx.x / (unsigned)pairs);
   const int b = p.by_heads.quotient(pair), kvh = pair - b * p.at.heads, part = blockIdx.y;
+  grid_dependency_wait();
   const Span sp = span_of(p, b, block);
   if (part == 0 && block == 0 && kvh == 0 && threadIdx.x == 0) {
     if (rows_of(p.at, b).y > p.max_q) record_error(&g_kv4_error, BCQ_ERR_SHAPE);

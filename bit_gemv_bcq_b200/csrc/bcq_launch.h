@@ -67,6 +67,26 @@ cudaError_t allow_smem(Kernel kernel, size_t bytes, std::atomic<uint64_t>& done)
   return e;
 }
 
+// Launches a kernel that may be set up while the kernel before it in the stream
+// still runs: it has to execute grid_dependency_wait() before it touches memory
+// (and before launch_dependents(), so that what the next kernel does early is
+// behind all that came before this one).
+template <typename... P, typename... A>
+cudaError_t launch_early(void (*kernel)(P...), dim3 grid, unsigned threads, size_t smem,
+                         cudaStream_t st, const A&... args) {
+  cudaLaunchAttribute attr = {};
+  attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr.val.programmaticStreamSerializationAllowed = 1;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = grid;
+  cfg.blockDim = dim3(threads);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = st;
+  cfg.attrs = &attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, kernel, P(args)...);
+}
+
 // As read_and_clear_device_error, for the kernels of bcq_i8.cu and of
 // bcq_kv4.cu, after the stream's synchronisation.
 cudaError_t read_and_clear_i8_error(int* code);

@@ -629,3 +629,75 @@ def test_side_stream():
     out, _ = _run(c, q, stream=side)
     side.synchronize()
     assert torch.equal(out, ref)
+
+
+def _steps(c, queries, rows, w, w_scale, out):
+    """Tokens one after the other with nothing between the calls; each call's inputs are written just before it
+    and written over just after it."""
+    q, k, n, x = queries[0].clone(), rows[0].clone(), torch.zeros_like(c.t_len), None
+    for i, (qi, ki) in enumerate(zip(queries, rows)):
+        q.copy_(qi), k.copy_(ki)
+        n.fill_(i + 1)
+        api.kv4_append(c.cache, k, k, c.t_table, n)
+        k.zero_()
+        out[i].copy_(api.kv4_attention(q, c.cache, c.t_table, n, max_kv=600).flatten(1))
+        a = api.kv4_attention(q, c.cache, c.t_table, n, max_kv=600)
+        n.zero_(), q.zero_()
+        x = api.linear_i8(a.flatten(1), w, w_scale)
+        a.zero_()
+        codes, scale = api.quantize_i8(x)
+        x.zero_()
+        x = api.gemm_i8(codes, scale, w, w_scale, dtype=F32)
+        out[i] += x.abs().clamp(max=1.0) * 2.0 ** -6
+
+
+@pytest.mark.parametrize("captured", [False, True])
+def test_calls_wait_for_what_came_before(captured):
+    """Kernels that are set up early read nothing early: in a row, in a graph, behind a fork and a join and a memset."""
+    g = torch.Generator().manual_seed(3)
+    S, B, H, D = 40, 3, 4, 128
+    c = Case([S] * B, [1] * B, H, D, 16)
+    queries, rows = (torch.randn(S, B, H, D, generator=g).half().cuda() for _ in range(2))
+    w, w_scale = api.quantize_i8(torch.randn(H * D, H * D, generator=g).half().cuda())
+    want, got = (torch.zeros(S, B, H * D, device="cuda", dtype=F16) for _ in range(2))
+    k, k_param = c.cache.k.clone(), c.cache.k_param.clone()
+    for i in range(S):                      # each call alone
+        n = torch.full((B,), i + 1, dtype=torch.int32, device="cuda")
+        api.kv4_append(c.cache, rows[i], rows[i], c.t_table, n)
+        torch.cuda.synchronize()
+        a = api.kv4_attention(queries[i], c.cache, c.t_table, n, max_kv=600).flatten(1)
+        torch.cuda.synchronize()
+        x = api.linear_i8(a, w, w_scale)
+        torch.cuda.synchronize()
+        codes, scale = api.quantize_i8(x)
+        torch.cuda.synchronize()
+        want[i] = a + api.gemm_i8(codes, scale, w, w_scale, dtype=F32).abs().clamp(max=1.0) * 2.0 ** -6
+    if not captured:
+        for _ in range(3):
+            c.cache.k.copy_(k), c.cache.k_param.copy_(k_param)
+            _steps(c, queries, rows, w, w_scale, got)
+            assert torch.equal(got, want)
+        return
+    side = torch.cuda.Stream()
+    other = torch.zeros(1 << 20, device="cuda")
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        here = torch.cuda.current_stream()
+        side.wait_stream(here)
+        with torch.cuda.stream(side):
+            other.add_(1)
+            c.cache.k_param.copy_(k_param)
+        c.cache.k.copy_(k)
+        here.wait_stream(side)
+        _steps(c, queries, rows, w, w_scale, got)
+        side.wait_stream(here)
+        with torch.cuda.stream(side):      # a call whose stream joins, and one behind a memset
+            out = api.kv4_attention(queries[0], c.cache, c.t_table, c.t_len, max_kv=600)
+        here.wait_stream(side)
+        last = api.kv4_attention(queries[0], c.cache, c.t_table, c.t_len, max_kv=600)
+    for _ in range(3):
+        got.zero_(), c.cache.k.zero_()
+        graph.replay()
+        torch.cuda.synchronize()
+        assert torch.equal(got, want)
+        assert torch.equal(out, last) and not torch.isnan(out).any()
