@@ -78,6 +78,10 @@ __device__ __forceinline__ float4 lds_f32x4(uint32_t addr) {
   return v;
 }
 
+__device__ __forceinline__ void sts_zero16(uint32_t addr) {
+  asm volatile("st.shared.v4.u32 [%0], {%1, %1, %1, %1};" ::"r"(addr), "r"(0u) : "memory");
+}
+
 // One block a row, which it holds in registers between the two looks at it
 // (NV vectors of eight a thread): a row is read once.  |x| is compared by its
 // bits, two at a time, which order like the values (an infinity or a NaN is
@@ -246,6 +250,15 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
   } else if (warp == 2) {
     if (PAIR) tmem_alloc_pair(slot, p.tmem_cols);
     else tmem_alloc(slot, p.tmem_cols);
+  }
+  if (PAIR) {
+    // rows of w's blocks beyond R: zeros
+    const uint32_t pad = (uint32_t)(128 - p.R) * 8;  // of 16 bytes, a block
+    for (uint32_t i = threadIdx.x; i < pad * (uint32_t)(S * p.G); i += kGemmThreads) {
+      const uint32_t block = i / pad;
+      sts_zero16(sbase + block * p.a_block + (uint32_t)p.R * kKBlock + (i - block * pad) * 16);
+    }
+    fence_proxy_async_smem();
   }
   umma_fence_before();
   if (PAIR) {
@@ -576,7 +589,7 @@ void plan_gemm(int M, int N, int K, int sms, GemmParams* p, size_t* smem, int* g
   p->KB = KB;
   p->bufs = p->tiles > p->workers && 2 * p->BT <= 512 ? 2 : 1;
   p->rows = p->R <= 64 && !pair ? 64 : 128;
-  p->a_block = (uint32_t)round_up(p->R, 8) * kKBlock;
+  p->a_block = (uint32_t)(pair ? 128 : round_up(p->R, 8)) * kKBlock;
   p->b_block = (uint32_t)(subs * p->BX) * kKBlock;
   const uint32_t block = p->a_block + p->b_block;
   // about 24 KB a stage: a wait costs the MMA warp about 100 cycles, as long
