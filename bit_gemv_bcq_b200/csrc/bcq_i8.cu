@@ -87,6 +87,9 @@ __device__ __forceinline__ void sts_zero16(uint32_t addr) {
 // bits, two at a time, which order like the values (an infinity or a NaN is
 // the largest of all).  VEC: rows start on 16 bytes; else element by element,
 // the row read twice.
+// Bound by the way of a block (load, two barriers, codes, store), of which eight
+// share an SM: 4096 x 4096 in 12.8 us (3.9 TB/s), 14336 x 4096 in 38.1 us (4.6
+// TB/s), a row of 4096 in 1.8 us.
 template <typename T, int NV, bool VEC>
 __global__ void __launch_bounds__(1024) quantize_i8_kernel(const uint16_t* __restrict__ x,
                                                            int64_t ldx, int K, int8_t* q,
@@ -144,7 +147,7 @@ __global__ void __launch_bounds__(1024) quantize_i8_kernel(const uint16_t* __res
 // ------------------------------------------------------------- the product
 
 // y^T in tiles of R <= 128 rows of w by BT <= 512 rows of x, in one instruction
-// or two of at most 256: the weight's rows
+// or (pairs) two of at most 256: the weight's rows
 // are the tensor core's M (its lanes of tensor memory), the tokens its N, so a
 // single token costs no more than the 16 columns that an instruction has at
 // least, and y's rows are written along the lanes.  Both operands come in
@@ -158,15 +161,24 @@ __global__ void __launch_bounds__(1024) quantize_i8_kernel(const uint16_t* __res
 // adds them up.  A ring slot always belongs to the same warp (the ring's depth
 // is a multiple of theirs): a warp that took a slot's next round could wait
 // for it before the round in progress is full, and a wait by parity would take
-// the round before that one for it.  R needs no alignment: the tensor core reads 64 or 128 rows of
-// the stage whatever they hold, and what they give for rows beyond R is not
-// looked at.
+// the round before that one for it.  R needs no alignment: the tensor core reads
+// 64 or 128 rows of the stage whatever they hold, and what they give for rows
+// beyond R is not looked at.
 //
 // PAIR: two CTAs of a cluster share an instruction (cta_group::2, M = 256).
 // Each holds R rows of w, half of the tile's rows of x, and the outputs of its
 // own R rows, so a CTA fetches BT / 2 rows of x instead of BT.  The CTA of rank
 // 0 issues for both; its `full` barriers count the copies of both, and
-// consumed stages and finished sums are told to both.
+// consumed stages and finished sums are told to both.  Rows of w's
+// blocks beyond R are zeros there, which cost the tensor core less power (333 x
+// 28672 x 8192: 77.6 against 79.4 us).
+//
+// What bounds it.  Few rows: the weight's way from memory, and some 3 us until it
+// flows (1 x 14336 x 4096 11.6 us, 16 x 4096 x 14336 12.6 us: 5 TB/s).  Many: at
+// full clocks the tensor core, 87 % of its cycles (4096 x 14336 x 4096 in 165 us,
+// 2.9 POP/s); kept up for longer, the board's power, which takes a quarter of the
+// clock (205 us with the quantiser; 148 us with zeros for codes).  Between: a
+// second round of tiles that is not full (333 x 28672 x 8192 in 76 us).
 struct GemmParams {
   const float* sx;
   const float* sw;
@@ -544,6 +556,11 @@ int round_up(int v, int to) { return (v + to - 1) / to * to; }
 // the memory's rate (about 24 bytes a cycle an SM).  Rounds of tiles count
 // whole; a tile's output costs about 15 cycles a column when nothing hides it,
 // a pair's start some 1000 cycles.
+// Measured (us: single CTAs | pairs | the model's choice of pairs with one or two
+// instructions, where there is one): 64 x 14336 x 4096 12.5 | 13.9, 128 rows 17.6
+// | 15.4, 256 rows 21.0 | 18.7, 512 rows 33.0 | 29.0 | 29.8, 333 x 28672 x 8192
+// 95.9 | 90.5 | 77.4, 1024 x 4096 x 4096 17.1 | 17.4 | 17.3, 4096 x 14336 x 4096
+// 181 | 164 | 165.
 void plan_gemm(int M, int N, int K, int sms, GemmParams* p, size_t* smem, int* grid, int* kind) {
   const int KB = (K + (int)kKBlock - 1) / (int)kKBlock;
   double best = 0;

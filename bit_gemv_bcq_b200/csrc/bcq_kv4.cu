@@ -179,6 +179,7 @@ struct Pair16<__nv_bfloat16> {
   using V = __nv_bfloat162;
 };
 
+// Rows in: z = fp16(lo), a = fp16((hi - lo) / 15), c = (x - z) / a of each group.
 // A block takes kRows rows, whose values it asks for before it knows their
 // places; eight lanes a group of 64, eight values a lane, one 32-bit word of
 // codes.  Least and greatest come from packed 16-bit compares that keep a NaN.
@@ -190,6 +191,9 @@ struct Pair16<__nv_bfloat16> {
 // fused multiply-adds.  Where a quotient lies within 1e-4 of a half (its error is
 // below 16 * 6 * 2^-24 < 6e-6, and the difference's rounding adds less) the
 // half decides in fp64, where x - z and (c + 1/2) a are exact.
+// Bound by its instructions, some 200 for 256 values: 8 x 1024 rows of 8 heads
+// of 128 take 15.1 us (43 MB, 2.8 TB/s), 64 rows 3.0 us (launch, and four loads
+// one after the other).
 template <typename T, int D, int kRows>
 __global__ void __launch_bounds__(kRowThreads, 4) kv4_append_kernel(const AppendParams p) {
   using V = typename Pair16<T>::V;
@@ -286,7 +290,10 @@ struct ReadParams {
   int T;
 };
 
-// Eight values (one word of codes) a thread and row.
+// Rows out: a c + z.  Eight values (one word of codes) a thread and row, its
+// four rows' loads in flight together.  Bound by memory from some thousand rows
+// on: 8 x 1024 rows of 8 heads of 128 as fp16 8.2 us (43 MB, 5.2 TB/s), 64 rows
+// 2.7 us.
 template <typename TO, int D, int kRows>
 __global__ void __launch_bounds__(kRowThreads) kv4_read_kernel(const ReadParams p) {
   constexpr int G = D / kKvGroup, kWords = D / 8;
@@ -369,6 +376,15 @@ __global__ void __launch_bounds__(kRowThreads) kv4_read_kernel(const ReadParams 
 // reads them, so no barrier but the warp's own), 16-byte pieces placed so that
 // the fragment loads have no bank conflicts.  A long sequence is split over
 // CTAs, whose partial results a second kernel joins in order.
+//
+// What bounds it: with all SMs busy the ALU pipe (masks and permutes of codes,
+// some 55 %, beside 90 % of the memory's rate in the steady state) -- a row over
+// 524288 positions takes 113 us (5.3 TB/s), 64 rows over up to 8192 each, ragged,
+// 84.7 us (3.9 TB/s); below that a CTA's start (page table, then codes, some 3
+// us) and the joining kernel: 131072 positions 37.7 us, 4001 positions 8.1 us.
+// Four CTAs of four warps an SM hide one another's loads: the registers of a
+// thread (128) leave no more, and three stages of 32 positions a warp are what
+// shared memory has room for.
 struct AttentionParams {
   Places at;
   const uint8_t* k;
@@ -1037,7 +1053,9 @@ __global__ void __launch_bounds__(kFewWarps * 32, NT == 1 && D <= 128 ? 4 : 2) k
 // Joins the parts of the rows that were split, in the same order whenever it
 // runs: a CTA a row and head.  Every part's (max, sum) at once first, which
 // give its weight; then D / 4 threads a part, 512 / D parts at a time, whose
-// loads wait for nothing.
+// loads wait for nothing.  Two rounds of loads from L2 bound it: some 2.5 us for
+// a row's 32 heads and 30 to 80 parts, of which the setting up goes on while the
+// parts are still computed.
 constexpr int kMostParts = 512;
 
 template <typename T, int D>
@@ -1185,11 +1203,14 @@ Places places_of(const bcq_kv4* c, const int32_t* table, int table_width, const 
 }
 
 // f(D, rows a block) as compile-time numbers: one row while more would leave
-// SMs idle, else four, whose loads are in flight together.
+// SMs idle, else four, whose places are found and whose loads are in flight
+// together.  In and out of a cache of 8 heads of 128 (us, one | four rows a
+// block): 64 rows 2.8 + 2.4 | 3.9 + 2.6, 512 rows 3.6 + 3.0 | 4.1 + 2.7, 1024
+// rows 5.5 + 3.7 | 4.6 + 3.0, 8192 rows 30.2 + 17.7 | 17.5 + 10.0.
 template <typename F>
 void by_shape(int D, int T, const F& f) {
   auto rows = [&](auto d) {
-    if (T < 1184) f(d, std::integral_constant<int, 1>());
+    if (T < 768) f(d, std::integral_constant<int, 1>());
     else f(d, std::integral_constant<int, 4>());
   };
   if (D == 64) rows(std::integral_constant<int, 64>());
@@ -1237,16 +1258,21 @@ void plan_parts(AttentionPlan* f, int64_t units, int B, int max_kv, int each, do
   }
 }
 
-// The few-row kernel passes over the positions once for every 16 rows, four
-// CTAs an SM (two where rows or values are many), with exact products of
-// queries and codes; the many-row kernel once for every 256 (128 where D =
-// 256), with keys rounded to fp16.  Over few positions those roundings do not
-// average out of lse (1e-5 of it below 500), and little is saved: such calls
-// stay with the first.
+// The few-row kernel passes over the positions once for every 16 rows (8 where
+// there are no more, or D = 256: 13.0 us in one pass for 16 rows and 8 x 2000
+// positions, 15.0 in two), four CTAs an SM (two where rows or values are many),
+// with exact products of queries and codes; the many-row kernel once for every
+// 256 (128 where D = 256), with keys rounded to fp16.  From which rows on the
+// second pays depends on the units of work (us, few | many): 64 rows 27.8 |
+// 39.5, 128 rows 37.7 | 39.9 (8 x 2000 positions of 8 heads), 70.5 | 43.5 (32 x
+// 1000), 44.6 | 34.0 (16 x 2000, D = 64), 46.2 | 53.5 (4 x 2000, D = 256).  Over
+// few positions the keys' roundings do not average out of lse (1e-5 of it below
+// 500), and little is saved (256 rows, 8 x 400: 27.0 | 26.8; 8 x 600: 32.4 |
+// 24.9): such calls stay with the first.
 AttentionPlan plan_attention(const bcq_kv4* c, int q_heads, int B, int max_q, int max_kv, int window) {
   AttentionPlan f;
   const int64_t rows = (int64_t)max_q * (q_heads / c->heads);
-  const bool many = rows > 96 && max_kv >= 512 && (window == 0 || window >= 512);
+  const bool many = rows > (c->head_dim == 256 ? 128 : 96) && max_kv >= 512 && (window == 0 || window >= 512);
   f.nt = many ? 0 : rows <= 8 || c->head_dim == 256 ? 1 : 2;
   f.rows = !many ? 8 * f.nt : c->head_dim == 256 ? 128 : 256;
   f.row_blocks = (int)std::min<int64_t>((rows + f.rows - 1) / f.rows, INT32_MAX);
