@@ -92,7 +92,7 @@ def build_fast(force: bool = False) -> str:
         subprocess.run([os.environ.get("CXX", "g++"), "-O2", "-std=c++17", "-fPIC", "-shared", "-w",
                         *[f"-I{d}" for d in inc], FAST_SRC, "-o", tmp,
                         "-L" + os.path.join(torch_dir, "lib"), "-lc10", "-lc10_cuda", "-ltorch_cpu",
-                        "-ltorch_python"], check=True)
+                        "-ltorch_cuda", "-ltorch_python"], check=True)
         os.replace(tmp, FAST)
     return FAST
 

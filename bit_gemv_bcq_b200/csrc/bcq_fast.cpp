@@ -11,7 +11,8 @@
 //
 // The library is not linked: api.py hands over its entry points' addresses.
 #include <ATen/ATen.h>
-#include <ATen/ops/empty.h>
+#include <ATen/cuda/EmptyTensor.h>
+#include <c10/cuda/CUDACachingAllocator.h>
 #include <c10/cuda/CUDAFunctions.h>
 #include <c10/cuda/CUDAStream.h>
 #include <torch/csrc/autograd/python_variable.h>
@@ -69,9 +70,13 @@ at::ScalarType type_of(long dtype) {
   return dtype == BCQ_F16 ? at::kHalf : dtype == BCQ_BF16 ? at::kBFloat16 : at::kFloat;
 }
 
+// (the dispatcher, and a tensor around a workspace, are a microsecond of the
+// call's)
 at::Tensor empty(const at::Tensor& like, at::IntArrayRef size, at::ScalarType type) {
-  return at::empty(size, like.options().dtype(type));
+  return at::Tensor(at::detail::empty_cuda(size, type, like.device(), std::nullopt));
 }
+// Memory in the current stream's order, until the end of the call.
+c10::DataPtr workspace(size_t bytes) { return c10::cuda::CUDACachingAllocator::get()->allocate(bytes); }
 
 // A matrix with contiguous rows that do not overlap; its row distance.
 bool matrix(const at::Tensor& t, int64_t* rows, int64_t* cols, int64_t* ld) {
@@ -169,10 +174,10 @@ PyObject* linear_i8(PyObject*, PyObject* const* a, Py_ssize_t n) {
   if (!product_out(a[3], M, N, x->scalar_type(), *x, index, &y, &ldy)) return no();
   const size_t need = p_linear_bytes((int)M, (int)K);
   if (need == 0) return no();
-  const at::Tensor ws = empty(*x, {(int64_t)need}, at::kByte);
+  const c10::DataPtr ws = workspace(need);
   if (!called([&] { return p_linear_i8(x->data_ptr(), dtype, ldx, (const int8_t*)w->data_ptr(), ldw,
                   (const float*)sw->data_ptr(), (int)M, (int)N, (int)K, y.data_ptr(), ldy,
-                  ws.data_ptr(), need, stream_of(index)); }))
+                  ws.get(), need, stream_of(index)); }))
     return no();
   return done(y, a[3]);
 }
@@ -289,13 +294,14 @@ PyObject* kv4_attention(PyObject*, PyObject* const* a, Py_ssize_t n) {
     return no();
   const int64_t D = s.c.head_dim;
   const size_t need = p_attention_bytes(&s.c, (int)T, (int)H, s.B, (int)max_q, (int)max_kv, (int)window);
-  at::Tensor out = empty(*q, {T, H, D}, q->scalar_type()), lse, ws;
+  at::Tensor out = empty(*q, {T, H, D}, q->scalar_type()), lse;
+  c10::DataPtr ws;
   if (lse_too) lse = empty(*q, {T, H}, at::kFloat);
-  if (need) ws = empty(*q, {(int64_t)need}, at::kByte);
+  if (need) ws = workspace(need);
   if (!called([&] { return p_kv4_attention(&s.c, q->data_ptr(), ld, hd, dtype_of(*q), (int)T, (int)H, s.table, s.W,
                       s.kv_len, s.cu, s.B, (int)max_q, (int)max_kv, causal, (int)window,
                       (float)scale, out.data_ptr(), H * D, D, lse_too ? (float*)lse.data_ptr() : nullptr,
-                      need ? ws.data_ptr() : nullptr, need, stream_of(s.index)); }))
+                      ws.get(), need, stream_of(s.index)); }))
     return no();
   if (!lse_too) return THPVariable_Wrap(out);
   return Py_BuildValue("(NN)", THPVariable_Wrap(out), THPVariable_Wrap(lse));

@@ -1238,8 +1238,8 @@ void plan_parts(AttentionPlan* f, int64_t units, int B, int max_kv, int each, do
   double best = 0;
   const double mean = B > 1 ? 0.75 * max_kv : max_kv, room = 148.0 * each;
   for (int s = 1; s <= kMostParts && (s == 1 || (int64_t)(s - 1) * 128 < max_kv); s += s < 80 ? 1 : s / 16) {
-    const int chunk = (int)std::min<int64_t>((((int64_t)max_kv + s - 1) / s + 127) / 128 * 128, 1 << 30);
-    const int parts = (max_kv + chunk - 1) / chunk;
+    const uint32_t chunk = std::min((((uint32_t)max_kv + (uint32_t)s - 1) / (uint32_t)s + 127) & ~127u, 1u << 30);
+    const int parts = (int)(((uint32_t)max_kv + chunk - 1) / chunk);
     const int64_t ctas = units * parts;
     double cost;
     if (ctas <= (int64_t)room) {
@@ -1253,7 +1253,7 @@ void plan_parts(AttentionPlan* f, int64_t units, int B, int max_kv, int each, do
     if (best == 0 || cost < best) {
       best = cost;
       f->splits = parts;
-      f->chunk = chunk;
+      f->chunk = (int)chunk;
     }
   }
 }
