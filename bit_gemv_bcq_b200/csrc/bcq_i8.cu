@@ -11,6 +11,7 @@
 
 #include "bcq.h"
 #include "bcq_device.cuh"
+#include "bcq_f32x2.cuh"
 #include "bcq_launch.h"
 #include "bcq_tcgen05.cuh"
 
@@ -61,15 +62,36 @@ __device__ __forceinline__ RowScale row_scale(uint32_t top) {
   return {pre, a * pre, __fdiv_rn(127.f, a * pre), top != 0 && top < Bits16<T>::kInf};
 }
 
-// In the low byte; rounding by adding 1.5 2^23 (conversion instructions run at
-// an eighth of the rate).
+// Codes of eight values (two a word), a byte each; rounding by adding 1.5 2^23
+// (conversion instructions run at an eighth of the rate).
 template <typename T>
-__device__ __forceinline__ uint32_t code_of(uint32_t bits, const RowScale& s) {
-  const float x = Bits16<T>::to_float(bits) * s.pre;
-  const float v = x * s.inv;
-  float up = v + 12582912.f;
-  if (fabsf(v - (up - 12582912.f)) > 0.4999f) up = __fdiv_rn(x * 127.f, s.as) + 12582912.f;
-  return __float_as_uint(up);
+__device__ __forceinline__ uint2 codes_of(const uint4& words, const RowScale& s) {
+  constexpr float kMagic = 12582912.f;
+  const uint32_t w[4] = {words.x, words.y, words.z, words.w};
+  const uint64_t pre = pack_f32x2(s.pre, s.pre), inv = pack_f32x2(s.inv, s.inv), minus = pack_f32x2(-1.f, -1.f),
+                 magic = pack_f32x2(kMagic, kMagic), no_magic = pack_f32x2(-kMagic, -kMagic);
+  float up[8], off = 0.f;
+#pragma unroll
+  for (int e = 0; e < 8; e += 2) {
+    const uint64_t x = pack_f32x2(Bits16<T>::to_float(w[e >> 1] & 0xFFFFu), Bits16<T>::to_float(w[e >> 1] >> 16));
+    const uint64_t v = mul_f32x2(mul_f32x2(x, pre), inv), u = add_f32x2(v, magic);
+    float a, b;
+    unpack_f32x2(u, up[e], up[e + 1]);
+    unpack_f32x2(fma_f32x2(add_f32x2(u, no_magic), minus, v), a, b);
+    off = max3(off, fabsf(a), fabsf(b));
+  }
+  if (off > 0.4999f) {
+#pragma unroll
+    for (int e = 0; e < 8; ++e) {
+      const float x = Bits16<T>::to_float((w[e >> 1] >> (16 * (e & 1))) & 0xFFFFu) * s.pre;
+      if (fabsf(fmaf(up[e] - kMagic, -1.f, x * s.inv)) > 0.4999f) up[e] = __fdiv_rn(x * 127.f, s.as) + kMagic;
+    }
+  }
+  auto four = [&](int e) {
+    return prmt(prmt(__float_as_uint(up[e]), __float_as_uint(up[e + 1]), 0x0040),
+                prmt(__float_as_uint(up[e + 2]), __float_as_uint(up[e + 3]), 0x0040), 0x5410);
+  };
+  return make_uint2(four(0), four(4));
 }
 
 __device__ __forceinline__ float4 lds_f32x4(uint32_t addr) {
@@ -88,13 +110,12 @@ __device__ __forceinline__ void sts_zero16(uint32_t addr) {
 // One block a row, which it holds in registers between the two looks at it
 // (NV vectors of eight a thread): a row is read once.  |x| is compared by its
 // bits, two at a time, which order like the values (an infinity or a NaN is
-// the largest of all).  VEC: rows start on 16 bytes; else element by element,
-// the row read twice.
-// Bound by the way of a block (load, two barriers, codes, store), of which eight
-// share an SM: 4096 x 4096 in 12.8 us (3.9 TB/s), 14336 x 4096 in 38.1 us (4.6
-// TB/s), a row of 4096 in 1.8 us.
+// the largest of all).  VEC: rows start on 16 bytes; else its values are loaded
+// one by one, twice.
+// Bound by the way of a block (load, two barriers, codes, store): 4096 x 4096 in
+// 11.2 us (4.5 TB/s), 14336 x 4096 in 31 us (5.6 TB/s), a row of 4096 in 1.5 us.
 template <typename T, int NV, bool VEC>
-__global__ void __launch_bounds__(1024) quantize_i8_kernel(const uint16_t* __restrict__ x,
+__global__ void __launch_bounds__(NV == 2 ? 256 : 1024, NV == 2 ? 8 : 1) quantize_i8_kernel(const uint16_t* __restrict__ x,
                                                            int64_t ldx, int K, int8_t* q,
                                                            int64_t ldq, float* scale) {
   __shared__ uint32_t s_max[32];
@@ -120,7 +141,19 @@ __global__ void __launch_bounds__(1024) quantize_i8_kernel(const uint16_t* __res
     top2 = __vmaxu2(top2, v[i].w & 0x7FFF7FFFu);
   }
   uint32_t top = max(top2 & 0xFFFFu, top2 >> 16);
-  for (int k = vecs * 8 + tid; k < K; k += threads) top = max(top, (uint32_t)row[k] & 0x7FFFu);
+  // eight values from k on, one by one, with zeros beyond the row
+  auto eight = [&](int k) {
+    uint32_t w[4] = {0, 0, 0, 0};
+#pragma unroll
+    for (int e = 0; e < 8; ++e)
+      if (k + e < K) w[e >> 1] |= (uint32_t)row[k + e] << (16 * (e & 1));
+    return make_uint4(w[0], w[1], w[2], w[3]);
+  };
+  for (int k = (vecs + tid) * 8; k < K; k += threads * 8) {
+    const uint4 x = eight(k);
+    const uint32_t y = __vmaxu2(__vmaxu2(x.x & 0x7FFF7FFFu, x.y & 0x7FFF7FFFu), __vmaxu2(x.z & 0x7FFF7FFFu, x.w & 0x7FFF7FFFu));
+    top = max(top, max(y & 0xFFFFu, y >> 16));
+  }
   top = __reduce_max_sync(0xFFFFFFFFu, top);
   if ((tid & 31) == 0) s_max[tid >> 5] = top;
   __syncthreads();
@@ -132,19 +165,17 @@ __global__ void __launch_bounds__(1024) quantize_i8_kernel(const uint16_t* __res
 #pragma unroll
   for (int i = 0; i < NV; ++i) {
     if (tid + i * threads >= vecs) continue;
-    uint2 out = make_uint2(0, 0);
-    if (rs.any) {
-      const uint32_t w[4] = {v[i].x, v[i].y, v[i].z, v[i].w};
-      uint32_t c[8];
-#pragma unroll
-      for (int e = 0; e < 8; ++e) c[e] = code_of<T>((w[e >> 1] >> (16 * (e & 1))) & 0xFFFFu, rs);
-      out.x = prmt(prmt(c[0], c[1], 0x0040), prmt(c[2], c[3], 0x0040), 0x5410);
-      out.y = prmt(prmt(c[4], c[5], 0x0040), prmt(c[6], c[7], 0x0040), 0x5410);
-    }
+    const uint2 out = rs.any ? codes_of<T>(v[i], rs) : make_uint2(0, 0);
     *reinterpret_cast<uint2*>(to + (int64_t)(tid + i * threads) * 8) = out;
   }
-  for (int k = vecs * 8 + tid; k < K; k += threads)
-    to[k] = (int8_t)(rs.any ? code_of<T>(row[k], rs) & 0xFFu : 0u);
+  for (int k = (vecs + tid) * 8; k < K; k += threads * 8) {
+    const uint2 out = rs.any ? codes_of<T>(eight(k), rs) : make_uint2(0, 0);
+    if (k + 8 <= K) {
+      *reinterpret_cast<uint2*>(to + k) = out;
+    } else {
+      for (int e = 0; k + e < K; ++e) to[k + e] = (int8_t)((e < 4 ? out.x : out.y) >> (8 * (e & 3)));
+    }
+  }
 }
 
 // ------------------------------------------------------------- the product
@@ -504,8 +535,14 @@ cudaError_t launch_quantize_t(const uint16_t* x, int M, int K, int64_t ldx, int8
     return launch_early(kernel, dim3((unsigned)M), threads, 0, st, x, ldx, K, q, ldq, scale);
   };
   if (!aligned(x, 16) || (ldx % 8 && M > 1)) return launch(quantize_i8_kernel<T, 1, false>, 256);
-  if (K <= 4096) return launch(quantize_i8_kernel<T, 2, true>, 256);
-  if (K <= 16384) return launch(quantize_i8_kernel<T, 4, true>, 512);
+  // Many rows: fewer threads a row, more rows an SM and loads in flight; few rows:
+  // more threads a row (us, few | many threads: 64 x 4096 2.6 | 2.0, 1024 x 4096
+  // 4.8 | 4.0, 4096 x 4096 11.2 | 11.8, 14336 x 4096 31.1 | 34.4; 333 x 14336 6.5 |
+  // 5.2, 1024 x 14336 11.5 | 12.7, 4096 x 14336 33.3 | 42.2).
+  if (K <= 4096 && M < 3000) return launch(quantize_i8_kernel<T, 2, true>, 256);
+  if (K <= 4096) return launch(quantize_i8_kernel<T, 4, true>, 128);
+  if (K <= 16384 && M < 1024) return launch(quantize_i8_kernel<T, 4, true>, 512);
+  if (K <= 16384) return launch(quantize_i8_kernel<T, 8, true>, 256);
   return launch(quantize_i8_kernel<T, 8, true>, 1024);
 }
 

@@ -11,6 +11,7 @@
 
 #include "bcq.h"
 #include "bcq_device.cuh"
+#include "bcq_f32x2.cuh"
 #include "bcq_launch.h"
 
 namespace bcq {
@@ -249,12 +250,19 @@ __global__ void __launch_bounds__(kRowThreads, 4) kv4_append_kernel(const Append
       if (ok && a > 0.f) {
         const float inv = __fdividef(1.f, a * 15.f);
         float f[8], c[8], off = 0.f;
+        const uint64_t minus_z = pack_f32x2(-z, -z), fifteen = pack_f32x2(15.f, 15.f), minus = pack_f32x2(-1.f, -1.f),
+                       magic = pack_f32x2(kMagic, kMagic), no_magic = pack_f32x2(-kMagic, -kMagic);
 #pragma unroll
-        for (int e = 0; e < 8; ++e) {
-          f[e] = bits_to_float<T>((w[e >> 1] >> (16 * (e & 1))) & 0xFFFFu);
-          const float q = __saturatef((f[e] - z) * inv);  // of 15
-          c[e] = __fsub_rn(__fmaf_rn(q, 15.f, kMagic), kMagic);
-          off = fmaxf(off, fabsf(__fmaf_rn(q, 15.f, -c[e])));
+        for (int e = 0; e < 8; e += 2) {
+          f[e] = bits_to_float<T>(w[e >> 1] & 0xFFFFu);
+          f[e + 1] = bits_to_float<T>(w[e >> 1] >> 16);
+          float x, y;
+          unpack_f32x2(add_f32x2(pack_f32x2(f[e], f[e + 1]), minus_z), x, y);
+          const uint64_t q = pack_f32x2(__saturatef(x * inv), __saturatef(y * inv));  // of 15
+          const uint64_t r = add_f32x2(fma_f32x2(q, fifteen, magic), no_magic);
+          unpack_f32x2(r, c[e], c[e + 1]);
+          unpack_f32x2(fma_f32x2(q, fifteen, mul_f32x2(r, minus)), x, y);
+          off = max3(off, fabsf(x), fabsf(y));
         }
         if (off > 0.4999f) {
 #pragma unroll

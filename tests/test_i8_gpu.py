@@ -70,6 +70,35 @@ def test_codes_and_scales_are_the_oracles(M, K, dtype):
 
 
 @pytest.mark.parametrize("dtype", [F16, BF16])
+@pytest.mark.parametrize("M,K,ld", [(2999, 72, 72), (3000, 72, 80), (8200, 1031, 1040), (1023, 5000, 5000),
+                                    (1024, 5000, 5008), (1030, 16384, 16384), (1030, 4100, 4101)])
+def test_many_rows(M, K, ld, dtype):
+    """The other shapes of a block, and rows whose last eight values are fewer."""
+    x = torch.full((M, ld), float("nan"), dtype=dtype, device="cuda")[:, :K]
+    x.copy_(_activations(M, K, dtype, M + K))
+    q, s = api.quantize_i8(x)
+    rq, rs = i8.quantize(_f64(x))
+    assert np.array_equal(q.cpu().numpy(), rq)
+    assert np.array_equal(s.cpu().numpy(), rs)
+
+
+@pytest.mark.parametrize("K", [5, 40, 97, 4100])
+@pytest.mark.parametrize("off", [0, 1])
+def test_columns_beyond_a_row_are_left(K, off):
+    x = _activations(3, K, F16, K)
+    base = torch.empty(3 * K + 1, dtype=F16, device="cuda")
+    view = base[off:off + 3 * K].view(3, K)
+    view.copy_(x)
+    ldq = -(-K // 16) * 16 + 16
+    q = torch.full((3, ldq), 99, dtype=torch.int8, device="cuda")
+    s = torch.zeros(3, device="cuda")
+    assert api.lib().bcq_quantize_i8(view.data_ptr(), 0, 3, K, K, q.data_ptr(), ldq, s.data_ptr(), None) == api.BCQ_OK
+    torch.cuda.synchronize()
+    assert (q[:, K:] == 99).all()
+    assert np.array_equal(q[:, :K].cpu().numpy(), i8.quantize(_f64(x))[0])
+
+
+@pytest.mark.parametrize("dtype", [F16, BF16])
 def test_halves_go_to_even_exactly(dtype):
     # max 254 u makes x = (2 j + 1) u the half j + 1/2 itself; its neighbours are not halves
     for u in (1.0, 2.0 ** -10, 2.0 ** -20 if dtype == BF16 else 2.0 ** -14):
