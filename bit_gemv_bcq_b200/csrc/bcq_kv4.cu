@@ -1234,35 +1234,46 @@ struct AttentionPlan {
 };
 
 // How many parts the positions are cut into.  `each` CTAs fit an SM; a CTA
-// costs its positions and `start` more, splitting at all `join` positions.
-// While all run at once the fullest SM decides, and fewer than `each` on it
-// run faster, though not in proportion (measured: 0.4, 0.55, 0.8 and 1 of the
-// time with 1 to 4 of 4).  Beyond that CTAs start as others end: the whole
-// work's share and half a part, or a part.  Of sequences of different lengths
-// three quarters of max_kv are thought to be there.
-void plan_parts(AttentionPlan* f, int64_t units, int B, int max_kv, int each, double start,
-                double join) {
-  static const double kPace[5] = {0, 0.4, 0.55, 0.8, 1.0};
-  double best = 0;
-  const double mean = B > 1 ? 0.75 * max_kv : max_kv, room = 148.0 * each;
-  for (int s = 1; s <= kMostParts && (s == 1 || (int64_t)(s - 1) * 128 < max_kv); s += s < 80 ? 1 : s / 16) {
-    const uint32_t chunk = std::min((((uint32_t)max_kv + (uint32_t)s - 1) / (uint32_t)s + 127) & ~127u, 1u << 30);
-    const int parts = (int)(((uint32_t)max_kv + chunk - 1) / chunk);
-    const int64_t ctas = units * parts;
-    double cost;
-    if (ctas <= (int64_t)room) {
-      const int fullest = (int)((ctas + 147) / 148);
-      cost = chunk * (each == 1 ? 1.0 : kPace[std::min(4, fullest * 4 / each)]) + start;
+// costs its positions and `start` more, splitting at all `join` positions and
+// some a part.  While all run at once the fullest SM decides, and fewer than
+// `each` on it run faster, though not in proportion; beyond that CTAs start as
+// others end: the whole work's share and `tail` of a part.  Of sequences of
+// different lengths seven tenths of max_kv are thought to be there, and half a
+// part more (of a window, all).  The numbers of the few-row kernel are fitted to
+// 68 calls (1 to 256 sequences, 300 to 262144 positions, heads of 64 to 256, each
+// over 10 to 20 parts): 2 % on average above the best part of each call.  (A
+// position of a head of 64 takes less, so a start and a joining are worth more of
+// them; of a head of 256 fewer.)
+struct PartsModel {
+  int each;
+  float there;  // of max_kv, on average
+  float start, join, join_part, tail;
+};
+void plan_parts(AttentionPlan* f, int64_t units, int max_kv, const PartsModel& m) {
+  static const float kPace[5] = {0, 0.43f, 0.72f, 0.865f, 1.0f};
+  const float room = 148.f * (float)m.each, mean = m.there * (float)max_kv;
+  float best = 0;
+  const uint32_t kv = (uint32_t)max_kv;
+  uint32_t chunk = ((kv + kMostParts - 1) / kMostParts + 127) & ~127u;
+  for (bool more = true; more; chunk += std::max(128u, (chunk / 8) & ~127u)) {
+    const uint32_t parts = (kv + chunk - 1) / chunk;
+    const float length = (float)std::min(chunk, kv), all = (float)parts;
+    const float ctas = (float)units * std::min(all, m.there * all + 0.5f);
+    float cost;
+    if (ctas <= room) {
+      const int fullest = ((int)ctas + 147) / 148;
+      cost = length * kPace[std::min(4, fullest * 4 / m.each)] + m.start;
     } else {
-      cost = std::max(chunk + start, (double)units * (mean + mean / max_kv * parts * start) / room +
-                                         (chunk + start) / 2);
+      cost = std::max(length * kPace[1] + m.start,
+                      ((float)units * mean + ctas * m.start) / room + m.tail * (length + m.start));
     }
-    cost += parts > 1 ? join + 2.5 * parts : 0;
+    cost += parts > 1 ? m.join + m.join_part * all : 0.f;
     if (best == 0 || cost < best) {
       best = cost;
-      f->splits = parts;
+      f->splits = (int)parts;
       f->chunk = (int)chunk;
     }
+    more = parts > 1 && (m.each == 1 || length * kPace[1] < best);  // longer ones cost more
   }
 }
 
@@ -1288,8 +1299,12 @@ AttentionPlan plan_attention(const bcq_kv4* c, int q_heads, int B, int max_q, in
   // what a block of rows sees at most
   const int seen = window == 0 ? max_kv
                                : (int)std::min<int64_t>(max_kv, (int64_t)window + f.rows * c->heads / q_heads + 32);
-  if (many) plan_parts(&f, units, B, seen, 1, 1024, 2048);
-  else plan_parts(&f, units, B, seen, f.nt == 1 && c->head_dim <= 128 ? 4 : 2, 160, 128);
+  const float there = B == 1 || seen < max_kv ? 1.f : 0.7f;
+  const float scale = c->head_dim == 64 ? 1.4f : c->head_dim == 256 ? 0.65f : 1.f;
+  if (many)
+    plan_parts(&f, units, seen, {1, there, 1024, 2048, 2.5f, 0.5f});
+  else
+    plan_parts(&f, units, seen, {f.nt == 1 && c->head_dim <= 128 ? 4 : 2, there, 335 * scale, 150 * scale, 2.4f * scale, 0.2f});
   return f;
 }
 
