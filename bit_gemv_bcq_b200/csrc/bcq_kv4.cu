@@ -1233,39 +1233,34 @@ struct AttentionPlan {
   int nt, rows, row_blocks, splits, chunk;
 };
 
-// How many parts the positions are cut into.  `each` CTAs fit an SM; a CTA
-// costs its positions and `start` more, splitting at all `join` positions and
-// some a part.  While all run at once the fullest SM decides, and fewer than
-// `each` on it run faster, though not in proportion; beyond that CTAs start as
-// others end: the whole work's share and `tail` of a part.  Of sequences of
-// different lengths seven tenths of max_kv are thought to be there, and half a
-// part more (of a window, all).  The numbers of the few-row kernel are fitted to
-// 68 calls (1 to 256 sequences, 300 to 262144 positions, heads of 64 to 256, each
-// over 10 to 20 parts): 2 % on average above the best part of each call.  (A
-// position of a head of 64 takes less, so a start and a joining are worth more of
-// them; of a head of 256 fewer.)
+// How many parts the positions are cut into, by a model of the time (us, which is
+// returned).  `each` CTAs fit an SM; a CTA takes `start`, and `per` a position
+// (beside each - 1 others); splitting at all takes `join`, and some a part.  While
+// all CTAs run at once the fullest SM decides, and fewer than `each` on it run
+// faster, though not in proportion; beyond that CTAs start as others end: the
+// whole work's share and `tail` of a CTA.  Of max_kv `there` is thought to be
+// there on average, and half a part more.
 struct PartsModel {
   int each;
-  float there;  // of max_kv, on average
-  float start, join, join_part, tail;
+  float there, per, start, join, join_part, tail;
 };
-void plan_parts(AttentionPlan* f, int64_t units, int max_kv, const PartsModel& m) {
-  static const float kPace[5] = {0, 0.43f, 0.72f, 0.865f, 1.0f};
+float plan_parts(AttentionPlan* f, int64_t units, int max_kv, const PartsModel& m) {
+  static const float kPace[5] = {0, 0.49f, 0.63f, 0.8f, 1.0f};
   const float room = 148.f * (float)m.each, mean = m.there * (float)max_kv;
   float best = 0;
   const uint32_t kv = (uint32_t)max_kv;
   uint32_t chunk = ((kv + kMostParts - 1) / kMostParts + 127) & ~127u;
   for (bool more = true; more; chunk += std::max(128u, (chunk / 8) & ~127u)) {
     const uint32_t parts = (kv + chunk - 1) / chunk;
-    const float length = (float)std::min(chunk, kv), all = (float)parts;
+    const float length = (float)std::min(chunk, kv) * m.per, all = (float)parts;
     const float ctas = (float)units * std::min(all, m.there * all + 0.5f);
     float cost;
     if (ctas <= room) {
       const int fullest = ((int)ctas + 147) / 148;
       cost = length * kPace[std::min(4, fullest * 4 / m.each)] + m.start;
     } else {
-      cost = std::max(length * kPace[1] + m.start,
-                      ((float)units * mean + ctas * m.start) / room + m.tail * (length + m.start));
+      cost = std::max(length * kPace[m.each == 1 ? 4 : 1] + m.start,
+                      ((float)units * mean * m.per + ctas * m.start) / room + m.tail * (length + m.start));
     }
     cost += parts > 1 ? m.join + m.join_part * all : 0.f;
     if (best == 0 || cost < best) {
@@ -1273,39 +1268,53 @@ void plan_parts(AttentionPlan* f, int64_t units, int max_kv, const PartsModel& m
       f->splits = (int)parts;
       f->chunk = (int)chunk;
     }
-    more = parts > 1 && (m.each == 1 || length * kPace[1] < best);  // longer ones cost more
+    more = parts > 1 && length * kPace[1] < best;  // longer ones cost more
   }
+  return best;
 }
 
 // The few-row kernel passes over the positions once for every 16 rows (8 where
 // there are no more, or D = 256: 13.0 us in one pass for 16 rows and 8 x 2000
 // positions, 15.0 in two), four CTAs an SM (two where rows or values are many),
 // with exact products of queries and codes; the many-row kernel once for every
-// 256 (128 where D = 256), with keys rounded to fp16.  From which rows on the
-// second pays depends on the units of work (us, few | many): 64 rows 27.8 |
-// 39.5, 128 rows 37.7 | 39.9 (8 x 2000 positions of 8 heads), 70.5 | 43.5 (32 x
-// 1000), 44.6 | 34.0 (16 x 2000, D = 64), 46.2 | 53.5 (4 x 2000, D = 256).  Over
-// few positions the keys' roundings do not average out of lse (1e-5 of it below
-// 500), and little is saved (256 rows, 8 x 400: 27.0 | 26.8; 8 x 600: 32.4 |
-// 24.9): such calls stay with the first.
+// 256 (128 where D = 256), with keys rounded to fp16.  Over few positions those
+// roundings do not average out of lse (1e-5 of it below 500), and little is
+// saved: such calls stay with the first; so do those that the second is not
+// thought to save a seventh.
+//
+// The models' numbers are fitted to 68 calls of the first (1 to 256 sequences,
+// 300 to 262144 positions, heads of 64 to 256) and 60 of the second, each over 10
+// to 20 parts: 2 and 1 % on average above the best part of each call, 3 % above
+// the better kernel's.  Measured (us, few | many): 64 rows over 4000 positions,
+// 8 heads of 128, 14.3 | 14.4, over 8 x 2000 21.8 | 25.1, 32 x 1000 41.0 | 42.0; 128
+// rows 19.9 | 17.3, 27.8 | 29.8, 70.6 | 43.5; 512 rows 46.7 | 32.5, 97.1 | 58.3, 231 |
+// 97.
 AttentionPlan plan_attention(const bcq_kv4* c, int q_heads, int B, int max_q, int max_kv, int window) {
-  AttentionPlan f;
-  const int64_t rows = (int64_t)max_q * (q_heads / c->heads);
-  const bool many = rows > (c->head_dim == 256 ? 128 : 96) && max_kv >= 512 && (window == 0 || window >= 512);
-  f.nt = many ? 0 : rows <= 8 || c->head_dim == 256 ? 1 : 2;
-  f.rows = !many ? 8 * f.nt : c->head_dim == 256 ? 128 : 256;
-  f.row_blocks = (int)std::min<int64_t>((rows + f.rows - 1) / f.rows, INT32_MAX);
-  const int64_t units = (int64_t)f.row_blocks * c->heads * B;
-  // what a block of rows sees at most
-  const int seen = window == 0 ? max_kv
-                               : (int)std::min<int64_t>(max_kv, (int64_t)window + f.rows * c->heads / q_heads + 32);
-  const float there = B == 1 || seen < max_kv ? 1.f : 0.7f;
-  const float scale = c->head_dim == 64 ? 1.4f : c->head_dim == 256 ? 0.65f : 1.f;
-  if (many)
-    plan_parts(&f, units, seen, {1, there, 1024, 2048, 2.5f, 0.5f});
-  else
-    plan_parts(&f, units, seen, {f.nt == 1 && c->head_dim <= 128 ? 4 : 2, there, 335 * scale, 150 * scale, 2.4f * scale, 0.2f});
-  return f;
+  const int D = c->head_dim, group = q_heads / c->heads;
+  const int64_t rows = (int64_t)max_q * group;
+  auto plan = [&](int nt, int block_rows, AttentionPlan* f) {
+    f->nt = nt;
+    f->rows = block_rows;
+    f->row_blocks = (int)std::min<int64_t>((rows + block_rows - 1) / block_rows, INT32_MAX);
+    const int64_t units = (int64_t)f->row_blocks * c->heads * B;
+    // what a block of rows sees at most
+    const int seen = window == 0 ? max_kv
+                                 : (int)std::min<int64_t>(max_kv, (int64_t)window + block_rows / group + 32);
+    const bool ragged = B > 1 && seen == max_kv;
+    if (nt > 0) {
+      const float per = D == 64 ? 0.0072f : D == 128 ? 0.0125f : 0.0143f;
+      return plan_parts(f, units, seen, {nt == 1 && D <= 128 ? 4 : 2, ragged ? 0.75f : 1.f, per, 2.75f, 2.f, 0.037f, 0.126f}) + 1.f;
+    }
+    const bool two = D != 256 && rows > 128;  // tiles
+    const float per = D == 64 ? (two ? 0.0209f : 0.0114f) : D == 128 ? (two ? 0.0254f : 0.0144f) : 0.023f;
+    const float out = 1e-6f * (float)B * (float)rows * (float)c->heads * (float)D;  // written and read for each part
+    return plan_parts(f, units, seen, {1, ragged ? 0.6f : 1.f, per, 6.f, 5.3f, 1.87f * out, 0.66f});
+  };
+  const int nt = rows <= 8 || D == 256 ? 1 : 2;
+  AttentionPlan few, many;
+  const float few_time = plan(nt, 8 * nt, &few);
+  if (rows <= 16 || max_kv < 512 || (window != 0 && window < 512)) return few;
+  return plan(0, D == 256 ? 128 : 256, &many) < 0.85f * few_time ? many : few;
 }
 
 template <typename T, int D, int NT>
