@@ -389,7 +389,7 @@ __global__ void __launch_bounds__(kRowThreads) kv4_read_kernel(const ReadParams 
 // some 55 %, beside 90 % of the memory's rate in the steady state) -- a row over
 // 524288 positions takes 113 us (5.3 TB/s), 64 rows over up to 8192 each, ragged,
 // 84.7 us (3.9 TB/s); below that a CTA's start (page table, then codes, some 3
-// us) and the joining kernel: 131072 positions 37.7 us, 4001 positions 8.1 us.
+// us) and the joining kernel: 131072 positions 37.7 us, 4001 positions 7.9 us.
 // Four CTAs of four warps an SM hide one another's loads: the registers of a
 // thread (128) leave no more, and three stages of 32 positions a warp are what
 // shared memory has room for.
