@@ -1266,7 +1266,7 @@ float plan_parts(AttentionPlan* f, int64_t units, int max_kv, const PartsModel& 
     if (best == 0 || cost < best) {
       best = cost;
       f->splits = (int)parts;
-      f->chunk = (int)chunk;
+      f->chunk = (int)std::min(chunk, (uint32_t)kMostPositions);
     }
     more = parts > 1 && length * kPace[1] < best;  // longer ones cost more
   }
