@@ -473,10 +473,12 @@ __global__ void __launch_bounds__(ManyShape<D>::kThreads, 1) kv4_many_kernel(con
                                 __uint_as_float(s[k >> 5][(k & 31) + 1]));
       const float now = fmaxf(fmaxf(x4[0], x4[1]), fmaxf(x4[2], x4[3])) * fs;
       const bool moved = now > m + 8.f;  // the first finite maximum moves from -infinity
+      bool behind = j == 0;  // the last step's product has been waited for
       if (__any_sync(0xFFFFFFFFu, moved)) {
         const float f = moved ? ex2(m - now) : 1.f;
         if (j > 0) {
           if (!(ok = wait(o_done + 8u * t, j - 1))) break;
+          behind = true;
           umma_fence_after();
 #pragma unroll 1
           for (int c = 0; c < D; c += 32) {
@@ -521,14 +523,16 @@ __global__ void __launch_bounds__(ManyShape<D>::kThreads, 1) kv4_many_kernel(con
       l += sa + sb;
       tmem_wait_st();
       umma_fence_before();
+      // Each round of a barrier is waited for in turn, this one before the next can
+      // end: a wait by parity would take a round that was passed over for one to
+      // come.
+      if (!behind && !(ok = wait(o_done + 8u * t, j - 1))) break;
       __syncwarp();
       if (lane == 0) mbar_arrive_cta(p_full + 8u * (2 * t + (j & 1)));
     }
     for (; taken < steps; ++taken) give_turn();  // after a wait that ran out: the other tile's warp goes on
     if (steps > 0 && ok) {
-      // the last scores come behind the product of two steps before, and a wait by
-      // parity has to be for the next round but none: one round at a time
-      ok = (steps < 2 || wait(o_done + 8u * t, steps - 2)) && wait(o_done + 8u * t, steps - 1);
+      ok = wait(o_done + 8u * t, steps - 1);
       umma_fence_after();
       if (ok && lds_u32v(sbase + S::kOffOdd)) look_for_nan(steps - 1);
     }

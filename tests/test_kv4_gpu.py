@@ -701,3 +701,17 @@ def test_calls_wait_for_what_came_before(captured):
         torch.cuda.synchronize()
         assert torch.equal(got, want)
         assert torch.equal(out, last) and not torch.isnan(out).any()
+
+
+@pytest.mark.parametrize("B,n,L,H,heads,D", [(1, 1024, 2048, 16, 16, 64), (2, 300, 1500, 16, 4, 128),
+                                             (3, 64, 900, 16, 2, 64), (2, 70, 1200, 16, 4, 256)])
+def test_many_calls_in_a_row(B, n, L, H, heads, D):
+    """No wait of any call runs out, and every call gives the same bits."""
+    c = Case([L] * B, [n] * B, heads, D, 64)
+    q = _queries(c.T, H, D, F16)
+    ref, ref_lse = _run(c, q, 4000)
+    bad = torch.zeros((), dtype=torch.int64, device="cuda")
+    for _ in range(400):
+        out, lse = _run(c, q, 4000)
+        bad += (out != ref).sum() + (lse != ref_lse).sum()
+    assert int(bad) == 0 and api.device_error() == api.BCQ_OK
