@@ -1227,7 +1227,8 @@ void by_shape(int D, int T, const F& f) {
 }
 
 // How a call's rows and positions are shared out: the kernel (nt: row groups of
-// eight a CTA of the few-row kernel, 0 the many-row kernel), rows of a CTA,
+// eight a CTA of the few-row kernel; 0 the many-row kernel, -1 with K in two
+// parts), rows of a CTA,
 // and parts of the positions.
 struct AttentionPlan {
   int nt, rows, row_blocks, splits, chunk;
@@ -1278,9 +1279,10 @@ float plan_parts(AttentionPlan* f, int64_t units, int max_kv, const PartsModel& 
 // positions, 15.0 in two), four CTAs an SM (two where rows or values are many),
 // with exact products of queries and codes; the many-row kernel once for every
 // 256 (128 where D = 256), with keys rounded to fp16.  Over few positions those
-// roundings do not average out of lse (1e-5 of it below 500), and little is
-// saved: such calls stay with the first; so do those that the second is not
-// thought to save a seventh.
+// roundings do not average out of lse (1e-5 of it below 500 positions): there
+// keys go in two parts, which takes 1.3 times as long (2.1 where D = 256 leaves
+// room for one set of them).  Calls that the second kernel is not thought to save
+// a seventh stay with the first.
 //
 // The models' numbers are fitted to 68 calls of the first (1 to 256 sequences,
 // 300 to 262144 positions, heads of 64 to 256) and 60 of the second, each over 10
@@ -1306,15 +1308,17 @@ AttentionPlan plan_attention(const bcq_kv4* c, int q_heads, int B, int max_q, in
       return plan_parts(f, units, seen, {nt == 1 && D <= 128 ? 4 : 2, ragged ? 0.75f : 1.f, per, 2.75f, 2.f, 0.037f, 0.126f}) + 1.f;
     }
     const bool two = D != 256 && rows > 128;  // tiles
-    const float per = D == 64 ? (two ? 0.0209f : 0.0114f) : D == 128 ? (two ? 0.0254f : 0.0144f) : 0.023f;
+    const float per = (D == 64 ? (two ? 0.0209f : 0.0114f) : D == 128 ? (two ? 0.0254f : 0.0144f) : 0.023f) *
+                      (nt == 0 ? 1.f : D == 256 ? 2.1f : 1.3f);
     const float out = 1e-6f * (float)B * (float)rows * (float)c->heads * (float)D;  // written and read for each part
     return plan_parts(f, units, seen, {1, ragged ? 0.6f : 1.f, per, 6.f, 5.3f, 1.87f * out, 0.66f});
   };
   const int nt = rows <= 8 || D == 256 ? 1 : 2;
   AttentionPlan few, many;
   const float few_time = plan(nt, 8 * nt, &few);
-  if (rows <= 16 || max_kv < 512 || (window != 0 && window < 512)) return few;
-  return plan(0, D == 256 ? 128 : 256, &many) < 0.85f * few_time ? many : few;
+  if (rows <= 16) return few;
+  const bool short_sums = max_kv < 512 || (window != 0 && window < 512);
+  return plan(short_sums ? -1 : 0, D == 256 ? 128 : 256, &many) < 0.85f * few_time ? many : few;
 }
 
 template <typename T, int D, int NT>
@@ -1327,14 +1331,14 @@ cudaError_t launch_few_t(const AttentionParams& p, cudaStream_t st) {
   return launch_early(kv4_few_kernel<T, D, NT>, grid, kFewWarps * 32, smem, st, p);
 }
 
-template <typename T, int D>
+template <typename T, int D, bool EXACT>
 cudaError_t launch_many_t(const AttentionParams& p, cudaStream_t st) {
-  constexpr size_t smem = ManyShape<D>::kSmem;
+  using S = ManyShape<D, EXACT>;
   static std::atomic<uint64_t> done{0};
-  cudaError_t e = allow_smem(kv4_many_kernel<T, D>, smem, done);
+  cudaError_t e = allow_smem(kv4_many_kernel<T, D, EXACT>, S::kSmem, done);
   if (e != cudaSuccess) return e;
   const dim3 grid((unsigned)((int64_t)p.row_blocks * p.at.heads * p.at.B), (unsigned)p.splits);
-  return launch_early(kv4_many_kernel<T, D>, grid, ManyShape<D>::kThreads, smem, st, p);
+  return launch_early(kv4_many_kernel<T, D, EXACT>, grid, S::kThreads, S::kSmem, st, p);
 }
 
 template <typename T, int D>
@@ -1345,12 +1349,9 @@ cudaError_t launch_join_t(const AttentionParams& p, cudaStream_t st) {
 template <typename T, int D>
 cudaError_t launch_attention_t(const AttentionParams& p, int nt, cudaStream_t st) {
   cudaError_t e;
-  if constexpr (D == 256)
-    e = nt == 0 ? launch_many_t<T, D>(p, st) : launch_few_t<T, D, 1>(p, st);
-  else
-    e = nt == 0   ? launch_many_t<T, D>(p, st)
-        : nt == 1 ? launch_few_t<T, D, 1>(p, st)
-                  : launch_few_t<T, D, 2>(p, st);
+  if (nt <= 0) e = nt == 0 ? launch_many_t<T, D, false>(p, st) : launch_many_t<T, D, true>(p, st);
+  else if constexpr (D == 256) e = launch_few_t<T, D, 1>(p, st);
+  else e = nt == 1 ? launch_few_t<T, D, 1>(p, st) : launch_few_t<T, D, 2>(p, st);
   return e == cudaSuccess && p.splits > 1 ? launch_join_t<T, D>(p, st) : e;
 }
 

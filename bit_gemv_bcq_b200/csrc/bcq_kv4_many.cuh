@@ -7,7 +7,12 @@
 // (one where D = 256 leaves tensor memory for no more), and 64 positions a
 // step.  Four warps for K and four for V turn the codes into fp16 operands in
 // shared memory, once for both tiles: c from its bits (1024 + c or 1024 + 16 c, exactly), then a c +
-// z with one rounding to fp16 (half a step, 2^-11).  One warp issues the
+// z with one rounding to fp16 (half a step, 2^-11); over few positions, where
+// that does not average out of lse, K's in two parts (2^-22), which doubles the
+// products and their operands (8 x 400 positions, 256 rows: 23.0 us, 27.0 in the
+// few-row kernel; 29 x 203, 987 rows, heads of 256: 108 against 291; 7 x 688, 4095
+// rows, windows of 128: 62 against 157; where both could be, 112 against 143 us for
+// 4 x 1000 rows with windows of 1000).  One warp issues the
 // products; four warps a tile do its softmax, a thread a row.  S has two
 // buffers a tile, so that a step's scores are there when the softmax of the
 // one before ends (steps of 128 positions leave tensor memory for one: the
@@ -36,22 +41,25 @@
 namespace bcq {
 namespace {
 
-template <int D>
+// EXACT: K's operands in two fp16 parts, for calls over few positions.
+template <int D, bool EXACT>
 struct ManyShape {
   static constexpr int kTiles = D == 256 ? 1 : 2;
   static constexpr int kTokens = 64;                         // of a step
-  static constexpr int kBufs = D == 256 ? 2 : 3;             // of K's and V's operands, each
+  static constexpr int kKParts = EXACT ? 2 : 1;
+  static constexpr int kVBufs = D == 256 ? 2 : 3;            // of V's operands
+  static constexpr int kKBufs = EXACT && D == 256 ? 1 : kVBufs;  // of K's
   static constexpr int kBlocks = D / 64;                     // 128-byte column blocks of a vector
   static constexpr uint32_t kQBlock = 128 * 128;             // bytes of 64 columns of 128 rows
   static constexpr uint32_t kQTile = kBlocks * kQBlock;
   static constexpr uint32_t kKvBlock = kTokens * 128;
   static constexpr uint32_t kKvTile = kBlocks * kKvBlock;
   static constexpr uint32_t kOffK = kTiles * kQTile;
-  static constexpr uint32_t kOffV = kOffK + kBufs * kKvTile;
-  static constexpr uint32_t kOffBar = kOffV + kBufs * kKvTile;
+  static constexpr uint32_t kOffV = kOffK + kKBufs * kKParts * kKvTile;
+  static constexpr uint32_t kOffBar = kOffV + kVBufs * kKvTile;
   // a step's mask words: the positions without a page, and V's groups that are
   // no numbers.  A ring of eight: K's operands of step j + 8 come after the
-  // scores of step j + 8 - kBufs, and so after the softmax of step j + 3.
+  // scores of step j + 8 - kKBufs, and so after the softmax of step j + 3.
   static constexpr int kPieces = D / 32;                     // 16-byte pieces of a vector's codes
   static constexpr int kPasses = kTokens * kPieces / 128;    // pieces a thread and step
   static constexpr int kPerWarp = 32 / kPieces;              // positions a warp and pass
@@ -122,9 +130,36 @@ __device__ __forceinline__ uint4 word_values(uint32_t w, __half2 a, __half2 z) {
   return *reinterpret_cast<const uint4*>(v);
 }
 
-template <typename T, int D>
-__global__ void __launch_bounds__(ManyShape<D>::kThreads, 1) kv4_many_kernel(const AttentionParams p) {
-  using S = ManyShape<D>;
+// The same, a c + z in fp32, as two fp16 parts.
+__device__ __forceinline__ void word_parts(uint32_t w, float a, float z, uint4& first, uint4& second) {
+  const uint64_t a2 = pack_f32x2(a, a), z2 = pack_f32x2(z, z), no_magic = pack_f32x2(-8388608.f, -8388608.f),
+                 minus = pack_f32x2(-1.f, -1.f);
+  const uint32_t low = w & 0x0F0F0F0Fu, high = (w >> 4) & 0x0F0F0F0Fu;
+  auto two = [&](uint32_t x, uint32_t from, uint32_t& p, uint32_t& q) {  // bytes from and from + 2
+    const float c0 = __uint_as_float(prmt(x, 0x4B000000u, 0x7440u + from));  // 2^23 + c
+    const float c1 = __uint_as_float(prmt(x, 0x4B000000u, 0x7442u + from));
+    const uint64_t v = fma_f32x2(a2, add_f32x2(pack_f32x2(c0, c1), no_magic), z2);
+    float f0, f1;
+    unpack_f32x2(v, f0, f1);
+    p = pack_f16(f0, f1);
+    const float2 back = __half22float2(*reinterpret_cast<const __half2*>(&p));
+    unpack_f32x2(fma_f32x2(pack_f32x2(back.x, back.y), minus, v), f0, f1);
+    q = pack_f16(f0, f1);
+  };
+  two(low, 0, first.x, second.x);
+  two(high, 0, first.y, second.y);
+  two(low, 1, first.z, second.z);
+  two(high, 1, first.w, second.w);
+}
+
+__device__ __forceinline__ void sts_v4(uint32_t addr, const uint4& v) {
+  asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(addr), "r"(v.x), "r"(v.y), "r"(v.z), "r"(v.w)
+               : "memory");
+}
+
+template <typename T, int D, bool EXACT>
+__global__ void __launch_bounds__(ManyShape<D, EXACT>::kThreads, 1) kv4_many_kernel(const AttentionParams p) {
+  using S = ManyShape<D, EXACT>;
   constexpr int G = D / kKvGroup;
   extern __shared__ unsigned char smem_raw[];
   const uint32_t sbase = (smem_u32(smem_raw) + 1023u) & ~1023u;
@@ -158,7 +193,7 @@ __global__ void __launch_bounds__(ManyShape<D>::kThreads, 1) kv4_many_kernel(con
     if (lane == 0) {
       mbar_init(q_full, (uint32_t)(4 * tiles));
       mbar_init(drain, 1);
-      for (int i = 0; i < S::kBufs; ++i) {
+      for (int i = 0; i < 3; ++i) {
         mbar_init(k_full + 8 * i, 4);
         mbar_init(k_empty + 8 * i, 1);
         mbar_init(v_full + 8 * i, 4);
@@ -209,16 +244,18 @@ __global__ void __launch_bounds__(ManyShape<D>::kThreads, 1) kv4_many_kernel(con
       if (one) {
         for (int t = 0; t < tiles; ++t) {
 #pragma unroll
-          for (int i = 0; i < D / 16; ++i)
+          for (int i = 0; i < S::kKParts * D / 16; ++i) {
+            const int c = i % (D / 16), part = i / (D / 16);
             umma_f16_ss(tmem + (uint32_t)((2 * t + (j & 1)) * S::kTokens),
-                        qd + (uint32_t)((t * S::kQTile + (i >> 2) * S::kQBlock + (i & 3) * 32) >> 4),
-                        kd + (uint32_t)((ka.slot * S::kKvTile + (i >> 2) * S::kKvBlock + (i & 3) * 32) >> 4),
+                        qd + (uint32_t)((t * S::kQTile + (c >> 2) * S::kQBlock + (c & 3) * 32) >> 4),
+                        kd + (uint32_t)(((S::kKParts * ka.slot + part) * S::kKvTile + (c >> 2) * S::kKvBlock + (c & 3) * 32) >> 4),
                         kIdS, i != 0);
+          }
           umma_commit(s_full + 8u * (2 * t + (j & 1)));
         }
         umma_commit(k_empty + 8u * ka.slot);
       }
-      ka.step(S::kBufs);
+      ka.step(S::kKBufs);
     };
     if (steps > 0 && ok) scores(0);
     for (int j = 0; j < steps && ok; ++j) {
@@ -239,7 +276,7 @@ __global__ void __launch_bounds__(ManyShape<D>::kThreads, 1) kv4_many_kernel(con
         }
       }
       if (ok && one) umma_commit(v_empty + 8u * va.slot);
-      va.step(S::kBufs);
+      va.step(S::kVBufs);
     }
     if (!ok) {
       give_up();
@@ -316,15 +353,26 @@ __global__ void __launch_bounds__(ManyShape<D>::kThreads, 1) kv4_many_kernel(con
         if (is_v && odd) az = 0;
         const uint4 c = x[i].codes;
         const __half2 f = *reinterpret_cast<const __half2*>(&az);
+        const uint32_t row = tile + (uint32_t)(i * 4 * S::kPerWarp * 128);
+        if (EXACT && !is_v) {
+          const float2 az32 = __half22float2(f);
+          const uint32_t words[4] = {c.x, c.y, c.z, c.w};
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            uint4 first, second;
+            word_parts(words[e], az32.x, az32.y, first, second);
+            if (odd) second = make_uint4(0, 0, 0, 0);
+            sts_v4(row + to[e], first);
+            sts_v4(row + S::kKvTile + to[e], second);
+          }
+          continue;
+        }
         const __half2 a = __low2half2(f), z = __high2half2(f);
         const uint4 v[4] = {word_values(c.x, a, z), word_values(c.y, a, z), word_values(c.z, a, z),
                             word_values(c.w, a, z)};
 #pragma unroll
         for (int e = 0; e < 4; ++e)
-          asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(
-                           tile + to[e] + (uint32_t)(i * 4 * S::kPerWarp * 128)),
-                       "r"(v[e].x), "r"(v[e].y), "r"(v[e].z), "r"(v[e].w)
-                       : "memory");
+          sts_v4(row + to[e], v[e]);
       }
       fence_proxy_async_smem();
     };
@@ -335,10 +383,10 @@ __global__ void __launch_bounds__(ManyShape<D>::kThreads, 1) kv4_many_kernel(con
     auto one_step = [&](int j, Piece (&now)[S::kPasses], Piece (&next)[S::kPasses]) {
       load(next, j + 1);
       if (at.round > 0 && !(ok = wait(empty + 8u * at.slot, at.round - 1))) return;
-      store(tiles_at + (uint32_t)at.slot * S::kKvTile, mask + (j & 7) * S::kWords, now);
+      store(tiles_at + (uint32_t)at.slot * (is_v ? 1 : S::kKParts) * S::kKvTile, mask + (j & 7) * S::kWords, now);
       __syncwarp();
       if (lane == 0) mbar_arrive_cta(full + 8u * at.slot);
-      at.step(S::kBufs);
+      at.step(is_v ? S::kVBufs : S::kKBufs);
     };
     load(x[0], 0);
     for (int j = 0; j < steps && ok; j += 2) {
