@@ -715,3 +715,59 @@ def test_many_calls_in_a_row(B, n, L, H, heads, D):
         out, lse = _run(c, q, 4000)
         bad += (out != ref).sum() + (lse != ref_lse).sum()
     assert int(bad) == 0 and api.device_error() == api.BCQ_OK
+
+
+@pytest.fixture(params=[(511, 0), (4000, 0)], ids=["short", "long"])
+def as_if_large(request, monkeypatch):
+    """Every call as if it might have thousands of rows: the kernel of many rows, with keys in two parts and in one."""
+    run, attention = _run, api.kv4_attention
+    args = dict(max_q=5000, max_kv=request.param[0])
+    monkeypatch.setitem(globals(), "_run", lambda c, q, hint=None, **kw: run(c, q, **{**kw, **args}))
+    monkeypatch.setattr(api, "kv4_attention", lambda *a, **kw: attention(*a, **{**kw, **args}))
+
+
+@pytest.mark.parametrize("causal,window", [(True, 0), (True, 1), (True, 64), (True, 600), (False, 0), (False, 9)])
+@pytest.mark.parametrize("lens,new", [([33, 100], [1, 1]), ([200], [140]), ([700, 90, 0], [150, 90, 3])])
+@pytest.mark.parametrize("D,H", [(64, 6), (128, 8), (256, 8)])
+def test_large_masks(as_if_large, lens, new, causal, window, D, H):
+    c = Case(lens, new, 2, D, 16, seed=window)
+    q = _queries(c.T, H, D, BF16 if window == 64 else F16, seed=2)
+    out, lse = _run(c, q, causal=causal, window=window)
+    _check_attention(c, q, out, lse, causal=causal, window=window)
+
+
+@pytest.mark.parametrize("lens,new,H,heads,D,page_size", [
+    ([5], [5], 2, 1, 64, 16), ([1], [1], 1, 1, 128, 16), ([300], [150], 12, 3, 128, 48), ([520], [400], 7, 1, 256, 48),
+    ([129, 5], [129, 5], 32, 2, 128, 16), ([70, 0, 71], [5, 0, 70], 6, 1, 256, 64), ([256], [256], 2, 2, 128, 128)])
+def test_large_rows(as_if_large, lens, new, H, heads, D, page_size):
+    test_several_rows(lens, new, H, heads, D, page_size, F16, None)
+
+
+@pytest.mark.parametrize("new", [1, 6, 140])
+@pytest.mark.parametrize("D", [64, 128, 256])
+def test_large_nan(as_if_large, new, D):
+    test_nan_stays_where_it_belongs(new, D, None)
+
+
+@pytest.mark.parametrize("D", [64, 128, 256])
+def test_large_strides_scales_and_missing_pages(as_if_large, D):
+    test_strided_queries_and_outputs(200, None)
+    test_rows_that_see_nothing(0, 300, 2, None)
+    for scale in (0.0, -0.3, 4.0):
+        test_scales_of_the_scores(scale, 160, None)
+    for dtype, mag in ((F16, 1e-4), (F16, 3e4), (BF16, 1e-12), (BF16, 1e30)):
+        test_queries_of_any_magnitude(dtype, mag, 150, None)
+    test_a_missing_page_under_many_rows(D)
+
+
+@pytest.mark.parametrize("B,n,L,H,heads,D", [(8, 100, 400, 16, 4, 64), (4, 150, 300, 16, 4, 128), (4, 100, 400, 8, 2, 256)])
+def test_many_short_calls_in_a_row(B, n, L, H, heads, D):
+    c = Case([L] * B, [n] * B, heads, D, 64)
+    q = _queries(c.T, H, D, F16)
+    kw = dict(max_q=5000)
+    ref, ref_lse = _run(c, q, 500, **kw)
+    bad = torch.zeros((), dtype=torch.int64, device="cuda")
+    for _ in range(400):
+        out, lse = _run(c, q, 500, **kw)
+        bad += (out != ref).sum() + (lse != ref_lse).sum()
+    assert int(bad) == 0 and api.device_error() == api.BCQ_OK
