@@ -102,7 +102,7 @@ __device__ __forceinline__ int64_t vector_at(const Places& p, int b, int j, int 
 
 constexpr int kRowThreads = 256;
 
-// Where kRows rows from t0 on go, found by the whole block: place[i] = index of
+// Where `rows` <= kRows rows from t0 on go, found by the whole block: place[i] = index of
 // the vector of head 0 (the other heads' lie page_size apart), -1 for a
 // position that the cache does not have, -2 for a row of no sequence.  Two
 // loads one after the other: the sequences' first rows and lengths (up to 256
@@ -114,11 +114,11 @@ struct RowPlaces {
   int cu[kRowThreads + 1], len[kRowThreads];
 };
 template <int kRows>
-__device__ __forceinline__ void locate_rows(const Places& p, int t0, int T, RowPlaces<kRows>& s) {
+__device__ __forceinline__ void locate_rows(const Places& p, int t0, int T, int rows, RowPlaces<kRows>& s) {
   const int tid = threadIdx.x;
   const bool kept = p.B <= kRowThreads;
   if (p.cu) {
-    if (tid < kRows) s.count[tid] = 0;
+    if (tid < rows) s.count[tid] = 0;
     if (kept) {
       if (tid == 0) s.cu[0] = p.cu[0];
       if (tid < p.B) s.len[tid] = p.kv_len[tid];
@@ -128,15 +128,15 @@ __device__ __forceinline__ void locate_rows(const Places& p, int t0, int T, RowP
     for (int b0 = 1; b0 <= p.B; b0 += kRowThreads) {
       const int end = b0 + tid <= p.B ? p.cu[b0 + tid] : INT32_MAX;
       if (kept && b0 + tid <= p.B) s.cu[b0 + tid] = end;
-#pragma unroll
-      for (int i = 0; i < kRows; ++i) {
+#pragma unroll 4
+      for (int i = 0; i < rows; ++i) {
         const int n = __popc(__ballot_sync(0xFFFFFFFFu, end <= t0 + i));
         if ((tid & 31) == 0 && n) atomicAdd(&s.count[i], n);
       }
     }
     __syncthreads();
   }
-  if (tid < kRows) {
+  if (tid < rows) {
     const int t = t0 + tid;
     int64_t at = -2;
     const int b = p.cu ? s.count[tid] : t;
@@ -158,6 +158,15 @@ __device__ __forceinline__ void locate_rows(const Places& p, int t0, int T, RowP
     s.place[tid] = at;
   }
   __syncthreads();
+}
+
+// Where a row has few words (few heads, small ones) a block's threads are shared
+// out among `sets` of kRows rows each: as many as fit, a power of two.
+constexpr int kMostSets = 16;  // a row has 16 words at least
+__device__ __host__ __forceinline__ int row_sets(int items) {
+  int sets = 1;
+  while (2 * sets * items <= kRowThreads) sets *= 2;
+  return sets;
 }
 
 struct AppendParams {
@@ -195,14 +204,16 @@ struct Pair16<__nv_bfloat16> {
 // Bound by its instructions, some 200 for 256 values: 8 x 1024 rows of 8 heads
 // of 128 take 15.1 us (43 MB, 2.8 TB/s), 64 rows 3.0 us (launch, and four loads
 // one after the other).
-template <typename T, int D, int kRows>
+template <typename T, int D, int kRows, bool SHARED>
 __global__ void __launch_bounds__(kRowThreads, 4) kv4_append_kernel(const AppendParams p) {
   using V = typename Pair16<T>::V;
   constexpr int G = D / kKvGroup, kWords = D / 8;
   constexpr float kMagic = 12582912.f;  // 1.5 * 2^23: adding it rounds to an integer, halves to even
-  __shared__ RowPlaces<kRows> places;
-  const int t0 = (int)blockIdx.x * kRows, heads = p.at.heads;
-  const int items = 2 * heads * kWords, lane = threadIdx.x & 31;
+  __shared__ RowPlaces<SHARED ? kRows * kMostSets : kRows> places;
+  const int heads = p.at.heads, items = 2 * heads * kWords;
+  const int sets = SHARED ? row_sets(items) : 1, threads = kRowThreads / sets;  // of a set
+  const int set = SHARED ? (int)threadIdx.x / threads : 0, first = (int)threadIdx.x - set * threads;
+  const int b0 = (int)blockIdx.x * kRows * sets, t0 = b0 + set * kRows;
   uint4 raw[kRows];
   auto fetch = [&](int i) {
     const int kv = i >= heads * kWords, in = kv ? i - heads * kWords : i;
@@ -217,19 +228,20 @@ __global__ void __launch_bounds__(kRowThreads, 4) kv4_append_kernel(const Append
   };
   grid_dependency_wait();
   launch_dependents();
-  fetch(threadIdx.x);
-  locate_rows<kRows>(p.at, t0, p.T, places);
-  for (int i = threadIdx.x; i - lane < items; i += kRowThreads) {  // whole warps
+  fetch(first);
+  locate_rows(p.at, b0, p.T, kRows * sets, places);
+  const int lane = threadIdx.x & 31;
+  for (int i = first; SHARED ? i == first : i - lane < items; i += threads) {  // whole warps
     const int kv = i >= heads * kWords, in = kv ? i - heads * kWords : i;
     const int h = in / kWords, word = in % kWords;
-    if (i >= kRowThreads) fetch(i);
+    if (i != first) fetch(i);
     uint8_t* const code = (kv ? p.code[1] : p.code[0]) + word * 4;
     __half2* const param = (kv ? p.param[1] : p.param[0]) + word / 8;
     const int64_t to_head = (int64_t)h * p.at.page_size;
 #pragma unroll
     for (int j = 0; j < kRows; ++j) {
-      const int64_t place = places.place[j];
-      if (place < 0) continue;  // for all of the block
+      const int64_t place = places.place[set * kRows + j];
+      if (!SHARED && place < 0) continue;  // for all of the block
       const uint32_t w[4] = {raw[j].x, raw[j].y, raw[j].z, raw[j].w};
       const V* v2 = reinterpret_cast<const V*>(w);
       const V lo2 = __hmin2_nan(__hmin2_nan(v2[0], v2[1]), __hmin2_nan(v2[2], v2[3]));
@@ -279,7 +291,7 @@ __global__ void __launch_bounds__(kRowThreads, 4) kv4_append_kernel(const Append
         const float hi16 = fmaf(c[7], 4096.f, fmaf(c[6], 256.f, fmaf(c[5], 16.f, c[4])));
         codes = prmt(__float_as_uint(lo16 + 8388608.f), __float_as_uint(hi16 + 8388608.f), 0x5410);
       }
-      if (i >= items) continue;
+      if (i >= items || place < 0) continue;
       const int64_t vec = place + to_head;
       *reinterpret_cast<uint32_t*>(code + vec * (D / 2)) = codes;
       if (word % 8 == 0) {
@@ -302,16 +314,19 @@ struct ReadParams {
 // four rows' loads in flight together.  Bound by memory from some thousand rows
 // on: 8 x 1024 rows of 8 heads of 128 as fp16 8.2 us (43 MB, 5.2 TB/s), 64 rows
 // 2.7 us.
-template <typename TO, int D, int kRows>
+template <typename TO, int D, int kRows, bool SHARED>
 __global__ void __launch_bounds__(kRowThreads) kv4_read_kernel(const ReadParams p) {
   constexpr int G = D / kKvGroup, kWords = D / 8;
-  __shared__ RowPlaces<kRows> places;
-  const int64_t* place = places.place;
-  const int t0 = (int)blockIdx.x * kRows, heads = p.at.heads;
+  __shared__ RowPlaces<SHARED ? kRows * kMostSets : kRows> places;
+  const int heads = p.at.heads, items = 2 * heads * kWords;
+  const int sets = SHARED ? row_sets(items) : 1, threads = kRowThreads / sets;  // of a set
+  const int set = SHARED ? (int)threadIdx.x / threads : 0, first = (int)threadIdx.x - set * threads;
+  const int b0 = (int)blockIdx.x * kRows * sets, t0 = b0 + set * kRows;
+  const int64_t* place = places.place + set * kRows;
   grid_dependency_wait();
   launch_dependents();
-  locate_rows<kRows>(p.at, t0, p.T, places);
-  for (int i = threadIdx.x; i < 2 * heads * kWords; i += kRowThreads) {
+  locate_rows(p.at, b0, p.T, kRows * sets, places);
+  for (int i = first; i < items; i += threads) {
     const int kv = i >= heads * kWords;
     const int in = kv ? i - heads * kWords : i;
     const int h = in / kWords, word = in % kWords;
@@ -1215,11 +1230,17 @@ Places places_of(const bcq_kv4* c, const int32_t* table, int table_width, const 
 // together.  In and out of a cache of 8 heads of 128 (us, one | four rows a
 // block): 64 rows 2.8 + 2.4 | 3.9 + 2.6, 512 rows 3.6 + 3.0 | 4.1 + 2.7, 1024
 // rows 5.5 + 3.7 | 4.6 + 3.0, 8192 rows 30.2 + 17.7 | 17.5 + 10.0.
+// From 4096 rows on, several side by side in a block where one has no more than
+// half as many words as the block has threads (in + out, us, four rows | sets of
+// four: 2 heads of 64, 16384 rows 20.0 + 8.7 | 8.1 + 7.0, 4 heads of 128, 8192 rows
+// 13.2 + 6.7 | 10.6 + 7.3, a head of 128, 2048 rows 4.3 + 2.7 | 5.5 + 4.3).
 template <typename F>
-void by_shape(int D, int T, const F& f) {
+void by_shape(int D, int heads, int T, const F& f) {
+  const int sets = row_sets(2 * heads * (D / 8));
   auto rows = [&](auto d) {
-    if (T < 768) f(d, std::integral_constant<int, 1>());
-    else f(d, std::integral_constant<int, 4>());
+    if (T < 768) f(d, std::integral_constant<int, 1>(), std::false_type(), T);
+    else if (sets == 1 || T < 4096) f(d, std::integral_constant<int, 4>(), std::false_type(), (T + 3) / 4);
+    else f(d, std::integral_constant<int, 4>(), std::true_type(), (T + 4 * sets - 1) / (4 * sets));
   };
   if (D == 64) rows(std::integral_constant<int, 64>());
   else if (D == 128) rows(std::integral_constant<int, 128>());
@@ -1396,11 +1417,12 @@ bcq_status bcq_kv4_append(const bcq_kv4* cache, const void* k, int64_t ld_k, int
                           T};
   cudaStream_t st = (cudaStream_t)stream;
   cudaError_t e = cudaSuccess;
-  by_shape(cache->head_dim, T, [&](auto d, auto rows) {
+  by_shape(cache->head_dim, cache->heads, T, [&](auto d, auto rows, auto shared, int count) {
     constexpr int D = decltype(d)::value, kRows = decltype(rows)::value;
-    const unsigned blocks = (unsigned)((T + kRows - 1) / kRows);
-    if (dtype == BCQ_F16) e = launch_early(kv4_append_kernel<__half, D, kRows>, blocks, kRowThreads, 0, st, p);
-    else e = launch_early(kv4_append_kernel<__nv_bfloat16, D, kRows>, blocks, kRowThreads, 0, st, p);
+    constexpr bool kShared = decltype(shared)::value;
+    const unsigned blocks = (unsigned)count;
+    if (dtype == BCQ_F16) e = launch_early(kv4_append_kernel<__half, D, kRows, kShared>, blocks, kRowThreads, 0, st, p);
+    else e = launch_early(kv4_append_kernel<__nv_bfloat16, D, kRows, kShared>, blocks, kRowThreads, 0, st, p);
   });
   return e == cudaSuccess ? BCQ_OK : BCQ_ERR_CUDA;
 }
@@ -1421,12 +1443,13 @@ bcq_status bcq_kv4_read(const bcq_kv4* cache, void* k, void* v, int dtype, int T
                         T};
   cudaStream_t st = (cudaStream_t)stream;
   cudaError_t e = cudaSuccess;
-  by_shape(cache->head_dim, T, [&](auto d, auto rows) {
+  by_shape(cache->head_dim, cache->heads, T, [&](auto d, auto rows, auto shared, int count) {
     constexpr int D = decltype(d)::value, kRows = decltype(rows)::value;
-    const unsigned blocks = (unsigned)((T + kRows - 1) / kRows);
-    if (dtype == BCQ_F16) e = launch_early(kv4_read_kernel<__half, D, kRows>, blocks, kRowThreads, 0, st, p);
-    else if (dtype == BCQ_BF16) e = launch_early(kv4_read_kernel<__nv_bfloat16, D, kRows>, blocks, kRowThreads, 0, st, p);
-    else e = launch_early(kv4_read_kernel<float, D, kRows>, blocks, kRowThreads, 0, st, p);
+    constexpr bool kShared = decltype(shared)::value;
+    const unsigned blocks = (unsigned)count;
+    if (dtype == BCQ_F16) e = launch_early(kv4_read_kernel<__half, D, kRows, kShared>, blocks, kRowThreads, 0, st, p);
+    else if (dtype == BCQ_BF16) e = launch_early(kv4_read_kernel<__nv_bfloat16, D, kRows, kShared>, blocks, kRowThreads, 0, st, p);
+    else e = launch_early(kv4_read_kernel<float, D, kRows, kShared>, blocks, kRowThreads, 0, st, p);
   });
   return e == cudaSuccess ? BCQ_OK : BCQ_ERR_CUDA;
 }

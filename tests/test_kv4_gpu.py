@@ -170,6 +170,41 @@ def test_append_writes_the_oracles_codes_and_nothing_else(lens, new, heads, D, p
     _check_cache(c, _expect_append(c, k, v))
 
 
+@pytest.mark.parametrize("heads,D", [(1, 64), (1, 128), (1, 256), (2, 64), (3, 64), (5, 64), (2, 128), (3, 128), (7, 64),
+                                     (8, 64)])
+def test_many_rows_of_few_heads_in_and_out(heads, D):
+    """Rows that share a block, some of them of no sequence, and a page that is missing."""
+    lens, new = [2500, 0, 70, 1900], [2300, 0, 70, 1833]
+    c, k, v = _append_case(lens, new, heads, D, 48, F16)
+    T = c.T
+    pad = lambda x: torch.cat([x[:5] * float("nan"), x, x[:9] * float("nan")])   # noqa: E731
+    cu = c.t_cu + 5
+    api.kv4_append(c.cache, pad(k), pad(v), c.t_table, c.t_len, cu)
+    d, _, _ = _append_case(lens, new, heads, D, 48, F16)
+    for b in range(4):                                        # the same, a few rows a call
+        for i in range(0, new[b], 350):
+            r = slice(int(c.cu[b]) + i, int(c.cu[b]) + min(i + 350, new[b]))
+            n = r.stop - r.start
+            api.kv4_append(d.cache, k[r], v[r], d.t_table[b:b + 1], _i32([lens[b] - new[b] + i + n]), _i32([0, n]))
+    for n in ("k", "k_param", "v", "v_param"):
+        assert torch.equal(getattr(c.cache, n).view(torch.uint8), getattr(d.cache, n).view(torch.uint8)), n
+    for dtype in (F16, F32):
+        rk, rv = (torch.full((T + 14, heads, D), 7.0, dtype=dtype, device="cuda") for _ in range(2))
+        api.kv4_read(c.cache, c.t_table, c.t_len, cu, dtype=dtype, k=rk, v=rv)
+        assert (rk[:5] == 7).all() and (rk[T + 5:] == 7).all() and (rv[T + 5:] == 7).all()
+        sk, sv = api.kv4_read(d.cache, d.t_table[3:], d.t_len[3:], _i32([0, 333]), tokens=333, dtype=dtype)
+        assert torch.equal(rk[T + 5 - 333:T + 5], sk) and torch.equal(rv[T + 5 - 333:T + 5], sv)
+    t = c.t_table.clone()
+    t[0, 10] = -1                                             # positions 480..527: rows 280..327 of the first
+    before = c.cache.k.clone()
+    api.kv4_append(c.cache, pad(k), pad(v), t, c.t_len, cu)
+    assert api.device_error() == api.BCQ_ERR_PAGE and torch.equal(before, c.cache.k)
+    gk, _ = api.kv4_read(c.cache, t, c.t_len, cu, tokens=T + 14)
+    assert api.device_error() == api.BCQ_ERR_PAGE
+    ok, _ = api.kv4_read(c.cache, c.t_table, c.t_len, cu, tokens=T + 14)
+    assert (gk[285:333] == 0).all() and torch.equal(gk[5:285], ok[5:285]) and torch.equal(gk[333:T + 5], ok[333:T + 5])
+
+
 @pytest.mark.parametrize("dtype", [F16, BF16])
 def test_append_one_row_each_without_cu(dtype):
     lens = [3, 17, 64, 1]
