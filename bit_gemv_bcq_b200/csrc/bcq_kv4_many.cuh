@@ -59,7 +59,9 @@ struct ManyShape {
   static constexpr uint32_t kOffBar = kOffV + kVBufs * kKvTile;
   // a step's mask words: the positions without a page, and V's groups that are
   // no numbers.  A ring of eight: K's operands of step j + 8 come after the
-  // scores of step j + 8 - kKBufs, and so after the softmax of step j + 3.
+  // scores of step j + 8 - kKBufs, and so after the softmax of step j + 3 (V's
+  // after the product of step j + 8 - kVBufs); step j's words are read for the
+  // last time as step j + 1 ends.
   static constexpr int kPieces = D / 32;                     // 16-byte pieces of a vector's codes
   static constexpr int kPasses = kTokens * kPieces / 128;    // pieces a thread and step
   static constexpr int kPerWarp = 32 / kPieces;              // positions a warp and pass
@@ -465,7 +467,9 @@ __global__ void __launch_bounds__(ManyShape<D, EXACT>::kThreads, 1) kv4_many_ker
       return (word[at] >> (q * S::kPerWarp + token % S::kPerWarp)) & 1u;
     };
     // Once something is odd (the words are rarely looked at): V's groups of step
-    // j, after its product.
+    // j.  Its flag and its words are there once its product is (the scores of
+    // step j + 1 say nothing of them: they are issued before V of step j is
+    // waited for), so this stands behind o_done's round j and reads the flag anew.
     auto look_for_nan = [&](int j) {
       const uint32_t* word = masks + (8 + (j & 7)) * S::kWords;
       const uint32_t* gone = masks + (j & 7) * S::kWords;
@@ -504,7 +508,6 @@ __global__ void __launch_bounds__(ManyShape<D, EXACT>::kThreads, 1) kv4_many_ker
       tmem_ld32(ts + 32, s[1]);
       tmem_wait_ld();
       const bool holes = __any_sync(0xFFFFFFFFu, odd != 0);
-      if (holes && j > 0) look_for_nan(j - 1);
       const int j0 = begin + j * S::kTokens;
       const uint32_t* gone = masks + (j & 7) * S::kWords;
       if (holes || j0 < lo_all || j0 + S::kTokens > hi_all) {
@@ -577,6 +580,7 @@ __global__ void __launch_bounds__(ManyShape<D, EXACT>::kThreads, 1) kv4_many_ker
       if (!behind && !(ok = wait(o_done + 8u * t, j - 1))) break;
       __syncwarp();
       if (lane == 0) mbar_arrive_cta(p_full + 8u * (2 * t + (j & 1)));
+      if (j > 0 && __any_sync(0xFFFFFFFFu, lds_u32v(sbase + S::kOffOdd) != 0)) look_for_nan(j - 1);
     }
     for (; taken < steps; ++taken) give_turn();  // after a wait that ran out: the other tile's warp goes on
     if (steps > 0 && ok) {

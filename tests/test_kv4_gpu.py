@@ -806,3 +806,40 @@ def test_many_short_calls_in_a_row(B, n, L, H, heads, D):
         out, lse = _run(c, q, 500, **kw)
         bad += (out != ref).sum() + (lse != ref_lse).sum()
     assert int(bad) == 0 and api.device_error() == api.BCQ_OK
+
+
+@pytest.mark.parametrize("B,n,L,H,heads,D", [(40, 64, 700, 16, 4, 128), (60, 40, 600, 12, 2, 64), (50, 32, 500, 8, 2, 256)])
+@pytest.mark.parametrize("hint", [500, 4000])
+def test_nan_values_in_every_step_of_a_full_grid(B, n, L, H, heads, D, hint):
+    """V's groups that are no numbers reach the rows that see them and no others, however late V's codes
+    come: a few at every 64 positions, more blocks of rows than SMs, the cache flushed from L2."""
+    c = Case([L] * B, [n] * B, heads, D, 16, seed=D)
+    rng = np.random.default_rng(D)
+    G = D // 64
+    param = c.arrays["v_param"].copy()
+    odd = np.zeros((B, L, heads, G), dtype=bool)
+    for b in range(B):
+        for j0 in range(0, L, 64):
+            for _ in range(2):
+                j, h, g = rng.integers(j0, min(j0 + 64, L)), rng.integers(heads), rng.integers(G)
+                if rng.integers(4):              # most of them where only some rows see them
+                    j = max(j, L - n + rng.integers(n))
+                odd[b, j, h, g] = True
+                param[c.table[b, j // 16], h, j % 16, g, rng.integers(2)] = np.nan
+    first = np.where(odd.any(1), odd.argmax(1), L)                            # [B][heads][G]
+    pos = np.arange(L - n, L)
+    want = pos[None, :, None, None] >= first[:, None]                          # [B][n][heads][G]
+    want = np.repeat(np.repeat(want, H // heads, 2).reshape(B * n, H, G), 64, 2)
+    assert want.any() and not want.all()
+    want = torch.from_numpy(want).cuda()
+    q = _queries(c.T, H, D, F16)
+    kw = dict(max_q=5000)                                                       # the kernel of many rows
+    clean, clean_lse = _run(c, q, hint, **kw)
+    c.cache.v_param.copy_(torch.from_numpy(param))
+    flush = torch.empty(256 << 20, dtype=torch.uint8, device="cuda")
+    wrong = torch.zeros((), dtype=torch.int64, device="cuda")
+    for i in range(60):
+        flush.fill_(i)
+        out, lse = _run(c, q, hint, **kw)
+        wrong += (torch.isnan(out) != want).sum() + (out != clean)[~want].sum() + (lse != clean_lse).sum()
+    assert int(wrong) == 0 and api.device_error() == api.BCQ_OK
