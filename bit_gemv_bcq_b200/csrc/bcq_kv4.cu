@@ -386,10 +386,17 @@ __global__ void __launch_bounds__(kRowThreads) kv4_read_kernel(const ReadParams 
 // word of codes fills the four registers) and 8 rows as the second, so 8 rows
 // of a key/value head (the query heads that share it, times the rows of the
 // call) fill an instruction.  Queries are scaled by a power of two to the top
-// of fp16's range.  p and p a are rounded to fp16 (half a step, 2^-11, each);
-// the maximum in use follows a row's own only when that has risen by more than
-// 2^4, and p is held times 1/2, so that p <= 8 and the largest a (8000) does
-// not overflow.  Scores, sums and outputs are fp32.
+// of fp16's range.  p and p a are rounded to fp16 (half a step, 2^-11, each).
+// So that neither falls among fp16's subnormals, whose step does not shrink with
+// them: the maximum in use follows a row's own only when that has risen by more
+// than 2^4, and p is held times 2^9, so it is at most 2^13 and keeps its 11 bits
+// down to 2^-23 of the row's largest; and a is taken times a power of two that a
+// warp has for each group, which brings the largest a among its positions so far
+// to 1/2 .. 2 (p a' is below 2^15 then, and keeps its bits where a is not below
+// 2^-13 of that largest; further down it is off by 2^-24 of the largest at most).
+// The power follows a larger a as the maximum in use follows a score, with one
+// look a stage, and is taken out of the sums at the end.  Scores, sums and outputs
+// are fp32.
 //
 // A scale or offset of V that is no number must not reach rows that do not see
 // its position (0 * NaN): where some row does not see all positions such
@@ -434,7 +441,8 @@ struct Span {
   int first_row, rows;   // of the sequence in the call
   int len;               // tokens in the cache, within the table
   int pos0;              // position of the sequence's first row
-  int begin, end;        // positions seen by some row of the block
+  int seen, end;         // positions seen by some row of the block
+  int begin;             // seen, down to a multiple of 32
   int chunk, parts;      // positions a part, parts
 };
 
@@ -449,7 +457,8 @@ __device__ __forceinline__ Span span_of(const AttentionParams& p, int b, int blo
   const int i0 = p.group.quotient(block * p.rows);                          // first and last row
   const int i1 = min(s.rows - 1, p.group.quotient((block + 1) * p.rows - 1));  // (of the sequence)
   s.end = p.causal ? min(s.len, s.pos0 + i1 + 1) : s.len;
-  s.begin = p.window > 0 ? max(0, s.pos0 + i0 - p.window + 1) & ~31 : 0;
+  s.seen = p.window > 0 ? max(0, s.pos0 + i0 - p.window + 1) : 0;
+  s.begin = s.seen & ~31;
   const int n = s.end - s.begin;
   if (i0 >= s.rows || n <= 0) {
     s.parts = i0 < s.rows ? 1 : 0;  // rows that see nothing are still written
@@ -562,9 +571,10 @@ __device__ __forceinline__ float score_factor(float scale, int n) {
 constexpr int kFewWarps = 4;    // of a CTA
 constexpr int kFewStages = 3;   // of a warp's ring
 constexpr int kFewTokens = 32;  // of a stage
-constexpr float kWeightBits = -1.f;   // p is held times 2^-1
-constexpr float kWeightScale = 0.5f;
+constexpr float kWeightBits = 9.f;    // p is held times 2^9
+constexpr float kWeightScale = 512.f;
 constexpr float kLazyBits = 4.f;      // how far a row's maximum may rise over the one in use
+constexpr uint32_t kFirstPower = 30u << 10;  // 2^15, of V's scales, by the bits of an fp16
 
 template <int D>
 struct FewShape {
@@ -783,6 +793,10 @@ __global__ void __launch_bounds__(kFewWarps * 32, NT == 1 && D <= 128 ? 4 : 2) k
 
   // nb: what is added to a score for p's exponent, kWeightBits - m
   float o[NT][G][4][4] = {}, zo[NT][4] = {}, m[NT][2], nb[NT][2] = {}, l[NT][2] = {};
+  uint32_t power[G];  // what V's scales are taken times, by an fp16's bits: (s + 15) 2^10 is 2^s
+#pragma unroll
+  for (int g = 0; g < G; ++g) power[g] = kFirstPower;
+  const uint32_t own_at = 2 * S::kCodes + S::kParam + (uint32_t)((lane >> 4) * S::kHalf + (lane & 15) * G * 4);
   uint32_t poison = 0;  // bit (nt * 2 + e) * G + g: that row's group is NaN
 #pragma unroll
   for (int nt = 0; nt < NT; ++nt) m[nt][0] = m[nt][1] = -INFINITY;
@@ -790,6 +804,8 @@ __global__ void __launch_bounds__(kFewWarps * 32, NT == 1 && D <= 128 ? 4 : 2) k
   // One stage: 32 positions from j0.  WHOLE: every row sees all of them.
   auto stage = [&](auto whole_type, uint32_t at0, int j0, uint32_t gone) {
     constexpr bool WHOLE = decltype(whole_type)::value;
+    uint32_t own_a[G];  // V's scales of one position a lane
+    lds_words<G>(at0 + own_at, own_a);
     // scores u[..]: positions r and r + 8 of each half, rows 2c and 2c + 1
     float u[2][NT][4];
 #pragma unroll
@@ -861,6 +877,17 @@ __global__ void __launch_bounds__(kFewWarps * 32, NT == 1 && D <= 128 ? 4 : 2) k
           }
     }
 
+    // the powers in use for V's scales
+    const bool own_seen = WHOLE || (j0 + lane >= sp.seen && j0 + lane < end && !((gone >> (lane >> 4)) & 1u));
+    uint32_t most = 0;
+#pragma unroll
+    for (int g = 0; g < G; ++g) {
+      own_a[g] &= 0x7FFFu;
+      if (!own_seen || own_a[g] >= 0x7C00u) own_a[g] = 0;
+      most = max(most, own_a[g] + power[g]);
+    }
+    const bool over = most > 31u << 10;  // a 2^s > 2
+
     // the maximum in use (a factor fs >= 0 makes u the score)
     float top[NT][2];
     bool moved = false;
@@ -871,29 +898,46 @@ __global__ void __launch_bounds__(kFewWarps * 32, NT == 1 && D <= 128 ? 4 : 2) k
         top[nt][e] = fmaxf(fmaxf(u[0][nt][e], u[0][nt][e + 2]), fmaxf(u[1][nt][e], u[1][nt][e + 2]));
         moved |= top[nt][e] * fs[nt][e] > m[nt][e] + kLazyBits;
       }
-    if (__any_sync(0xFFFFFFFFu, moved)) {
+    if (__any_sync(0xFFFFFFFFu, moved || over)) {
+      if (__any_sync(0xFFFFFFFFu, moved)) {
 #pragma unroll
-      for (int nt = 0; nt < NT; ++nt)
+        for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-        for (int e = 0; e < 2; ++e) {
-          float t = top[nt][e];
-          t = fmaxf(t, __shfl_xor_sync(0xFFFFFFFFu, t, 4));
-          t = fmaxf(t, __shfl_xor_sync(0xFFFFFFFFu, t, 8));
-          t = fmaxf(t, __shfl_xor_sync(0xFFFFFFFFu, t, 16));
-          const float now = fmaxf(m[nt][e], t * fs[nt][e]);
-          const float fix = now == -INFINITY ? 1.f : ex2(m[nt][e] - now);
-          m[nt][e] = now;
-          nb[nt][e] = now == -INFINITY ? 0.f : kWeightBits - now;
-          l[nt][e] *= fix;
-          zo[nt][e] *= fix;
+          for (int e = 0; e < 2; ++e) {
+            float t = top[nt][e];
+            t = fmaxf(t, __shfl_xor_sync(0xFFFFFFFFu, t, 4));
+            t = fmaxf(t, __shfl_xor_sync(0xFFFFFFFFu, t, 8));
+            t = fmaxf(t, __shfl_xor_sync(0xFFFFFFFFu, t, 16));
+            const float now = fmaxf(m[nt][e], t * fs[nt][e]);
+            const float fix = now == -INFINITY ? 1.f : ex2(m[nt][e] - now);
+            m[nt][e] = now;
+            nb[nt][e] = now == -INFINITY ? 0.f : kWeightBits - now;
+            l[nt][e] *= fix;
+            zo[nt][e] *= fix;
 #pragma unroll
-          for (int g = 0; g < G; ++g)
+            for (int g = 0; g < G; ++g)
 #pragma unroll
-            for (int j = 0; j < 4; ++j) {
-              o[nt][g][j][e] *= fix;
-              o[nt][g][j][e + 2] *= fix;
-            }
-        }
+              for (int j = 0; j < 4; ++j) {
+                o[nt][g][j][e] *= fix;
+                o[nt][g][j][e + 2] *= fix;
+              }
+          }
+      }
+#pragma unroll
+      for (int g = 0; g < G; ++g) {
+        const uint32_t a = __reduce_max_sync(0xFFFFFFFFu, own_a[g]);
+        if (a + power[g] <= 31u << 10) continue;
+        // a 2^s from 1/2 on (below 4 for a scale beyond 2^15, which has no smaller power)
+        const uint32_t now = max(1u << 10, (29u << 10) - min(a & 0x7C00u, 28u << 10));
+        const float fix = power_of_two((int)(now >> 10) - (int)(power[g] >> 10));
+        power[g] = now;
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+          for (int j = 0; j < 4; ++j)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) o[nt][g][j][e] *= fix;
+      }
     }
 
     // weights, and the second product
@@ -919,12 +963,15 @@ __global__ void __launch_bounds__(kFewWarps * 32, NT == 1 && D <= 128 ? 4 : 2) k
       if (!WHOLE) {
         bool odd = false;
 #pragma unroll
-        for (int k = 0; k < 4; ++k)
+        for (int k = 0; k < 4; ++k) {
+          const int j = j0 + half * 16 + 2 * c + (k & 1) + 8 * (k >> 1);
+          const bool in = j >= sp.seen && j < end && !((gone >> half) & 1u);  // by some row
 #pragma unroll
           for (int g = 0; g < G; ++g) {
             odd |= odd_half2(az[k][g]);
-            az[k][g] = finite_half2(az[k][g]);
+            az[k][g] = in ? finite_half2(az[k][g]) : 0u;
           }
+        }
         if (__any_sync(0xFFFFFFFFu, odd)) {
 #pragma unroll
           for (int e8 = 0; e8 < 2; ++e8) {
@@ -953,7 +1000,9 @@ __global__ void __launch_bounds__(kFewWarps * 32, NT == 1 && D <= 128 ? 4 : 2) k
       for (int nt = 0; nt < NT; ++nt) mma16816(zo[nt], za, 0u, zb, 0u, b0[nt], b1[nt]);
 #pragma unroll
       for (int g = 0; g < G; ++g) {
-        const uint32_t a01 = prmt(az[0][g], az[1][g], 0x5410), a23 = prmt(az[2][g], az[3][g], 0x5410);
+        const uint32_t by = power[g] | power[g] << 16;
+        const uint32_t a01 = mul_half2(prmt(az[0][g], az[1][g], 0x5410), by),
+                       a23 = mul_half2(prmt(az[2][g], az[3][g], 0x5410), by);
         // word r of the group, of positions 2c, 2c + 1, 2c + 8, 2c + 9
         const uint32_t va = at + v_at[g];
         const uint32_t v0 = lds_u32v(va), v1 = lds_u32v(va + 4 * S::kRow);
@@ -1022,12 +1071,14 @@ __global__ void __launch_bounds__(kFewWarps * 32, NT == 1 && D <= 128 ? 4 : 2) k
         sm[2 * row + 1] = l[nt][e];
       }
 #pragma unroll
-      for (int g = 0; g < G; ++g)
+      for (int g = 0; g < G; ++g) {
+        const float back = power_of_two(39 - (int)(power[g] >> 10));  // 2^(24 - s)
 #pragma unroll
         for (int j = 0; j < 4; ++j)
           *reinterpret_cast<float2*>(so + row * D + g * kKvGroup + 8 * r + 2 * j) =
-              make_float2(fmaf(o[nt][g][j][e], 0x1p24f, z[g]),
-                          fmaf(o[nt][g][j][e + 2] - o[nt][g][j][e], 0x1p20f, z[g]));
+              make_float2(fmaf(o[nt][g][j][e], back, z[g]),
+                          fmaf(o[nt][g][j][e + 2] - o[nt][g][j][e], back * 0.0625f, z[g]));
+      }
     }
   __syncthreads();
   for (int id = threadIdx.x; id < row_n * (D / 4); id += kFewWarps * 32) {

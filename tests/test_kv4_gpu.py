@@ -843,3 +843,70 @@ def test_nan_values_in_every_step_of_a_full_grid(B, n, L, H, heads, D, hint):
         out, lse = _run(c, q, hint, **kw)
         wrong += (torch.isnan(out) != want).sum() + (out != clean)[~want].sum() + (lse != clean_lse).sum()
     assert int(wrong) == 0 and api.device_error() == api.BCQ_OK
+
+
+def _values_of_any_size(mag, peak, n, new, H, heads, D, seed=0):
+    """A cache whose first position outweighs each other one e^peak times, for queries of ones and scale 1 / D,
+    and whose V has scales about `mag` ("grows": from 1e-4 to 1 with the position)."""
+    c = Case([n, 40], [new, 1], heads, D, 64, seed=seed)
+    rng = np.random.default_rng(seed)
+    shape = c.arrays["v_param"].shape[:-1]
+    a = np.full(shape, 1e-4 if mag == "grows" else mag)
+    if mag == "grows":
+        at = np.arange(n)
+        a.transpose(0, 2, 1, 3)[c.table[0][at // 64], at % 64] = (1e-4 * 1e4 ** (at / n))[:, None, None]
+    a = (a * (1 + 0.01 * rng.integers(0, 2, shape))).astype(np.float16)
+    v = np.stack([a, (-7.5 * a.astype(np.float64)).astype(np.float16)], -1)
+    v[np.isnan(c.arrays["v_param"][..., 0])] = np.nan                          # where no token is
+    k = np.zeros_like(c.arrays["k_param"])
+    for b in range(2):
+        k[c.table[b, 0], :, 0, :, 1] = peak
+    c.arrays.update(k_param=k, v_param=v)
+    c.cache.k_param.copy_(torch.from_numpy(k))
+    c.cache.v_param.copy_(torch.from_numpy(v))
+    return c
+
+
+@pytest.mark.parametrize("dtype,new,H,heads,D", [(F16, 1, 4, 1, 128), (BF16, 1, 2, 2, 64), (F16, 3, 2, 1, 256),
+                                                 (BF16, 3, 8, 2, 128), (F16, 1, 16, 1, 64)])
+@pytest.mark.parametrize("peak", [0.0, 9.0])
+@pytest.mark.parametrize("mag", [2000.0, 0.3, 6e-3, 3e-4, 3e-5, "grows"])
+def test_values_of_any_magnitude(mag, peak, dtype, new, H, heads, D):
+    """Few rows, positions in one part: each weight p and each p a is off by u of itself, whatever V's magnitude and
+    however one position outweighs the rest.  The kernel's scores are products of exact operands summed in fp32 (the
+    offsets' in two fp16 parts, 2^-22); p a c is rounded twice and p z once; and what lies 2^23 below the row's
+    largest, or 2^13 below V's largest scale, adds a step of 2^-33 of the largest a position."""
+    n = 8000
+    c = _values_of_any_size(mag, peak, n, new, H, heads, D)
+    q = torch.ones(c.T, H, D, dtype=dtype, device="cuda")
+    out, lse = _run(c, q, max_kv=128, scale=1.0 / D)
+    ro, rl, m = kv4.attention(_f64(q), *(c.arrays[x] for x in ("k", "k_param", "v", "v_param")), c.table, c.lens, c.cu,
+                              1.0 / D)
+    ds = m["s"] * (2.0 ** -22 + 4 * D * E) + 16 * E * (1 + m["s"])
+    largest = np.nanmax(np.abs(c.arrays["v_param"].astype(np.float64)).sum(-1)) * 15
+    tol = (m["v"] * (2 * ds + 2 * U + 4 * n * E)[..., None] + n * 2.0 ** -33 * largest +
+           torch.finfo(dtype).eps / 2 * np.abs(ro) + 2.0 ** -25)
+    err = np.abs(_f64(out) - ro)
+    assert (err <= tol).all(), f"worst {(err / tol).max():.2f} of the tolerance, {err.max():.2e}"
+    assert (np.abs(_f64(lse) - rl) <= ds + 4 * n * E + 2 * E * np.abs(rl)).all()
+
+
+@pytest.mark.parametrize("new", [1, 6, 140])
+@HINTS
+def test_what_no_row_sees_has_no_effect(new, hint):
+    """Finite numbers of any size behind a sequence's end, in front of its window and beside a hole change no bit."""
+    c = Case([175, 50], [new, 1], 2, 128, 16)
+    q = _queries(c.T, 8, 128, F16)
+    c.cache.v_param.mul_(1e-3)
+    for kw in (dict(), dict(window=21)):
+        ref, ref_lse = _run(c, q, hint, **kw)
+        keep = [getattr(c.cache, x).clone() for x in ("k_param", "v_param")]
+        for b in range(2):
+            first = max(0, c.lens[b] - c.new[b] - 20) if kw else 0
+            for j in [*range(first), *range(c.lens[b], 16 * c.table.shape[1])]:
+                for x in (c.cache.k_param, c.cache.v_param):
+                    x[int(c.table[b, j // 16]), :, j % 16] = 6e4 * (-1) ** j
+        out, lse = _run(c, q, hint, **kw)
+        assert torch.equal(out, ref) and torch.equal(lse, ref_lse)
+        for x, y in zip((c.cache.k_param, c.cache.v_param), keep):
+            x.copy_(y)
