@@ -19,7 +19,9 @@
 // softmax then waits for two products a step, 5200 cycles for 128 positions).
 // P replaces S in tensor memory, in fp16 (the second rounding of 2^-11); O
 // stays there, and is scaled only when a row's maximum has risen by more than
-// 2^8 over the one in use, so p stays below 256.
+// 2^8 over the one in use.  p is held times 2^7, so it is at most 2^15 and keeps
+// its 11 bits down to 2^-21 of the row's largest; below, a position is off by
+// 2^-32 of that at most.
 // Queries are scaled by a power of two a row to the top of fp16's range.
 // Within eight values of a vector both operands have the order 0 4 1 5 2 6 3 7,
 // in which masks yield them; outputs are put right as they are written.
@@ -40,6 +42,8 @@
 
 namespace bcq {
 namespace {
+
+constexpr float kManyBits = 7.f;  // p is held times 2^7
 
 // EXACT: K's operands in two fp16 parts, for calls over few positions.
 template <int D, bool EXACT>
@@ -547,7 +551,7 @@ __global__ void __launch_bounds__(ManyShape<D, EXACT>::kThreads, 1) kv4_many_ker
         }
       }
       const float base = m == -INFINITY ? 0.f : m;
-      const uint64_t fs2 = pack_f32x2(fs, fs), base2 = pack_f32x2(-base, -base);
+      const uint64_t fs2 = pack_f32x2(fs, fs), base2 = pack_f32x2(kManyBits - base, kManyBits - base);
       uint64_t sum2[2] = {0, 0};
       take_turn();
       ++taken;
@@ -593,7 +597,8 @@ __global__ void __launch_bounds__(ManyShape<D, EXACT>::kThreads, 1) kv4_many_ker
     } else {
       // ------------------------------------------------------------ the outputs
       const bool none = m == -INFINITY && l == 0.f, split = sp.parts > 1;
-      const float inv = none ? 0.f : split ? kWeightScale : 1.f / l;
+      constexpr float kPartScale = kWeightScale / 128.f;  // a part's weights are held as the few-row kernel's
+      const float inv = none ? 0.f : split ? kPartScale : 1.f / l;
       const int64_t at = ((int64_t)part * p.T + token) * p.q_heads + h;
       for (int c = 0; c < D; c += 32) {
         uint32_t o[32];
@@ -630,9 +635,9 @@ __global__ void __launch_bounds__(ManyShape<D, EXACT>::kThreads, 1) kv4_many_ker
       if (live && split) {
         float* ml = p.part + (int64_t)p.splits * p.T * p.q_heads * D + at * 2;
         ml[0] = m;
-        ml[1] = l * kWeightScale;
+        ml[1] = l * kPartScale;
       } else if (live && p.lse) {
-        p.lse[token * p.q_heads + h] = none ? -INFINITY : (m + log2f(l)) * 0.69314718055994531f;
+        p.lse[token * p.q_heads + h] = none ? -INFINITY : (m + log2f(l) - kManyBits) * 0.69314718055994531f;
       }
     }
   }

@@ -910,3 +910,26 @@ def test_what_no_row_sees_has_no_effect(new, hint):
         assert torch.equal(out, ref) and torch.equal(lse, ref_lse)
         for x, y in zip((c.cache.k_param, c.cache.v_param), keep):
             x.copy_(y)
+
+
+@pytest.mark.parametrize("kw,adds", [(dict(max_q=5000, max_kv=4000), 32), (dict(max_kv=128), 64), (dict(), 64)],
+                         ids=["many", "few", "few, split"])
+@pytest.mark.parametrize("peak", [12.5, 13.25, 13.5])
+@pytest.mark.parametrize("D", [64, 256])
+def test_a_long_tail_of_small_weights_counts(D, peak, kw, adds):
+    """One position and, e^peak times lighter each, 2^18 others that weigh half as much together or more; V is 1.
+    Weights are off by u, and fp32 sums of n positions, 16 at a time in two parts or by four warps, by 2 E each."""
+    n = 2 ** 18
+    c = Case([n], [1], 1, D, 256)
+    c.cache.k_param.zero_()
+    c.cache.v_param.zero_()
+    c.cache.v_param[..., 1] = 1.0
+    c.cache.k_param[int(c.table[0, 0]), :, 0, :, 1] = peak
+    tol = U + 2 * E * (n / adds + 64)
+    for dtype in (BF16, F16):
+        q = torch.ones(1, 1, D, dtype=dtype, device="cuda")
+        out, lse = _run(c, q, scale=1.0 / D, **kw)
+        err = np.abs(_f64(out) - 1).max()
+        assert err <= tol + torch.finfo(dtype).eps / 2, err
+        want = peak + np.log1p((n - 1) * np.exp(-peak))
+        assert abs(float(lse) - want) <= 2 * E * (n / adds + 64) + 64 * E * want
