@@ -101,6 +101,8 @@ def lib():
         L.bcq_device_error.argtypes = [P]
         L.bcq_debug_wait_timeout.restype = I
         L.bcq_debug_wait_timeout.argtypes = [I, P]
+        L.bcq_debug_impatient.restype = I
+        L.bcq_debug_impatient.argtypes = [I]
         L.bcq_quantize.restype = I
         L.bcq_quantize.argtypes = [P, I, I, I, I, I, P, P, P, P, P]
         L.bcq_quantize_zp.restype = I
@@ -131,7 +133,7 @@ EXPORTED = ("bcq_status_string", "bcq_version", "bcq_packed_planes_bytes",
             "bcq_pack_planes", "bcq_packed_scales_bytes", "bcq_pack_scales",
             "bcq_workspace_bytes", "bcq_gemm", "bcq_plan_query", "bcq_route_query", "bcq_set_pdl",
             "bcq_gemm_host", "bcq_gemm_noalloc", "bcq_build_lut", "bcq_device_error",
-            "bcq_debug_wait_timeout", "bcq_quantize", "bcq_gemm_zp", "bcq_quantize_zp",
+            "bcq_debug_wait_timeout", "bcq_debug_impatient", "bcq_quantize", "bcq_gemm_zp", "bcq_quantize_zp",
             "bcq_quantize_i8", "bcq_gemm_i8", "bcq_linear_i8_workspace_bytes", "bcq_linear_i8",
             "bcq_kv4_append", "bcq_kv4_read", "bcq_kv4_attention_workspace_bytes",
             "bcq_kv4_attention")
@@ -1019,3 +1021,9 @@ def device_error(stream=None) -> int:
 def debug_wait_timeout(limit_us: int, stream=None) -> None:
     _check(lib().bcq_debug_wait_timeout(int(limit_us), _stream(stream)),
            "bcq_debug_wait_timeout")
+
+
+def debug_impatient(on: bool) -> None:
+    """While on, barrier waits of gemm_i8, linear_i8 and kv4_attention give up
+    at random, or after 0.2 ms instead of 2 s (bcq_debug_impatient)."""
+    _check(lib().bcq_debug_impatient(1 if on else 0), "bcq_debug_impatient")

@@ -454,6 +454,11 @@ bcq_status check_gemm_args(const uint16_t* x, const uint32_t* planes,
   return validate_gemm(x, planes, alpha, zq, p, p_row, M, N, K, p_H, group, y, ws, ws_bytes);
 }
 
+namespace {
+std::atomic<bool> g_impatient{false};
+}  // namespace
+bool impatient() { return g_impatient.load(std::memory_order_relaxed); }
+
 }  // namespace bcq
 
 using namespace bcq;
@@ -654,6 +659,12 @@ bcq_status bcq_device_error(void* stream) {
     if (code == 0) code = more;
   }
   return (bcq_status)code;
+}
+
+bcq_status bcq_debug_impatient(int on) {
+  if (on != 0 && on != 1) return BCQ_ERR_SHAPE;
+  g_impatient.store(on != 0, std::memory_order_relaxed);
+  return BCQ_OK;
 }
 
 bcq_status bcq_debug_wait_timeout(int limit_us, void* stream) {

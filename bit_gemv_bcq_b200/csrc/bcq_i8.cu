@@ -103,6 +103,9 @@ __device__ __forceinline__ float4 lds_f32x4(uint32_t addr) {
 __device__ __forceinline__ void prefetch_tensormap(const CUtensorMap* map) {
   asm volatile("prefetch.tensormap [%0];" ::"l"(map) : "memory");
 }
+__device__ __forceinline__ void sts_cluster(uint32_t cluster_addr, uint32_t v) {
+  asm volatile("st.shared::cluster.u32 [%0], %1;" ::"r"(cluster_addr), "r"(v) : "memory");
+}
 __device__ __forceinline__ void sts_zero16(uint32_t addr) {
   asm volatile("st.shared.v4.u32 [%0], {%1, %1, %1, %1};" ::"r"(addr), "r"(0u) : "memory");
 }
@@ -232,12 +235,12 @@ struct GemmParams {
   uint32_t kg_step;     // 2^16 KG / workers: where a worker starts along K
   int overlap;          // the kernel before is the quantiser, which writes x's codes and nothing of w
   uint32_t a_block, b_block, b_off, bar_off, tmem_cols;
-  unsigned long long timeout_ns;
 };
 
 constexpr int kGemmThreads = 448;  // w, x, MMA, MMA, eight output warps, MMA, MMA
 constexpr int kMaxGemmStages = 32;
 constexpr uint32_t kKBlock = 128;
+constexpr unsigned long long kWaitNs = 2000000000ull;  // 2 s
 
 // Where a CTA is on its way through its tiles and, within each, K.
 struct GemmCursor {
@@ -265,8 +268,9 @@ struct GemmCursor {
 };
 
 // PAIR: see above; SUBS: instructions along the tile's rows of x (two in pairs
-// only; loops over them would slow the issue of small tiles' copies).
-template <typename TO, bool PAIR, int SUBS>
+// only; loops over them would slow the issue of small tiles' copies); IMPATIENT:
+// see bcq_debug_impatient (as an argument it costs 3 % of a long product).
+template <typename TO, bool PAIR, int SUBS, bool IMPATIENT>
 __global__ void __launch_bounds__(kGemmThreads, 1)
     gemm_i8_kernel(const __grid_constant__ CUtensorMap wmap, const __grid_constant__ CUtensorMap xmap,
                    const GemmParams p) {
@@ -281,7 +285,7 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
   const int worker = PAIR ? (int)blockIdx.x >> 1 : (int)blockIdx.x;
   const uint32_t full = sbase + p.bar_off, empty = full + 8u * S, accfull = empty + 8u * S,
                  accempty = accfull + 16u, drain = accempty + 16u, slot = drain + 32u,
-                 sx_off = slot + 16u;
+                 failed = slot + 4u, sx_off = slot + 16u;
   if (warp <= 1 && lane == 0) prefetch_tensormap(warp == 0 ? &wmap : &xmap);
   if (warp == 0) {
     for (int i = lane; i < S; i += 32) {
@@ -293,6 +297,7 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
       mbar_init(accempty + 8u * lane, PAIR ? 16 : 8);
     }
     if (lane < 4) mbar_init(drain + 8u * lane, 1);
+    if (lane == 0) sts_f32(failed, 0.f);
     fence_mbar_init();
   } else if (warp == 2) {
     if (PAIR) tmem_alloc_pair(slot, p.tmem_cols);
@@ -326,7 +331,20 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
   // of L2 at the same time.
   const int kg_first = (int)(((uint32_t)worker * p.kg_step) >> 16);
   auto wait = [&](uint32_t bar, uint32_t parity) {
-    return __all_sync(0xFFFFFFFFu, mbar_wait_bounded(bar, parity, p.timeout_ns)) != 0;
+    return __all_sync(0xFFFFFFFFu, IMPATIENT ? mbar_wait_impatient(bar, parity) : mbar_wait_bounded(bar, parity, kWaitNs)) != 0;
+  };
+  // for what is in flight at the end
+  auto end = [&](uint32_t bar, uint32_t parity) {
+    return IMPATIENT ? mbar_look(bar, parity, 1000000) : mbar_wait_bounded(bar, parity, kWaitNs);
+  };
+  // A wait that ran out is recorded, and its warp does no more work; but it comes
+  // to every barrier that other warps come to, and what it has in flight ends
+  // before its CTA does.
+  auto give_up = [&]() {
+    if (lane != 0) return;
+    record_error(&g_i8_error, BCQ_ERR_TIMEOUT);
+    if (PAIR)
+      for (uint32_t i = 0; i < 2; ++i) sts_cluster(map_rank(failed, i), 1u);
   };
 
   if (warp <= 1) {
@@ -344,16 +362,13 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
       const int nt = p.mt == 1 ? c.tile : c.tile / p.mt;
       return is_w ? (PAIR ? 2 * nt + rank : nt) * p.R : (c.tile - nt * p.mt) * p.BT + rank * p.BX;
     };
-    int row = first_row();
+    int row = first_row(), issued = 0;  // copies' stages, the last S of them
     for (int i = 0; i < total; ++i) {
       if (i >= S && !wait(empty + 8u * c.slot, c.phase ^ 1u)) {
-        if (one) record_error(&g_i8_error, BCQ_ERR_TIMEOUT);
-        // the copies in flight (a pair's are all told to rank 0, which the
-        // other CTA waits for at the end)
-        for (int j = rank == 0 ? i - S : i; j < i; ++j)
-          mbar_wait_bounded(full + 8u * (j % S), (uint32_t)(j / S) & 1u, p.timeout_ns);
+        give_up();
         break;
       }
+      issued = min(S, i + 1);
       const int kb = c.kg * p.G, n = min(p.G, p.KB - kb);
       if (one) {
         const uint32_t bar = full + 8u * c.slot;
@@ -370,6 +385,12 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
       }
       if (c.step(p.KG, S, p.workers)) row = first_row();
     }
+    // The copies end before the CTA does, whoever has given up (a pair's are all
+    // told to rank 0, which the other CTA waits for): slots from c.slot on hold the
+    // round before c's.
+    bool there = rank == 0;
+    for (int i = 0; i < issued && there; ++i)
+      there = end(full + 8u * i, c.phase ^ (issued == S && i >= c.slot ? 1u : 0u));
   } else if (warp < 4 || warp >= 12) {
     // --------------------------------------------------------------- the sums
     const int issuer = warp < 4 ? warp - 2 : warp - 10;
@@ -429,12 +450,13 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
       }
       if (ok && one) commit(accfull + 8u * buf);
     }
-    if (!ok) {
+    if (!ok) give_up();
+    if (rank == 0 && issuer < p.issuers) {  // the products end before the CTA does
       if (one) {
-        record_error(&g_i8_error, BCQ_ERR_TIMEOUT);
-        commit(drain + 8u * issuer);
+        if (PAIR) umma_commit_pair_here(drain + 8u * issuer);
+        else umma_commit(drain + 8u * issuer);
       }
-      mbar_wait_bounded(drain + 8u * issuer, 0, p.timeout_ns);
+      end(drain + 8u * issuer, 0);
     }
   } else {
     // ------------------------------------------------------------ the outputs
@@ -444,6 +466,7 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
     const int split = ((p.BT >> 4) + 1) / 2 * 16;
     const int r = lane < each ? quarter * each + lane : 1 << 20;
     grid_dependency_wait();  // sx, and y's last use
+    bool ok = true;
     for (int t = 0; t < mine; ++t) {
       const int tile = worker + t * p.workers;
       const int nt = p.mt == 1 ? tile : tile / p.mt;
@@ -457,10 +480,8 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
       for (int c = (int)threadIdx.x - 128; c < p.BT; c += 256)
         sts_f32(sxs + 4u * c, c < cols ? p.sx[m0 + c] : 0.f);
       named_barrier_sync(1, 256);
-      if (!wait(accfull + 8u * buf, (uint32_t)(p.bufs == 2 ? t >> 1 : t) & 1u)) {
-        if (lane == 0) record_error(&g_i8_error, BCQ_ERR_TIMEOUT);
-        break;
-      }
+      if (ok && !(ok = wait(accfull + 8u * buf, (uint32_t)(p.bufs == 2 ? t >> 1 : t) & 1u))) give_up();
+      if (!ok) continue;  // to the next tile's barrier
       umma_fence_after();
       if (quarter * each < p.R) {
         const int c_first = half * split, c_end = half ? cols : min(cols, split);
@@ -507,7 +528,17 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
   __syncwarp();
   umma_fence_before();
   __syncthreads();
-  if (PAIR) cluster_sync();  // neither CTA leaves while the other uses its memory
+  if (PAIR) {
+    cluster_sync();  // neither CTA leaves while the other uses its memory
+    if (lds_u32v(failed)) {
+      // copies of rank 1 that rank 0 no longer expected have a millisecond (they
+      // take some microseconds)
+      const unsigned long long t0 = globaltimer_ns();
+      while (globaltimer_ns() - t0 < 1000000ull) {
+      }
+      cluster_sync();
+    }
+  }
   if (warp == 2) {
     umma_fence_after();
     if (PAIR) tmem_dealloc_pair(tmem, p.tmem_cols);
@@ -526,7 +557,6 @@ bool sizes_ok(int M, int K) { return M >= 0 && K >= 1 && K <= BCQ_I8_MAX_K; }
 bool is16(int dtype) { return dtype == BCQ_F16 || dtype == BCQ_BF16; }
 
 constexpr size_t kMaxSmem = 232448;                          // 227 KiB per CTA on sm_100
-constexpr unsigned long long kWaitNs = 2000000000ull;         // 2 s
 
 template <typename T>
 cudaError_t launch_quantize_t(const uint16_t* x, int M, int K, int64_t ldx, int8_t* q, int64_t ldq,
@@ -685,11 +715,14 @@ int sm_count() {
   return n;
 }
 
-template <typename TO, bool PAIR, int SUBS>
+template <typename TO, bool PAIR, int SUBS, bool IMPATIENT = false>
 cudaError_t launch_gemm_t(const CUtensorMap& wmap, const CUtensorMap& xmap, const GemmParams& p,
                           size_t smem, int grid, cudaStream_t st) {
+  if constexpr (std::is_same_v<TO, __half> && !IMPATIENT)
+    if (impatient()) return launch_gemm_t<TO, PAIR, SUBS, true>(wmap, xmap, p, smem, grid, st);
+  const auto kernel = gemm_i8_kernel<TO, PAIR, SUBS, IMPATIENT>;
   static std::atomic<uint64_t> done{0};
-  const cudaError_t e = allow_smem(gemm_i8_kernel<TO, PAIR, SUBS>, kMaxSmem, done);
+  const cudaError_t e = allow_smem(kernel, kMaxSmem, done);
   if (e != cudaSuccess) return e;
   cudaLaunchAttribute attr[2] = {};
   int n = 0;
@@ -708,7 +741,7 @@ cudaError_t launch_gemm_t(const CUtensorMap& wmap, const CUtensorMap& xmap, cons
   cfg.stream = st;
   cfg.attrs = attr;
   cfg.numAttrs = (unsigned)n;
-  return cudaLaunchKernelEx(&cfg, gemm_i8_kernel<TO, PAIR, SUBS>, wmap, xmap, p);
+  return cudaLaunchKernelEx(&cfg, kernel, wmap, xmap, p);
 }
 
 // overlap: the kernel before in the stream is the quantiser, whose codes and
@@ -726,7 +759,6 @@ cudaError_t launch_gemm(const int8_t* x, int64_t ldx, const float* sx, const int
   p.M = M;
   p.N = N;
   p.K = K;
-  p.timeout_ns = kWaitNs;
   p.overlap = overlap;
   size_t smem = 0;
   int grid = 0;

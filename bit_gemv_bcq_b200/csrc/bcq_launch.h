@@ -87,6 +87,9 @@ cudaError_t launch_early(void (*kernel)(P...), dim3 grid, unsigned threads, size
   return cudaLaunchKernelEx(&cfg, kernel, P(args)...);
 }
 
+// Whether bcq_debug_impatient is on.
+bool impatient();
+
 // As read_and_clear_device_error, for the kernels of bcq_i8.cu and of
 // bcq_kv4.cu, after the stream's synchronisation.
 cudaError_t read_and_clear_i8_error(int* code);

@@ -157,6 +157,11 @@ __device__ __forceinline__ void umma_commit_pair(uint32_t bar) {
       "h"((uint16_t)3)
       : "memory");
 }
+// Arrive on this CTA's barrier only.
+__device__ __forceinline__ void umma_commit_pair_here(uint32_t bar) {
+  asm volatile("tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(bar)
+               : "memory");
+}
 __device__ __forceinline__ void umma_i8_ss_pair(uint32_t d, uint64_t adesc, uint64_t bdesc,
                                                 uint32_t idesc, uint32_t accumulate) {
   asm volatile(
@@ -164,6 +169,22 @@ __device__ __forceinline__ void umma_i8_ss_pair(uint32_t d, uint64_t adesc, uint
       "tcgen05.mma.cta_group::2.kind::i8 [%0], %1, %2, %3, p;\n\t}" ::"r"(d),
       "l"(adesc), "l"(bdesc), "r"(idesc), "r"(accumulate)
       : "memory");
+}
+
+// Waits that end early, for bcq_debug_impatient.  As mbar_wait_bounded, without
+// the thread's sleep, which is no shorter than some hundred microseconds.
+__device__ __forceinline__ bool mbar_look(uint32_t bar, uint32_t parity, unsigned long long limit_ns) {
+  const unsigned long long t0 = globaltimer_ns();
+#pragma unroll 1
+  do {
+    if (mbar_test(bar, parity)) return true;
+  } while (globaltimer_ns() - t0 < limit_ns);
+  return false;
+}
+// Gives up after 0.2 ms, and one time in 128 as soon as it would have to wait.
+__device__ __forceinline__ bool mbar_wait_impatient(uint32_t bar, uint32_t parity) {
+  if (mbar_test(bar, parity)) return true;
+  return (clock() & 127) != 0 && mbar_look(bar, parity, 200000);
 }
 
 // Shared-memory descriptor of a K-major operand in rows of 128 bytes with the

@@ -596,6 +596,16 @@ bcq_status bcq_device_error(void* stream);
  */
 bcq_status bcq_debug_wait_timeout(int limit_us, void* stream);
 
+/*
+ * Test hook for what follows a wait that runs out: while it is on (1; 0: off, as
+ * at first), the kernels of the 8-bit product with fp16 outputs and of attention
+ * of many fp16 rows of 128 over the 4-bit cache, in the calls that the process
+ * makes, give up some barrier waits at random as soon as they would have to wait,
+ * and the others after 0.2 ms instead of 2 s.  A kernel that gives up records
+ * BCQ_ERR_TIMEOUT and ends, with outputs of no meaning.
+ */
+bcq_status bcq_debug_impatient(int on);
+
 #ifdef __cplusplus
 }
 #endif

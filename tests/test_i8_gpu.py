@@ -307,3 +307,25 @@ def test_side_stream_and_two_graphs_at_once():
     graphs[0].replay()
     torch.cuda.synchronize()
     assert torch.equal(outs[0], api.linear_i8(xs[0], w, sw))
+
+
+@pytest.mark.parametrize("M,N,K", [(16, 60000, 4096), (3, 30000, 8192), (400, 16384, 4096), (1024, 8192, 2048), (77, 1111, 1003)])
+def test_waits_that_run_out_are_reported(M, N, K):
+    """Whichever wait of a kernel gives up first, in one CTA or in one of a pair, the call ends and says so."""
+    x, sx = _codes(M, K, 1)
+    w, sw = _codes(N, K, 2)
+    ref = api.gemm_i8(x, sx, w, sw)
+    try:
+        given_up = 0
+        for _ in range(30):
+            api.debug_impatient(True)
+            y = api.gemm_i8(x, sx, w, sw)
+            status = api.device_error()
+            assert status == api.BCQ_ERR_TIMEOUT or (status == api.BCQ_OK and torch.equal(y, ref))
+            given_up += status == api.BCQ_ERR_TIMEOUT
+            api.debug_impatient(False)
+            y = api.gemm_i8(x, sx, w, sw)
+            assert api.device_error() == api.BCQ_OK and torch.equal(y, ref)
+        assert given_up
+    finally:
+        api.debug_impatient(False)

@@ -320,3 +320,9 @@ def test_kv4_binding_refusals(host):
         lambda: api.kv4_attention(q, c, table, n, cu, out=host(5, 1, 128).expand(5, 4, 128)),
         lambda: api.kv4_attention(q, c, table, n, cu, out=host(1, 4, 128).expand(5, 4, 128)),
     ])
+
+
+def test_impatience_is_a_switch():
+    L = api.lib()
+    assert L.bcq_debug_impatient(2) == api.BCQ_ERR_SHAPE and L.bcq_debug_impatient(-1) == api.BCQ_ERR_SHAPE
+    assert L.bcq_debug_impatient(1) == api.BCQ_OK and L.bcq_debug_impatient(0) == api.BCQ_OK
