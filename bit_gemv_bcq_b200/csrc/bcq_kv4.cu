@@ -1403,14 +1403,17 @@ cudaError_t launch_few_t(const AttentionParams& p, cudaStream_t st) {
   return launch_early(kv4_few_kernel<T, D, NT>, grid, kFewWarps * 32, smem, st, p);
 }
 
-template <typename T, int D, bool EXACT>
+template <typename T, int D, bool EXACT, bool IMPATIENT = false>
 cudaError_t launch_many_t(const AttentionParams& p, cudaStream_t st) {
   using S = ManyShape<D, EXACT>;
+  if constexpr (std::is_same_v<T, __half> && D == 128 && !IMPATIENT)
+    if (impatient()) return launch_many_t<T, D, EXACT, true>(p, st);
+  const auto kernel = kv4_many_kernel<T, D, EXACT, IMPATIENT>;
   static std::atomic<uint64_t> done{0};
-  cudaError_t e = allow_smem(kv4_many_kernel<T, D, EXACT>, S::kSmem, done);
+  cudaError_t e = allow_smem(kernel, S::kSmem, done);
   if (e != cudaSuccess) return e;
   const dim3 grid((unsigned)((int64_t)p.row_blocks * p.at.heads * p.at.B), (unsigned)p.splits);
-  return launch_early(kv4_many_kernel<T, D, EXACT>, grid, S::kThreads, S::kSmem, st, p);
+  return launch_early(kernel, grid, S::kThreads, S::kSmem, st, p);
 }
 
 template <typename T, int D>

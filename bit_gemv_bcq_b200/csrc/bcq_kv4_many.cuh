@@ -163,7 +163,8 @@ __device__ __forceinline__ void sts_v4(uint32_t addr, const uint4& v) {
                : "memory");
 }
 
-template <typename T, int D, bool EXACT>
+// IMPATIENT: see bcq_debug_impatient (as an argument it costs 3 %).
+template <typename T, int D, bool EXACT, bool IMPATIENT>
 __global__ void __launch_bounds__(ManyShape<D, EXACT>::kThreads, 1) kv4_many_kernel(const AttentionParams p) {
   using S = ManyShape<D, EXACT>;
   constexpr int G = D / kKvGroup;
@@ -220,14 +221,17 @@ __global__ void __launch_bounds__(ManyShape<D, EXACT>::kThreads, 1) kv4_many_ker
   __syncthreads();
   umma_fence_after();
   const uint32_t tmem = lds_u32v(slot);
-  constexpr unsigned long long kWaitNs = 2000000000ull;
+  constexpr unsigned long long kWaitNs = 2000000000ull;  // 2 s
   // A waiting thread that sleeps takes some 400 cycles to wake: look a while first.
   auto wait = [&](uint32_t at, int round) {
+    if (IMPATIENT) return __all_sync(0xFFFFFFFFu, mbar_wait_impatient(at, (uint32_t)round & 1u)) != 0;
     bool there = false;
 #pragma unroll 1
     for (int i = 0; i < 64 && !there; ++i) there = mbar_test(at, (uint32_t)round & 1u);
     return __all_sync(0xFFFFFFFFu, there || mbar_wait_bounded(at, (uint32_t)round & 1u, kWaitNs)) != 0;
   };
+  // A warp whose wait ran out does no more work, but comes to every barrier that
+  // other warps come to; the products in flight end before the CTA does.
   auto give_up = [&]() {
     if (lane == 0) record_error(&g_kv4_error, BCQ_ERR_TIMEOUT);
   };
@@ -284,11 +288,9 @@ __global__ void __launch_bounds__(ManyShape<D, EXACT>::kThreads, 1) kv4_many_ker
       if (ok && one) umma_commit(v_empty + 8u * va.slot);
       va.step(S::kVBufs);
     }
-    if (!ok) {
-      give_up();
-      if (one) umma_commit(drain);
-      mbar_wait_bounded(drain, 0, kWaitNs);
-    }
+    if (!ok) give_up();
+    if (one) umma_commit(drain);
+    mbar_wait_bounded(drain, 0, kWaitNs);
     }
   } else if (warp >= kCodeWarp0) {
     // --------------------------------------------------------------- the codes
@@ -586,7 +588,10 @@ __global__ void __launch_bounds__(ManyShape<D, EXACT>::kThreads, 1) kv4_many_ker
       if (lane == 0) mbar_arrive_cta(p_full + 8u * (2 * t + (j & 1)));
       if (j > 0 && __any_sync(0xFFFFFFFFu, lds_u32v(sbase + S::kOffOdd) != 0)) look_for_nan(j - 1);
     }
-    for (; taken < steps; ++taken) give_turn();  // after a wait that ran out: the other tile's warp goes on
+    for (; taken < steps; ++taken) {  // after a wait that ran out: the other tile's warp has its turns
+      take_turn();
+      give_turn();
+    }
     if (steps > 0 && ok) {
       ok = wait(o_done + 8u * t, steps - 1);
       umma_fence_after();

@@ -933,3 +933,27 @@ def test_a_long_tail_of_small_weights_counts(D, peak, kw, adds):
         assert err <= tol + torch.finfo(dtype).eps / 2, err
         want = peak + np.log1p((n - 1) * np.exp(-peak))
         assert abs(float(lse) - want) <= 2 * E * (n / adds + 64) + 64 * E * want
+
+
+@pytest.mark.parametrize("B,n,L,H,heads,D", [(4, 300, 900, 16, 4, 128), (1, 200, 6000, 8, 2, 128), (40, 60, 300, 2, 2, 128)])
+@pytest.mark.parametrize("hint", [500, 4000])
+def test_waits_that_run_out_are_reported(B, n, L, H, heads, D, hint):
+    """Whichever wait of the kernel of many rows gives up first, the call ends and says so."""
+    c = Case([L] * B, [n] * B, heads, D, 64)
+    q = _queries(c.T, H, D, F16)
+    kw = dict(max_q=5000)
+    ref, ref_lse = _run(c, q, hint, **kw)
+    try:
+        given_up = 0
+        for _ in range(30):
+            api.debug_impatient(True)
+            out, lse = _run(c, q, hint, **kw)
+            status = api.device_error()
+            assert status == api.BCQ_ERR_TIMEOUT or (status == api.BCQ_OK and torch.equal(out, ref) and torch.equal(lse, ref_lse))
+            given_up += status == api.BCQ_ERR_TIMEOUT
+            api.debug_impatient(False)
+            out, lse = _run(c, q, hint, **kw)
+            assert api.device_error() == api.BCQ_OK and torch.equal(out, ref) and torch.equal(lse, ref_lse)
+        assert given_up
+    finally:
+        api.debug_impatient(False)
