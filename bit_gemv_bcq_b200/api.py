@@ -955,8 +955,8 @@ def kv4_attention(q: torch.Tensor, cache: Kv4Cache, table: torch.Tensor, kv_len:
 
     cu gives each sequence its rows (without it, one each); max_q is the most
     rows that a sequence has (T when not given), max_kv the plan's guess at the
-    longest kv_len (the table's width when not given; any value is right, a
-    near one fast); window > 0 lets a row see that many positions, its own the
+    longest kv_len (the table's width when not given; any value is right, to
+    the roundings that bcq.h states, a near one fast); window > 0 lets a row see that many positions, its own the
     last; scale is 1 / sqrt(D) when not given.  A row that sees nothing gives
     zeros and -inf; rows that cu gives to no sequence are left as they were."""
     if stream is None and out is None:

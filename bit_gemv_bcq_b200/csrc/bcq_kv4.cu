@@ -574,6 +574,7 @@ constexpr int kFewTokens = 32;  // of a stage
 constexpr float kWeightBits = 9.f;    // p is held times 2^9
 constexpr float kWeightScale = 512.f;
 constexpr float kLazyBits = 4.f;      // how far a row's maximum may rise over the one in use
+constexpr int kFewSeen = 512;         // below so many positions the many-row kernel has keys in two parts
 constexpr uint32_t kFirstPower = 30u << 10;  // 2^15, of V's scales, by the bits of an fp16
 
 template <int D>
@@ -1299,9 +1300,8 @@ void by_shape(int D, int heads, int T, const F& f) {
 }
 
 // How a call's rows and positions are shared out: the kernel (nt: row groups of
-// eight a CTA of the few-row kernel; 0 the many-row kernel, -1 with K in two
-// parts), rows of a CTA,
-// and parts of the positions.
+// eight a CTA of the few-row kernel; 0 the many-row kernel, -1 the same where all
+// rows see few positions), rows of a CTA, and parts of the positions.
 struct AttentionPlan {
   int nt, rows, row_blocks, splits, chunk;
 };
@@ -1350,11 +1350,10 @@ float plan_parts(AttentionPlan* f, int64_t units, int max_kv, const PartsModel& 
 // there are no more, or D = 256: 13.0 us in one pass for 16 rows and 8 x 2000
 // positions, 15.0 in two), four CTAs an SM (two where rows or values are many),
 // with exact products of queries and codes; the many-row kernel once for every
-// 256 (128 where D = 256), with keys rounded to fp16.  Over few positions those
-// roundings do not average out of lse (1e-5 of it below 500 positions): there
-// keys go in two parts, which takes 1.3 times as long (2.1 where D = 256 leaves
-// room for one set of them).  Calls that the second kernel is not thought to save
-// a seventh stay with the first.
+// 256 (128 where D = 256), with keys rounded to fp16, or, in the blocks of rows that
+// see few positions, in two parts, which takes 1.06 to 1.17 times as long (1.35 where
+// D = 256 leaves room for one set of them).  Calls that the second kernel is not thought to
+// save a seventh stay with the first.
 //
 // The models' numbers are fitted to 68 calls of the first (1 to 256 sequences,
 // 300 to 262144 positions, heads of 64 to 256) and 60 of the second, each over 10
@@ -1381,7 +1380,7 @@ AttentionPlan plan_attention(const bcq_kv4* c, int q_heads, int B, int max_q, in
     }
     const bool two = D != 256 && rows > 128;  // tiles
     const float per = (D == 64 ? (two ? 0.0209f : 0.0114f) : D == 128 ? (two ? 0.0254f : 0.0144f) : 0.023f) *
-                      (nt == 0 ? 1.f : D == 256 ? 2.1f : 1.3f);
+                      (nt == 0 ? 1.f : D == 256 ? 1.35f : 1.12f);
     const float out = 1e-6f * (float)B * (float)rows * (float)c->heads * (float)D;  // written and read for each part
     return plan_parts(f, units, seen, {1, ragged ? 0.6f : 1.f, per, 6.f, 5.3f, 1.87f * out, 0.66f});
   };
@@ -1389,8 +1388,8 @@ AttentionPlan plan_attention(const bcq_kv4* c, int q_heads, int B, int max_q, in
   AttentionPlan few, many;
   const float few_time = plan(nt, 8 * nt, &few);
   if (rows <= 16) return few;
-  const bool short_sums = max_kv < 512 || (window != 0 && window < 512);
-  return plan(short_sums ? -1 : 0, D == 256 ? 128 : 256, &many) < 0.85f * few_time ? many : few;
+  const bool few_seen = max_kv < kFewSeen || (window != 0 && window < kFewSeen);
+  return plan(few_seen ? -1 : 0, D == 256 ? 128 : 256, &many) < 0.85f * few_time ? many : few;
 }
 
 template <typename T, int D, int NT>
@@ -1403,12 +1402,12 @@ cudaError_t launch_few_t(const AttentionParams& p, cudaStream_t st) {
   return launch_early(kv4_few_kernel<T, D, NT>, grid, kFewWarps * 32, smem, st, p);
 }
 
-template <typename T, int D, bool EXACT, bool IMPATIENT = false>
+template <typename T, int D, bool IMPATIENT = false>
 cudaError_t launch_many_t(const AttentionParams& p, cudaStream_t st) {
-  using S = ManyShape<D, EXACT>;
+  using S = ManyShape<D>;
   if constexpr (std::is_same_v<T, __half> && D == 128 && !IMPATIENT)
-    if (impatient()) return launch_many_t<T, D, EXACT, true>(p, st);
-  const auto kernel = kv4_many_kernel<T, D, EXACT, IMPATIENT>;
+    if (impatient()) return launch_many_t<T, D, true>(p, st);
+  const auto kernel = kv4_many_kernel<T, D, IMPATIENT>;
   static std::atomic<uint64_t> done{0};
   cudaError_t e = allow_smem(kernel, S::kSmem, done);
   if (e != cudaSuccess) return e;
@@ -1424,7 +1423,7 @@ cudaError_t launch_join_t(const AttentionParams& p, cudaStream_t st) {
 template <typename T, int D>
 cudaError_t launch_attention_t(const AttentionParams& p, int nt, cudaStream_t st) {
   cudaError_t e;
-  if (nt <= 0) e = nt == 0 ? launch_many_t<T, D, false>(p, st) : launch_many_t<T, D, true>(p, st);
+  if (nt <= 0) e = launch_many_t<T, D>(p, st);
   else if constexpr (D == 256) e = launch_few_t<T, D, 1>(p, st);
   else e = nt == 1 ? launch_few_t<T, D, 1>(p, st) : launch_few_t<T, D, 2>(p, st);
   return e == cudaSuccess && p.splits > 1 ? launch_join_t<T, D>(p, st) : e;

@@ -7,12 +7,15 @@
 // (one where D = 256 leaves tensor memory for no more), and 64 positions a
 // step.  Four warps for K and four for V turn the codes into fp16 operands in
 // shared memory, once for both tiles: c from its bits (1024 + c or 1024 + 16 c, exactly), then a c +
-// z with one rounding to fp16 (half a step, 2^-11); over few positions, where
-// that does not average out of lse, K's in two parts (2^-22), which doubles the
-// products and their operands (8 x 400 positions, 256 rows: 23.0 us, 27.0 in the
-// few-row kernel; 29 x 203, 987 rows, heads of 256: 108 against 291; 7 x 688, 4095
-// rows, windows of 128: 62 against 157; where both could be, 112 against 143 us for
-// 4 x 1000 rows with windows of 1000).  One warp issues the
+// z with one rounding to fp16 (half a step, 2^-11).  That puts an error of up to
+// 2^-11 of |scale| sum |q K| on a score; over many positions of like weight it
+// averages out of lse, over few it does not.  So a block of rows one of which sees
+// fewer than kFewSeen positions has K's in two parts (2^-22), which doubles the
+// products and their operands; a block of a prompt's later rows, or of a longer
+// sequence of the same call, has not (us, one part | two | the few-row kernel: 8
+// prompts of 200 to 400 new tokens, 32 heads of 128 on 8, 47.8 | 53.1 | 147; windows
+// of 256 over 4 x 1000 new tokens, 16 heads of 64 on 4, 34.3 | 36.5 | 60.0; 8 x 100
+// rows over 400 positions, 16 heads of 256 on 4, 23.4 | 31.8 | 38.7).  One warp issues the
 // products; four warps a tile do its softmax, a thread a row.  S has two
 // buffers a tile, so that a step's scores are there when the softmax of the
 // one before ends (steps of 128 positions leave tensor memory for one: the
@@ -45,26 +48,28 @@ namespace {
 
 constexpr float kManyBits = 7.f;  // p is held times 2^7
 
-// EXACT: K's operands in two fp16 parts, for calls over few positions.
-template <int D, bool EXACT>
+template <int D>
 struct ManyShape {
   static constexpr int kTiles = D == 256 ? 1 : 2;
   static constexpr int kTokens = 64;                         // of a step
-  static constexpr int kKParts = EXACT ? 2 : 1;
-  static constexpr int kVBufs = D == 256 ? 2 : 3;            // of V's operands
-  static constexpr int kKBufs = EXACT && D == 256 ? 1 : kVBufs;  // of K's
+  // K's and V's operands share six tiles (four where D = 256): three buffers each,
+  // or two of K's in two parts and two of V's.  (More shared memory leaves less
+  // to L1: with nine tiles 2 x 2048 new tokens took 228 us, 219 with six.)
+  static constexpr int kBufs = D == 256 ? 2 : 3;             // of K's, and of V's
+  static constexpr int kKBufs2 = D == 256 ? 1 : 2;           // of K's in two parts
+  static constexpr int kVBufs2 = 2;                          // of V's beside them
+  static_assert(2 * kKBufs2 + kVBufs2 <= 2 * kBufs, "operands' tiles");
   static constexpr int kBlocks = D / 64;                     // 128-byte column blocks of a vector
   static constexpr uint32_t kQBlock = 128 * 128;             // bytes of 64 columns of 128 rows
   static constexpr uint32_t kQTile = kBlocks * kQBlock;
   static constexpr uint32_t kKvBlock = kTokens * 128;
   static constexpr uint32_t kKvTile = kBlocks * kKvBlock;
   static constexpr uint32_t kOffK = kTiles * kQTile;
-  static constexpr uint32_t kOffV = kOffK + kKBufs * kKParts * kKvTile;
-  static constexpr uint32_t kOffBar = kOffV + kVBufs * kKvTile;
+  static constexpr uint32_t kOffBar = kOffK + 2 * kBufs * kKvTile;
   // a step's mask words: the positions without a page, and V's groups that are
   // no numbers.  A ring of eight: K's operands of step j + 8 come after the
-  // scores of step j + 8 - kKBufs, and so after the softmax of step j + 3 (V's
-  // after the product of step j + 8 - kVBufs); step j's words are read for the
+  // scores of step j + 8 - kBufs, and so after the softmax of step j + 3 (V's
+  // after the product of step j + 8 - kBufs); step j's words are read for the
   // last time as step j + 1 ends.
   static constexpr int kPieces = D / 32;                     // 16-byte pieces of a vector's codes
   static constexpr int kPasses = kTokens * kPieces / 128;    // pieces a thread and step
@@ -163,16 +168,26 @@ __device__ __forceinline__ void sts_v4(uint32_t addr, const uint4& v) {
                : "memory");
 }
 
+// Whether some row of a block sees fewer than kFewSeen positions: the first one
+// sees the fewest under a causal mask, else the last one.
+__device__ __forceinline__ bool few_seen(const AttentionParams& p, const Span& sp, int block) {
+  auto seen = [&](int i) {
+    const int pos = sp.pos0 + i;
+    return (p.causal ? min(sp.len, pos + 1) : sp.len) - (p.window > 0 ? max(0, pos - p.window + 1) : 0);
+  };
+  const int i0 = p.group.quotient(block * p.rows), i1 = p.group.quotient((block + 1) * p.rows - 1);
+  return min(seen(i0), seen(min(i1, sp.rows - 1))) < kFewSeen;
+}
+
 // IMPATIENT: see bcq_debug_impatient (as an argument it costs 3 %).
-template <typename T, int D, bool EXACT, bool IMPATIENT>
-__global__ void __launch_bounds__(ManyShape<D, EXACT>::kThreads, 1) kv4_many_kernel(const AttentionParams p) {
-  using S = ManyShape<D, EXACT>;
+template <typename T, int D, bool IMPATIENT>
+__global__ void __launch_bounds__(ManyShape<D>::kThreads, 1) kv4_many_kernel(const AttentionParams p) {
+  using S = ManyShape<D>;
   constexpr int G = D / kKvGroup;
   extern __shared__ unsigned char smem_raw[];
   const uint32_t sbase = (smem_u32(smem_raw) + 1023u) & ~1023u;
   uint32_t* masks = reinterpret_cast<uint32_t*>(smem_raw + (sbase - smem_u32(smem_raw)) + S::kOffMask);
   const int warp = __shfl_sync(0xFFFFFFFFu, (int)threadIdx.x >> 5, 0), lane = threadIdx.x & 31;
-
   // the last blocks of rows see the most: theirs go first, of every sequence
   // and head
   const int pairs = p.at.heads * p.at.B, pair = (int)(blockIdx.x % (unsigned)pairs);
@@ -185,6 +200,10 @@ __global__ void __launch_bounds__(ManyShape<D, EXACT>::kThreads, 1) kv4_many_ker
     if (p.at.kv_len[b] != sp.len) record_error(&g_kv4_error, BCQ_ERR_PAGE);
   }
   if (part >= sp.parts) return;
+  const bool two_parts = few_seen(p, sp, block);  // of K's operands
+  const int k_bufs = two_parts ? S::kKBufs2 : S::kBufs, v_bufs = two_parts ? S::kVBufs2 : S::kBufs;
+  const uint32_t k_step = two_parts ? 2 * S::kKvTile : S::kKvTile;  // a second part follows the first
+  const uint32_t off_v = S::kOffK + (uint32_t)k_bufs * k_step;
   const int row0 = block * p.rows, row_n = min(p.rows, sp.rows * p.group.d - row0);
   const int begin = sp.begin + part * sp.chunk, end = min(sp.end, begin + sp.chunk);
   const int steps = end > begin ? (end - begin + S::kTokens - 1) / S::kTokens : 0;
@@ -240,57 +259,71 @@ __global__ void __launch_bounds__(ManyShape<D, EXACT>::kThreads, 1) kv4_many_ker
     if (S::kTiles == 2) asm volatile("setmaxnreg.dec.sync.aligned.u32 56;");
     if (warp == kMmaWarp) {
     // ------------------------------------------------------------ the products
-    const bool one = elect_one();
-    // fp16 A and B, fp32 D, M = 128; V has its values (N) contiguous
-    constexpr uint32_t kIdS = (1u << 4) | ((uint32_t)(S::kTokens >> 3) << 17) | (8u << 24);
-    constexpr uint32_t kIdO = (1u << 4) | (1u << 16) | ((uint32_t)(D >> 3) << 17) | (8u << 24);
-    const uint64_t qd = umma_desc_sw128(sbase), kd = umma_desc_sw128(sbase + S::kOffK);
-    const uint64_t vd = umma_desc_blocks(sbase + S::kOffV, S::kKvBlock, 1024);
-    bool ok = steps == 0 || wait(q_full, 0);
-    RingAt ka, va;
-    auto scores = [&](int j) {  // of step j, both tiles
-      if (!(ok = wait(k_full + 8u * ka.slot, ka.round))) return;
-      umma_fence_after();
-      if (one) {
-        for (int t = 0; t < tiles; ++t) {
-#pragma unroll
-          for (int i = 0; i < S::kKParts * D / 16; ++i) {
-            const int c = i % (D / 16), part = i / (D / 16);
-            umma_f16_ss(tmem + (uint32_t)((2 * t + (j & 1)) * S::kTokens),
-                        qd + (uint32_t)((t * S::kQTile + (c >> 2) * S::kQBlock + (c & 3) * 32) >> 4),
-                        kd + (uint32_t)(((S::kKParts * ka.slot + part) * S::kKvTile + (c >> 2) * S::kKvBlock + (c & 3) * 32) >> 4),
-                        kIdS, i != 0);
-          }
-          umma_commit(s_full + 8u * (2 * t + (j & 1)));
-        }
-        umma_commit(k_empty + 8u * ka.slot);
-      }
-      ka.step(S::kKBufs);
-    };
-    if (steps > 0 && ok) scores(0);
-    for (int j = 0; j < steps && ok; ++j) {
-      // the next scores go over the last step's weights, behind the product
-      // that reads them
-      if (j + 1 < steps) scores(j + 1);
-      if (!ok || !(ok = wait(v_full + 8u * va.slot, va.round))) break;
-      for (int t = 0; t < tiles; ++t) {
-        const int s = 2 * t + (j & 1);
-        if (!(ok = wait(p_full + 8u * s, j >> 1))) break;
+    // (a choice within the loop keeps addresses out of the uniform registers: 4 %)
+    auto products = [&](auto two_type) {
+      constexpr bool kTwo = decltype(two_type)::value;
+      constexpr uint32_t kStep = kTwo ? 2 * S::kKvTile : S::kKvTile;
+      constexpr uint32_t kOffV = S::kOffK + (kTwo ? S::kKBufs2 : S::kBufs) * kStep;
+      const bool one = elect_one();
+      // fp16 A and B, fp32 D, M = 128; V has its values (N) contiguous
+      constexpr uint32_t kIdS = (1u << 4) | ((uint32_t)(S::kTokens >> 3) << 17) | (8u << 24);
+      constexpr uint32_t kIdO = (1u << 4) | (1u << 16) | ((uint32_t)(D >> 3) << 17) | (8u << 24);
+      const uint64_t qd = umma_desc_sw128(sbase), kd = umma_desc_sw128(sbase + S::kOffK);
+      const uint64_t vd = umma_desc_blocks(sbase + kOffV, S::kKvBlock, 1024);
+      bool ok = steps == 0 || wait(q_full, 0);
+      RingAt ka, va;
+      auto scores = [&](int j) {  // of step j, both tiles
+        if (!(ok = wait(k_full + 8u * ka.slot, ka.round))) return;
         umma_fence_after();
         if (one) {
+          for (int t = 0; t < tiles; ++t) {
 #pragma unroll
-          for (int i = 0; i < S::kTokens / 16; ++i)
-            umma_f16_ts(tmem + (uint32_t)(S::kOCol + t * D), tmem + (uint32_t)(s * S::kTokens + i * 8),
-                        vd + (uint32_t)((va.slot * S::kKvTile + i * 2048) >> 4), kIdO, (j | i) != 0);
-          umma_commit(o_done + 8u * t);
+            for (int c = 0; c < D / 16; ++c)
+              umma_f16_ss(tmem + (uint32_t)((2 * t + (j & 1)) * S::kTokens),
+                          qd + (uint32_t)((t * S::kQTile + (c >> 2) * S::kQBlock + (c & 3) * 32) >> 4),
+                          kd + (uint32_t)((ka.slot * kStep + (c >> 2) * S::kKvBlock + (c & 3) * 32) >> 4),
+                          kIdS, c != 0);
+            if (kTwo) {
+#pragma unroll
+              for (int c = 0; c < D / 16; ++c)
+                umma_f16_ss(tmem + (uint32_t)((2 * t + (j & 1)) * S::kTokens),
+                            qd + (uint32_t)((t * S::kQTile + (c >> 2) * S::kQBlock + (c & 3) * 32) >> 4),
+                            kd + (uint32_t)((ka.slot * kStep + S::kKvTile + (c >> 2) * S::kKvBlock + (c & 3) * 32) >> 4),
+                            kIdS, 1);
+            }
+            umma_commit(s_full + 8u * (2 * t + (j & 1)));
+          }
+          umma_commit(k_empty + 8u * ka.slot);
         }
+        ka.step(kTwo ? S::kKBufs2 : S::kBufs);
+      };
+      if (steps > 0 && ok) scores(0);
+      for (int j = 0; j < steps && ok; ++j) {
+        // the next scores go over the last step's weights, behind the product
+        // that reads them
+        if (j + 1 < steps) scores(j + 1);
+        if (!ok || !(ok = wait(v_full + 8u * va.slot, va.round))) break;
+        for (int t = 0; t < tiles; ++t) {
+          const int s = 2 * t + (j & 1);
+          if (!(ok = wait(p_full + 8u * s, j >> 1))) break;
+          umma_fence_after();
+          if (one) {
+#pragma unroll
+            for (int i = 0; i < S::kTokens / 16; ++i)
+              umma_f16_ts(tmem + (uint32_t)(S::kOCol + t * D), tmem + (uint32_t)(s * S::kTokens + i * 8),
+                          vd + (uint32_t)((va.slot * S::kKvTile + i * 2048) >> 4), kIdO, (j | i) != 0);
+            umma_commit(o_done + 8u * t);
+          }
+        }
+        if (ok && one) umma_commit(v_empty + 8u * va.slot);
+        va.step(kTwo ? S::kVBufs2 : S::kBufs);
       }
-      if (ok && one) umma_commit(v_empty + 8u * va.slot);
-      va.step(S::kVBufs);
-    }
-    if (!ok) give_up();
-    if (one) umma_commit(drain);
-    mbar_wait_bounded(drain, 0, kWaitNs);
+      if (!ok) give_up();
+      if (one) umma_commit(drain);
+      mbar_wait_bounded(drain, 0, kWaitNs);
+    };
+    if (two_parts) products(std::true_type());
+    else products(std::false_type());
     }
   } else if (warp >= kCodeWarp0) {
     // --------------------------------------------------------------- the codes
@@ -301,7 +334,7 @@ __global__ void __launch_bounds__(ManyShape<D, EXACT>::kThreads, 1) kv4_many_ker
     const int piece = lane / S::kPerWarp, sub = lane % S::kPerWarp;
     const uint8_t* code = (is_v ? p.v : p.k) + piece * 16;
     const __half2* param = (is_v ? p.v_param : p.k_param) + (piece >> 1);
-    const uint32_t tiles_at = sbase + (is_v ? S::kOffV : S::kOffK), full = is_v ? v_full : k_full,
+    const uint32_t tiles_at = sbase + (is_v ? off_v : S::kOffK), full = is_v ? v_full : k_full,
                    empty = is_v ? v_empty : k_empty;
     uint32_t* mask = masks + (is_v ? 8 * S::kWords : 0);
     struct Piece {
@@ -362,7 +395,7 @@ __global__ void __launch_bounds__(ManyShape<D, EXACT>::kThreads, 1) kv4_many_ker
         const uint4 c = x[i].codes;
         const __half2 f = *reinterpret_cast<const __half2*>(&az);
         const uint32_t row = tile + (uint32_t)(i * 4 * S::kPerWarp * 128);
-        if (EXACT && !is_v) {
+        if (!is_v && two_parts) {
           const float2 az32 = __half22float2(f);
           const uint32_t words[4] = {c.x, c.y, c.z, c.w};
 #pragma unroll
@@ -391,10 +424,10 @@ __global__ void __launch_bounds__(ManyShape<D, EXACT>::kThreads, 1) kv4_many_ker
     auto one_step = [&](int j, Piece (&now)[S::kPasses], Piece (&next)[S::kPasses]) {
       load(next, j + 1);
       if (at.round > 0 && !(ok = wait(empty + 8u * at.slot, at.round - 1))) return;
-      store(tiles_at + (uint32_t)at.slot * (is_v ? 1 : S::kKParts) * S::kKvTile, mask + (j & 7) * S::kWords, now);
+      store(tiles_at + (uint32_t)at.slot * (is_v ? S::kKvTile : k_step), mask + (j & 7) * S::kWords, now);
       __syncwarp();
       if (lane == 0) mbar_arrive_cta(full + 8u * at.slot);
-      at.step(is_v ? S::kVBufs : S::kKBufs);
+      at.step(is_v ? v_bufs : k_bufs);
     };
     load(x[0], 0);
     for (int j = 0; j < steps && ok; j += 2) {

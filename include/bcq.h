@@ -548,15 +548,29 @@ size_t bcq_kv4_attention_workspace_bytes(const bcq_kv4* cache, int T, int q_head
  *   max_q   no sequence has more rows than this in the call (rows behind it
  *           are left as they were, and BCQ_ERR_SHAPE is recorded).
  *   max_kv  the plan's guess at the longest kv_len, 1..; longer ones are
- *           computed all the same.
+ *           computed all the same.  Like T, max_q and the sizes it decides
+ *           between a kernel for few rows and one for many, whose roundings
+ *           differ (below).
  *   scale   a finite factor.
  *   workspace, workspace_bytes
  *           device, bcq_kv4_attention_workspace_bytes(..) bytes, 16-byte
  *           aligned (NULL allowed when that is 0); needs no initial value and
  *           keeps none.  Calls that may run at the same time need workspaces
  *           of their own.
- * Scores, sums and outputs are fp32 until the last rounding.  Results do not
- * depend on scheduling.
+ * Scores, maxima, sums and outputs are fp32 until the last rounding; what the
+ * products take is 16 bits wide:
+ *   weights p, rounded to fp16 (half a step, 2^-11 of each; a weight below 2^-21
+ *   of its row's largest, by up to 2^-32 of that);
+ *   with few rows a key/value head (always up to 16, decode steps and drafts
+ *   among them): p times V's scale, once more to fp16; scores are products of
+ *   exact operands;
+ *   with many: V's values a c + z, to fp16; K's too, in two parts (2^-22) for
+ *   rows that see fewer than 512 positions and for those beside them in a block
+ *   of 256 (128 with D = 256), so only a row that sees 512 or more has scores
+ *   that are off by up to 2^-11 of |scale| sum_d |q_d K_jd|.
+ * An output is then off by about 2^-10 of sum_j p_j |V_j|, lse by the scores'
+ * error, averaged over the positions that weigh.  Results do not depend on
+ * scheduling.
  * Errors as for bcq_kv4_append; a scale that is not finite -> BCQ_ERR_SHAPE.
  */
 bcq_status bcq_kv4_attention(const bcq_kv4* cache, const void* q, int64_t ld_q, int64_t hd_q,

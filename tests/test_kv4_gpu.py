@@ -957,3 +957,19 @@ def test_waits_that_run_out_are_reported(B, n, L, H, heads, D, hint):
         assert given_up
     finally:
         api.debug_impatient(False)
+
+
+@pytest.mark.parametrize("D,H,heads", [(64, 4, 1), (128, 8, 2), (256, 4, 2)])
+@pytest.mark.parametrize("lens,new", [([700], [700]), ([1500, 40, 300], [200, 40, 150])])
+@pytest.mark.parametrize("kw", [dict(), dict(window=400), dict(causal=False)])
+def test_rows_that_see_few_positions_have_exact_scores(D, H, heads, lens, new, kw):
+    """The kernel of many rows, whatever the call's other rows and its hint are: keys in two fp16 parts, 2^-22."""
+    c = Case(lens, new, heads, D, 16, seed=D)
+    q = _queries(c.T, H, D, F16, seed=4)
+    _, lse = _run(c, q, max_q=5000, max_kv=4000, **kw)
+    _, rl, m = kv4.attention(_f64(q), *(c.arrays[x] for x in ("k", "k_param", "v", "v_param")), c.table, c.lens, c.cu,
+                             float(np.float32(D ** -0.5)), kw.get("causal", True), kw.get("window", 0))
+    ds = m["s"] * (2.0 ** -22 + 4 * D * E) + 16 * E * (1 + m["s"])
+    few = np.concatenate([[kv4.visible(n, r, i, **kw).sum() < 512 for i in range(r)] for n, r in zip(lens, new)])
+    err = np.abs(_f64(lse) - rl)
+    assert (err <= ds + 4 * 512 * E + 2 * E * np.abs(rl))[few].all(), f"{err[few].max():.1e} of {ds[few].max():.1e}"
