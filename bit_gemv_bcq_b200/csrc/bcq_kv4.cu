@@ -639,7 +639,7 @@ __global__ void __launch_bounds__(kFewWarps * 32, NT == 1 && D <= 128 ? 4 : 2) k
   auto look_up = [&](int s) {   // page table entries of stages s .. s + 15
     const int j = begin + ((s + (lane >> 1)) * kFewWarps + warp) * kFewTokens + (lane & 1) * 16;
     vecs = 0xFFFFFFFFu;
-    if (j < end) {
+    if (j < end && j + 16 > sp.seen) {  // (a page in front of every row's window need not be there)
       const int64_t vec = vector_at(p.at, b, j, kvh);
       if (vec >= 0) vecs = (uint32_t)vec;
       else record_error(&g_kv4_error, BCQ_ERR_PAGE);

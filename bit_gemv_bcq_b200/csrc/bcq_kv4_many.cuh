@@ -352,7 +352,7 @@ __global__ void __launch_bounds__(ManyShape<D>::kThreads, 1) kv4_many_kernel(con
       const int at = begin + (j + lane / S::kPasses) * S::kTokens +
                      (lane % S::kPasses * 4 + w) * S::kPerWarp;
       vecs = kNone;
-      if (at < end) {
+      if (at < end && at + S::kPerWarp > sp.seen) {  // (a page in front of every row's window need not be there)
         const int64_t found = vector_at(p.at, b, at, kvh);
         vecs = (uint32_t)found;
         if (found < 0) record_error(&g_kv4_error, BCQ_ERR_PAGE);

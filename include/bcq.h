@@ -536,7 +536,8 @@ size_t bcq_kv4_attention_workspace_bytes(const bcq_kv4* cache, int T, int q_head
  * with the key/value head h / (q_heads / heads) and j over the positions
  * 0..kv_len-1 of t's sequence, those that the masks leave: with causal != 0 j
  * <= pos(t) = kv_len - n + i, and with window > 0 j > pos(t) - window.  A row
- * that nothing is left for gives zeros (and lse -infinity).
+ * that nothing is left for gives zeros (and lse -infinity).  Pages that lie whole
+ * in front of every row's window are not looked at and may be gone.
  *
  *   q       device, [T][q_heads][D] of `dtype` (BCQ_F16 or BCQ_BF16), rows
  *           ld_q and heads hd_q elements apart; base 16-byte aligned,

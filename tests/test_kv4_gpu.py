@@ -973,3 +973,22 @@ def test_rows_that_see_few_positions_have_exact_scores(D, H, heads, lens, new, k
     few = np.concatenate([[kv4.visible(n, r, i, **kw).sum() < 512 for i in range(r)] for n, r in zip(lens, new)])
     err = np.abs(_f64(lse) - rl)
     assert (err <= ds + 4 * 512 * E + 2 * E * np.abs(rl))[few].all(), f"{err[few].max():.1e} of {ds[few].max():.1e}"
+
+
+@pytest.mark.parametrize("new,max_q", [(1, 1), (6, 6), (140, 140), (1, 5000), (140, 5000)])
+@pytest.mark.parametrize("D", [64, 128, 256])
+def test_pages_in_front_of_every_window_may_be_gone(new, max_q, D):
+    """A table whose entries before the first row's window are no pages: nothing to record, and the same bits."""
+    lens = [75 + new, 190 + new, 17 + new, 49 + new]
+    c = Case(lens, [new] * 4, 2, D, 16)
+    q = _queries(c.T, 8, D, F16)
+    for window in (1, 16, 20, 33):
+        ref, ref_lse = _run(c, q, 4000, max_q=max_q, window=window)
+        assert api.device_error() == api.BCQ_OK
+        t = c.t_table.clone()
+        for b, n in enumerate(lens):
+            t[b, :max(0, n - new - window + 1) // 16] = -1
+        out, lse = api.kv4_attention(q, c.cache, t, c.t_len, c.t_cu, max_q=max_q, max_kv=4000, window=window,
+                                     return_lse=True)
+        assert api.device_error() == api.BCQ_OK, window
+        assert torch.equal(out, ref) and torch.equal(lse, ref_lse), window
