@@ -474,7 +474,9 @@ __global__ void __launch_bounds__(ManyShape<D>::kThreads, 1) kv4_many_kernel(con
       }
       const float top = bits_to_float<T>(max(top2 & 0xFFFFu, top2 >> 16));  // not finite: power 0
       const int up = row_power(top);
-      const float mul = p.scale < 0.f ? -power_of_two(up) : p.scale == 0.f ? 0.f : power_of_two(up);
+      // (a row with an infinity or a NaN is NaN, also where all of its scores were -infinity)
+      const float mul = !(top < INFINITY) ? __uint_as_float(0x7FC00000u)
+                        : p.scale < 0.f ? -power_of_two(up) : p.scale == 0.f ? 0.f : power_of_two(up);
       fs = score_factor(p.scale, -up);
       const uint32_t to = sbase + (uint32_t)t * S::kQTile + (uint32_t)r * 128u;
 #pragma unroll

@@ -552,7 +552,9 @@ size_t bcq_kv4_attention_workspace_bytes(const bcq_kv4* cache, int T, int q_head
  *           computed all the same.  Like T, max_q and the sizes it decides
  *           between a kernel for few rows and one for many, whose roundings
  *           differ (below).
- *   scale   a finite factor.
+ *   scale   a finite factor.  A row of q with an infinity or a NaN gives NaN;
+ *           one whose largest |q| times |scale| passes 2^100 (scores beyond
+ *           fp32) has results of no meaning.
  *   workspace, workspace_bytes
  *           device, bcq_kv4_attention_workspace_bytes(..) bytes, 16-byte
  *           aligned (NULL allowed when that is 0); needs no initial value and

@@ -992,3 +992,21 @@ def test_pages_in_front_of_every_window_may_be_gone(new, max_q, D):
                                      return_lse=True)
         assert api.device_error() == api.BCQ_OK, window
         assert torch.equal(out, ref) and torch.equal(lse, ref_lse), window
+
+
+@pytest.mark.parametrize("new,max_q", [(1, 1), (40, 40), (40, 5000)])
+@pytest.mark.parametrize("scale", [0.1, -0.1, 0.0])
+@pytest.mark.parametrize("D", [64, 128, 256])
+def test_rows_with_an_infinity_are_nan(new, max_q, scale, D):
+    """Also where every score is -infinity: that is no row which sees nothing."""
+    c = Case([new], [new], 1, D, 16)
+    c.cache.k_param[..., 0], c.cache.k_param[..., 1] = 0, 1      # K is 1
+    c.cache.v_param.nan_to_num_()
+    q = _queries(new, 4, D, F16)
+    ref, ref_lse = _run(c, q, 4000, max_q=max_q, scale=scale)
+    q[0, 1, 3], q[0, 2, 5], q[-1, 3, D - 1] = float("-inf"), float("inf"), float("-inf")
+    out, lse = _run(c, q, 4000, max_q=max_q, scale=scale)
+    odd = torch.zeros(new, 4, dtype=torch.bool)
+    odd[0, 1] = odd[0, 2] = odd[-1, 3] = True
+    assert torch.isnan(out[odd]).all() and torch.isnan(lse[odd]).all()
+    assert torch.equal(out[~odd], ref[~odd]) and torch.equal(lse[~odd], ref_lse[~odd])
