@@ -485,7 +485,7 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
       umma_fence_after();
       if (quarter * each < p.R) {
         const int c_first = half * split, c_end = half ? cols : min(cols, split);
-        TO* y = static_cast<TO*>(p.y) + (int64_t)(m0 + c_first) * p.ldy + n;
+        TO* y = static_cast<TO*>(p.y) + ((int64_t)m0 + c_first) * p.ldy + n;
         const uint32_t acc = tmem + (uint32_t)(buf * p.issuers * p.BT) + ((uint32_t)(quarter * 32) << 16);
         for (int c = c_first; c < c_end; c += 16) {
           uint32_t v[16];
@@ -616,7 +616,8 @@ bool encode_codes(CUtensorMap* map, const int8_t* p, int64_t rows, int64_t K, in
            CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-int round_up(int v, int to) { return (v + to - 1) / to * to; }
+int64_t ceil_div(int64_t v, int64_t by) { return (v + by - 1) / by; }
+int round_up(int64_t v, int to) { return (int)(ceil_div(v, to) * to); }
 
 // The tile and the kernel (*kind: 0 single CTAs, 1 pairs, 2 pairs with two
 // instructions along x's rows) that a model of one SM's time likes
@@ -635,21 +636,24 @@ int round_up(int v, int to) { return (v + to - 1) / to * to; }
 void plan_gemm(int M, int N, int K, int sms, GemmParams* p, size_t* smem, int* grid, int* kind) {
   const int KB = (K + (int)kKBlock - 1) / (int)kKBlock;
   double best = 0;
-  const int mt0 = (M + 255) / 256;
   for (int two = 0; two < 2; ++two) {
     const int workers = two ? sms / 2 : sms;
     for (int subs = 1; subs <= 1 + two; ++subs) {
-      for (int mt = (M + 256 * subs - 1) / (256 * subs); mt <= mt0 + 4; ++mt) {
-        const int BS = round_up((M + mt * subs - 1) / (mt * subs), two ? 32 : 16), BT = subs * BS;
-        if ((int64_t)BT * (mt - 1) >= M || (two && BS < 64) || (subs == 2 && BS < 128) || BS > 256) continue;
+      // every BS that is the least for its number of tiles, up to four more of them
+      // than whole ones would be
+      const int step = two ? 32 : 16, least_bs = subs == 2 ? 128 : two ? 64 : 16;
+      for (int BS = std::min(256, round_up(ceil_div(M, subs), step)); BS >= least_bs; BS -= step) {
+        const int BT = subs * BS;
+        const int64_t mt = ceil_div(M, BT);
+        if (BS != round_up(ceil_div(M, mt * subs), step) || mt > ceil_div(M, 256) + 4) continue;
         const int rows_most = two ? 256 : 128;
-        const int64_t least = ((int64_t)(N + rows_most - 1) / rows_most * mt + workers - 1) / workers;
+        const int64_t least = ceil_div(ceil_div(N, rows_most) * mt, workers);
         for (int64_t rounds = least; rounds <= least + 2; ++rounds) {
           const int64_t nt_most = std::max<int64_t>(1, rounds * workers / mt);
-          int64_t rows = std::min<int64_t>(rows_most, std::max<int64_t>(8, (N + nt_most - 1) / nt_most));
+          int64_t rows = std::min<int64_t>(rows_most, std::max<int64_t>(8, ceil_div(N, nt_most)));
           if (two) rows = (rows + 1) / 2 * 2;
           const int R = (int)(two ? rows / 2 : rows);
-          const int64_t nt = (N + rows - 1) / rows, tiles = nt * mt, whole = (tiles + workers - 1) / workers;
+          const int64_t nt = ceil_div(N, rows), tiles = nt * mt, whole = ceil_div(tiles, workers);
           const int BX = two ? BS / 2 : BS;
           const double core = 4.0 * subs * std::max(BS / 2.0, 32.0 + BX / 4.0);
           const double l2 = 128.0 * (R + subs * BX) / 50.0, dram = mt == 1 ? 128.0 * R / 24.0 : 0;
@@ -664,7 +668,7 @@ void plan_gemm(int M, int N, int K, int sms, GemmParams* p, size_t* smem, int* g
             *kind = two + subs - 1;
             p->BS = BS;
             p->BX = BX;
-            p->mt = mt;
+            p->mt = (int)mt;
             p->tiles = (int)tiles;
             p->workers = (int)std::min<int64_t>(workers, tiles);
           }

@@ -329,3 +329,20 @@ def test_waits_that_run_out_are_reported(M, N, K):
         assert given_up
     finally:
         api.debug_impatient(False)
+
+
+@pytest.mark.parametrize("N", [1, 3])
+def test_as_many_rows_as_an_int_counts(N):
+    M, K = 2 ** 31 - 1, 9
+    if torch.cuda.mem_get_info()[0] + torch.cuda.memory_reserved() < 80 << 30:
+        pytest.skip("needs 80 GB")
+    x = torch.empty(M, 16, dtype=torch.int8, device="cuda").random_(-127, 128)[:, :K]
+    sx = torch.empty(M, device="cuda").uniform_(1e-3, 1e-2)
+    w, sw = _codes(N, K, 2)
+    y = api.gemm_i8(x, sx, w, sw)
+    assert api.device_error() == api.BCQ_OK
+    for part in (slice(0, 5000), slice(M // 2, M // 2 + 5000), slice(M - 5000, M)):
+        ref = i8.gemm(_f64(x[part]), _f64(sx[part]), _f64(w), _f64(sw))
+        _check_product(y[part], ref, part)
+    del x, sx, y
+    torch.cuda.empty_cache()
