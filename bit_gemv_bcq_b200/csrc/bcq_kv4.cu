@@ -1277,22 +1277,37 @@ Places places_of(const bcq_kv4* c, const int32_t* table, int table_width, const 
           table_width * c->page_size, divisor(c->page_size)};
 }
 
-// f(D, rows a block) as compile-time numbers: one row while more would leave
-// SMs idle, else four, whose places are found and whose loads are in flight
-// together.  In and out of a cache of 8 heads of 128 (us, one | four rows a
-// block): 64 rows 2.8 + 2.4 | 3.9 + 2.6, 512 rows 3.6 + 3.0 | 4.1 + 2.7, 1024
-// rows 5.5 + 3.7 | 4.6 + 3.0, 8192 rows 30.2 + 17.7 | 17.5 + 10.0.
-// From 4096 rows on, several side by side in a block where one has no more than
-// half as many words as the block has threads (in + out, us, four rows | sets of
-// four: 2 heads of 64, 16384 rows 20.0 + 8.7 | 8.1 + 7.0, 4 heads of 128, 8192 rows
-// 13.2 + 6.7 | 10.6 + 7.3, a head of 128, 2048 rows 4.3 + 2.7 | 5.5 + 4.3).
+// How the rows of a call, in or out, are shared out: one row a block up to T =
+// `one`, else four, whose places are found and whose loads are in flight together;
+// from `side_by_side` rows on several fours in a block, where a row has no more
+// than `words` words (and a block so that it holds them).
+//
+// In (us, one | four rows a block): up to 592 rows all blocks of one row fit the
+// SMs at once, and a row waits for fewer loads (512 rows of 1, 8 heads of 128 and
+// 32 of 64: 3.2 | 3.8, 3.7 | 4.3, 5.2 | 6.1; 640 of the first two 4.5 | 4.1, 5.0 | 4.6,
+// 768 of the third 6.7 | 6.7).  Rows of four turns of the block's loop or more go on
+// to twice as many (32 heads of 128: 768 rows 10.2 | 10.9, 1024 11.2 | 11.1, 2048
+// 19.8 | 16.3; of 256: 1024 rows 18.7 | 19.1, 2048 37.6 | 30.8).
+// Out: 384 rows of 8 heads of 128, 32 of 64 and 32 of 128 2.9 | 2.8, 3.4 | 3.4, 4.4 |
+// 4.6, 512 rows 3.1 | 2.8, 3.6 | 3.4, 5.0 | 4.6.
+// Side by side (us, four rows | sets of four), in: 2048 rows of 2 heads of 64 or
+// 128 4.1 | 5.8, 4.4 | 4.8, 4096 rows 7.0 | 5.9, 6.9 | 5.6, of 8 heads of 64 7.6 | 6.5.
+// Out: 8192 rows of 2 heads of 64 or 128 5.1 | 4.8, 5.4 | 6.0, 12288 rows 6.9 | 5.5, 7.5 |
+// 6.3, of 8 heads of 64 8.9 | 9.4, 65536 rows 42.2 | 43.9.
+struct RowsRule {
+  int one, side_by_side, words;
+};
+RowsRule rows_in_rule(int words) { return {words >= 4 * kRowThreads ? 1184 : 592, 4096, kRowThreads / 2}; }
+RowsRule rows_out_rule() { return {444, 10240, kRowThreads / 4}; }
+
+// f(D, rows a block, whether side by side, blocks), the first three as compile-time
+// numbers; words: of a row's K and V.
 template <typename F>
-void by_shape(int D, int heads, int T, const F& f) {
-  const int sets = row_sets(2 * heads * (D / 8));
+void by_shape(int D, int words, int T, const RowsRule& rule, const F& f) {
   auto rows = [&](auto d) {
-    if (T < 768) f(d, std::integral_constant<int, 1>(), std::false_type(), T);
-    else if (sets == 1 || T < 4096) f(d, std::integral_constant<int, 4>(), std::false_type(), (T + 3) / 4);
-    else f(d, std::integral_constant<int, 4>(), std::true_type(), (T + 4 * sets - 1) / (4 * sets));
+    if (T <= rule.one) f(d, std::integral_constant<int, 1>(), std::false_type(), T);
+    else if (words > rule.words || T < rule.side_by_side) f(d, std::integral_constant<int, 4>(), std::false_type(), (T + 3) / 4);
+    else f(d, std::integral_constant<int, 4>(), std::true_type(), (T + 4 * row_sets(words) - 1) / (4 * row_sets(words)));
   };
   if (D == 64) rows(std::integral_constant<int, 64>());
   else if (D == 128) rows(std::integral_constant<int, 128>());
@@ -1470,7 +1485,8 @@ bcq_status bcq_kv4_append(const bcq_kv4* cache, const void* k, int64_t ld_k, int
                           T};
   cudaStream_t st = (cudaStream_t)stream;
   cudaError_t e = cudaSuccess;
-  by_shape(cache->head_dim, cache->heads, T, [&](auto d, auto rows, auto shared, int count) {
+  const int words = 2 * cache->heads * (cache->head_dim / 8);
+  by_shape(cache->head_dim, words, T, rows_in_rule(words), [&](auto d, auto rows, auto shared, int count) {
     constexpr int D = decltype(d)::value, kRows = decltype(rows)::value;
     constexpr bool kShared = decltype(shared)::value;
     const unsigned blocks = (unsigned)count;
@@ -1496,7 +1512,8 @@ bcq_status bcq_kv4_read(const bcq_kv4* cache, void* k, void* v, int dtype, int T
                         T};
   cudaStream_t st = (cudaStream_t)stream;
   cudaError_t e = cudaSuccess;
-  by_shape(cache->head_dim, cache->heads, T, [&](auto d, auto rows, auto shared, int count) {
+  const int words = 2 * cache->heads * (cache->head_dim / 8);
+  by_shape(cache->head_dim, words, T, rows_out_rule(), [&](auto d, auto rows, auto shared, int count) {
     constexpr int D = decltype(d)::value, kRows = decltype(rows)::value;
     constexpr bool kShared = decltype(shared)::value;
     const unsigned blocks = (unsigned)count;

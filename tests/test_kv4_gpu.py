@@ -1010,3 +1010,34 @@ def test_rows_with_an_infinity_are_nan(new, max_q, scale, D):
     odd[0, 1] = odd[0, 2] = odd[-1, 3] = True
     assert torch.isnan(out[odd]).all() and torch.isnan(lse[odd]).all()
     assert torch.equal(out[~odd], ref[~odd]) and torch.equal(lse[~odd], ref_lse[~odd])
+
+
+@pytest.mark.parametrize("heads,D", [(1, 64), (2, 128), (2, 256), (8, 128), (32, 128), (32, 256)])
+def test_rows_in_and_out_whatever_shares_a_block(heads, D):
+    """Each number of rows on both sides of where the kernels change: the same codes and values as 100 rows a call."""
+    most = 10300 if heads * D <= 256 else 4100 if heads * D <= 1024 else 1190
+    c, k, v = _append_case([most], [most], heads, D, 64, F16)
+    for i in range(0, most, 100):
+        r = slice(i, min(i + 100, most))
+        api.kv4_append(c.cache, k[r], v[r], c.t_table, _i32([r.stop]), _i32([0, r.stop - i]))
+    parts = ("k", "k_param", "v", "v_param")
+    want = {n: getattr(c.cache, n).clone() for n in parts}
+    ok, ov = (torch.cat(x) for x in zip(*(api.kv4_read(c.cache, c.t_table, _i32([min(i + 100, most)]),
+                                                      _i32([0, min(100, most - i)]), tokens=min(100, most - i))
+                                          for i in range(0, most, 100))))
+    for T in (444, 445, 592, 593, 1184, 1185, 4095, 4096, 10239, 10240, 10300):
+        if T > most:
+            continue
+        for n in parts:
+            getattr(c.cache, n).zero_()
+        api.kv4_append(c.cache, k[:T], v[:T], c.t_table, _i32([T]), _i32([0, T]))
+        for i in range(T, most, 100):                            # the rest, as before
+            r = slice(i, min(i + 100, most))
+            api.kv4_append(c.cache, k[r], v[r], c.t_table, _i32([r.stop]), _i32([0, r.stop - i]))
+        at = torch.arange(most, device="cuda")
+        page, pos = c.t_table[0].long()[at // 64], at % 64
+        for n in parts:
+            a, b = (x.view(torch.uint8)[page, :, pos] for x in (getattr(c.cache, n), want[n]))
+            assert torch.equal(a, b), (T, n)
+        rk, rv = api.kv4_read(c.cache, c.t_table, _i32([T]), _i32([0, T]), tokens=T)
+        assert torch.equal(rk, ok[:T]) and torch.equal(rv, ov[:T]), T
