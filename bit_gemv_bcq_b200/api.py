@@ -22,6 +22,7 @@ from __future__ import annotations
 import contextlib
 import ctypes
 import os
+import warnings
 from dataclasses import dataclass, field
 
 import numpy as np
@@ -607,13 +608,25 @@ _FAST_ENTRY_POINTS = ("bcq_quantize_i8", "bcq_gemm_i8", "bcq_linear_i8_workspace
 _fast_module = None
 
 
+class _NoFast:
+    """In place of the module where it is not built: leaves every call to the code here."""
+
+    def __getattr__(self, name):
+        return lambda *args: NotImplemented
+
+
 def _fast():
     """The module of the fast calls, bound to the library."""
     global _fast_module
     if _fast_module is None:
         L = lib()
-        from . import _fast as module
-        module.bind(*(ctypes.cast(getattr(L, n), ctypes.c_void_p).value for n in _FAST_ENTRY_POINTS))
+        try:
+            from . import _fast as module
+            module.bind(*(ctypes.cast(getattr(L, n), ctypes.c_void_p).value for n in _FAST_ENTRY_POINTS))
+        except ImportError as e:
+            warnings.warn(f"the binding's fast calls are missing ({e}): each call takes some microseconds more; "
+                          "`python bit_gemv_bcq_b200/build.py` builds them", RuntimeWarning, stacklevel=3)
+            module = _NoFast()
         _fast_module = module
     return _fast_module
 

@@ -5,15 +5,17 @@ Each translation unit of csrc/ is compiled to an object under _build/ (in
 parallel; an object is rebuilt only when its source or a header it includes
 changed), then the objects are linked.  The CUDA runtime is linked
 statically and its symbols are kept private to the library, so the
-process's other CUDA users (torch) are not affected.  The binding's fast
+process's other CUDA users (torch) are not affected.  Then the binding's fast
 calls (csrc/bcq_fast.cpp, a CPython module over torch's headers) become
-_fast.so next to it, with g++.
+_fast.so next to it, with g++, where torch, its headers, Python's and the
+compiler are there; the library and the binding work without.
 """
 from __future__ import annotations
 
 import glob
 import os
 import re
+import shutil
 import subprocess
 import sys
 from concurrent.futures import ThreadPoolExecutor
@@ -76,20 +78,31 @@ def _compile(nvcc: str, src: str, verbose: bool) -> str:
     return obj
 
 
-def build_fast(force: bool = False) -> str:
+def build_fast(force: bool = False) -> str | None:
     """_fast.so against the torch of this interpreter (its headers and
-    libraries' names; nothing of it is loaded)."""
+    libraries' names; nothing of it is loaded).  None, and no module of an
+    older build, where something that it takes is missing."""
     import importlib.util
     import sysconfig
-    torch_dir = os.path.dirname(importlib.util.find_spec("torch").origin)
+    spec = importlib.util.find_spec("torch")
+    torch_dir = os.path.dirname(spec.origin) if spec and spec.origin else ""
+    python_h = os.path.join(sysconfig.get_paths()["include"], "Python.h")
+    cxx = os.environ.get("CXX", "g++")
+    for what, there in (("torch", torch_dir), ("torch's headers", os.path.isdir(os.path.join(torch_dir, "include"))),
+                        (python_h, os.path.exists(python_h)), (cxx, shutil.which(cxx.split()[0]))):
+        if not there:
+            print(f"{os.path.basename(FAST)} is left out: no {what}", file=sys.stderr)
+            if os.path.exists(FAST):
+                os.unlink(FAST)
+            return None
     version = os.path.join(torch_dir, "version.py")
     if force or _stale(FAST, [FAST_SRC, os.path.join(INCLUDE, "bcq.h"), version]):
         cuda = os.environ.get("CUDA_HOME", "/usr/local/cuda")
         inc = [os.path.join(torch_dir, "include"),
                os.path.join(torch_dir, "include", "torch", "csrc", "api", "include"),
-               os.path.join(cuda, "include"), sysconfig.get_paths()["include"], INCLUDE]
+               os.path.join(cuda, "include"), os.path.dirname(python_h), INCLUDE]
         tmp = FAST + f".tmp{os.getpid()}"
-        subprocess.run([os.environ.get("CXX", "g++"), "-O2", "-std=c++17", "-fPIC", "-shared", "-w",
+        subprocess.run([*cxx.split(), "-O2", "-std=c++17", "-fPIC", "-shared", "-w",
                         *[f"-I{d}" for d in inc], FAST_SRC, "-o", tmp,
                         "-L" + os.path.join(torch_dir, "lib"), "-lc10", "-lc10_cuda", "-ltorch_cpu",
                         "-ltorch_cuda", "-ltorch_python"], check=True)
@@ -98,7 +111,6 @@ def build_fast(force: bool = False) -> str:
 
 
 def build(force: bool = False, verbose: bool = False) -> str:
-    build_fast(force)
     nvcc = os.environ.get("NVCC", "nvcc")
     os.makedirs(OBJ, exist_ok=True)
     srcs = sources()
@@ -111,6 +123,7 @@ def build(force: bool = False, verbose: bool = False) -> str:
         tmp = LIB + f".tmp{os.getpid()}"
         subprocess.run([nvcc, *ARCH, *LFLAGS, "-shared", "-o", tmp, *objs], check=True)
         os.replace(tmp, LIB)
+    build_fast(force)
     return LIB
 
 

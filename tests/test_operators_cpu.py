@@ -326,3 +326,34 @@ def test_impatience_is_a_switch():
     L = api.lib()
     assert L.bcq_debug_impatient(2) == api.BCQ_ERR_SHAPE and L.bcq_debug_impatient(-1) == api.BCQ_ERR_SHAPE
     assert L.bcq_debug_impatient(1) == api.BCQ_OK and L.bcq_debug_impatient(0) == api.BCQ_OK
+
+
+def test_the_library_is_built_without_torch_or_a_compiler(monkeypatch, tmp_path, capsys):
+    """The fast calls' module is left out, one of an older build with it; libbcq.so is not."""
+    import importlib.util
+    fast = tmp_path / "_fast.so"
+    monkeypatch.setattr(libbuild, "FAST", str(fast))
+    find = importlib.util.find_spec
+    for change in ("torch", "compiler"):
+        fast.write_bytes(b"old")
+        with monkeypatch.context() as m:
+            if change == "torch":
+                m.setattr(importlib.util, "find_spec", lambda name, *a: None if name == "torch" else find(name, *a))
+            else:
+                m.setenv("CXX", str(tmp_path / "no-such-compiler"))
+            assert libbuild.build() == libbuild.LIB
+        assert not fast.exists() and "left out" in capsys.readouterr().err
+
+
+def test_the_binding_works_without_the_fast_calls(monkeypatch, L):
+    import sys
+    import bit_gemv_bcq_b200 as package
+    monkeypatch.setattr(api, "_fast_module", None)
+    monkeypatch.setitem(sys.modules, "bit_gemv_bcq_b200._fast", None)
+    monkeypatch.delattr(package, "_fast", raising=False)
+    with pytest.warns(RuntimeWarning, match="fast calls"):
+        f = api._fast()
+    assert f.quantize_i8(1) is NotImplemented and f.kv4_append(1, 2) is NotImplemented
+    assert api._fast() is f
+    with pytest.raises(ValueError, match="CUDA tensor"):       # the longer way refuses as ever
+        api.quantize_i8(torch.zeros(2, 16, dtype=torch.float16))
