@@ -5,9 +5,11 @@
 // need nothing special: tensors of one CUDA device, which is the current one,
 // on its current stream, in shapes and distances that the library takes.  For
 // anything else, a call that is to be refused among it, it does nothing and
-// returns NotImplemented, and api.py goes on.  So what is accepted and what is
-// raised is written down there alone; here a call of kv4_attention takes half
-// the host's time (its smallest takes less than that on the GPU).
+// returns NotImplemented, and api.py goes on and raises what there is to raise.
+// What a usual call is, is checked here once more: a check that api.py gains or
+// loses has its counterpart below (test_both_ways_refuse_the_same_calls compares
+// them).  A call of kv4_attention takes half the host's time here (its smallest
+// takes less than that on the GPU).
 //
 // The library is not linked: api.py hands over its entry points' addresses.
 #include <ATen/ATen.h>

@@ -1041,3 +1041,63 @@ def test_rows_in_and_out_whatever_shares_a_block(heads, D):
             assert torch.equal(a, b), (T, n)
         rk, rv = api.kv4_read(c.cache, c.t_table, _i32([T]), _i32([0, T]), tokens=T)
         assert torch.equal(rk, ok[:T]) and torch.equal(rv, ov[:T]), T
+
+
+def test_both_ways_refuse_the_same_calls():
+    """The fast calls' own checks let nothing through that the binding's longer way refuses."""
+    h, f32, i8 = torch.float16, torch.float32, torch.int8
+    Z = lambda *n, dtype=h: torch.zeros(*n, dtype=dtype, device="cuda")          # noqa: E731
+    c = Case([40, 70], [2, 3], 2, 128, 16)
+    cache, tab, n, cu = c.cache, c.t_table, c.t_len, c.t_cu
+    q, k = Z(5, 8, 128), Z(5, 2, 128)
+    x8, s8, w8, t8 = Z(4, 64, dtype=i8), Z(4, dtype=f32), Z(6, 64, dtype=i8), Z(6, dtype=f32)
+    wide = Z(9, 1100)
+
+    def att(q=q, t=tab, n=n, cu=cu, **kw):
+        return lambda **s: api.kv4_attention(q, cache, t, n, cu, **kw, **s)
+
+    def app(k=k, v=k, t=tab, n=n, cu=cu):
+        return lambda **s: api.kv4_append(cache, k, v, t, n, cu, **s)
+
+    def read(t=tab, n=n, cu=cu, **kw):
+        return lambda **s: api.kv4_read(cache, t, n, cu, **kw, **s)
+
+    def gemm(x=x8, s=s8, w=w8, t=t8, **kw):
+        return lambda **st: api.gemm_i8(x, s, w, t, **kw, **st)
+
+    def lin(x=Z(4, 64), w=w8, t=t8, **kw):
+        return lambda **st: api.linear_i8(x, w, t, **kw, **st)
+
+    bad = [
+        att(q=q.float()), att(q=q[:, :, :64]), att(q=q[0]), att(q=Z(5, 7, 128)), att(q=Z(5, 0, 128)), att(q=Z(4, 8, 130)[:, :, 1:129]),
+        att(q=wide[:5, 3:1027].view(5, 8, 128)), att(q=Z(128, 8, 5).permute(2, 1, 0)), att(q=Z(5, 512, 128)), att(cu=None),
+        att(t=tab.long()), att(t=tab[0]), att(t=tab.t()), att(t=tab[:, :0]), att(n=n.long()), att(n=n[:1]), att(n=n[None]),
+        att(cu=cu[:2]), att(cu=cu.long()), att(max_q=0), att(max_kv=0), att(max_q=-1), att(window=-1), att(max_q=2 ** 31),
+        att(max_kv=2 ** 32 + 1), att(window=2 ** 33), att(scale=float("nan")), att(scale=float("inf")), att(scale=1e300),
+        att(max_q=1.5), att(t=tab.cpu()), att(cu=cu.cpu()),
+        app(k=k.float()), app(v=k.bfloat16()), app(v=k[:4]), app(k=Z(5, 3, 128)), app(k=k[..., :64], v=k[..., :64]), app(cu=None),
+        app(k=Z(5, 2, 129)[..., :128]), app(t=tab.long()), app(n=n[:1]),
+        read(tokens=5, dtype=torch.int8), read(), read(tokens=-1), read(cu=None, tokens=5), read(tokens=5, t=tab[0]),
+        gemm(x=x8[:, :60]), gemm(x=x8.half()), gemm(w=w8[:, :48]), gemm(s=s8[:3]), gemm(s=s8.half()), gemm(t=t8[None]),
+        gemm(x=Z(4, 72, dtype=i8)[:, 8:]), gemm(x=Z(4, 72, dtype=i8)[:, :64]), gemm(x=x8[:1].expand(4, 64)), gemm(dtype=torch.int8),
+        gemm(out=Z(4, 5)), gemm(out=Z(4, 6, dtype=f32)), gemm(out=Z(6, 4).t()), gemm(out=Z(1, 6).expand(4, 6)),
+        lin(x=Z(4, 64, dtype=f32)), lin(x=Z(4, 63)), lin(x=Z(64, 4).t()), lin(x=Z(64)), lin(out=Z(4, 6, dtype=f32)), lin(t=t8[:5]),
+        lambda **s: api.quantize_i8(Z(4, 64, dtype=f32), **s), lambda **s: api.quantize_i8(Z(64, 4).t(), **s),
+        lambda **s: api.quantize_i8(Z(4, 0), **s), lambda **s: api.quantize_i8(Z(2, 65537), **s),
+        lambda **s: api.quantize_i8(Z(1, 8).expand(3, 8), **s),
+    ]
+    st = torch.cuda.current_stream()
+    for i, call in enumerate(bad):
+        raised = []
+        for kw in ({}, {"stream": st}):
+            try:
+                call(**kw)
+                raised.append(None)
+            except Exception as e:
+                raised.append((type(e), str(e)))
+        assert raised[0] == raised[1], (i, raised)
+        if raised[0] is None:            # taken by both: the same bits
+            a, b = call(), call(stream=st)
+            for x, y in zip(*((z if isinstance(z, tuple) else (z,)) for z in (a, b))):
+                assert x is None or torch.equal(x.contiguous().view(torch.uint8), y.contiguous().view(torch.uint8)), i
+    assert api.device_error() == api.BCQ_OK
