@@ -100,9 +100,6 @@ __device__ __forceinline__ float4 lds_f32x4(uint32_t addr) {
   return v;
 }
 
-__device__ __forceinline__ void prefetch_tensormap(const CUtensorMap* map) {
-  asm volatile("prefetch.tensormap [%0];" ::"l"(map) : "memory");
-}
 __device__ __forceinline__ void sts_cluster(uint32_t cluster_addr, uint32_t v) {
   asm volatile("st.shared::cluster.u32 [%0], %1;" ::"r"(cluster_addr), "r"(v) : "memory");
 }
@@ -286,7 +283,7 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
   const uint32_t full = sbase + p.bar_off, empty = full + 8u * S, accfull = empty + 8u * S,
                  accempty = accfull + 16u, drain = accempty + 16u, slot = drain + 32u,
                  failed = slot + 4u, sx_off = slot + 16u;
-  if (warp <= 1 && lane == 0) prefetch_tensormap(warp == 0 ? &wmap : &xmap);
+  if (warp <= 1 && lane == 0) tma_prefetch_map(warp == 0 ? &wmap : &xmap);
   if (warp == 0) {
     for (int i = lane; i < S; i += 32) {
       mbar_init(full + 8u * i, 2);
