@@ -667,6 +667,15 @@ def _new(like: torch.Tensor, shape, dtype, stream) -> torch.Tensor:
     return t
 
 
+def _hold(stream, *tensors) -> None:
+    """A call on `stream` (not None) uses these: their memory is not handed out
+    again before it has ended, though its owner may let go of them at once."""
+    if stream is not None:
+        for t in tensors:
+            if t is not None:
+                t.record_stream(stream)
+
+
 def _need_matrix(t: torch.Tensor, name: str, dtypes, index=None) -> int:
     """A CUDA matrix of one of `dtypes` (on device `index`) whose rows are
     contiguous; returns the distance of its rows in elements."""
@@ -734,6 +743,7 @@ def quantize_i8(x: torch.Tensor, stream=None):
     scale = _new(x, (M,), torch.float32, stream)
     _run("bcq_quantize_i8", index, x.data_ptr(), _DTYPES[x.dtype], M, K, ldx, q.data_ptr(), ldq,
          scale.data_ptr(), st)
+    _hold(stream, x)
     return (q if ldq == K else q[:, :K]), scale
 
 
@@ -761,6 +771,7 @@ def gemm_i8(x: torch.Tensor, x_scale: torch.Tensor, w: torch.Tensor, w_scale: to
     st = _raw_stream(stream, index)
     _run("bcq_gemm_i8", index, x.data_ptr(), ldx, x_scale.data_ptr(), w.data_ptr(), ldw,
          w_scale.data_ptr(), M, N, K, out.data_ptr(), _DTYPES[dtype], ldy, st)
+    _hold(stream, x, x_scale, w, w_scale, out)
     return out
 
 
@@ -787,6 +798,7 @@ def linear_i8(x: torch.Tensor, w: torch.Tensor, w_scale: torch.Tensor,
     ws = _new(x, (need,), torch.uint8, stream)
     _run("bcq_linear_i8", index, x.data_ptr(), _DTYPES[x.dtype], ldx, w.data_ptr(), ldw,
          w_scale.data_ptr(), M, N, K, out.data_ptr(), ldy, ws.data_ptr(), need, st)
+    _hold(stream, x, w, w_scale, out)
     return out
 
 
@@ -847,6 +859,9 @@ class Kv4Cache:
     @property
     def heads(self) -> int:
         return self.k.shape[1]
+
+    def _tensors(self):
+        return self.k, self.k_param, self.v, self.v_param
 
     def _c(self):
         """(reference to the library's struct, heads, page_size, D); the
@@ -918,6 +933,7 @@ def kv4_append(cache: Kv4Cache, k: torch.Tensor, v: torch.Tensor, table: torch.T
     B, W, p_table, p_len, p_cu = _need_places(table, kv_len, cu, T, index)
     _run("bcq_kv4_append", index, c, k.data_ptr(), ldk, hdk, v.data_ptr(), ldv, hdv,
          _DTYPES[k.dtype], T, p_table, W, p_len, p_cu, B, _raw_stream(stream, index))
+    _hold(stream, *cache._tensors(), k, v, table, kv_len, cu)
 
 
 def kv4_read(cache: Kv4Cache, table: torch.Tensor, kv_len: torch.Tensor,
@@ -953,6 +969,7 @@ def kv4_read(cache: Kv4Cache, table: torch.Tensor, kv_len: torch.Tensor,
                 raise ValueError(f"{name} must be {list(shape)} on cuda:{index}, 16-byte aligned")
     _run("bcq_kv4_read", index, c, k.data_ptr(), v.data_ptr(), _DTYPES[dtype], T, p_table, W, p_len,
          p_cu, B, _raw_stream(stream, index))
+    _hold(stream, *cache._tensors(), k, v, table, kv_len, cu)
     return k, v
 
 
@@ -1006,6 +1023,7 @@ def kv4_attention(q: torch.Tensor, cache: Kv4Cache, table: torch.Tensor, kv_len:
          D ** -0.5 if scale is None else scale, out.data_ptr(), ldo, hdo,
          None if lse is None else lse.data_ptr(), None if ws is None else ws.data_ptr(), need,
          _raw_stream(stream, index))
+    _hold(stream, *cache._tensors(), q, table, kv_len, cu, out)
     return (out, lse) if return_lse else out
 
 

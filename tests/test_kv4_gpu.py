@@ -1101,3 +1101,45 @@ def test_both_ways_refuse_the_same_calls():
             for x, y in zip(*((z if isinstance(z, tuple) else (z,)) for z in (a, b))):
                 assert x is None or torch.equal(x.contiguous().view(torch.uint8), y.contiguous().view(torch.uint8)), i
     assert api.device_error() == api.BCQ_OK
+
+
+def test_tensors_let_go_at_once_outlive_a_call_on_another_stream():
+    """Inputs that nobody holds when a call on a side stream returns: their memory is not written over before it runs."""
+    side = torch.cuda.Stream()
+    c, k, v = _append_case([40, 70], [5, 70], 2, 128, 16, F16)
+    q, x = _queries(75, 8, 128, F16), _queries(75, 4, 128, F16).view(75, 512)
+    w, ws = api.quantize_i8(torch.randn(384, 512, device="cuda").half())
+    codes, scale = api.quantize_i8(x)
+    parts = lambda: [getattr(c.cache, n) for n in ("k", "k_param", "v", "v_param")]   # noqa: E731
+    places = [c.t_table, c.t_len, c.t_cu]
+    before = [t.clone() for t in parts()]
+    api.kv4_append(c.cache, k, v, *places)
+    after = [t.clone() for t in parts()]
+    calls = [(lambda q, *t, **s: api.kv4_attention(q, api.Kv4Cache(*t[:4]), *t[4:], max_q=70, **s), [q, *after, *places]),
+             (lambda *t, **s: api.kv4_read(api.Kv4Cache(*t[:4]), *t[4:], tokens=75, **s)[0], [*after, *places]),
+             (api.linear_i8, [x, w, ws]), (api.gemm_i8, [codes, scale, w, ws]),
+             (lambda x, **s: api.quantize_i8(x, **s)[0], [x])]
+    for i, (call, args) in enumerate(calls):
+        want = call(*args)
+        mine = [t.clone() for t in args]
+        sizes = sorted({t.numel() * t.element_size() for t in mine})
+        torch.cuda.synchronize()
+        with torch.cuda.stream(side):
+            torch.cuda._sleep(20_000_000)                                      # some 10 ms
+        y = call(*mine, stream=side)
+        del mine
+        junk = [torch.full((n,), 77, dtype=torch.uint8, device="cuda") for n in sizes for _ in range(4)]
+        torch.cuda.synchronize()
+        assert torch.equal(y, want), i
+        del junk
+    mine, into = [t.clone() for t in (k, v, *places)], [t.clone() for t in before]
+    torch.cuda.synchronize()
+    with torch.cuda.stream(side):
+        torch.cuda._sleep(20_000_000)
+    api.kv4_append(api.Kv4Cache(*into), *mine, stream=side)
+    sizes = sorted({t.numel() * t.element_size() for t in mine})
+    del mine
+    junk = [torch.full((n,), 77, dtype=torch.uint8, device="cuda") for n in sizes for _ in range(4)]
+    torch.cuda.synchronize()
+    assert all(torch.equal(a.view(torch.uint8), b.view(torch.uint8)) for a, b in zip(into, after))
+    assert api.device_error() == api.BCQ_OK
