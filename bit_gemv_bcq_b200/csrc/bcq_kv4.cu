@@ -1366,8 +1366,8 @@ float plan_parts(AttentionPlan* f, int64_t units, int max_kv, const PartsModel& 
 // positions, 15.0 in two), four CTAs an SM (two where rows or values are many),
 // with exact products of queries and codes; the many-row kernel once for every
 // 256 (128 where D = 256), with keys rounded to fp16, or, in the blocks of rows that
-// see few positions, in two parts, which takes 1.06 to 1.17 times as long (1.35 where
-// D = 256 leaves room for one set of them).  Calls that the second kernel is not thought to
+// see few positions, in two parts, which takes 1.05 to 1.15 times as long (1.2 to 1.35
+// where D = 256 leaves room for one set of them).  Calls that the second kernel is not thought to
 // save a seventh stay with the first.
 //
 // The models' numbers are fitted to 68 calls of the first (1 to 256 sequences,
@@ -1395,7 +1395,7 @@ AttentionPlan plan_attention(const bcq_kv4* c, int q_heads, int B, int max_q, in
     }
     const bool two = D != 256 && rows > 128;  // tiles
     const float per = (D == 64 ? (two ? 0.0209f : 0.0114f) : D == 128 ? (two ? 0.0254f : 0.0144f) : 0.023f) *
-                      (nt == 0 ? 1.f : D == 256 ? 1.35f : 1.12f);
+                      (nt == 0 ? 1.f : D == 256 ? 1.3f : 1.1f);
     const float out = 1e-6f * (float)B * (float)rows * (float)c->heads * (float)D;  // written and read for each part
     return plan_parts(f, units, seen, {1, ragged ? 0.6f : 1.f, per, 6.f, 5.3f, 1.87f * out, 0.66f});
   };

@@ -13,9 +13,9 @@
 // fewer than kFewSeen positions has K's in two parts (2^-22), which doubles the
 // products and their operands; a block of a prompt's later rows, or of a longer
 // sequence of the same call, has not (us, one part | two | the few-row kernel: 8
-// prompts of 200 to 400 new tokens, 32 heads of 128 on 8, 47.8 | 53.1 | 147; windows
+// prompts of 200 to 400 new tokens, 32 heads of 128 on 8, 48.0 | 52.0 | 147; windows
 // of 256 over 4 x 1000 new tokens, 16 heads of 64 on 4, 34.3 | 36.5 | 60.0; 8 x 100
-// rows over 400 positions, 16 heads of 256 on 4, 23.4 | 31.8 | 38.7).  One warp issues the
+// rows over 400 positions, 16 heads of 256 on 4, 22.9 | 30.5 | 38.7).  One warp issues the
 // products; four warps a tile do its softmax, a thread a row.  S has two
 // buffers a tile, so that a step's scores are there when the softmax of the
 // one before ends (steps of 128 positions leave tensor memory for one: the
@@ -37,8 +37,8 @@
 // where the tensor core needs 1280 (the exponentials alone 1024 of the special-
 // function units, the rest issue and the way to and from tensor memory), and the
 // last CTAs, which see the most.  2 x 2048 new tokens over their prompts, 32
-// heads of 128 on 8: 584 TFLOP/s; a chunk of 2048 over 4096, 16 heads of 256 on 4:
-// 681 TFLOP/s (of 1642 that a dense bf16 product reaches).
+// heads of 128 on 8: 561 TFLOP/s; a chunk of 2048 that ends at 4096, 16 heads of 256
+// on 4: 669 TFLOP/s (of 1642 that a dense bf16 product reaches).
 #pragma once
 
 #include "bcq_tcgen05.cuh"
@@ -54,7 +54,7 @@ struct ManyShape {
   static constexpr int kTokens = 64;                         // of a step
   // K's and V's operands share six tiles (four where D = 256): three buffers each,
   // or two of K's in two parts and two of V's.  (More shared memory leaves less
-  // to L1: with nine tiles 2 x 2048 new tokens took 228 us, 219 with six.)
+  // to L1: with nine tiles 2 x 2048 new tokens took 228 us, 220 with six.)
   static constexpr int kBufs = D == 256 ? 2 : 3;             // of K's, and of V's
   static constexpr int kKBufs2 = D == 256 ? 1 : 2;           // of K's in two parts
   static constexpr int kVBufs2 = 2;                          // of V's beside them
@@ -259,7 +259,9 @@ __global__ void __launch_bounds__(ManyShape<D>::kThreads, 1) kv4_many_kernel(con
     if (S::kTiles == 2) asm volatile("setmaxnreg.dec.sync.aligned.u32 56;");
     if (warp == kMmaWarp) {
     // ------------------------------------------------------------ the products
-    // (a choice within the loop keeps addresses out of the uniform registers: 4 %)
+    // (a choice within the loop keeps addresses out of the uniform registers, 4 %;
+    // both parts' instructions written out one behind the other would not fit the
+    // registers, 8 % where D = 256)
     auto products = [&](auto two_type) {
       constexpr bool kTwo = decltype(two_type)::value;
       constexpr uint32_t kStep = kTwo ? 2 * S::kKvTile : S::kKvTile;
@@ -277,19 +279,14 @@ __global__ void __launch_bounds__(ManyShape<D>::kThreads, 1) kv4_many_kernel(con
         umma_fence_after();
         if (one) {
           for (int t = 0; t < tiles; ++t) {
-#pragma unroll
-            for (int c = 0; c < D / 16; ++c)
-              umma_f16_ss(tmem + (uint32_t)((2 * t + (j & 1)) * S::kTokens),
-                          qd + (uint32_t)((t * S::kQTile + (c >> 2) * S::kQBlock + (c & 3) * 32) >> 4),
-                          kd + (uint32_t)((ka.slot * kStep + (c >> 2) * S::kKvBlock + (c & 3) * 32) >> 4),
-                          kIdS, c != 0);
-            if (kTwo) {
+#pragma unroll 1
+            for (int part = 0; part < (kTwo ? 2 : 1); ++part) {
+              const uint64_t k = kd + ((ka.slot * kStep + (uint32_t)part * S::kKvTile) >> 4);
 #pragma unroll
               for (int c = 0; c < D / 16; ++c)
                 umma_f16_ss(tmem + (uint32_t)((2 * t + (j & 1)) * S::kTokens),
                             qd + (uint32_t)((t * S::kQTile + (c >> 2) * S::kQBlock + (c & 3) * 32) >> 4),
-                            kd + (uint32_t)((ka.slot * kStep + S::kKvTile + (c >> 2) * S::kKvBlock + (c & 3) * 32) >> 4),
-                            kIdS, 1);
+                            k + (uint32_t)(((c >> 2) * S::kKvBlock + (c & 3) * 32) >> 4), kIdS, c != 0 || part != 0);
             }
             umma_commit(s_full + 8u * (2 * t + (j & 1)));
           }
@@ -379,9 +376,11 @@ __global__ void __launch_bounds__(ManyShape<D>::kThreads, 1) kv4_many_kernel(con
     for (int e = 0; e < 4; ++e)
       to[e] = (uint32_t)((piece >> 1) * S::kKvBlock + (w * S::kPerWarp + sub) * 128) +
               ((uint32_t)(((piece & 1) * 4 + e) ^ ((w * S::kPerWarp + sub) & 7)) << 4);
-    // into a tile; for V what is no number becomes zero.  The mask word of a
-    // pass: lanes of a position without a page (K), or of such a group (V)
-    auto store = [&](uint32_t tile, uint32_t* word_at, const Piece (&x)[S::kPasses]) {
+    // into a tile (kTwo: K's in two parts); for V what is no number becomes zero.
+    // The mask word of a pass: lanes of a position without a page (K), or of such
+    // a group (V)
+    auto store = [&](auto two_type, uint32_t tile, uint32_t* word_at, const Piece (&x)[S::kPasses]) {
+      constexpr bool kTwo = decltype(two_type)::value;
 #pragma unroll
       for (int i = 0; i < S::kPasses; ++i) {
         uint32_t az = x[i].az;
@@ -395,16 +394,18 @@ __global__ void __launch_bounds__(ManyShape<D>::kThreads, 1) kv4_many_kernel(con
         const uint4 c = x[i].codes;
         const __half2 f = *reinterpret_cast<const __half2*>(&az);
         const uint32_t row = tile + (uint32_t)(i * 4 * S::kPerWarp * 128);
-        if (!is_v && two_parts) {
+        if (kTwo) {
           const float2 az32 = __half22float2(f);
-          const uint32_t words[4] = {c.x, c.y, c.z, c.w};
-#pragma unroll
+          uint4 rest = c;  // (a word after the other: all at once they would not fit the registers)
+#pragma unroll 1
           for (int e = 0; e < 4; ++e) {
             uint4 first, second;
-            word_parts(words[e], az32.x, az32.y, first, second);
+            word_parts(rest.x, az32.x, az32.y, first, second);
             if (odd) second = make_uint4(0, 0, 0, 0);
-            sts_v4(row + to[e], first);
-            sts_v4(row + S::kKvTile + to[e], second);
+            const uint32_t at = row + (to[0] ^ ((uint32_t)e << 4));
+            sts_v4(at, first);
+            sts_v4(at + S::kKvTile, second);
+            rest = make_uint4(rest.y, rest.z, rest.w, rest.x);
           }
           continue;
         }
@@ -419,21 +420,26 @@ __global__ void __launch_bounds__(ManyShape<D>::kThreads, 1) kv4_many_kernel(con
     };
     // a step's codes are asked for a step ahead
     bool ok = true;
-    RingAt at;
-    Piece x[2][S::kPasses];
-    auto one_step = [&](int j, Piece (&now)[S::kPasses], Piece (&next)[S::kPasses]) {
-      load(next, j + 1);
-      if (at.round > 0 && !(ok = wait(empty + 8u * at.slot, at.round - 1))) return;
-      store(tiles_at + (uint32_t)at.slot * (is_v ? S::kKvTile : k_step), mask + (j & 7) * S::kWords, now);
-      __syncwarp();
-      if (lane == 0) mbar_arrive_cta(full + 8u * at.slot);
-      at.step(is_v ? v_bufs : k_bufs);
+    auto all_steps = [&](auto two_type) {
+      RingAt at;
+      Piece x[2][S::kPasses];
+      auto one_step = [&](int j, Piece (&now)[S::kPasses], Piece (&next)[S::kPasses]) {
+        load(next, j + 1);
+        if (at.round > 0 && !(ok = wait(empty + 8u * at.slot, at.round - 1))) return;
+        store(two_type, tiles_at + (uint32_t)at.slot * (is_v ? S::kKvTile : k_step), mask + (j & 7) * S::kWords, now);
+        __syncwarp();
+        if (lane == 0) mbar_arrive_cta(full + 8u * at.slot);
+        at.step(is_v ? v_bufs : k_bufs);
+      };
+      load(x[0], 0);
+      for (int j = 0; j < steps && ok; j += 2) {
+        one_step(j, x[0], x[1]);
+        if (ok && j + 1 < steps) one_step(j + 1, x[1], x[0]);
+      }
     };
-    load(x[0], 0);
-    for (int j = 0; j < steps && ok; j += 2) {
-      one_step(j, x[0], x[1]);
-      if (ok && j + 1 < steps) one_step(j + 1, x[1], x[0]);
-    }
+    // (a choice within the loop: 152 -> 193 us for 2048 rows of 256 over 4096)
+    if (two_parts && !is_v) all_steps(std::true_type());
+    else all_steps(std::false_type());
     if (!ok) give_up();
   } else {
     // -------------------------------------------------------------- the softmax
