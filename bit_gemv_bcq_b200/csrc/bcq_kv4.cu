@@ -409,9 +409,13 @@ __global__ void __launch_bounds__(kRowThreads) kv4_read_kernel(const ReadParams 
 //
 // What bounds it: with all SMs busy the ALU pipe (masks and permutes of codes,
 // some 55 %, beside 90 % of the memory's rate in the steady state) -- a row over
-// 524288 positions takes 113 us (5.3 TB/s), 64 rows over up to 8192 each, ragged,
-// 84.7 us (3.9 TB/s); below that a CTA's start (page table, then codes, some 3
-// us) and the joining kernel: 131072 positions 37.7 us, 4001 positions 7.9 us.
+// 524288 positions takes 120 us (5.0 TB/s), 64 rows over up to 8192 each, ragged,
+// 86.6 us (3.8 TB/s); below that a CTA's start (page table, then codes, some 3
+// us) and the joining kernel: 131072 positions 38.5 us, 4001 positions 8.0 us.
+// The looks at V's scales and their powers are 2 to 4 % of that.  (A second product
+// with what the rounding of p a leaves, the codes' operands being there, would
+// bring fp16 outputs of decode steps from 5.8e-4 of their norm to 3.1e-4, an
+// output's own rounding being 2.1e-4, and take 2 to 10 % more: 64 rows 95.1 us.)
 // Four CTAs of four warps an SM hide one another's loads: the registers of a
 // thread (128) leave no more, and three stages of 32 positions a warp are what
 // shared memory has room for.
@@ -1142,6 +1146,9 @@ __global__ void __launch_bounds__(128) kv4_join_kernel(const AttentionParams p) 
   const int64_t id = blockIdx.x;
   const int t = (int)((uint32_t)id / (uint32_t)p.q_heads), h = (int)((uint32_t)id % (uint32_t)p.q_heads);
   const int tid = threadIdx.x, set = tid / kLanes, lane = tid % kLanes;
+  // Row offsets and lengths are read ahead of the wait: the kernel whose parts are
+  // joined writes neither, and lets this one start only behind its own wait, when
+  // whatever wrote them has ended.
   const int b = sequence_of(p.at, t);
   Span sp = {};
   if (b >= 0)
@@ -1322,7 +1329,9 @@ struct AttentionPlan {
 };
 
 // How many parts the positions are cut into, by a model of the time (us, which is
-// returned).  `each` CTAs fit an SM; a CTA takes `start`, and `per` a position
+// returned) on the 148 SMs of a B200, on which its numbers were fitted (a constant:
+// the workspace's size must not depend on the device that is current when it is
+// asked for).  `each` CTAs fit an SM; a CTA takes `start`, and `per` a position
 // (beside each - 1 others); splitting at all takes `join`, and some a part.  While
 // all CTAs run at once the fullest SM decides, and fewer than `each` on it run
 // faster, though not in proportion; beyond that CTAs start as others end: the
@@ -1332,9 +1341,10 @@ struct PartsModel {
   int each;
   float there, per, start, join, join_part, tail;
 };
+constexpr int kSms = 148;
 float plan_parts(AttentionPlan* f, int64_t units, int max_kv, const PartsModel& m) {
   static const float kPace[5] = {0, 0.49f, 0.63f, 0.8f, 1.0f};
-  const float room = 148.f * (float)m.each, mean = m.there * (float)max_kv;
+  const float room = (float)kSms * (float)m.each, mean = m.there * (float)max_kv;
   float best = 0;
   const uint32_t kv = (uint32_t)max_kv;
   uint32_t chunk = ((kv + kMostParts - 1) / kMostParts + 127) & ~127u;
@@ -1344,7 +1354,7 @@ float plan_parts(AttentionPlan* f, int64_t units, int max_kv, const PartsModel& 
     const float ctas = (float)units * std::min(all, m.there * all + 0.5f);
     float cost;
     if (ctas <= room) {
-      const int fullest = ((int)ctas + 147) / 148;
+      const int fullest = ((int)ctas + kSms - 1) / kSms;
       cost = length * kPace[std::min(4, fullest * 4 / m.each)] + m.start;
     } else {
       cost = std::max(length * kPace[m.each == 1 ? 4 : 1] + m.start,

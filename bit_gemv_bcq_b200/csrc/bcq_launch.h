@@ -68,9 +68,12 @@ cudaError_t allow_smem(Kernel kernel, size_t bytes, std::atomic<uint64_t>& done)
 }
 
 // Launches a kernel that may be set up while the kernel before it in the stream
-// still runs: it has to execute grid_dependency_wait() before it touches memory
-// (and before launch_dependents(), so that what the next kernel does early is
-// behind all that came before this one).
+// still runs: it has to execute grid_dependency_wait() before it touches what
+// that one reads or writes, and before launch_dependents().  Every kernel does
+// the second, so all that came before the one before has ended when a kernel
+// starts, and what only earlier ones wrote may be read ahead of the wait (the
+// weight by the product behind its quantiser, lengths and row offsets by the
+// kernel that joins attention's parts).
 template <typename... P, typename... A>
 cudaError_t launch_early(void (*kernel)(P...), dim3 grid, unsigned threads, size_t smem,
                          cudaStream_t st, const A&... args) {
