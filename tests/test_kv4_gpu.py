@@ -1143,3 +1143,27 @@ def test_tensors_let_go_at_once_outlive_a_call_on_another_stream():
     torch.cuda.synchronize()
     assert all(torch.equal(a.view(torch.uint8), b.view(torch.uint8)) for a, b in zip(into, after))
     assert api.device_error() == api.BCQ_OK
+
+
+@pytest.mark.parametrize("heads,D", [(1, 64), (2, 128), (3, 256)])
+@pytest.mark.parametrize("B", [257, 700])
+def test_more_sequences_than_a_block_has_threads(B, heads, D):
+    """Their row offsets no longer lie in shared memory: in, out and attention, some sequences without rows or tokens."""
+    rng = np.random.default_rng(B + D)
+    new = [int(x) for x in rng.integers(0, 4, B)]
+    lens = [n + int(x) for n, x in zip(new, rng.integers(0, 40, B))]
+    new[5] = lens[5] = 0
+    c, k, v = _append_case(lens, new, heads, D, 16, F16)
+    api.kv4_append(c.cache, k, v, c.t_table, c.t_len, c.t_cu)
+    want = _expect_append(c, k, v)
+    _check_cache(c, want)
+    c.arrays = want
+    rk, rv = api.kv4_read(c.cache, c.t_table, c.t_len, c.t_cu, tokens=c.T, dtype=F32)
+    for got, x in ((rk, k), (rv, v)):
+        code, param = kv4.quantize(_f64(x))
+        assert np.array_equal(got.cpu().numpy(), kv4.values(kv4.pack(code), param).astype(np.float32))
+    q = _queries(c.T, 2 * heads, D, F16)
+    out, lse = _run(c, q)
+    _check_attention(c, q, out, lse)
+    out, lse = _run(c, q, 4000, max_q=5000)
+    _check_attention(c, q, out, lse)
