@@ -571,9 +571,9 @@ size_t bcq_kv4_attention_workspace_bytes(const bcq_kv4* cache, int T, int q_head
  *   rows that see fewer than 512 positions and for those beside them in a block
  *   of 256 (128 with D = 256), so only a row that sees 512 or more has scores
  *   that are off by up to 2^-11 of |scale| sum_d |q_d K_jd|.
- * An output is then off by about 2^-10 of sum_j p_j |V_j|, lse by the scores'
- * error, averaged over the positions that weigh.  Results do not depend on
- * scheduling.
+ * An output is then off by up to 2^-10 of sum_j p_j (a_j c_j + |z_j|) (and, where
+ * scores are, by what that makes of the weights), lse by the scores' error,
+ * averaged over the positions that weigh.  Results do not depend on scheduling.
  * Errors as for bcq_kv4_append; a scale that is not finite -> BCQ_ERR_SHAPE.
  */
 bcq_status bcq_kv4_attention(const bcq_kv4* cache, const void* q, int64_t ld_q, int64_t hd_q,
