@@ -415,7 +415,7 @@ __global__ void __launch_bounds__(kRowThreads) kv4_read_kernel(const ReadParams 
 // The looks at V's scales and their powers are 2 to 4 % of that.  (A second product
 // with what the rounding of p a leaves, the codes' operands being there, would
 // bring fp16 outputs of decode steps from 5.8e-4 of their norm to 3.1e-4, an
-// output's own rounding being 2.1e-4, and take 2 to 10 % more: 64 rows 95.1 us.)
+// output's own rounding being 2.1e-4, and take 2 to 11 % more: 64 rows 95.1 us.)
 // Four CTAs of four warps an SM hide one another's loads: the registers of a
 // thread (128) leave no more, and three stages of 32 positions a warp are what
 // shared memory has room for.
